@@ -54,7 +54,7 @@ typedef enum {
     SV_ERR_DEVICE_DATA = 5    /* returned only by sv_read_device_error: bad device data  */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 /* spec_cache.h only */ } sv_dtype;
 
 /* Device-data error codes stored in the workspace's sticky error word. */
 enum {

@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(HERE, "libspecverify.so")
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_WORKSPACE, SV_ERR_CUDA, SV_ERR_UNSUPPORTED, SV_ERR_DEVICE_DATA = range(6)
 SV_F32, SV_BF16 = 0, 1
 DEV_ERRORS = {0: "ok", 1: "bad layout", 2: "bad token", 3: "bad temperature", 4: "bad top_p",
-              5: "bad uniform", 6: "bad penalty", 7: "timeout", 8: "bad history"}
+              5: "bad uniform", 6: "bad penalty", 7: "timeout", 8: "bad history", 9: "bad page", 10: "no pages",
+              11: "shared page"}
 
 
 class SvParams(C.Structure):
@@ -238,3 +239,14 @@ def sv_read_device_error(workspace):
     if st not in (SV_OK, SV_ERR_DEVICE_DATA):
         raise SvError(st, "sv_read_device_error")
     return int(code.value), int(bad.value)
+
+
+def __getattr__(name):
+    """The cache-side calls (cache.py, which imports torch) by the package's name."""
+    if name in ("spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
+                "spec_page_compact", "spec_page_copy", "sv_attention_workspace_bytes", "sv_page_workspace_bytes",
+                "SvKvCache", "SV_F16"):
+        from . import cache
+        globals()[name] = f = getattr(cache, name)
+        return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -27,7 +27,8 @@ def sources():
 
 def deps():
     out = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    out.append(os.path.join(os.path.dirname(HERE), "include", "spec_verify.h"))
+    include = os.path.join(os.path.dirname(HERE), "include")
+    out.extend(os.path.join(include, f) for f in sorted(os.listdir(include)))
     return out
 
 

@@ -1,0 +1,207 @@
+// cache_append.cu -- spec_append: per-head norm and rotation of the new tokens' queries and keys
+// and the append of keys and values to the paged cache.
+//
+// Mathematics: y = x * rsqrt(mean(x^2) + eps) * w; each pair (a, z) of y turns by the angle
+// t * inv_freq[j].  The angle in turns is the exact product of the position t and inv_freq / 2 pi
+// modulo 1, kept as a 64-bit binary fraction: inv_freq = m 2^e, so m * round(2^64 / 2 pi) shifted
+// by e is inv_freq / 2 pi within 2^-64 (plus the shift's own truncation), and its product with t,
+// wrapping at 2^64, is the fraction of a turn within t * 2^-63.  Only then does it become a float
+// (24 bits of a half turn), so the rotation is as exact at position 10^6 as at 0.
+#include <math.h>
+
+#include "sv_cache.cuh"
+
+namespace svc {
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const void *qw, *kw;
+    const float *inv_freq;
+    void *out;
+    int32_t *hdr;
+    float eps, rope_scale;
+    int Hq, half, interleaved;
+};
+
+// inv_freq / (2 pi) as a 64-bit binary fraction of a turn, modulo 1.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    const uint64_t inv2pi = 0x28BE60DB9391054Aull;   // round(2^64 / (2 pi))
+    const uint32_t u = __float_as_uint(f);
+    const int ex = (u >> 23) & 0xff;
+    const uint64_t m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int sh = 150 - (ex ? ex : 1);              // f = m 2^-sh
+    const uint64_t lo = m * inv2pi, hi = __umul64hi(m, inv2pi);
+    uint64_t t;
+    if (sh <= 0) t = sh > -64 ? lo << -sh : 0;
+    else if (sh < 64) t = (lo >> sh) | (hi << (64 - sh));
+    else t = sh < 128 ? hi >> (sh - 64) : 0;
+    return (u >> 31) ? 0 - t : t;
+}
+
+constexpr int AT = 256;   // threads per CTA
+
+// One CTA per row.  LPH lanes hold one head, 8 elements each (a power of two >= head_dim / 8), so
+// a warp holds 32 / LPH heads; the CTA walks over the row's query, key and value heads.
+template <typename E, int LPH>
+__global__ void __launch_bounds__(AT) append_kernel(const Batch A, const Cache C, const AppendArgs P) {
+    __shared__ float2 turn[128];      // (cos, sin) * rope_scale of each pair
+    __shared__ float ex[AT / 32][32 / LPH][LPH * 8 + 4];
+    __shared__ int64_t slot;          // the token's offset in the cache, or -1
+    __shared__ int state;             // 0: unused row, 1: used, 2: in error
+    __shared__ int pos_s;
+    const int r = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 32) check_requests(A, C.max_pages << C.page_shift, P.hdr, r, A.R);
+    if (threadIdx.x == 0) {
+        const int b = request_of(A, r);
+        int st = 0, pos = 0;
+        if (b >= 0) {
+            const Span s = span_of(A, C.max_pages << C.page_shift, b);
+            if (s.err) {
+                st = 2;
+            } else if (r - s.row0 < s.n) {
+                pos = s.len - s.n + (r - s.row0);
+                const int page = __ldg(C.table + (int64_t)b * C.max_pages + (pos >> C.page_shift));
+                if (page < 0 || page >= C.num_pages) {
+                    record_error(P.hdr, SV_DEV_BAD_PAGE, b);
+                    st = 2;
+                } else {
+                    st = 1;
+                    slot = page * C.page_stride + (pos & ((1 << C.page_shift) - 1)) * C.token_stride;
+                }
+            }
+        }
+        state = st;
+        pos_s = pos;
+    }
+    __syncthreads();
+    const int D = C.D, Hq = P.Hq, Hk = C.heads;
+    const int st = state;
+    E *out = static_cast<E *>(P.out) + r * P.out_stride;
+    if (st != 1) {
+        const uint32_t w = st == 2 ? Num<E>::NAN2 : 0u;
+        for (int i = threadIdx.x; i < Hq * D / 8; i += AT) reinterpret_cast<uint4 *>(out)[i] = make_uint4(w, w, w, w);
+        return;
+    }
+    for (int j = threadIdx.x; j < P.half; j += AT) {
+        const float f = __ldg(P.inv_freq + j);
+        const uint64_t t = turns_of(f) * (uint64_t)(uint32_t)pos_s;
+        float s, c;
+        sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &s, &c);
+        if (!(fabsf(f) < INFINITY)) s = c = NAN;
+        turn[j] = make_float2(c * P.rope_scale, s * P.rope_scale);
+    }
+    __syncthreads();
+    const int64_t at = slot;
+    const int sub = lane % LPH, grp = lane / LPH;
+    const bool in = sub * 8 < D;
+    const int rot = 2 * P.half;
+    float *mine = ex[warp][grp];
+    constexpr int HPC = AT / LPH;   // heads per CTA pass
+    const int heads = Hq + 2 * Hk;
+    for (int h0 = 0; h0 < heads; h0 += HPC) {
+        const int h = h0 + warp * (32 / LPH) + grp;
+        const bool on = in && h < heads;
+        const E *src = static_cast<const E *>(P.q) + r * P.q_stride + (int64_t)h * D;
+        E *dst = out + (int64_t)h * D;
+        const E *w = static_cast<const E *>(P.qw);
+        bool turned = true;
+        if (h >= Hq + Hk) {
+            src = static_cast<const E *>(P.v) + r * P.v_stride + (int64_t)(h - Hq - Hk) * D;
+            dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
+            w = nullptr;
+            turned = false;
+        } else if (h >= Hq) {
+            src = static_cast<const E *>(P.k) + r * P.k_stride + (int64_t)(h - Hq) * D;
+            dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
+            w = static_cast<const E *>(P.kw);
+        }
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (on) raw = *reinterpret_cast<const uint4 *>(src + sub * 8);
+        float x[8];
+        unpack8<E>(raw, x);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (on && w) {
+            float g[8];
+            unpack8<E>(*reinterpret_cast<const uint4 *>(w + sub * 8), g);
+            const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[i] *= inv * g[i];
+        }
+        if (P.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                if (turned && sub * 8 + i < rot) {
+                    const float2 t = turn[(sub * 8 + i) / 2];
+                    const float a = x[i], z = x[i + 1];
+                    x[i] = a * t.x - z * t.y;
+                    x[i + 1] = a * t.y + z * t.x;
+                }
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) mine[sub * 8 + i] = x[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int d = sub * 8 + i;
+                if (turned && d < rot) {
+                    const bool low = d < P.half;
+                    const float2 t = turn[low ? d : d - P.half];
+                    const float o = mine[low ? d + P.half : d - P.half];
+                    x[i] = low ? x[i] * t.x - o * t.y : o * t.y + x[i] * t.x;
+                }
+            }
+        }
+        if (on) *reinterpret_cast<uint4 *>(dst + sub * 8) = turned ? pack8<E>(x) : raw;
+    }
+}
+
+template <typename E>
+static cudaError_t launch_append(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {
+    const int lanes = C.D / 8;
+    if (lanes <= 8) append_kernel<E, 8><<<A.R, AT, 0, st>>>(A, C, P);
+    else if (lanes <= 16) append_kernel<E, 16><<<A.R, AT, 0, st>>>(A, C, P);
+    else append_kernel<E, 32><<<A.R, AT, 0, st>>>(A, C, P);
+    return cudaGetLastError();
+}
+
+}  // namespace svc
+
+using namespace svc;
+
+extern "C" sv_status spec_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, int32_t num_q_heads, const void *q_weight, const void *k_weight,
+                                 float eps, const float *inv_freq, int32_t rotary_dim, int32_t interleaved,
+                                 float rope_scale, const int32_t *num_drafts, const int32_t *row_offsets,
+                                 const int32_t *kv_seq_len, int32_t B, int32_t k_max, int32_t total_rows,
+                                 sv_kv_cache cache, void *out_q, int64_t out_q_stride, void *workspace,
+                                 void *stream) {
+    Batch A;
+    Cache C;
+    const sv_status bad = check_batch(num_drafts, row_offsets, kv_seq_len, B, k_max, total_rows, num_q_heads, cache,
+                                      256, A, C);
+    if (bad != SV_OK) return bad;
+    if (!q || !k || !v || !out_q || !workspace) return SV_ERR_INVALID_ARG;
+    if (rotary_dim < 0 || rotary_dim % 2 || rotary_dim > cache.head_dim || (rotary_dim && !inv_freq))
+        return SV_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !(eps < INFINITY) || !(fabsf(rope_scale) < INFINITY)) return SV_ERR_INVALID_ARG;
+    const int64_t qw = (int64_t)num_q_heads * cache.head_dim, kw = (int64_t)cache.num_heads * cache.head_dim;
+    if (q_stride < qw || out_q_stride < qw || k_stride < kw || v_stride < kw) return SV_ERR_INVALID_ARG;
+    if ((q_stride | k_stride | v_stride | out_q_stride) % 8 || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(out_q) || !aligned16(q_weight) || !aligned16(k_weight))
+        return SV_ERR_UNSUPPORTED;
+    if ((uintptr_t)workspace & 255) return SV_ERR_WORKSPACE;
+    const AppendArgs P{q, k, v, q_stride, k_stride, v_stride, out_q_stride, q_weight, k_weight, inv_freq, out_q,
+                       static_cast<int32_t *>(workspace), eps, rope_scale, num_q_heads, rotary_dim / 2, interleaved};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache.dtype == SV_BF16 ? launch_append<__nv_bfloat16>(A, C, P, st)
+                                                 : launch_append<__half>(A, C, P, st);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}

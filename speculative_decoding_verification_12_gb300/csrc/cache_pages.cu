@@ -1,0 +1,662 @@
+// cache_pages.cu -- page bookkeeping of the paged KV cache: reserve, fork, release, compact, copy.
+//
+// The only record of what is free is ref_count itself (0: free), and pages are taken lowest id
+// first, in request order: rank r of the free pages goes to the r-th page asked for.  Both ranks
+// are prefix sums, so a call is two scans joined by rank: one thread-block cluster counts the
+// free pages of its warps' slices, exchanges the counts through distributed shared memory, and
+// writes the first pages asked for as a list; its first CTA then walks the requests.  Nothing
+// depends on the order of atomics, and no free list has to be kept consistent between calls.
+// These kernels move a few hundred KB at most and are bound by latency (launch, two dependent
+// passes over the counts, one cluster barrier); only spec_page_copy is bound by bandwidth.
+#include <cooperative_groups.h>
+#include <limits.h>
+
+#include "sv_cache.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace svc {
+
+constexpr int PT = 1024;              // threads per bookkeeping CTA
+constexpr int PW = PT / 32;
+constexpr int PAGES_PER_CTA = 8192;   // cluster CTAs: one per so many pages, at most 8
+
+struct PageState {
+    int32_t *len, *table, *ref;
+    int B, max_pages, num_pages, page_size;
+    int32_t *hdr;
+    int32_t *list;      // workspace: num_pages entries
+    int32_t *result;    // workspace: B entries (fork: the child's length, or -1)
+    int32_t *used;      // workspace: pages in use (compact)
+};
+
+struct PageWs {
+    size_t list, result, used, total;
+};
+static inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+static inline PageWs page_ws(int B, int num_pages) {
+    PageWs L;
+    L.used = HEADER;
+    L.list = 2 * HEADER;
+    L.result = up256(L.list + (size_t)num_pages * 4);
+    L.total = up256(L.result + (size_t)B * 4);
+    return L;
+}
+
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+
+// Inclusive prefix sum over the warp.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((int)(threadIdx.x & 31) >= o) x += y;
+    }
+    return x;
+}
+
+// Exclusive prefix sum over the CTA; *total receives the sum.  tmp: PW + 1 words.
+__device__ __forceinline__ long long cta_scan(long long x, long long *tmp, long long *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long inc = warp_scan(x);
+    __syncthreads();
+    if (lane == 31) tmp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const long long w = tmp[lane];
+        const long long s = warp_scan(w);
+        tmp[lane] = s - w;
+        if (lane == 31) tmp[PW] = s;
+    }
+    __syncthreads();
+    *total = tmp[PW];
+    return tmp[warp] + inc - x;
+}
+
+// A warp's slice of the pool: [lo, hi), a multiple of 128 pages long except at the pool's end.
+struct Slice {
+    int lo, hi;
+};
+__device__ __forceinline__ Slice slice_of(int num_pages, int rank, int nranks) {
+    const int warp = rank * PW + (int)(threadIdx.x >> 5), nw = nranks * PW;
+    const long long per = (((long long)num_pages + nw - 1) / nw + 127) / 128 * 128;
+    Slice s;
+    s.lo = (int)min((long long)num_pages, per * warp);
+    s.hi = (int)min((long long)num_pages, per * (warp + 1));
+    return s;
+}
+
+// Bits 0..3: which of the lane's 4 pages at i (within the slice) are in use; `have`: which exist.
+__device__ __forceinline__ int used4(const int32_t *ref, int i, int hi, int &have) {
+    int v[4] = {0, 0, 0, 0};
+    have = 0;
+    if (i + 4 <= hi && ((uintptr_t)(ref + i) & 15) == 0) {
+        const int4 w = *reinterpret_cast<const int4 *>(ref + i);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        have = 15;
+    } else {
+        for (int t = 0; t < 4; t++)
+            if (i + t < hi) v[t] = ref[i + t], have |= 1 << t;
+    }
+    int m = 0;
+    for (int t = 0; t < 4; t++) m |= (v[t] != 0) << t;
+    return m;
+}
+
+// Exclusive prefix of this warp's count over all warps of the cluster, and the total.
+// counts: this CTA's PW + 1 shared words.  Contains cluster barriers.
+__device__ __forceinline__ int cluster_prefix(int count, int *counts, int *total) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) counts[warp] = count;
+    __syncthreads();
+    if (warp == 0) {
+        const int c = counts[lane];
+        const int s = warp_scan(c);
+        __syncwarp();
+        counts[lane] = s - c;
+        if (lane == 31) counts[PW] = s;
+    }
+    cl.sync();
+    int before = 0, all = 0;
+    for (unsigned r = 0; r < cl.num_blocks(); r++) {
+        const int c = cl.map_shared_rank(counts, r)[PW];
+        all += c;
+        if (r < cl.block_rank()) before += c;
+    }
+    *total = all;
+    return before + counts[warp];
+}
+
+// Writes the lowest `want` free pages to S.list in ascending order and returns how many free
+// pages there are; the list is visible to the whole cluster on return.
+__device__ __forceinline__ int list_free(const PageState &S, long long want, int *counts) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31;
+    const Slice sl = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
+    int count = 0;
+    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
+        int have;
+        const int m = used4(S.ref, i, sl.hi, have);
+        count += __popc(have & ~m);
+    }
+    count = warp_sum(count);
+    int total;
+    int at = cluster_prefix(count, counts, &total);
+    for (int base = sl.lo; base < sl.hi && at < want; base += 128) {
+        const int i = base + 4 * lane;
+        int have;
+        const int m = used4(S.ref, i, sl.hi, have);
+        const int f = have & ~m, c = __popc(f);
+        const int inc = warp_scan(c);
+        int r = at + inc - c;
+        for (int t = 0; t < 4; t++)
+            if (f >> t & 1) {
+                if (r < want) S.list[r] = i + t;
+                r++;
+            }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    __threadfence();
+    cl.sync();
+    return total;
+}
+
+// ---------------------------------------------------------------------------------------------
+// reserve
+// ---------------------------------------------------------------------------------------------
+
+struct Want {
+    int err, have, grown;
+    long long need;
+};
+
+__device__ __forceinline__ Want want_of(const PageState &S, const int32_t *nd, int b) {
+    Want w = {0, 0, 0, 0};
+    const int k = nd[b], len = S.len[b];
+    if (k == -1) return w;
+    const long long grown = (long long)len + k + 1;
+    if (k < -1 || len < 0 || grown > (long long)S.max_pages * S.page_size) {
+        w.err = SV_DEV_BAD_LAYOUT;
+        return w;
+    }
+    w.have = len / S.page_size + (len % S.page_size != 0);
+    w.grown = (int)grown;
+    w.need = (grown + S.page_size - 1) / S.page_size - w.have;
+    if (len % S.page_size) {   // the partly filled page: this request's alone
+        const int p = S.table[(int64_t)b * S.max_pages + w.have - 1];
+        if (p < 0 || p >= S.num_pages) w.err = SV_DEV_BAD_PAGE;
+        else if (S.ref[p] != 1) w.err = S.ref[p] > 1 ? SV_DEV_SHARED_PAGE : SV_DEV_BAD_PAGE;
+        if (w.err) w.need = 0;
+    }
+    return w;
+}
+
+__global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const int32_t *nd) {
+    __shared__ int counts[PW + 1];
+    __shared__ long long tmp[PW + 1];
+    const int lane = threadIdx.x & 31;
+    long long sum = 0, want = 0;
+    for (int b = threadIdx.x; b < S.B; b += PT) sum += want_of(S, nd, b).need;
+    cta_scan(sum, tmp, &want);
+    // (never past the list, whatever the counts say on the second look)
+    const long long free = min((long long)list_free(S, want, counts), want);
+    if (cg::this_cluster().block_rank() != 0) return;
+    long long before = 0;
+    for (int b0 = 0; b0 < S.B; b0 += PT) {
+        const int b = b0 + (int)threadIdx.x;
+        const bool in = b < S.B;
+        Want w = {0, 0, 0, 0};
+        if (in) w = want_of(S, nd, b);
+        long long all;
+        const long long at = before + cta_scan(w.need, tmp, &all);
+        before += all;
+        if (w.need > 0 && at + w.need > free) {
+            w.err = SV_DEV_NO_PAGES;
+            w.need = 0;
+        }
+        if (in && w.err) {
+            record_error(S.hdr, w.err, b);
+            if (S.len[b] >= 0) S.len[b] = -1 - S.len[b];
+        } else if (in && nd[b] >= 0) {
+            S.len[b] = w.grown;
+        }
+        int32_t *row = S.table + (int64_t)b * S.max_pages + w.have;
+        const int small = w.need <= 4 ? (int)w.need : 0;
+        for (int i = 0; i < small; i++) {
+            const int p = S.list[at + i];
+            row[i] = p;
+            S.ref[p] = 1;
+        }
+        // longer ones (a prompt's pages) by the whole warp
+        for (unsigned m = __ballot_sync(0xffffffffu, w.need > 4); m; m &= m - 1) {
+            const int l = __ffs(m) - 1;
+            const long long n = __shfl_sync(0xffffffffu, w.need, l), a = __shfl_sync(0xffffffffu, at, l);
+            int32_t *to = reinterpret_cast<int32_t *>(__shfl_sync(0xffffffffu, (unsigned long long)row, l));
+            for (long long i = lane; i < n; i += 32) {
+                const int p = S.list[a + i];
+                to[i] = p;
+                S.ref[p] = 1;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------------------------
+
+struct ForkArgs {
+    const int32_t *parents, *children, *fork_len;   // fork_len may be NULL
+    int32_t *src, *dst;
+    int F;
+};
+
+// The error of fork f as the state was before the call, its length and its partly filled page.
+__device__ __forceinline__ int fork_check(const PageState &S, const ForkArgs &K, int f, int &n, int &tail) {
+    const int p = K.parents[f], c = K.children[f];
+    n = 0;
+    tail = -1;
+    if (p < 0 || p >= S.B || c < 0 || c >= S.B || S.len[c] != 0) return SV_DEV_BAD_LAYOUT;
+    const int len = S.len[p];
+    n = K.fork_len ? K.fork_len[f] : len;
+    if (n < 1 || n > len || (long long)n > (long long)S.max_pages * S.page_size) return SV_DEV_BAD_LAYOUT;
+    if (n % S.page_size) {
+        tail = S.table[(int64_t)p * S.max_pages + n / S.page_size];
+        if (tail < 0 || tail >= S.num_pages || S.ref[tail] < 1) return SV_DEV_BAD_PAGE;
+    }
+    return 0;
+}
+
+// Decides every fork, takes the fresh pages and sets the children's lengths (fork_share does the
+// tables).  An empty child goes to the lowest f that names it: that f's claim is the smallest
+// value INT_MIN + f left in its length.
+__global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkArgs K) {
+    __shared__ int counts[PW + 1];
+    __shared__ long long tmp[PW + 1];
+    const int free = list_free(S, K.F, counts);
+    if (cg::this_cluster().block_rank() != 0) return;
+    for (int f = threadIdx.x; f < K.F; f += PT) {
+        int n, tail;
+        const int err = fork_check(S, K, f, n, tail);
+        const int c = K.children[f];
+        const bool claims = c >= 0 && c < S.B && S.len[c] == 0;
+        S.result[f] = err ? -err : n;
+        K.src[f] = tail;
+        K.dst[f] = claims ? 1 : 0;
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < K.F; f += PT)
+        if (K.dst[f]) atomicMin(S.len + K.children[f], INT_MIN + f);
+    __syncthreads();
+    long long before = 0;
+    for (int f0 = 0; f0 < K.F; f0 += PT) {
+        const int f = f0 + (int)threadIdx.x;
+        const bool in = f < K.F;
+        int n = 0, tail = -1, err = 0;
+        bool mine = false;
+        if (in) {
+            n = S.result[f];
+            err = n < 0 ? -n : 0;
+            tail = K.src[f];
+            mine = K.dst[f] && __ldcg(S.len + K.children[f]) == INT_MIN + f;
+            if (!mine && !err) err = SV_DEV_BAD_LAYOUT;
+        }
+        const int need = (in && !err && tail >= 0) ? 1 : 0;
+        long long all;
+        const long long at = before + cta_scan(need, tmp, &all);
+        before += all;
+        int fresh = -1;
+        if (need) {
+            if (at >= free) err = SV_DEV_NO_PAGES;
+            else fresh = S.list[at];
+        }
+        if (in) {
+            if (err) record_error(S.hdr, err, f);
+            if (mine) S.len[K.children[f]] = err ? -1 : n;
+            if (fresh >= 0) S.ref[fresh] = 1;
+            S.result[f] = err ? -1 : n;
+            K.src[f] = fresh >= 0 ? tail : -1;
+            K.dst[f] = fresh;
+        }
+    }
+}
+
+constexpr int ST = 256, SPT = 4;   // threads per CTA, table entries per thread
+
+__global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkArgs K) {
+    const int f = blockIdx.x;
+    const int n = S.result[f];
+    if (n < 0) return;
+    const int32_t *from = S.table + (int64_t)K.parents[f] * S.max_pages;
+    int32_t *to = S.table + (int64_t)K.children[f] * S.max_pages;
+    const int full = n / S.page_size, fresh = K.dst[f];
+#pragma unroll
+    for (int t = 0; t < SPT; t++) {
+        const int j = (blockIdx.y * SPT + t) * ST + threadIdx.x;
+        if (j >= S.max_pages) break;
+        int p = -1;
+        if (j < full) {
+            p = from[j];
+            if (p >= S.num_pages || p < -1) {
+                record_error(S.hdr, SV_DEV_BAD_PAGE, f);
+                p = -1;
+            } else if (p >= 0 && atomicAdd(S.ref + p, 1) < 1) {
+                atomicSub(S.ref + p, 1);
+                record_error(S.hdr, SV_DEV_BAD_PAGE, f);
+                p = -1;
+            }
+        } else if (j == full) {
+            p = fresh;
+        }
+        to[j] = p;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// release
+// ---------------------------------------------------------------------------------------------
+
+constexpr int RELEASE_CHUNK = ST * SPT;
+
+// Gives one entry back; returns whether it held anything.
+__device__ __forceinline__ bool give_back(const PageState &S, int32_t *e, int b) {
+    const int p = *e;
+    if (p == -1) return false;
+    *e = -1;
+    if (p < 0 || p >= S.num_pages) {
+        record_error(S.hdr, SV_DEV_BAD_PAGE, b);
+    } else if (atomicSub(S.ref + p, 1) < 1) {
+        atomicAdd(S.ref + p, 1);
+        record_error(S.hdr, SV_DEV_BAD_PAGE, b);
+    }
+    return true;
+}
+
+// One CTA per request and direction (y = 0: past the length, upward; 1: before the window,
+// downward), RELEASE_CHUNK entries at a time until a chunk holds nothing.
+__global__ void __launch_bounds__(ST) release_kernel(const PageState S, int window, int sinks) {
+    const int b = blockIdx.x;
+    const int len = S.len[b];
+    if (len < 0) return;
+    int32_t *row = S.table + (int64_t)b * S.max_pages;
+    const int keep = len / S.page_size + (len % S.page_size != 0);
+    if (keep > S.max_pages) {
+        if (threadIdx.x == 0) record_error(S.hdr, SV_DEV_BAD_LAYOUT, b);
+        return;
+    }
+    if (blockIdx.y == 0) {
+        for (int base = keep; base < S.max_pages; base += RELEASE_CHUNK) {
+            bool any = false;
+#pragma unroll
+            for (int t = 0; t < SPT; t++) {
+                const int j = base + t * ST + threadIdx.x;
+                if (j < S.max_pages) any |= give_back(S, row + j, b);
+            }
+            if (!__syncthreads_or(any)) break;
+        }
+    } else {
+        // pages [first, last): all tokens >= sinks, all tokens <= len - window
+        const int first = sinks / S.page_size + (sinks % S.page_size != 0);
+        const long long gone = (long long)len - window + 1;
+        const int last = gone > 0 ? (int)(gone / S.page_size) : 0;
+        for (int top = last; top > first; top -= RELEASE_CHUNK) {
+            bool any = false;
+#pragma unroll
+            for (int t = 0; t < SPT; t++) {
+                const int j = top - 1 - t * ST - (int)threadIdx.x;
+                if (j >= first) any |= give_back(S, row + j, b);
+            }
+            if (!__syncthreads_or(any)) break;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------------------------
+
+// The r-th used page at or above U (pages in use) pairs with the r-th free page below U; there
+// are equally many.  S.list becomes the map from page to page for ids >= U.
+__global__ void __launch_bounds__(PT) compact_kernel(const PageState S, int32_t *src, int32_t *dst, int cap) {
+    __shared__ int counts[3][PW + 1];
+    cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31;
+    const Slice sl = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
+    int count = 0;
+    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
+        int have;
+        count += __popc(used4(S.ref, i, sl.hi, have));
+    }
+    int U, moves, holes;
+    cluster_prefix(warp_sum(count), counts[0], &U);
+    int up = 0, down = 0;
+    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
+        int have;
+        const int m = used4(S.ref, i, sl.hi, have);
+        const int below = U <= i ? 0 : (U >= i + 4 ? 15 : (1 << (U - i)) - 1);   // ids < U
+        up += __popc(m & ~below);
+        down += __popc(have & ~m & below);
+    }
+    int at_up = cluster_prefix(warp_sum(up), counts[1], &moves);
+    int at_down = cluster_prefix(warp_sum(down), counts[2], &holes);
+    for (int base = sl.lo; base < sl.hi; base += 128) {
+        const int i = base + 4 * lane;
+        int have;
+        const int m = used4(S.ref, i, sl.hi, have);
+        const int below = U <= i ? 0 : (U >= i + 4 ? 15 : (1 << (U - i)) - 1);
+        const int fu = m & ~below, fd = have & ~m & below, free_above = have & ~m & ~below;
+        const int iu = warp_scan(__popc(fu)), id = warp_scan(__popc(fd));
+        int ru = at_up + iu - __popc(fu), rd = at_down + id - __popc(fd);
+        for (int t = 0; t < 4; t++) {
+            if (fu >> t & 1) {
+                if (ru < cap) src[ru] = i + t;
+                else S.list[i + t] = i + t;   // past the capacity: stays
+                ru++;
+            }
+            if (fd >> t & 1) {
+                if (rd < cap) dst[rd] = i + t;
+                rd++;
+            }
+            if (free_above >> t & 1) S.list[i + t] = i + t;
+        }
+        at_up += __shfl_sync(0xffffffffu, iu, 31);
+        at_down += __shfl_sync(0xffffffffu, id, 31);
+    }
+    __threadfence();
+    cl.sync();
+    const int n = min(moves, cap), step = cl.num_blocks() * PT;
+    for (int r = cl.block_rank() * PT + threadIdx.x; r < cap; r += step) {
+        if (r < n) {
+            const int a = __ldcg(src + r), d = __ldcg(dst + r);
+            S.ref[d] = S.ref[a];
+            S.ref[a] = 0;
+            S.list[a] = d;
+        } else {
+            src[r] = dst[r] = -1;
+        }
+    }
+    if (cl.block_rank() == 0 && threadIdx.x == 0) *S.used = U;
+    cl.sync();   // no CTA leaves while another may still read its counts
+}
+
+__global__ void __launch_bounds__(ST) remap_kernel(const PageState S) {
+    const int U = *S.used;
+    const long long total = (long long)S.B * S.max_pages;
+    for (long long j = (long long)blockIdx.x * ST + threadIdx.x; j < total; j += (long long)gridDim.x * ST) {
+        const int p = S.table[j];
+        if (p < U) continue;
+        const int to = p < S.num_pages ? S.list[p] : p;
+        if (p >= S.num_pages || (to == p && S.ref[p] == 0)) record_error(S.hdr, SV_DEV_BAD_PAGE, (int)(j / S.max_pages));
+        else S.table[j] = to;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// copy
+// ---------------------------------------------------------------------------------------------
+
+struct CopyArgs {
+    char *k, *v;
+    const int32_t *src, *dst;
+    int64_t page_bytes, page_stride, layer_stride;
+    int32_t *hdr;
+    int num_pages, layers, n;
+};
+
+constexpr int CT = 256, CU = 8;   // threads per CTA, 16-byte loads in flight per thread
+
+__global__ void __launch_bounds__(CT) copy_kernel(const CopyArgs A) {
+    const long long per_pair = (long long)A.layers * (A.v ? 2 : 1);
+    const long long items = per_pair * A.n;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int i = (int)(it / per_pair), part = (int)(it % per_pair);
+        const int s = __ldg(A.src + i), d = __ldg(A.dst + i);
+        if (s < 0 || d < 0) continue;
+        if (s >= A.num_pages || d >= A.num_pages) {
+            if (part == 0 && threadIdx.x == 0) record_error(A.hdr, SV_DEV_BAD_PAGE, i);
+            continue;
+        }
+        char *base = (part >= A.layers ? A.v : A.k) + (part % A.layers) * A.layer_stride;
+        const uint4 *from = reinterpret_cast<const uint4 *>(base + s * A.page_stride);
+        uint4 *to = reinterpret_cast<uint4 *>(base + d * A.page_stride);
+        const long long words = A.page_bytes / 16;
+        for (long long w0 = 0; w0 < words; w0 += CT * CU) {
+            uint4 x[CU];
+#pragma unroll
+            for (int u = 0; u < CU; u++) {
+                const long long w = w0 + u * CT + threadIdx.x;
+                if (w < words) x[u] = __ldcs(from + w);
+            }
+#pragma unroll
+            for (int u = 0; u < CU; u++) {
+                const long long w = w0 + u * CT + threadIdx.x;
+                if (w < words) __stcs(to + w, x[u]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------------
+
+static sv_status check_pages(int32_t B, const void *table, int32_t max_pages, const void *ref, int32_t num_pages,
+                             int32_t page_size, const void *ws) {
+    if (B < 1 || max_pages < 1 || num_pages < 1 || page_size < 1 || !table || !ref || !ws) return SV_ERR_INVALID_ARG;
+    if (B >= MAXB || max_pages > (1 << 20) || num_pages >= (1 << 28) || (long long)B * max_pages >= (1ll << 40) ||
+        (long long)max_pages * page_size > 0x7fffffffll)
+        return SV_ERR_UNSUPPORTED;
+    if ((uintptr_t)ws & 255) return SV_ERR_WORKSPACE;
+    return SV_OK;
+}
+
+static PageState page_state(int32_t *len, int32_t B, int32_t *table, int32_t max_pages, int32_t *ref,
+                            int32_t num_pages, int32_t page_size, void *ws) {
+    const PageWs L = page_ws(B, num_pages);
+    char *w = static_cast<char *>(ws);
+    return PageState{len, table, ref, B, max_pages, num_pages, page_size, reinterpret_cast<int32_t *>(w),
+                     reinterpret_cast<int32_t *>(w + L.list), reinterpret_cast<int32_t *>(w + L.result),
+                     reinterpret_cast<int32_t *>(w + L.used)};
+}
+
+// Launches a bookkeeping kernel as one cluster.
+template <typename... P, typename... A>
+static cudaError_t launch_cluster(void (*kernel)(P...), int num_pages, cudaStream_t st, A... args) {
+    int ctas = 1;
+    while (ctas < 8 && (long long)ctas * PAGES_PER_CTA < num_pages) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(PT);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace svc
+
+using namespace svc;
+
+extern "C" size_t sv_page_workspace_bytes(int32_t B, int32_t num_pages) {
+    if (B < 1 || num_pages < 1 || B >= MAXB || num_pages >= (1 << 28)) return 0;
+    return page_ws(B, num_pages).total;
+}
+
+extern "C" sv_status spec_page_reserve(const int32_t *num_drafts, int32_t *kv_seq_len, int32_t B,
+                                       int32_t *block_table, int32_t max_pages, int32_t *ref_count, int32_t num_pages,
+                                       int32_t page_size, void *workspace, size_t workspace_bytes, void *stream) {
+    const sv_status bad = check_pages(B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
+    if (bad != SV_OK) return bad;
+    if (!num_drafts || !kv_seq_len) return SV_ERR_INVALID_ARG;
+    if (workspace_bytes < page_ws(B, num_pages).total) return SV_ERR_WORKSPACE;
+    const PageState S = page_state(kv_seq_len, B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
+    return launch_cluster(reserve_kernel, num_pages, static_cast<cudaStream_t>(stream), S, num_drafts) == cudaSuccess
+               ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_page_fork(const int32_t *parents, const int32_t *children, const int32_t *fork_len,
+                                    int32_t num_forks, int32_t *kv_seq_len, int32_t B, int32_t *block_table,
+                                    int32_t max_pages, int32_t *ref_count, int32_t num_pages, int32_t page_size,
+                                    int32_t *copy_src, int32_t *copy_dst, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    const sv_status bad = check_pages(B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
+    if (bad != SV_OK) return bad;
+    if (!kv_seq_len || num_forks < 1 || !parents || !children || !copy_src || !copy_dst) return SV_ERR_INVALID_ARG;
+    if (num_forks > B) return SV_ERR_UNSUPPORTED;
+    if (workspace_bytes < page_ws(B, num_pages).total) return SV_ERR_WORKSPACE;
+    const PageState S = page_state(kv_seq_len, B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
+    const ForkArgs K{parents, children, fork_len, copy_src, copy_dst, num_forks};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (launch_cluster(fork_kernel, num_pages, st, S, K) != cudaSuccess) return SV_ERR_CUDA;
+    fork_share<<<dim3(num_forks, (max_pages + RELEASE_CHUNK - 1) / RELEASE_CHUNK), ST, 0, st>>>(S, K);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_page_release(const int32_t *kv_seq_len, int32_t B, int32_t *block_table, int32_t max_pages,
+                                       int32_t *ref_count, int32_t num_pages, int32_t page_size, int32_t window,
+                                       int32_t sinks, void *workspace, void *stream) {
+    const sv_status bad = check_pages(B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
+    if (bad != SV_OK) return bad;
+    if (!kv_seq_len || window < 0 || sinks < 0) return SV_ERR_INVALID_ARG;
+    const PageState S = page_state(const_cast<int32_t *>(kv_seq_len), B, block_table, max_pages, ref_count, num_pages,
+                                   page_size, workspace);
+    release_kernel<<<dim3(B, window ? 2 : 1), ST, 0, static_cast<cudaStream_t>(stream)>>>(S, window, sinks);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_page_compact(int32_t B, int32_t *block_table, int32_t max_pages, int32_t *ref_count,
+                                       int32_t num_pages, int32_t *copy_src, int32_t *copy_dst, int32_t capacity,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+    const sv_status bad = check_pages(B, block_table, max_pages, ref_count, num_pages, 1, workspace);
+    if (bad != SV_OK) return bad;
+    if (capacity < 1 || !copy_src || !copy_dst) return SV_ERR_INVALID_ARG;
+    if (workspace_bytes < page_ws(B, num_pages).total) return SV_ERR_WORKSPACE;
+    const PageState S = page_state(nullptr, B, block_table, max_pages, ref_count, num_pages, 1, workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (launch_cluster(compact_kernel, num_pages, st, S, copy_src, copy_dst, capacity) != cudaSuccess)
+        return SV_ERR_CUDA;
+    const long long blocks = ((long long)B * max_pages + ST * 4 - 1) / (ST * 4);
+    remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), ST, 0, st>>>(S);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_page_copy(void *k, void *v, int64_t page_bytes, int64_t page_stride, int32_t num_layers,
+                                    int64_t layer_stride, int32_t num_pages, const int32_t *copy_src,
+                                    const int32_t *copy_dst, int32_t n, void *workspace, void *stream) {
+    if (!k || !copy_src || !copy_dst || !workspace || n < 1 || num_pages < 1 || num_layers < 1 || page_bytes < 1 ||
+        page_stride < page_bytes || layer_stride < 0 || (num_layers > 1 && layer_stride == 0))
+        return SV_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || (page_bytes | page_stride | layer_stride) % 16) return SV_ERR_UNSUPPORTED;
+    if ((uintptr_t)workspace & 255) return SV_ERR_WORKSPACE;
+    const CopyArgs A{static_cast<char *>(k), static_cast<char *>(v), copy_src, copy_dst, page_bytes, page_stride,
+                     layer_stride, static_cast<int32_t *>(workspace), num_pages, num_layers, n};
+    const long long items = (long long)n * num_layers * (v ? 2 : 1);
+    copy_kernel<<<(unsigned)(items < 1216 ? items : 1216), CT, 0, static_cast<cudaStream_t>(stream)>>>(A);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
