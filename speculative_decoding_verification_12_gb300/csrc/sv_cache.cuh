@@ -98,6 +98,7 @@ struct Num<__nv_bfloat16> {
         return *reinterpret_cast<const uint32_t *>(&r);
     }
     static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr bool BF16 = true;
 };
 template <>
 struct Num<__half> {
@@ -109,6 +110,7 @@ struct Num<__half> {
         return *reinterpret_cast<const uint32_t *>(&r);
     }
     static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr bool BF16 = false;
 };
 
 template <typename E>
