@@ -16,10 +16,11 @@
 // batches, one long request and windows need no other schedule.  A row tile whose keys lie in several
 // CTAs' ranges leaves a part per CTA in the workspace, and the second kernel joins them in order.
 //
-// A CTA: one producer warp (tensor copies of pages into a ring of K and V tiles), one warp that
-// issues the matrix instructions (S and O in tensor memory, P back in tensor memory as an operand),
-// and two groups of 4 warps, a thread per row, for softmax and epilogue.  With one row tile the
-// groups take alternate key tiles, each with its own m, l and O, joined at the end; with two, each
+// A CTA: a front warp that turns the CTA's range into segments (a row tile and its key tiles here) and
+// loads their queries, a warp for K and one for V (tensor copies of pages into two rings of tiles),
+// one that issues the matrix instructions (S and O in tensor memory, P back in tensor memory as an
+// operand), and two groups of 4 warps, a thread per row, for softmax and epilogue.  With one row tile
+// the groups take alternate key tiles, each with its own m, l and O, joined at the end; with two, each
 // has its own.
 #include <math.h>
 
@@ -32,11 +33,13 @@ namespace svc {
 
 constexpr int TILE = 128;                // tokens per key tile, rows per row tile
 constexpr int BLK = TILE * 128;          // bytes of 128 rows x 64 elements
-constexpr int NTHREADS = 320;            // 2 x 4 softmax warps, producer, matrix issue
-constexpr int W_LOAD = 8, W_MMA = 9;
+constexpr int NTHREADS = 384;            // 2 x 4 softmax warps, then one warp for each of:
+constexpr int W_K = 8, W_MMA = 9, W_V = 10;   // keys, matrix instructions, values, and the front warp
 constexpr int MAX_CTAS = 160;
 constexpr int PART_ROWS = 256;           // rows of a part
-constexpr int MAX_STAGES = 14;
+constexpr int P_COL = TILE / 2;          // weights lie over the upper half of their scores
+constexpr int MAX_STAGES = 7;            // of each of the two rings
+constexpr int OVERHEAD = 1;              // cost of a row tile beside its key tiles, in key tiles
 
 struct AttnArgs {
     const void *q;
@@ -50,7 +53,10 @@ struct AttnArgs {
     float c;           // |scale| log2(e)
     uint32_t qflip;    // sign flip of two queries (scale < 0)
     int qzero;         // scale == 0
-    int Hq, G, window, sinks, q_tiles, stages;
+    int Hq, G, window, sinks;
+    int k_stages, v_stages;
+    int q_tiles;       // row tiles of 128 that a request may have at a time: 1 or 2
+    int q_rows;        // rows of a query buffer (a multiple of 8); two buffers if q_tiles == 1
 };
 
 struct AttnWs {
@@ -64,6 +70,11 @@ __host__ __device__ inline AttnWs attn_ws(int D) {
     L.total = L.o + (size_t)2 * MAX_CTAS * PART_ROWS * (D <= 64 ? 64 : 128) * 4;
     return L;
 }
+
+template <int V>
+struct Const {
+    static constexpr int N = V;
+};
 
 // What a request asks of the kernel.
 struct Req {
@@ -86,43 +97,21 @@ __device__ __forceinline__ Req req_of(const Batch &A, const Cache &C, const Attn
     r.nt = s.n ? r.ns + (s.len + TILE - 1) / TILE - r.w0 : 0;
     return r;
 }
-__device__ __forceinline__ long long units_of(const Req &r, int heads) { return (long long)r.nt * r.mt * heads; }
+// A request's cost, in units of a key tile.
+__device__ __forceinline__ long long units_of(const Req &r, int heads) {
+    return r.nt ? (long long)(r.nt + OVERHEAD) * r.mt * heads : 0;
+}
 
-// A CTA's share of one row tile: key tiles [t0, t1) of [0, nt).
-struct Seg : Req {
-    int b, kvh, m, t0, t1;
-    long long first;   // global index of the row tile's first unit
+// A segment, as the front warp hands it out (64 bytes): key tiles [t0, t1) of the nt of row tile m of
+// key head kvh of request b.  nt == 0 ends the list.
+struct __align__(16) Seg {
+    int row0, n, len, M, lo, w0, ns, nt;   // as in Req
+    int b, kvh, m, t0, t1, pad[3];
     __device__ __forceinline__ int base(int t) const { return (t < ns ? t : w0 + t - ns) * TILE; }
     __device__ __forceinline__ bool two() const { return M > TILE; }
 };
-
-// Walks over a CTA's range of units.  Every role walks by itself.
-struct Walk {
-    long long pos, hi, pre;   // next unit, end, units before request b
-    int b;
-    Req r;
-    __device__ __forceinline__ bool next(const Batch &A, const Cache &C, const AttnArgs &P, Seg &s) {
-        if (pos >= hi) return false;
-        long long w = units_of(r, C.heads);
-        while (pos >= pre + w) {
-            pre += w;
-            b++;
-            r = req_of(A, C, P, b);
-            w = units_of(r, C.heads);
-        }
-        const int u = (int)((pos - pre) / r.nt);   // row tile within the request
-        s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.mt = r.mt, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns;
-        s.nt = r.nt;
-        s.b = b;
-        s.kvh = u / r.mt;
-        s.m = u % r.mt;
-        s.first = pre + (long long)u * r.nt;
-        s.t0 = (int)(pos - s.first);
-        s.t1 = (int)min((long long)r.nt, hi - s.first);
-        pos = s.first + s.t1;
-        return true;
-    }
-};
+constexpr int SEGS = 32;                 // segments in flight between the front warp and the others
+constexpr int SEG_READERS = 11;          // warps that take each of them
 
 // Whether the row at position pos sees token j.
 __device__ __forceinline__ bool sees(const AttnArgs &P, int pos, int j) {
@@ -135,30 +124,22 @@ __device__ __forceinline__ uint32_t seen_mask(const AttnArgs &P, int pos, int j)
     if (P.window) m &= ~low_bits(pos - P.window + 1 - j) | low_bits(P.sinks - j);
     return m;
 }
-__device__ __forceinline__ bool seen_by_all(const AttnArgs &P, const Req &s, int j) {
+__device__ __forceinline__ bool seen_by_all(const AttnArgs &P, const Seg &s, int j) {
     return j <= s.len - s.n && (!P.window || j > s.len - 1 - P.window || j < P.sinks);
 }
-__device__ __forceinline__ bool seen_by_any(const AttnArgs &P, const Req &s, int j) {
+__device__ __forceinline__ bool seen_by_any(const AttnArgs &P, const Seg &s, int j) {
     return j < s.len && (j >= s.lo || j < P.sinks);
 }
 // Whether every row sees all 128 tokens from base on.
-__device__ __forceinline__ bool whole_tile(const AttnArgs &P, const Req &s, int base) {
+__device__ __forceinline__ bool whole_tile(const AttnArgs &P, const Seg &s, int base) {
     return base + TILE - 1 <= s.len - s.n && (!P.window || base > s.len - 1 - P.window || base + TILE - 1 < P.sinks);
 }
 
-// Places in the ring of a row tile's K and V tiles, in the order they are used: K0, K1, V0, K2, V1, ...
-__device__ __forceinline__ uint32_t k_item(int t) { return t ? 2 * t - 1 : 0; }
-__device__ __forceinline__ uint32_t v_item(int t, int nt) { return t < nt - 1 ? 2 * t + 2 : 2 * t + 1; }
-
-struct Ring {
-    uint32_t base, full, empty;   // shared addresses: tiles, barriers
-    uint32_t count;               // items before the current row tile
-    int stages;
-    uint32_t stage, phase;
-    __device__ __forceinline__ void at(uint32_t item) {
-        const uint32_t i = count + item, round = i / stages;
-        stage = i - round * stages;
-        phase = round & 1;
+// A position in a ring of tiles: the stage, and the parity of its turn.
+struct Place {
+    uint32_t stage, parity;
+    __device__ __forceinline__ void advance(uint32_t stages) {
+        if (++stage == stages) stage = 0, parity ^= 1;
     }
 };
 
@@ -173,20 +154,18 @@ __device__ __forceinline__ bool finite16(uint32_t h) {
 // the non-finite elements of one that only some rows see (the epilogue gives those to the rows that
 // do).  Returns whether it took any of the latter.
 template <typename E, int DP>
-__device__ __forceinline__ bool clean_values(const AttnArgs &P, const Req &s, int base, int tok, char *tile) {
+__device__ __forceinline__ bool clean_values(const AttnArgs &P, const Seg &s, int base, int tok, char *tile) {
     const int j = base + tok;
     if (seen_by_all(P, s, j)) return false;
     const bool any = seen_by_any(P, s, j);
     bool took = false;
-    for (int blk = 0; blk < DP / 64; blk++) {
-        uint4 *row = reinterpret_cast<uint4 *>(tile + blk * BLK + tok * 128);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            if (!any) {
-                row[i] = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-            }
-            uint4 w = row[i];
+#pragma unroll 1
+    for (int i = 0; i < DP / 8; i++) {
+        // (a different 16 bytes of the row per lane: no two of 8 lanes share a bank)
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (i >> 3) * BLK + tok * 128 + (((i ^ tok) & 7) << 4));
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (any) {
+            w = *at;
             uint32_t *p = &w.x;
             bool hit = false;
 #pragma unroll
@@ -194,18 +173,22 @@ __device__ __forceinline__ bool clean_values(const AttnArgs &P, const Req &s, in
                 if (!finite16<E>(p[e] & 0xffffu)) p[e] &= 0xffff0000u, hit = true;
                 if (!finite16<E>(p[e] >> 16)) p[e] &= 0xffffu, hit = true;
             }
-            if (hit) row[i] = w, took = true;
+            if (!hit) continue;
+            took = true;
         }
+        *at = w;
     }
     return took;
 }
 
-// The non-finite elements that clean_values took, for the row at position pos: columns
-// [col, col + 16) of the tokens in this segment that the row sees and another does not.
-template <typename E>
-__device__ __noinline__ void add_non_finite(const Cache &C, const AttnArgs &P, const Seg &s, int pos, int col, float *o) {
+// The non-finite elements that clean_values took, for the row at position pos, added to its result
+// after it was stored: `put(d, x)` adds x to element d, for d in [c0, c1).
+template <typename E, typename F>
+__device__ __forceinline__ void add_non_finite(const Cache &C, const AttnArgs &P, const Seg &s, int pos, int c0, int c1, F put) {
+#pragma unroll 1
     for (int side = 0; side < 2; side++) {
         const int from = side ? s.lo : s.len - s.n + 1, to = side ? min(s.len, s.lo + s.n - 1) : s.len;
+#pragma unroll 1
         for (int j = from; j < to; j++) {
             if (side && (!P.window || j > s.len - s.n)) break;   // (the causal side has it)
             const int tile = j / TILE, t = tile >= s.w0 ? tile - s.w0 + s.ns : tile;
@@ -214,24 +197,17 @@ __device__ __noinline__ void add_non_finite(const Cache &C, const AttnArgs &P, c
             if (page < 0 || page >= C.num_pages) continue;
             const E *v = static_cast<const E *>(C.v) + page * C.page_stride +
                          (j & ((1 << C.page_shift) - 1)) * C.token_stride + s.kvh * C.head_stride;
-            for (int i = 0; i < 16 && col + i < C.D; i++) {
-                const float x = (float)v[col + i];
-                if (!(fabsf(x) < INFINITY)) o[i] += x;
+#pragma unroll 1
+            for (int d = c0; d < c1; d++) {
+                const float x = (float)v[d];
+                if (!(fabsf(x) < INFINITY)) put(d, x);
             }
         }
     }
 }
 
-// Barrier of the 256 softmax threads; whether any of them passed true.
-__device__ __forceinline__ bool softmax_barrier_or(bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "tcgen05.fence::before_thread_sync;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)x) : "memory");
-    return r != 0;
-}
+// Barriers, flags and the groups' exchange, at the start of shared memory.
+constexpr int SMALL = 5120;
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -242,34 +218,47 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     constexpr float BIAS = Num<E>::BF16 ? 0.f : 8.f;
     // the running maximum may lag by this many powers of two before O is scaled down
     constexpr float LAG = Num<E>::BF16 ? 8.f : 6.f;
+    constexpr int NW = NTHREADS / 32;
     extern __shared__ __align__(1024) char smem[];
-    // [Q tiles][ring][barriers and small state]
-    char *const ring_p = smem + P.q_tiles * STAGE;
-    char *const small = ring_p + P.stages * STAGE;
-    uint64_t *const bars = reinterpret_cast<uint64_t *>(small);              // 2 MAX_STAGES + 8
-    float2 *const ex = reinterpret_cast<float2 *>(small + 512);              // [2][128] (m, l)
+    // [barriers and small state][two query buffers][ring of K tiles][ring of V tiles]; the matrix
+    // instruction reads 128 rows from a query buffer whatever it holds: the rows past it are other
+    // bytes of this memory, and reach only rows of S, P and O that nothing uses
+    const int q_block = P.q_rows * 128, q_buffer = NB * q_block;
+    char *const q_p = smem + SMALL;
+    char *const k_p = q_p + 2 * q_buffer, *const v_p = k_p + P.k_stages * STAGE;
+    int *const ctl = reinterpret_cast<int *>(smem + 384);                    // dead, tmem, -, -, patched[2][4], bad[16]
+    float2 *const ex = reinterpret_cast<float2 *>(smem + 512);               // [2][128] (m, l)
     long long *const scan = reinterpret_cast<long long *>(ex);               // the set-up's scratch, before ex is used
-    int *const ctl = reinterpret_cast<int *>(small + 256 + 128 + 64);        // dead, tmem, patched[2], bad[8]
-    const uint32_t bar0 = smem_addr(bars);
-    const uint32_t full = bar0, empty = bar0 + 8 * MAX_STAGES, s_full = bar0 + 16 * MAX_STAGES, p_full = s_full + 16,
-                   o_done = p_full + 16, q_full = o_done + 16, drained = q_full + 8;
-    volatile int *const dead = ctl;
-    volatile int *const patched = ctl + 2, *const bad = ctl + 4;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Seg *const segs = reinterpret_cast<Seg *>(smem + 2560);                  // [SEGS]
+    const uint32_t seg_full = smem_addr(smem + 4608), seg_empty = seg_full + 8 * SEGS;
+    const uint32_t k_full = smem_addr(smem), k_empty = k_full + 8 * MAX_STAGES, v_full = k_empty + 8 * MAX_STAGES,
+                   v_empty = v_full + 8 * MAX_STAGES, s_full = v_empty + 8 * MAX_STAGES, p_full = s_full + 16,
+                   o_done = p_full + 16, q_full = o_done + 16, q_empty = q_full + 16, both = q_empty + 16,
+                   drained = both + 16;
+    volatile int *const dead = ctl, *const patched = ctl + 4, *const bad = ctl + 12;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_tiles == 1 ? 2 : 1;
 
     if (tid == 0) {
-        for (int i = 0; i < P.stages; i++) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-        for (int g = 0; g < 2; g++) mbar_init(s_full + 8 * g, 1), mbar_init(p_full + 8 * g, 4), mbar_init(o_done + 8 * g, 1);
-        mbar_init(q_full, 8);
+        for (int i = 0; i < MAX_STAGES; i++) {
+            mbar_init(k_full + 8 * i, 1), mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_full + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int g = 0; g < 2; g++) {
+            mbar_init(s_full + 8 * g, 1), mbar_init(p_full + 8 * g, 4), mbar_init(o_done + 8 * g, 1);
+            mbar_init(q_full + 8 * g, 1), mbar_init(q_empty + 8 * g, 1), mbar_init(both + 8 * g, 8);
+        }
         mbar_init(drained, 1);
+        for (int i = 0; i < SEGS; i++) mbar_init(seg_full + 8 * i, 1), mbar_init(seg_empty + 8 * i, SEG_READERS);
         ctl[0] = 0;
+        for (int i = 0; i < 8; i++) patched[i] = -1;
+        for (int i = 0; i < 16; i++) bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == W_MMA) tmem_alloc(smem_addr(ctl + 1), 512);
     grid_wait();   // the work before this on the stream may still be writing what follows
 
     // the batch's units, and where this CTA's range begins
-    constexpr int NW = NTHREADS / 32;
     long long &start_pre = scan[NW], &total_units = scan[NW + 1], &start_b = scan[NW + 2];
     long long sum = 0;
     for (int b = tid; b < A.B; b += NTHREADS) sum += units_of(req_of(A, C, P, b), C.heads);
@@ -314,197 +303,386 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl + 1);
     grid_launch_dependents();
 
-    Walk walk;
-    Seg s;
-    walk.pos = lo, walk.hi = hi;
-    if (lo < hi) {
-        walk.pre = start_pre;
-        walk.b = (int)start_b;
-        walk.r = req_of(A, C, P, walk.b);
-    }
-    Ring ring{smem_addr(ring_p), full, empty, 0, P.stages, 0, 0};
+    // Takes segment k into registers; false at the end of the list, or when a wait ran out (ok).
+    bool ok = true;
+    auto take = [&](int k, Seg &s, bool release) {
+        const int slot = k & (SEGS - 1);
+        ok = warp_wait(seg_full + 8 * slot, k / SEGS & 1, dead);
+        if (!ok) return false;
+        int4 *to = reinterpret_cast<int4 *>(&s);
+        const int4 *from = reinterpret_cast<const int4 *>(segs + slot);
+#pragma unroll
+        for (int i = 0; i < 4; i++) to[i] = from[i];
+        __syncwarp();
+        if (release && lane == 0) mbar_arrive(seg_empty + 8 * slot);
+        return s.nt > 0;
+    };
 
-    if (warp == W_LOAD) {
-        const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box;
-        uint32_t stage = 0, phase = 1, loads = 0;   // the first round finds every stage empty
-        bool ok = true;
-        for (int seg = 0; ok && walk.next(A, C, P, s); seg++) {
-            if (lane == 0) bad[seg & 7] = 0;
-            __syncwarp();
-            // this lane's page of a key tile, or -1
-            auto page_of = [&](int t) {
-                const int j = s.base(t) + lane * box;
-                if (lane >= npg || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
-                const int id = __ldg(C.table + (int64_t)s.b * C.max_pages + (j >> C.page_shift));
-                if (id >= 0 && id < C.num_pages) return id;
-                bad[seg & 7] = 1;
-                record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
-                return -1;
+    if (warp >= 8) {
+    regs_down<88>();   // to the softmax warps: 2 x 208 + 88 = 3 x 168
+    if (warp == W_K || warp == W_V) {
+        // Keys, or values, of each segment's tiles.
+        const bool is_v = warp == W_V;
+        const CUtensorMap *const map = is_v ? &map_v : &map_k;
+        const uint32_t ring = smem_addr(is_v ? v_p : k_p), full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty,
+                       stages = is_v ? v_stages : k_stages;
+        Seg s;
+        const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
+        const int sub = lane & (npg - 1), lane_tile = lane / npg;
+        Place at{0, 1};   // the first round finds every stage empty
+        uint32_t loads = 0;
+        for (int seg = 0; ok && take(seg, s, true); seg++) {
+            // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
+            // serves several tiles, and is issued that many tiles ahead of its use
+            const int32_t *table = C.table + (int64_t)s.b * C.max_pages;
+            auto fetch = [&](int t) {
+                t += lane_tile;
+                const int j = s.base(t) + sub * box;
+                if (t >= s.t1 || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
+                return (int)min((uint32_t)__ldg(table + (j >> C.page_shift)), (uint32_t)C.num_pages);   // (num_pages: not a page)
             };
-            auto load = [&](const CUtensorMap *map, int t, int id) {
+            int ids = -1, ahead = fetch(s.t0), t_ids = s.t0 - tpl;
+#pragma unroll 1
+            for (int t = s.t0; t < s.t1; t++) {
+                if (t == t_ids + tpl) {
+                    ids = ahead;
+                    t_ids = t;
+                    ahead = fetch(t + tpl);
+                }
+                // this lane's page of tile t (lanes below npg), or -1
+                int id = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
+                if (lane >= npg) id = -1;
+                if (id == C.num_pages) {
+                    bad[seg & 15] = seg + 1;
+                    record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
+                    id = -1;
+                }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128 * NB;
                 __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
-                ok = warp_wait(empty + 8 * stage, phase, dead);
-                if (!ok) return;
+                ok = warp_wait(empty + 8 * at.stage, at.parity, dead);
+                if (!ok) break;
                 loads++;
-                if (lane == 0) mbar_expect(full + 8 * stage, bytes);
+                if (lane == 0) mbar_expect(full + 8 * at.stage, bytes);
                 __syncwarp();
                 if (id >= 0) {
-                    const uint32_t dst = ring.base + stage * STAGE + lane * box * 128;
+                    const uint32_t dst = ring + at.stage * STAGE + sub * box * 128;
                     for (int blk = 0; blk < NB; blk++)
-                        tma_load_4d(dst + blk * BLK, map, full + 8 * stage, blk * 64, s.base(t) & (P_ - 1) & ~(box - 1),
+                        tma_load_4d(dst + blk * BLK, map, full + 8 * at.stage, blk * 64, s.base(t) & (P_ - 1) & ~(box - 1),
                                     s.kvh, id);
                 }
-                if (++stage == (uint32_t)P.stages) stage = 0, phase ^= 1;
-            };
-            int id = page_of(s.t0);
-            load(&map_k, s.t0, id);
-            for (int t = s.t0; ok && t < s.t1; t++) {
-                int nid = -1;
-                if (t + 1 < s.t1) {
-                    nid = page_of(t + 1);
-                    load(&map_k, t + 1, nid);
-                }
-                if (ok) load(&map_v, t, id);
-                id = nid;
+                __syncwarp();
+                at.advance(stages);
             }
         }
         if (!ok) {   // let the copies in flight land before the CTA may end
             const unsigned long long t0 = now_ns();
-            for (uint32_t i = loads > (uint32_t)P.stages ? loads - P.stages : 0; i < loads; i++)
-                while (!mbar_try(full + 8 * (i % P.stages), i / P.stages & 1) && now_ns() - t0 < WAIT_NS) {}
+            for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
+                while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns() - t0 < WAIT_NS) {}
         }
     } else if (warp == W_MMA) {
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = mma_idesc(Num<E>::BF16, TILE, TILE, false);
-            constexpr uint32_t idesc_o = mma_idesc(Num<E>::BF16, TILE, DP, true);
-            const uint64_t qd = smem_desc(smem_addr(smem), 16);
-            uint32_t np[2] = {0, 0};   // P tiles taken, per group
-            bool ok = true;
-            for (int seg = 0; ok && walk.next(A, C, P, s); seg++) {
-                const int nt = s.t1 - s.t0, two = s.two(), nv = nt << two;
-                auto scores = [&](int v) {
-                    const int t = v >> two, g = v & 1;
-                    ring.at(k_item(t));
-                    if (!mbar_wait(full + 8 * ring.stage, ring.phase, dead)) return false;
-                    tc_fence_after();
-                    const uint64_t kd = smem_desc(ring.base + ring.stage * STAGE, 16);
-                    const uint64_t qg = qd + (uint64_t)((two ? g : 0) * STAGE >> 4);
-#pragma unroll
-                    for (int k = 0; k < DP / 16; k++) {
-                        const uint64_t step = (uint64_t)(((k >> 2) * BLK + (k & 3) * 32) >> 4);
-                        mma_ss(tmem + g * TILE, qg + step, kd + step, idesc_s, k > 0);
+        // Matrix instructions.  Over all segments the row tiles' products come in one sequence: tile v
+        // of a segment, or, with two row tiles, row tile v & 1 of key tile v >> 1.  The groups take it
+        // in turn, S runs two ahead of P V, and so the next segment's scores are ready while this
+        // one's last tiles are still with the groups.  The whole warp runs this; one lane issues.
+        // The path from a group's weights to its next scores is the kernel's longest chain, so P V and
+        // that S are issued together, the commits after both, and whether K is there is asked before.
+        // A commit costs the issuing lane some 140 cycles: there are two a product, S is there (the
+        // softmax group then frees the K tile) and the V tile is free.  A group learns of its last
+        // product of a segment by o_done; earlier ones are complete when a later S is.
+        constexpr uint32_t idesc_s = mma_idesc(Num<E>::BF16, TILE, TILE, false);
+        const int steps = (C.D + 15) / 16;                              // of 16 columns: nothing past head_dim
+        const uint32_t idesc_o = mma_idesc(Num<E>::BF16, TILE, 0, true) | (uint32_t)(steps * 2) << 17;
+        const bool leader = elect();
+        const uint64_t k_desc = smem_desc(smem_addr(k_p), 16), v_desc = smem_desc(smem_addr(v_p), BLK),
+                       q_desc = smem_desc(smem_addr(q_p), 16);
+        const uint32_t q_step = q_block >> 4;
+        int sseg = 0, oseg = 0;                                     // segments opened
+        int sv = 0, snv = 0, stwo = 0, ov = 0, onv = 0, otwo = 0;   // product, products and kind of the current ones
+        auto open = [&](int &k, int &v, int &nv, int &two, bool release) {
+            Seg s;
+            v = nv = 0;
+            if (!take(k++, s, release)) return;
+            two = s.two();
+            nv = (s.t1 - s.t0) << two;
+        };
+        open(sseg, sv, snv, stwo, false);
+        if (ok) open(oseg, ov, onv, otwo, true);
+        Place ks{0, 0}, vs{0, 0}, qs{0, 0};
+        uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each group's next P
+        int lead = 0;                      // products whose S, but not P V, is issued: at most 2
+        uint32_t spins = 0;
+        unsigned long long t0 = 0;
+        // the next S has its operands
+        auto s_ready = [&]() {
+            return snv && (sv || warp_try(q_full + 8 * qs.stage, qs.parity)) && warp_try(k_full + 8 * ks.stage, ks.parity);
+        };
+#pragma unroll 1
+        while (ok && onv) {
+            bool do_s = s_ready(), do_o = false;
+            if (lead == 2 || !do_s) {
+                do_o = lead > 0 && warp_try(p_full + 8 * go, np >> go & 1) && warp_try(v_full + 8 * vs.stage, vs.parity);
+                if (!do_o) {
+                    bool late = *dead;
+                    if ((++spins & 255) == 0) {
+                        if (spins == 256) t0 = now_ns();
+                        else late |= now_ns() - t0 > WAIT_NS;
                     }
-                    mma_commit(s_full + 8 * g);
-                    if (!two || (v & 1)) mma_commit(empty + 8 * ring.stage);
-                    return true;
-                };
-                auto outputs = [&](int v) {
-                    const int t = v >> two, g = v & 1;
-                    if (!mbar_wait(p_full + 8 * g, np[g]++ & 1, dead)) return false;
-                    ring.at(v_item(t, nt));
-                    if (!mbar_wait(full + 8 * ring.stage, ring.phase, dead)) return false;
-                    tc_fence_after();
-                    const uint64_t vd = smem_desc(ring.base + ring.stage * STAGE, BLK);
+                    if (__any_sync(0xffffffffu, late)) {
+                        *dead = 1;
+                        ok = false;
+                    }
+                    continue;
+                }
+                if (!do_s) do_s = s_ready();
+            }
+            spins = 0;
+            tc_fence_after();
+            const bool last_use = !otwo || (ov & 1);
+            if (leader) {
+                if (do_o) {
+                    const uint64_t vd = v_desc + (uint64_t)(vs.stage * STAGE >> 4);
 #pragma unroll
                     for (int k = 0; k < TILE / 16; k++)
-                        mma_ts(tmem + 2 * TILE + g * TILE, tmem + g * TILE + k * 8, vd + (uint64_t)(k * 2048 >> 4),
-                               idesc_o, v >= 2 || k > 0);
-                    mma_commit(o_done + 8 * g);
-                    if (!two || (v & 1)) mma_commit(empty + 8 * ring.stage);
-                    return true;
-                };
-                ok = mbar_wait(q_full, seg & 1, dead);
-                tc_fence_after();
-                for (int v = 0; ok && v < min(2, nv); v++) ok = scores(v);
-                for (int v = 0; ok && v < nv; v++) {
-                    ok = outputs(v);
-                    if (ok && v + 2 < nv) ok = scores(v + 2);
+                        mma_ts(tmem + 2 * TILE + go * TILE, tmem + go * TILE + P_COL + k * 8, vd + (uint64_t)(k * 2048 >> 4),
+                               idesc_o, ov >= 2 || k > 0);
                 }
-                ring.count += 2 * nt;
+                if (do_s) {
+                    const uint64_t kd = k_desc + (uint64_t)(ks.stage * STAGE >> 4);
+                    const uint64_t qd = q_desc + (uint64_t)((stwo ? sv & 1 : qs.stage) * q_buffer >> 4);
+                    auto issue = [&](auto n) {
+#pragma unroll
+                        for (int k = 0; k < decltype(n)::N; k++)
+                            mma_ss(tmem + gs * TILE, qd + (uint64_t)((k >> 2) * q_step + (k & 3) * 2),
+                                   kd + (uint64_t)((k >> 2) * (BLK >> 4) + (k & 3) * 2), idesc_s, k > 0);
+                    };
+                    if (DP == 64) issue(Const<4>());
+                    else if (steps == 8) issue(Const<8>());
+                    else if (steps == 5) issue(Const<5>());
+                    else if (steps == 6) issue(Const<6>());
+                    else issue(Const<7>());
+                    mma_commit(s_full + 8 * gs);
+                    if (sv == snv - 1) mma_commit(q_empty + 8 * qs.stage);
+                }
+                if (do_o) {
+                    if (last_use) mma_commit(v_empty + 8 * vs.stage);
+                    if (ov >= onv - 2) mma_commit(o_done + 8 * go);
+                }
             }
-            if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
-                mma_commit(drained);
-                const unsigned long long t0 = now_ns();
-                while (!mbar_try(drained, 0) && now_ns() - t0 < WAIT_NS) {}
+            __syncwarp();
+            if (do_o) {
+                if (last_use) vs.advance(v_stages);
+                np ^= 1u << go;
+                go ^= 1;
+                lead--;
+                if (++ov == onv) open(oseg, ov, onv, otwo, true);
             }
+            if (do_s && ok) {
+                if (!stwo || (sv & 1)) ks.advance(k_stages);
+                gs ^= 1;
+                lead++;
+                if (++sv == snv) {
+                    qs.advance(q_bufs);
+                    open(sseg, sv, snv, stwo, false);
+                }
+            }
+        }
+        if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
+            if (leader) mma_commit(drained);
+            const unsigned long long t0 = now_ns();
+            while (!mbar_try(drained, 0) && now_ns() - t0 < WAIT_NS) {}
         }
         __syncwarp();
     } else {
+        // Front: the segments of this CTA's range, in order, and their queries, swizzled as the matrix
+        // instruction reads them.  Requests are looked at 32 at a time, row tiles of one 16 at a time.
+        uint32_t pushed = 0, loaded = 0;
+        long long pos = lo, pre = lo < hi ? start_pre : 0;
+        int b = lo < hi ? (int)start_b : 0, b_base = -32;
+        Req r = {};
+        Place at{0, 1};
+        if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
+        __syncwarp();
+        auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
+            const uint32_t slot = k & (SEGS - 1);
+            const bool free = mbar_wait(seg_empty + 8 * slot, (k / SEGS & 1) ^ 1, dead);
+            if (free) {
+                segs[slot] = s;
+                mbar_arrive(seg_full + 8 * slot);
+            }
+            return free;
+        };
+#pragma unroll 1
+        for (bool more = lo < hi, ended = false; ok;) {
+#pragma unroll 1
+            while (ok && more && pushed - loaded < 12) {
+                if (b - b_base >= 32) {
+                    b_base = b;
+                    r.nt = 0;
+                    if (b + lane < A.B) r = req_of(A, C, P, b + lane);
+                }
+                const int i = b - b_base;
+                Seg s;
+                s.row0 = __shfl_sync(0xffffffffu, r.row0, i), s.n = __shfl_sync(0xffffffffu, r.n, i);
+                s.len = __shfl_sync(0xffffffffu, r.len, i), s.M = __shfl_sync(0xffffffffu, r.M, i);
+                s.lo = __shfl_sync(0xffffffffu, r.lo, i), s.w0 = __shfl_sync(0xffffffffu, r.w0, i);
+                s.ns = __shfl_sync(0xffffffffu, r.ns, i), s.nt = __shfl_sync(0xffffffffu, r.nt, i);
+                const int mt = __shfl_sync(0xffffffffu, r.mt, i), per = s.nt + OVERHEAD, all = mt * C.heads;
+                if (s.nt) {
+                    const int u0 = (int)((pos - pre) / per);
+                    const int u1 = min(min(all, u0 + 16), (int)min((long long)all, (hi - pre + per - 1) / per));
+                    const int u = u0 + lane;
+                    const long long first = pre + (long long)u * per;   // the row tile's first unit
+                    s.b = b;
+                    s.kvh = u / mt;
+                    s.m = u - s.kvh * mt;
+                    s.t0 = (int)max(lo - first - OVERHEAD, 0ll);
+                    s.t1 = (int)min((long long)per, hi - first) - OVERHEAD;
+                    const bool any = u < u1 && s.t1 > s.t0;   // (else nothing, or the overhead alone)
+                    const uint32_t mask = __ballot_sync(0xffffffffu, any);
+                    if (any) {
+                        ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
+                        if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
+                            const long long last = first + OVERHEAD + s.nt;
+                            P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    pushed += __popc(mask);
+                    pos = pre + (long long)u1 * per;
+                    if (u1 < all) {
+                        more = pos < hi;
+                        continue;
+                    }
+                    pre = pos;
+                }
+                b++;
+                more = pos < hi && b < A.B;
+            }
+            if (!more && !ended && ok) {
+                Seg s = {};
+                if (lane == 0) ok = push(pushed, s);
+                ok = __all_sync(0xffffffffu, ok);
+                ended = true;
+            }
+            if (!ok || loaded == pushed) break;
+            const Seg &s = segs[loaded & (SEGS - 1)];   // (not written again before it is loaded)
+            const int row0 = s.m * 2 * TILE, rows = min(s.M - row0, 2 * TILE);
+            const bool two = s.two();
+            const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D;
+            constexpr int CH = DP / 8, U = 8;
+            const int total = rows * CH;
+#pragma unroll 1
+            for (int i0 = lane; i0 < total + 32; i0 += 32 * U) {
+                uint4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int i = i0 + 32 * u, row = i / CH, ch = i % CH, rr = row0 + row, tok = rr / P.G;
+                    w[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < total && ch * 8 < C.D && !P.qzero)
+                        w[u] = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)(rr - tok * P.G) * C.D + ch * 8);
+                }
+                if (i0 < 32) {   // the buffer's last user is through
+                    ok = warp_wait(q_empty + 8 * at.stage, at.parity, dead);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int i = i0 + 32 * u, row = i / CH, ch = i % CH;
+                    if (i >= total) continue;
+                    w[u].x ^= P.qflip, w[u].y ^= P.qflip, w[u].z ^= P.qflip, w[u].w ^= P.qflip;
+                    char *to = q_p + (two ? row >> 7 : at.stage) * q_buffer + (ch >> 3) * q_block + (row & 127) * 128 +
+                               (((ch & 7) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(to) = w[u];
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(q_full + 8 * at.stage);
+            loaded++;
+            at.advance(q_bufs);
+        }
+    }
+    } else {
+        regs_up<208>();
+        // Softmax and epilogue: group g, a thread per row.
+        Seg s;
         const int g = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
         const uint32_t t_s = tmem + g * TILE + lanes, t_o = tmem + 2 * TILE + lanes;
         const int D = C.D, Hq = P.Hq;
-        uint32_t ns_ = 0;   // S tiles taken
-        bool ok = true;
-        for (int seg = 0; ok && walk.next(A, C, P, s); seg++) {
+        uint32_t ns_ = 0, turn = 0, tiles = 0, parts = 0, pairs = 0;   // S tiles taken; products, key tiles, epilogues, joint ones
+#pragma unroll 1
+        for (int seg = 0; ok && take(seg, s, true); seg++) {
             const int nt = s.t1 - s.t0;
             const bool two = s.two();
+            const int mine = (g ^ turn) & 1;      // this group's row tile, or its first key tile
+            const uint32_t tile0 = tiles;
+            turn += nt << two;
+            tiles += nt;
+            if (!two && mine >= nt) continue;     // a single key tile, and the other group's turn
+            const bool pair = !two && nt > 1;     // both groups hold a part of every row
             const int rows = min(s.M - s.m * 2 * TILE, 2 * TILE);   // of this row tile
-            // queries, swizzled as the matrix instruction reads them
-            for (int i = tid; i < rows * (DP / 8); i += 256) {
-                const int r = i / (DP / 8), ch = i % (DP / 8);
-                const int rr = s.m * 2 * TILE + r, tok = rr / P.G;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (ch * 8 < D && !P.qzero)
-                    w = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.q) + (s.row0 + tok) * P.q_stride +
-                                                         (int64_t)(s.kvh * P.G + rr - tok * P.G) * D + ch * 8);
-                w.x ^= P.qflip, w.y ^= P.qflip, w.z ^= P.qflip, w.w ^= P.qflip;
-                char *to = smem + (r >> 7) * STAGE + (ch >> 3) * BLK + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4 *>(to) = w;
-            }
-            fence_proxy_async();
-            if (tid == 0) patched[seg & 1] = 0;   // (last read before the previous segment's barrier)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-
-            const int rt = two ? g * TILE + row : row;             // this thread's row of the row tile
+            const int rt = two ? mine * TILE + row : row;           // this thread's row of it
             const bool active = rt < rows;
-            const bool warp_on = (two ? g * TILE : 0) + (warp & 3) * 32 < rows;
+            const bool warp_on = (two ? mine * TILE : 0) + (warp & 3) * 32 < rows;
             const int rr = s.m * 2 * TILE + rt, tok = rr / P.G;
             const int pos = s.len - s.n + tok;
             float m = -INFINITY, l = 0.f;
             bool any_tile = false;
-            for (int t = two ? 0 : g; t < nt; t += two ? 1 : 2) {
+#pragma unroll 1
+            for (int t = two ? 0 : mine; t < nt; t += two ? 1 : 2) {
                 if (!warp_wait(s_full + 8 * g, ns_++ & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if ((warp & 3) == 0 && lane == 0 && (!two || mine)) mbar_arrive(k_empty + 8 * ((tile0 + t) % k_stages));
                 const int base = s.base(s.t0 + t);
                 const bool whole = whole_tile(P, s, base);
-                if (!whole && (!two || g == 0)) {
-                    ring.at(v_item(t, nt));
-                    if (!warp_wait(full + 8 * ring.stage, ring.phase, dead)) {
+                if (!whole && (!two || mine == 0)) {
+                    const uint32_t round = (tile0 + t) / v_stages, stage = tile0 + t - round * v_stages;
+                    if (!warp_wait(v_full + 8 * stage, round & 1, dead)) {
                         ok = false;
                         break;
                     }
-                    if (clean_values<E, DP>(P, s, base, row, ring_p + ring.stage * STAGE)) patched[seg & 1] = 1;
+                    if (clean_values<E, DP>(P, s, base, row, v_p + stage * STAGE)) patched[4 * g + (seg & 3)] = seg;
                     fence_proxy_async();
                     __syncwarp();
                 }
                 if (warp_on) {
-                    // S comes in four times 32 columns, twice (maximum, then weights): a thread's 128
-                    // scores at once would leave no registers
-                    uint32_t x[2][32];
-                    auto masked = [&](int i) {
+                    // 128 scores a thread in four times 32 columns; three of the four stay in registers
+                    // from the maximum to the weights, the first is loaded again in their shadow
+                    uint32_t x[3][32];
+                    auto masked = [&](uint32_t *v, int i) {
                         if (whole) return;
                         const uint32_t see = seen_mask(P, pos, base + 32 * i);
 #pragma unroll
-                        for (int k = 0; k < 32; k++)
-                            x[i & 1][k] = (see >> k & 1) ? x[i & 1][k] : 0xff800000u;   // -inf
+                        for (int k = 0; k < 32; k++) v[k] = (see >> k & 1) ? v[k] : 0xff800000u;   // -inf
                     };
                     float top[4] = {m, m, m, m};
+                    auto largest = [&](const uint32_t *v) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    };
                     tmem_ld32(t_s, x[0]);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        tmem_wait_ld();
-                        after_wait32(x[i & 1]);
-                        if (i < 3) tmem_ld32(t_s + 32 * (i + 1), x[(i + 1) & 1]);
-                        masked(i);
-#pragma unroll
-                        for (int k = 0; k < 32; k++) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[i & 1][k]));
-                    }
+                    tmem_ld32(t_s + 32, x[1]);
+                    tmem_ld32(t_s + 64, x[2]);
+                    tmem_wait_ld();
+                    after_wait32(x[0]);
+                    after_wait32(x[1]);
+                    after_wait32(x[2]);
+                    masked(x[0], 0);
+                    largest(x[0]);
+                    tmem_ld32(t_s + 96, x[0]);
+                    masked(x[1], 1);
+                    largest(x[1]);
+                    masked(x[2], 2);
+                    largest(x[2]);
+                    tmem_wait_ld();
+                    after_wait32(x[0]);
+                    masked(x[0], 3);
+                    largest(x[0]);
                     const float new_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // lift the running maximum, and scale O and l down, only where it lags too far
                     const bool lift = active && (m == -INFINITY ? new_m > m : (new_m - m) * P.c > LAG);
@@ -513,14 +691,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                         if (lift) m = new_m;
                         if (any_tile) {
                             l *= f;
-                            // the group's last product is complete before O changes
-                            if (!warp_wait(o_done + 8 * g, (ns_ - 2) & 1, dead)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 0; i < DP; i += 32) {
+                            // (the group's last product is complete: it was issued before this S)
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(t_o + g * TILE + i, o);
                                 tmem_wait_ld();
@@ -532,26 +705,32 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                         }
                     }
                     const float off = BIAS - (m == -INFINITY ? 0.f : m * P.c);
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    tmem_ld32(t_s, x[0]);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
+                    const uint64_t cc = pair_of(P.c, P.c), offs = pair_of(off, off);
+                    uint64_t sum[2] = {0, 0};
+                    auto weights = [&](const uint32_t *v, int i) {
                         uint32_t w[16];
-                        tmem_wait_ld();
-                        after_wait32(x[i & 1]);
-                        if (i < 3) tmem_ld32(t_s + 32 * (i + 1), x[(i + 1) & 1]);
-                        masked(i);
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float a = ex2(fmaf(__uint_as_float(x[i & 1][k]), P.c, off));
-                            const float b = ex2(fmaf(__uint_as_float(x[i & 1][k + 1]), P.c, off));
-                            sum[k & 3] += a;
-                            sum[(k & 3) + 1] += b;
+                            float a, b;
+                            split(fma2(pair_of(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, offs), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair_of(a, b));
                             w[k / 2] = Num<E>::down(a, b);
                         }
-                        tmem_st16(t_s + 16 * i, w);   // over columns already read
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_st16(t_s + P_COL + 16 * i, w);   // over columns 64.. of S, which are all in registers
+                    };
+                    weights(x[2], 2);
+                    tmem_ld32(t_s, x[2]);
+                    weights(x[0], 3);
+                    weights(x[1], 1);
+                    tmem_wait_ld();
+                    after_wait32(x[2]);
+                    masked(x[2], 0);
+                    weights(x[2], 0);
+                    float s0, s1;
+                    split(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                     tmem_wait_st();
                 }
                 any_tile = true;
@@ -559,27 +738,27 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * g);
             }
-            if (ok && any_tile) ok = warp_wait(o_done + 8 * g, (ns_ - 1) & 1, dead);
-            if (!two) ex[g * TILE + row] = make_float2(m, l);
-            // both groups are through; whether a wait ran out is decided once for all 8 warps
-            ok = !softmax_barrier_or(!ok || *dead);
-            tc_fence_after();
+            if (ok) ok = warp_wait(o_done + 8 * g, parts++ & 1, dead);
+            if (ok && pair) {   // the other group's maxima, sums and O
+                ex[g * TILE + row] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(both);
+                ok = warp_wait(both, pairs & 1, dead);
+            }
             if (!ok) break;
-            const bool patch = patched[seg & 1] != 0, broken = bad[seg & 7] != 0;
+            tc_fence_after();
+            const bool patch = patched[seg & 3] == seg || patched[4 + (seg & 3)] == seg, broken = bad[seg & 15] == seg + 1;
             const bool direct = s.t0 == 0 && s.t1 == s.nt;
             if (warp_on) {
                 // the part's maximum and sum, and the factors of the (up to) two sums O
                 float f0 = 1.f, f1 = 0.f;
-                if (!two && nt > 1) {
+                if (pair) {
                     const float2 a = ex[row], b = ex[TILE + row];
                     m = fmaxf(a.x, b.x);
                     f0 = a.x == m ? 1.f : ex2((a.x - m) * P.c);
                     f1 = b.x == m ? 1.f : ex2((b.x - m) * P.c);
                     l = a.y * f0 + b.y * f1;
-                } else if (!two) {
-                    const float2 a = ex[row];
-                    m = a.x;
-                    l = a.y;
                 }
                 if (broken) l = NAN;
                 const float inv = (l == 0.f && !direct) ? 0.f : 1.f / l;
@@ -589,23 +768,23 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 const int slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
                 const int head = s.kvh * P.G + rr - tok * P.G;
                 const int64_t orow = (int64_t)(s.row0 + tok) * Hq + head;
-                const uint32_t t0_ = two ? t_o + g * TILE : t_o;
-                const int c0 = two ? 0 : g * (DP / 2), c1 = two ? DP : c0 + DP / 2;
+                const uint32_t t0_ = pair ? t_o : t_o + g * TILE;
+                const int c0 = pair ? g * (DP / 2) : 0, c1 = min(D, pair ? c0 + DP / 2 : DP);
+#pragma unroll 1
                 for (int c = c0; c < c1; c += 16) {
                     uint32_t a[16], b[16];
                     float o[16];
                     tmem_ld16(t0_ + c, a);
-                    if (!two && nt > 1) tmem_ld16(t0_ + TILE + c, b);
+                    if (pair) tmem_ld16(t0_ + TILE + c, b);
                     tmem_wait_ld();
                     after_wait16(a);
                     after_wait16(b);
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         o[i] = __uint_as_float(a[i]) * f0;
-                        if (!two && nt > 1) o[i] += __uint_as_float(b[i]) * f1;
+                        if (pair) o[i] += __uint_as_float(b[i]) * f1;
                     }
                     if (active) {
-                        if (patch) add_non_finite<E>(C, P, s, pos, c, o);
                         if (direct) {
                             E *to = static_cast<E *>(P.out) + orow * D + c;
                             if (c < D) *reinterpret_cast<uint4 *>(to) = pack8<E>(o);
@@ -618,22 +797,27 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     }
                     __syncwarp();
                 }
+                if (patch && active) {
+                    add_non_finite<E>(C, P, s, pos, c0, c1, [&](int d, float x) {
+                        if (direct) {
+                            E &y = static_cast<E *>(P.out)[orow * D + d];
+                            y = (E)((float)y + x);
+                        } else {
+                            P.part_o[(((int64_t)slot * (DP / 4) + d / 4) * PART_ROWS + rt) * 4 + d % 4] += x;
+                        }
+                    });
+                }
                 if (active && c0 == 0) {
                     if (!direct) P.part_lse[slot * PART_ROWS + rt] = lse2;
                     else if (P.lse) P.lse[orow] = lse2 * 0.6931471805599453f;
                 }
             }
             tc_fence_before();
-            ring.count += 2 * nt;
-        }
-        if (tid == 0) {
-            // the last segment, if it begins here and ends elsewhere, is this CTA's to describe
-            int4 d = make_int4(-1, 0, 0, 0);
-            if (lo < hi && s.t0 == 0 && s.t1 < s.nt) {
-                const long long last = s.first + s.nt;   // the CTA that holds unit last - 1
-                d = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
+            if (pair) {   // neither group's next product may overwrite an O that the other still reads
+                __syncwarp();
+                if (lane == 0) mbar_arrive(both + 8);
+                ok = warp_wait(both + 8, pairs++ & 1, dead);
             }
-            P.desc[cta] = d;
         }
     }
     tc_fence_before();
@@ -718,17 +902,19 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
             const int f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
             const int h = __shfl_sync(0xffffffffu, head, l), e = A.R - __shfl_sync(0xffffffffu, tail, l);
             const bool er = __shfl_sync(0xffffffffu, err, l) != 0;
-            auto fill = [&](int r0, int r1, bool nan) {
+#pragma unroll 1
+            for (int part = 0; part < 3; part++) {   // the request's unused rows; rows before the first, after the last request
+                const int r0 = part == 0 ? f : part == 1 ? 0 : e, r1 = part == 0 ? t : part == 1 ? h : A.R;
+                const bool nan = part == 0 && er;
                 const uint32_t w = nan ? Num<E>::NAN2 : 0u;
                 const int64_t n = (int64_t)(r1 - r0) * P.Hq * C.D / 8, hn = (int64_t)(r1 - r0) * P.Hq;
                 uint4 *o = reinterpret_cast<uint4 *>(static_cast<E *>(P.out) + (int64_t)r0 * P.Hq * C.D);
+#pragma unroll 1
                 for (int64_t i = lane; i < n; i += 32) o[i] = make_uint4(w, w, w, w);
                 if (P.lse)
+#pragma unroll 1
                     for (int64_t i = lane; i < hn; i += 32) P.lse[(int64_t)r0 * P.Hq + i] = nan ? NAN : 0.f;
-            };
-            fill(f, t, er);
-            fill(0, h, false);
-            fill(e, A.R, false);
+            }
         }
     }
 }
@@ -759,11 +945,11 @@ static bool encode(CUtensorMap *map, const sv_kv_cache &c, void *ptr) {
     const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2, (cuuint64_t)c.page_stride * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)(c.page_size < TILE ? c.page_size : TILE), 1, 1}, one[4] = {1, 1, 1, 1};
     return f(map, c.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, ptr, dims,
-             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, c.head_dim % 64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int SMEM_MAX = 232448, SMALL = 512 + 2 * TILE * 8;
+constexpr int SMEM_MAX = 232448;
 
 template <typename E, int DP>
 static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, const sv_kv_cache &cache, cudaStream_t st) {
@@ -775,12 +961,16 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return SV_ERR_CUDA;
     P.q_tiles = (A.k_max + 1) * P.G > TILE ? 2 : 1;
-    P.stages = (SMEM_MAX - SMALL - P.q_tiles * STAGE) / STAGE;
-    if (P.stages > MAX_STAGES) P.stages = MAX_STAGES;
-    const int smem = (P.q_tiles + P.stages) * STAGE + SMALL;
+    P.q_rows = P.q_tiles == 2 ? TILE : ((A.k_max + 1) * P.G + 7) / 8 * 8;
+    const int q_bytes = 2 * P.q_rows * DP * 2;
+    // values wait longer than keys for their use: the odd stage is theirs
+    const int stages = (SMEM_MAX - SMALL - q_bytes) / STAGE;
+    P.k_stages = stages / 2 < MAX_STAGES ? stages / 2 : MAX_STAGES;
+    P.v_stages = stages - P.k_stages < MAX_STAGES ? stages - P.k_stages : MAX_STAGES;
+    const int smem = SMALL + q_bytes + (P.k_stages + P.v_stages) * STAGE;
     // no more CTAs than the batch can have units
     const long long most = (long long)A.B * C.heads * (((long long)(A.k_max + 1) * P.G + 2 * TILE - 1) / (2 * TILE)) *
-                           ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE);
+                           ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + OVERHEAD);
     int ctas = nsm < MAX_CTAS ? nsm : MAX_CTAS;
     if (most < ctas) ctas = (int)most;
     if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)

@@ -39,12 +39,15 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Waits for the phase of the given parity; false once the wait has run out, here or in another
-// warp of the CTA (*dead is then set).
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *dead) {
-    const unsigned long long t0 = now_ns();
-    while (!mbar_try(bar, parity)) {
+// warp of the CTA (*dead is then set).  The clock is read only now and then: reading the timer
+// takes longer than most of these waits.
+static __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *dead) {
+    unsigned long long t0 = 0;
+    for (uint32_t n = 1; !mbar_try(bar, parity); n++) {
         if (*dead) return false;
-        if (now_ns() - t0 > WAIT_NS) {
+        if (n & 255) continue;
+        if (t0 == 0) t0 = now_ns();
+        else if (now_ns() - t0 > WAIT_NS) {
             *dead = 1;
             return false;
         }
@@ -58,6 +61,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // The same for a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead));
+}
+
+__device__ __forceinline__ bool warp_try(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try(bar, parity));
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -171,6 +178,45 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 operations in one instruction; a pair is two registers, low element first.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// One lane of a converged warp, always the same.  Issuing from an elected lane in code that the
+// whole warp runs keeps descriptors in uniform registers; from a lane's own branch each matrix
+// instruction took about 60 cycles.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Moves registers between the warpgroups of a CTA (multiples of 8; all four warps together).
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
