@@ -1,16 +1,20 @@
-"""Builds the CUDA library in-tree for sm_103a (GB300) with nvcc.
+"""Builds the CUDA library in-tree for sm_103a (GB300) with nvcc, and the compiled binding with g++.
 
-The shared object lands next to this file as libspecverify.so.  It links the CUDA runtime
-dynamically, so a process that already loaded PyTorch's libcudart.so.13 shares it.
+The shared objects land next to this file as libspecverify.so and _binding.so.  The library links
+the CUDA runtime dynamically, so a process that already loaded PyTorch's libcudart.so.13 shares
+it; the binding links PyTorch's libraries, which its user has loaded.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libspecverify.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,12 +36,27 @@ def deps():
     return out
 
 
+def start_binding(tmp: str):
+    """The g++ process that compiles the binding to `tmp`."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the binding needs PyTorch's headers")
+    torch = list(spec.submodule_search_locations)[0]
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{torch}/include",
+           f"-I{sysconfig.get_paths()['include']}", "-o", tmp, os.path.join(CSRC, "binding.cpp"), f"-L{torch}/lib",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{torch}/lib"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libspecverify.so unless it is newer than every source.  Each translation unit
-    (one per logits dtype and scheme, plus the entry points) compiles in its own nvcc process,
-    in parallel; one link makes the library."""
-    if not force and os.path.exists(LIB):
-        t = os.path.getmtime(LIB)
+    """Compile libspecverify.so and _binding.so unless they are newer than every source.  Each
+    translation unit (one per logits dtype and scheme, the entry points, the cache-side kernels)
+    compiles in its own process, in parallel; one link makes the library."""
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
+        t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
         if all(os.path.getmtime(p) <= t for p in deps()):
             return LIB
     tag = f"{os.getpid()}"
@@ -49,6 +68,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         objs.append(obj)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    binding_tmp = BINDING + f".tmp{tag}"
+    procs.append(("binding.cpp", start_binding(binding_tmp)))
     failed = False
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -57,16 +78,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         failed = failed or pr.returncode != 0
     try:
         if failed:
-            raise RuntimeError("nvcc failed building libspecverify.so")
+            raise RuntimeError("compiling libspecverify.so or _binding.so failed")
         tmp = LIB + f".tmp{tag}"
         res = subprocess.run([nvcc(), *ARCH, "-shared", "-cudart", "shared", "-Xlinker",
                               "-rpath,/usr/local/cuda/lib64", "-o", tmp, *objs], capture_output=True, text=True)
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("linking libspecverify.so failed")
+        os.replace(binding_tmp, BINDING)
         os.replace(tmp, LIB)
     finally:
-        for o in objs:
+        for o in [*objs, binding_tmp]:
             if os.path.exists(o):
                 os.remove(o)
     return LIB

@@ -40,136 +40,164 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
 }
 
 constexpr int AT = 256;   // threads per CTA
+constexpr int AU = 4;     // heads per thread and pass, all loaded before the first is used
 
-// One CTA per row.  LPH lanes hold one head, 8 elements each (a power of two >= head_dim / 8), so
-// a warp holds 32 / LPH heads; the CTA walks over the row's query, key and value heads.
-template <typename E, int LPH>
-__global__ void __launch_bounds__(AT) append_kernel(const Batch A, const Cache C, const AppendArgs P) {
+// How the two elements of a pair come together.
+enum { PAIR_NEXT, PAIR_LANES, PAIR_ANY };   // neighbours; whole lanes apart (shuffle); any distance
+
+// One CTA per row.  LPH lanes hold one head, 8 elements each (a power of two >= head_dim / 8), so a
+// thread's elements are the same in every head it meets: its rotations and weights stay in registers.
+// The row's data, the weights and the turns of the frequencies are all asked for before the chain
+// request -> length -> page is through, which is what the row waits for.
+template <typename E, int LPH, int PAIR>
+__global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cache C, const AppendArgs P) {
     __shared__ float2 turn[128];      // (cos, sin) * rope_scale of each pair
-    __shared__ float ex[AT / 32][32 / LPH][LPH * 8 + 4];
-    __shared__ int64_t slot;          // the token's offset in the cache, or -1
-    __shared__ int state;             // 0: unused row, 1: used, 2: in error
-    __shared__ int pos_s;
-    const int r = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 32) check_requests(A, C.max_pages << C.page_shift, P.hdr, r, A.R);
-    if (threadIdx.x == 0) {
-        const int b = request_of(A, r);
-        int st = 0, pos = 0;
+    __shared__ float ex[PAIR == PAIR_ANY ? AT * 8 : 1];
+    __shared__ int64_t slot;          // the token's offset in the cache
+    __shared__ int state, pos_s;      // state: 0: unused row, 1: used, 2: in error
+    const int r = blockIdx.x, tid = threadIdx.x;
+    const int D = C.D, Hq = P.Hq, Hk = C.heads, heads = Hq + 2 * Hk;
+    constexpr int HPC = AT / LPH;     // heads per CTA and step
+    const int sub = tid % LPH, h_first = tid / LPH;
+    const bool in = sub * 8 < D;
+
+    uint4 raw[AU];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < AU; u++) {
+            const int h = h0 + u * HPC + h_first;
+            const E *src = static_cast<const E *>(P.q) + r * P.q_stride + (int64_t)h * D;
+            if (h >= Hq) src = static_cast<const E *>(P.k) + r * P.k_stride + (int64_t)(h - Hq) * D;
+            if (h >= Hq + Hk) src = static_cast<const E *>(P.v) + r * P.v_stride + (int64_t)(h - Hq - Hk) * D;
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (in && h < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + sub * 8);
+        }
+    };
+    if (tid == AT - 1) check_requests(A, C.max_pages << C.page_shift, P.hdr, r, A.R);
+    int st = 0, pos = 0, b = -1;
+    if (tid == AT - 32) {
+        b = request_of(A, r);
         if (b >= 0) {
             const Span s = span_of(A, C.max_pages << C.page_shift, b);
-            if (s.err) {
-                st = 2;
-            } else if (r - s.row0 < s.n) {
+            if (s.err) st = 2;
+            else if (r - s.row0 < s.n) {
                 pos = s.len - s.n + (r - s.row0);
-                const int page = __ldg(C.table + (int64_t)b * C.max_pages + (pos >> C.page_shift));
-                if (page < 0 || page >= C.num_pages) {
-                    record_error(P.hdr, SV_DEV_BAD_PAGE, b);
-                    st = 2;
-                } else {
-                    st = 1;
-                    slot = page * C.page_stride + (pos & ((1 << C.page_shift) - 1)) * C.token_stride;
-                }
+                st = 1;
             }
         }
         state = st;
         pos_s = pos;
     }
+    load(0);
+    uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
+    if (in && P.qw) qw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.qw) + sub * 8);
+    if (in && P.kw) kw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.kw) + sub * 8);
+    const float f = tid < P.half ? __ldg(P.inv_freq + tid) : 0.f;
+    const uint64_t t = turns_of(f);
     __syncthreads();
-    const int D = C.D, Hq = P.Hq, Hk = C.heads;
-    const int st = state;
+    if (st == 1) {   // (its thread alone) the page, while the others turn the angles
+        const int page = __ldg(C.table + (int64_t)b * C.max_pages + (pos >> C.page_shift));
+        if (page < 0 || page >= C.num_pages) {
+            record_error(P.hdr, SV_DEV_BAD_PAGE, b);
+            state = 2;
+        } else {
+            slot = page * C.page_stride + (pos & ((1 << C.page_shift) - 1)) * C.token_stride;
+        }
+    }
+    if (tid < P.half) {
+        float sn, cs;
+        sincospif((float)(int32_t)(uint32_t)(t * (uint64_t)(uint32_t)pos_s >> 32) * 0x1p-31f, &sn, &cs);
+        if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
+        turn[tid] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
+    }
+    __syncthreads();
     E *out = static_cast<E *>(P.out) + r * P.out_stride;
-    if (st != 1) {
-        const uint32_t w = st == 2 ? Num<E>::NAN2 : 0u;
-        for (int i = threadIdx.x; i < Hq * D / 8; i += AT) reinterpret_cast<uint4 *>(out)[i] = make_uint4(w, w, w, w);
+    if (state != 1) {
+        const uint32_t w = state == 2 ? Num<E>::NAN2 : 0u;
+        for (int i = tid; i < Hq * D / 8; i += AT) reinterpret_cast<uint4 *>(out)[i] = make_uint4(w, w, w, w);
         return;
     }
-    for (int j = threadIdx.x; j < P.half; j += AT) {
-        const float f = __ldg(P.inv_freq + j);
-        const uint64_t t = turns_of(f) * (uint64_t)(uint32_t)pos_s;
-        float s, c;
-        sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &s, &c);
-        if (!(fabsf(f) < INFINITY)) s = c = NAN;
-        turn[j] = make_float2(c * P.rope_scale, s * P.rope_scale);
-    }
-    __syncthreads();
-    const int64_t at = slot;
-    const int sub = lane % LPH, grp = lane / LPH;
-    const bool in = sub * 8 < D;
+    // this thread's rotations: element i turns by (c, s) to x c + partner s (s signed)
     const int rot = 2 * P.half;
-    float *mine = ex[warp][grp];
-    constexpr int HPC = AT / LPH;   // heads per CTA pass
-    const int heads = Hq + 2 * Hk;
-    for (int h0 = 0; h0 < heads; h0 += HPC) {
-        const int h = h0 + warp * (32 / LPH) + grp;
-        const bool on = in && h < heads;
-        const E *src = static_cast<const E *>(P.q) + r * P.q_stride + (int64_t)h * D;
-        E *dst = out + (int64_t)h * D;
-        const E *w = static_cast<const E *>(P.qw);
-        bool turned = true;
-        if (h >= Hq + Hk) {
-            src = static_cast<const E *>(P.v) + r * P.v_stride + (int64_t)(h - Hq - Hk) * D;
-            dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
-            w = nullptr;
-            turned = false;
-        } else if (h >= Hq) {
-            src = static_cast<const E *>(P.k) + r * P.k_stride + (int64_t)(h - Hq) * D;
-            dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
-            w = static_cast<const E *>(P.kw);
+    float c[8], s[8];
+    const bool low = sub * 8 < P.half;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int d = sub * 8 + i;
+        c[i] = 1.f;
+        s[i] = 0.f;
+        if (d < rot) {
+            const bool first = PAIR == PAIR_NEXT ? i % 2 == 0 : d < P.half;
+            const float2 cs = turn[PAIR == PAIR_NEXT ? d / 2 : (first ? d : d - P.half)];
+            c[i] = cs.x;
+            s[i] = first ? -cs.y : cs.y;
         }
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (on) raw = *reinterpret_cast<const uint4 *>(src + sub * 8);
-        float x[8];
-        unpack8<E>(raw, x);
-        float ss = 0.f;
+    }
+    const int partner = PAIR == PAIR_LANES && sub * 8 < rot ? (tid & 31) + (low ? P.half / 8 : -(P.half / 8)) : tid & 31;
+    const int64_t at = slot;
+    for (int h0 = 0; h0 < heads; h0 += AU * HPC) {
+        if (h0) load(h0);
 #pragma unroll
-        for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
+        for (int u = 0; u < AU; u++) {
+            const int h = h0 + u * HPC + h_first;
+            if (h0 + u * HPC >= heads) break;   // (the whole CTA)
+            const bool is_v = h >= Hq + Hk, is_k = h >= Hq;
+            E *dst = out + (int64_t)h * D;
+            if (is_k) dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
+            if (is_v) dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
+            float x[8];
+            unpack8<E>(raw[u], x);
+            float ss = 0.f;
 #pragma unroll
-        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (on && w) {
-            float g[8];
-            unpack8<E>(*reinterpret_cast<const uint4 *>(w + sub * 8), g);
-            const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
+            for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-            for (int i = 0; i < 8; i++) x[i] *= inv * g[i];
-        }
-        if (P.interleaved) {
+            for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (is_k ? P.kw != nullptr : P.qw != nullptr) {
+                float g[8];
+                unpack8<E>(is_k ? kw : qw, g);
+                const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                if (turned && sub * 8 + i < rot) {
-                    const float2 t = turn[(sub * 8 + i) / 2];
-                    const float a = x[i], z = x[i + 1];
-                    x[i] = a * t.x - z * t.y;
-                    x[i + 1] = a * t.y + z * t.x;
-                }
+                for (int i = 0; i < 8; i++) x[i] *= inv * g[i];
             }
-        } else {
             __syncwarp();
+            float y[8];
+            if (PAIR == PAIR_NEXT) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) mine[sub * 8 + i] = x[i];
-            __syncwarp();
+                for (int i = 0; i < 8; i++) y[i] = x[i ^ 1];
+            } else if (PAIR == PAIR_LANES) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int d = sub * 8 + i;
-                if (turned && d < rot) {
-                    const bool low = d < P.half;
-                    const float2 t = turn[low ? d : d - P.half];
-                    const float o = mine[low ? d + P.half : d - P.half];
-                    x[i] = low ? x[i] * t.x - o * t.y : o * t.y + x[i] * t.x;
+                for (int i = 0; i < 8; i++) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
+            } else {
+                float *mine = ex + (tid - sub) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; i++) mine[sub * 8 + i] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int d = sub * 8 + i;
+                    y[i] = d < rot ? mine[d < P.half ? d + P.half : d - P.half] : 0.f;
                 }
+                __syncwarp();
             }
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[i] = sub * 8 + i < rot ? fmaf(y[i], s[i], x[i] * c[i]) : x[i];
+            if (in && h < heads) *reinterpret_cast<uint4 *>(dst + sub * 8) = is_v ? raw[u] : pack8<E>(x);
         }
-        if (on) *reinterpret_cast<uint4 *>(dst + sub * 8) = turned ? pack8<E>(x) : raw;
     }
 }
 
+template <typename E, int LPH>
+static cudaError_t launch_heads(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {
+    if (P.interleaved || P.half == 0) append_kernel<E, LPH, PAIR_NEXT><<<A.R, AT, 0, st>>>(A, C, P);
+    else if (P.half % 8 == 0) append_kernel<E, LPH, PAIR_LANES><<<A.R, AT, 0, st>>>(A, C, P);
+    else append_kernel<E, LPH, PAIR_ANY><<<A.R, AT, 0, st>>>(A, C, P);
+    return cudaGetLastError();
+}
 template <typename E>
 static cudaError_t launch_append(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {
     const int lanes = C.D / 8;
-    if (lanes <= 8) append_kernel<E, 8><<<A.R, AT, 0, st>>>(A, C, P);
-    else if (lanes <= 16) append_kernel<E, 16><<<A.R, AT, 0, st>>>(A, C, P);
-    else append_kernel<E, 32><<<A.R, AT, 0, st>>>(A, C, P);
-    return cudaGetLastError();
+    return lanes <= 8 ? launch_heads<E, 8>(A, C, P, st) : lanes <= 16 ? launch_heads<E, 16>(A, C, P, st)
+                                                                      : launch_heads<E, 32>(A, C, P, st);
 }
 
 }  // namespace svc
