@@ -72,9 +72,14 @@ def _load():
     l = _lib()
     _binding.init(*(C.cast(getattr(l, name), C.c_void_p).value for name in (
         "spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
-        "spec_page_compact", "spec_page_copy")), torch._C._cuda_getCurrentRawStream)
+        "spec_page_compact", "spec_page_copy", "spec_rollback")), torch._C._cuda_getCurrentRawStream)
     _native = _binding
     return _binding
+
+
+def rollback(kv_seq_len, accept_len, num_drafts, workspace, stream) -> int:
+    """The status of spec_rollback (the package's call of that name raises on it)."""
+    return (_native or _load()).rollback(kv_seq_len, accept_len, num_drafts, workspace, stream)
 
 
 def spec_append(q, k, v, q_weight, k_weight, eps: float, inv_freq, k_cache, v_cache, block_table, kv_seq_len,

@@ -1,4 +1,4 @@
-// binding.cpp -- the cache-side calls as Python functions: checks of the torch tensors, then one call
+// binding.cpp -- the cache-side calls and spec_rollback as Python functions: checks of the torch tensors, then one call
 // into libspecverify.so.  The same checks written in Python cost 12 to 15 us a call on the host that
 // drives a GB300, more than several of the kernels run.
 //
@@ -23,6 +23,7 @@ struct Entry {
     decltype(&spec_page_release) release;
     decltype(&spec_page_compact) compact;
     decltype(&spec_page_copy) copy;
+    decltype(&spec_rollback) rollback;
     PyObject *raw_stream;   // torch._C._cuda_getCurrentRawStream
 } lib;
 
@@ -298,6 +299,16 @@ sv_status copy(Args a) {
                     count32(n, "copy_src"), ws, a.stream(5));
 }
 
+// kv_seq_len, accept_len, num_drafts, workspace, stream
+sv_status rollback(Args a) {
+    int64_t n;
+    size_t bytes;
+    int32_t *ln = static_cast<int32_t *>(a.data(0, "kv_seq_len", I32, -1, &n));
+    const int32_t *acc = ints(a.data(1, "accept_len", I32, n)), *nd = ints(a.data(2, "num_drafts", I32, n));
+    void *ws = a.workspace(3, &bytes);
+    return lib.rollback(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
+}
+
 template <sv_status (*F)(Args), int N>
 PyObject *call(PyObject *, PyObject *const *v, Py_ssize_t n) {
     if (n != N) {
@@ -320,12 +331,12 @@ PyObject *call(PyObject *, PyObject *const *v, Py_ssize_t n) {
 
 // Addresses of the entry points in the order of Entry, then the raw-stream function.
 PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "expected 8 arguments");
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "expected 9 arguments");
         return nullptr;
     }
-    void *p[7];
-    for (int i = 0; i < 7; i++) {
+    void *p[8];
+    for (int i = 0; i < 8; i++) {
         p[i] = PyLong_AsVoidPtr(v[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -339,8 +350,9 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
     lib.release = reinterpret_cast<decltype(lib.release)>(p[4]);
     lib.compact = reinterpret_cast<decltype(lib.compact)>(p[5]);
     lib.copy = reinterpret_cast<decltype(lib.copy)>(p[6]);
-    Py_INCREF(v[7]);
-    lib.raw_stream = v[7];
+    lib.rollback = reinterpret_cast<decltype(lib.rollback)>(p[7]);
+    Py_INCREF(v[8]);
+    lib.raw_stream = v[8];
     Py_RETURN_NONE;
 }
 
@@ -353,6 +365,7 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("release", (call<release, 8>)),
                          FAST("compact", (call<compact, 6>)),
                          FAST("copy", (call<copy, 6>)),
+                         FAST("rollback", (call<rollback, 5>)),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Checks of tensors before the cache-side calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

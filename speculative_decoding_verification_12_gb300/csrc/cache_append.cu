@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "sv_cache.cuh"
+#include "sv_tc.cuh"
 
 namespace svc {
 
@@ -41,28 +42,35 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
 
 constexpr int AT = 256;   // threads per CTA
 constexpr int AU = 4;     // heads per thread and pass, all loaded before the first is used
+constexpr int ROWS = 32;  // rows per CTA at most
 
 // How the two elements of a pair come together.
 enum { PAIR_NEXT, PAIR_LANES, PAIR_ANY };   // neighbours; whole lanes apart (shuffle); any distance
 
-// One CTA per row.  LPH lanes hold one head, 8 elements each (a power of two >= head_dim / 8), so a
-// thread's elements are the same in every head it meets: its rotations and weights stay in registers.
-// The row's data, the weights and the turns of the frequencies are all asked for before the chain
-// request -> length -> page is through, which is what the row waits for.
+// Each CTA takes a few rows in a row.  LPH lanes hold one head, 8 elements each (a power of two >=
+// head_dim / 8), so a thread's elements are the same in every head it meets.
+//
+// What bounds it: 24 KB of a row in and out at the memory's rate is 4 ns, but each row waits for the
+// chain offsets -> length -> page.  So a CTA walks that chain once, a lane of one warp per row, while
+// the first row's data, the weights and the turns of the frequencies are under way, and asks for the
+// next row's data before it turns to the next row.
 template <typename E, int LPH, int PAIR>
-__global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cache C, const AppendArgs P) {
-    __shared__ float2 turn[128];      // (cos, sin) * rope_scale of each pair
+__global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cache C, const AppendArgs P, int per_cta) {
+    __shared__ float2 turn[2][128];   // (cos, sin) * rope_scale of each pair, of even and odd rows
     __shared__ float ex[PAIR == PAIR_ANY ? AT * 8 : 1];
-    __shared__ int64_t slot;          // the token's offset in the cache
-    __shared__ int state, pos_s;      // state: 0: unused row, 1: used, 2: in error
-    const int r = blockIdx.x, tid = threadIdx.x;
-    const int D = C.D, Hq = P.Hq, Hk = C.heads, heads = Hq + 2 * Hk;
+    __shared__ int64_t slot[ROWS];    // the tokens' offsets in the cache
+    __shared__ int state[ROWS], pos[ROWS];   // state: 0: unused row, 1: used, 2: in error
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int first = blockIdx.x * per_cta, rows = min(per_cta, A.R - first);
+    const int D = C.D, Hq = P.Hq, Hk = C.heads, heads = Hq + 2 * Hk, max_tokens = C.max_pages << C.page_shift;
     constexpr int HPC = AT / LPH;     // heads per CTA and step
     const int sub = tid % LPH, h_first = tid / LPH;
     const bool in = sub * 8 < D;
 
+    grid_wait();
+    grid_launch_dependents();
     uint4 raw[AU];
-    auto load = [&](int h0) {
+    auto load = [&](int r, int h0) {
 #pragma unroll
         for (int u = 0; u < AU; u++) {
             const int h = h0 + u * HPC + h_first;
@@ -73,125 +81,141 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
             if (in && h < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + sub * 8);
         }
     };
-    if (tid == AT - 1) check_requests(A, C.max_pages << C.page_shift, P.hdr, r, A.R);
-    int st = 0, pos = 0, b = -1;
-    if (tid == AT - 32) {
-        b = request_of(A, r);
-        if (b >= 0) {
-            const Span s = span_of(A, C.max_pages << C.page_shift, b);
+    if (tid >= AT - 32) {
+        const int r = first + lane;
+        const int b = request_of_rows(A, first, rows);   // (each lane its row's)
+        int st = 0, p = 0, page = -1;
+        if (lane < rows && b >= 0) {
+            const Span s = span_of(A, max_tokens, b);
             if (s.err) st = 2;
-            else if (r - s.row0 < s.n) {
-                pos = s.len - s.n + (r - s.row0);
+            else if (r >= s.row0 && r - s.row0 < s.n) {
                 st = 1;
+                p = s.len - s.n + (r - s.row0);
+                page = __ldg(C.table + (int64_t)b * C.max_pages + (p >> C.page_shift));
+                if (page < 0 || page >= C.num_pages) {
+                    record_error(P.hdr, SV_DEV_BAD_PAGE, b);
+                    st = 2;
+                }
             }
         }
-        state = st;
-        pos_s = pos;
+        if (lane < rows) {
+            state[lane] = st;
+            pos[lane] = p;
+            slot[lane] = page * C.page_stride + (p & ((1 << C.page_shift) - 1)) * C.token_stride;
+        }
+    } else if (tid >= AT - 64) {
+        check_requests(A, max_tokens, P.hdr, blockIdx.x * 32 + lane, gridDim.x * 32);
     }
-    load(0);
+    load(first, 0);
     uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
     if (in && P.qw) qw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.qw) + sub * 8);
     if (in && P.kw) kw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.kw) + sub * 8);
     const float f = tid < P.half ? __ldg(P.inv_freq + tid) : 0.f;
     const uint64_t t = turns_of(f);
-    __syncthreads();
-    if (st == 1) {   // (its thread alone) the page, while the others turn the angles
-        const int page = __ldg(C.table + (int64_t)b * C.max_pages + (pos >> C.page_shift));
-        if (page < 0 || page >= C.num_pages) {
-            record_error(P.hdr, SV_DEV_BAD_PAGE, b);
-            state = 2;
-        } else {
-            slot = page * C.page_stride + (pos & ((1 << C.page_shift) - 1)) * C.token_stride;
-        }
-    }
-    if (tid < P.half) {
-        float sn, cs;
-        sincospif((float)(int32_t)(uint32_t)(t * (uint64_t)(uint32_t)pos_s >> 32) * 0x1p-31f, &sn, &cs);
-        if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
-        turn[tid] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
-    }
-    __syncthreads();
-    E *out = static_cast<E *>(P.out) + r * P.out_stride;
-    if (state != 1) {
-        const uint32_t w = state == 2 ? Num<E>::NAN2 : 0u;
-        for (int i = tid; i < Hq * D / 8; i += AT) reinterpret_cast<uint4 *>(out)[i] = make_uint4(w, w, w, w);
-        return;
-    }
-    // this thread's rotations: element i turns by (c, s) to x c + partner s (s signed)
     const int rot = 2 * P.half;
-    float c[8], s[8];
     const bool low = sub * 8 < P.half;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int d = sub * 8 + i;
-        c[i] = 1.f;
-        s[i] = 0.f;
-        if (d < rot) {
-            const bool first = PAIR == PAIR_NEXT ? i % 2 == 0 : d < P.half;
-            const float2 cs = turn[PAIR == PAIR_NEXT ? d / 2 : (first ? d : d - P.half)];
-            c[i] = cs.x;
-            s[i] = first ? -cs.y : cs.y;
+    const int partner = PAIR == PAIR_LANES && sub * 8 < rot ? lane + (low ? P.half / 8 : -(P.half / 8)) : lane;
+    __syncthreads();
+
+#pragma unroll 1
+    for (int i = 0; i < rows; i++) {
+        const int r = first + i, st = state[i];
+        if (tid < P.half) {
+            float sn, cs;
+            sincospif((float)(int32_t)(uint32_t)(t * (uint64_t)(uint32_t)pos[i] >> 32) * 0x1p-31f, &sn, &cs);
+            if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
+            turn[i & 1][tid] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
         }
-    }
-    const int partner = PAIR == PAIR_LANES && sub * 8 < rot ? (tid & 31) + (low ? P.half / 8 : -(P.half / 8)) : tid & 31;
-    const int64_t at = slot;
-    for (int h0 = 0; h0 < heads; h0 += AU * HPC) {
-        if (h0) load(h0);
+        __syncthreads();   // (and no one is still at the row before the last, whose turns these were)
+        E *out = static_cast<E *>(P.out) + r * P.out_stride;
+        if (st != 1) {
+            const uint32_t w = st == 2 ? Num<E>::NAN2 : 0u;
+            for (int j = tid; j < Hq * D / 8; j += AT) reinterpret_cast<uint4 *>(out)[j] = make_uint4(w, w, w, w);
+            if (i + 1 < rows) load(r + 1, 0);
+            continue;
+        }
+        // this thread's rotations: element e turns by (c, s) to x c + partner s (s signed)
+        float c[8], s[8];
 #pragma unroll
-        for (int u = 0; u < AU; u++) {
-            const int h = h0 + u * HPC + h_first;
-            if (h0 + u * HPC >= heads) break;   // (the whole CTA)
-            const bool is_v = h >= Hq + Hk, is_k = h >= Hq;
-            E *dst = out + (int64_t)h * D;
-            if (is_k) dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
-            if (is_v) dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
-            float x[8];
-            unpack8<E>(raw[u], x);
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (is_k ? P.kw != nullptr : P.qw != nullptr) {
-                float g[8];
-                unpack8<E>(is_k ? kw : qw, g);
-                const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
-#pragma unroll
-                for (int i = 0; i < 8; i++) x[i] *= inv * g[i];
+        for (int e = 0; e < 8; e++) {
+            const int d = sub * 8 + e;
+            c[e] = 1.f;
+            s[e] = 0.f;
+            if (d < rot) {
+                const bool head = PAIR == PAIR_NEXT ? e % 2 == 0 : d < P.half;
+                const float2 cs = turn[i & 1][PAIR == PAIR_NEXT ? d / 2 : (head ? d : d - P.half)];
+                c[e] = cs.x;
+                s[e] = head ? -cs.y : cs.y;
             }
-            __syncwarp();
-            float y[8];
-            if (PAIR == PAIR_NEXT) {
+        }
+        const int64_t at = slot[i];
+#pragma unroll 1
+        for (int h0 = 0; h0 < heads; h0 += AU * HPC) {
+            if (h0) load(r, h0);
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[i] = x[i ^ 1];
-            } else if (PAIR == PAIR_LANES) {
+            for (int u = 0; u < AU; u++) {
+                const int h = h0 + u * HPC + h_first;
+                if (h0 + u * HPC >= heads) break;   // (the whole CTA)
+                const bool is_v = h >= Hq + Hk, is_k = h >= Hq;
+                E *dst = out + (int64_t)h * D;
+                if (is_k) dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
+                if (is_v) dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
+                float x[8];
+                unpack8<E>(raw[u], x);
+                float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
-            } else {
-                float *mine = ex + (tid - sub) * 8;
+                for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-                for (int i = 0; i < 8; i++) mine[sub * 8 + i] = x[i];
-                __syncwarp();
+                for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (is_k ? P.kw != nullptr : P.qw != nullptr) {
+                    float g[8];
+                    unpack8<E>(is_k ? kw : qw, g);
+                    const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int d = sub * 8 + i;
-                    y[i] = d < rot ? mine[d < P.half ? d + P.half : d - P.half] : 0.f;
+                    for (int e = 0; e < 8; e++) x[e] *= inv * g[e];
                 }
                 __syncwarp();
-            }
+                float y[8];
+                if (PAIR == PAIR_NEXT) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) x[i] = sub * 8 + i < rot ? fmaf(y[i], s[i], x[i] * c[i]) : x[i];
-            if (in && h < heads) *reinterpret_cast<uint4 *>(dst + sub * 8) = is_v ? raw[u] : pack8<E>(x);
+                    for (int e = 0; e < 8; e++) y[e] = x[e ^ 1];
+                } else if (PAIR == PAIR_LANES) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
+                } else {
+                    float *mine = ex + (tid - sub) * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) mine[sub * 8 + e] = x[e];
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int d = sub * 8 + e;
+                        y[e] = d < rot ? mine[d < P.half ? d + P.half : d - P.half] : 0.f;
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++) x[e] = sub * 8 + e < rot ? fmaf(y[e], s[e], x[e] * c[e]) : x[e];
+                if (in && h < heads) *reinterpret_cast<uint4 *>(dst + sub * 8) = is_v ? raw[u] : pack8<E>(x);
+            }
         }
+        if (i + 1 < rows) load(r + 1, 0);
     }
 }
 
 template <typename E, int LPH>
 static cudaError_t launch_heads(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {
-    if (P.interleaved || P.half == 0) append_kernel<E, LPH, PAIR_NEXT><<<A.R, AT, 0, st>>>(A, C, P);
-    else if (P.half % 8 == 0) append_kernel<E, LPH, PAIR_LANES><<<A.R, AT, 0, st>>>(A, C, P);
-    else append_kernel<E, LPH, PAIR_ANY><<<A.R, AT, 0, st>>>(A, C, P);
-    return cudaGetLastError();
+    int dev = 0, nsm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // one wave of resident CTAs where the rows allow
+    int per = (A.R + 3 * nsm - 1) / (3 * nsm);
+    if (per > ROWS) per = ROWS;
+    const int grid = (A.R + per - 1) / per;
+    if (P.interleaved || P.half == 0) return launch_dependent(append_kernel<E, LPH, PAIR_NEXT>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
+    if (P.half % 8 == 0) return launch_dependent(append_kernel<E, LPH, PAIR_LANES>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
+    return launch_dependent(append_kernel<E, LPH, PAIR_ANY>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
 }
 template <typename E>
 static cudaError_t launch_append(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {

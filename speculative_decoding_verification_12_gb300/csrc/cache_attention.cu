@@ -49,7 +49,7 @@ struct AttnArgs {
     int32_t *hdr;
     int4 *desc;        // workspace, per CTA: the row tile whose first part, but not last, it holds
     float *part_lse;   // workspace, [2 * MAX_CTAS][PART_ROWS]: log2 of the part's sum
-    float *part_o;     // workspace, [2 * MAX_CTAS][DP / 4][PART_ROWS][4]
+    float *part_o;     // workspace, [2 * MAX_CTAS][PART_ROWS][DP]
     float c;           // |scale| log2(e)
     uint32_t qflip;    // sign flip of two queries (scale < 0)
     int qzero;         // scale == 0
@@ -112,6 +112,11 @@ struct __align__(16) Seg {
 };
 constexpr int SEGS = 32;                 // segments in flight between the front warp and the others
 constexpr int SEG_READERS = 11;          // warps that take each of them
+
+// a / b for a >= 0, b > 0: nearly always in 32 bits, where it takes a tenth of the time.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return (a >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 
 // Whether the row at position pos sees token j.
 __device__ __forceinline__ bool sees(const AttnArgs &P, int pos, int j) {
@@ -239,63 +244,66 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_tiles == 1 ? 2 : 1;
 
-    if (tid == 0) {
-        for (int i = 0; i < MAX_STAGES; i++) {
-            mbar_init(k_full + 8 * i, 1), mbar_init(k_empty + 8 * i, 1);
-            mbar_init(v_full + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
-        }
-        for (int g = 0; g < 2; g++) {
-            mbar_init(s_full + 8 * g, 1), mbar_init(p_full + 8 * g, 4), mbar_init(o_done + 8 * g, 1);
-            mbar_init(q_full + 8 * g, 1), mbar_init(q_empty + 8 * g, 1), mbar_init(both + 8 * g, 8);
-        }
-        mbar_init(drained, 1);
-        for (int i = 0; i < SEGS; i++) mbar_init(seg_full + 8 * i, 1), mbar_init(seg_empty + 8 * i, SEG_READERS);
-        ctl[0] = 0;
-        for (int i = 0; i < 8; i++) patched[i] = -1;
-        for (int i = 0; i < 16; i++) bad[i] = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // one thread per barrier: the rings and pairs in a row from k_full, then the segments'
+    constexpr int NBARS = 4 * MAX_STAGES + 13;
+    if (tid < NBARS) {
+        const int p = tid - 4 * MAX_STAGES;   // s_full, p_full, o_done, q_full, q_empty, both: two each; drained
+        mbar_init(k_full + 8 * tid, p < 0 ? 1 : p / 2 == 1 ? 4 : p / 2 == 5 ? 8 : 1);
+    } else if (tid >= 128 && tid < 128 + 2 * SEGS) {
+        mbar_init(seg_full + 8 * (tid - 128), tid < 128 + SEGS ? 1 : SEG_READERS);
+    } else if (tid >= 256 && tid < 256 + 28 && tid != 257) {   // (1 is the tensor memory's address)
+        ctl[tid - 256] = tid >= 260 && tid < 268 ? -1 : 0;   // patched: -1
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (warp == W_MMA) tmem_alloc(smem_addr(ctl + 1), 512);
     grid_wait();   // the work before this on the stream may still be writing what follows
 
-    // the batch's units, and where this CTA's range begins
-    long long &start_pre = scan[NW], &total_units = scan[NW + 1], &start_b = scan[NW + 2];
-    long long sum = 0;
-    for (int b = tid; b < A.B; b += NTHREADS) sum += units_of(req_of(A, C, P, b), C.heads);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) scan[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        long long t = 0;
-        for (int w = 0; w < NW; w++) t += scan[w];
-        total_units = t;
-    }
-    __syncthreads();
-    const long long T = total_units;
-    const int nc = (int)min((long long)gridDim.x, T), cta = blockIdx.x;
-    const long long lo = cta < nc ? T * cta / nc : 0, hi = cta < nc ? T * (cta + 1) / nc : 0;
-    if (lo < hi) {   // (the whole CTA)
-        long long before = 0;
-        for (int b0 = 0; before <= lo; b0 += NTHREADS) {
+    // the batch's units, and where this CTA's range begins: prefix sums over the requests, NTHREADS at a
+    // time (a batch of up to that many is looked at once)
+    long long &start_pre = scan[NW], &start_b = scan[NW + 1];
+    long long T = 0, lo = 0, hi = 0, before = 0;
+    int nc = 0;
+    const int cta = blockIdx.x;
+    __syncthreads();   // (barriers and flags are set)
+#pragma unroll 1
+    for (int pass = A.B <= NTHREADS; pass < 2; pass++) {   // pass 0 sums, pass 1 finds
+        before = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < A.B; b0 += NTHREADS) {
             const int b = b0 + tid;
             const long long w = b < A.B ? units_of(req_of(A, C, P, b), C.heads) : 0;
             long long inc = w;
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
-            __syncthreads();
+            if (b0) __syncthreads();
             if (lane == 31) scan[warp] = inc;
             __syncthreads();
             long long pre = before + inc - w, all = 0;
+#pragma unroll 1
             for (int i = 0; i < NW; i++) {
-                if (i < warp) pre += scan[i];
-                all += scan[i];
+                const long long x = scan[i];
+                if (i < warp) pre += x;
+                all += x;
             }
-            if (pre <= lo && lo < pre + w) start_b = b, start_pre = pre;
             before += all;
-            if (b0 + NTHREADS >= A.B) break;
+            if (pass == 0) continue;
+            if (b0 == 0) {
+                if (A.B <= NTHREADS) T = all;
+                nc = (int)min((long long)gridDim.x, T);
+                if (cta < nc) {   // [T cta / nc, T (cta + 1) / nc)
+                    const long long q = quotient(T, nc);
+                    const int rest = (int)(T - q * nc);
+                    lo = q * cta + rest * cta / nc;
+                    hi = q * (cta + 1) + rest * (cta + 1) / nc;
+                }
+            }
+            if (lo < hi && pre <= lo && lo < pre + w) start_b = b, start_pre = pre;
         }
+        if (pass == 0) T = before;
+        __syncthreads();
     }
     tc_fence_before();
     __syncthreads();
@@ -375,9 +383,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             }
         }
         if (!ok) {   // let the copies in flight land before the CTA may end
-            const unsigned long long t0 = now_ns();
+            const uint32_t t0 = now_ns32();
             for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
-                while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns() - t0 < WAIT_NS) {}
+                while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
         }
     } else if (warp == W_MMA) {
         // Matrix instructions.  Over all segments the row tiles' products come in one sequence: tile v
@@ -410,8 +418,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         Place ks{0, 0}, vs{0, 0}, qs{0, 0};
         uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each group's next P
         int lead = 0;                      // products whose S, but not P V, is issued: at most 2
-        uint32_t spins = 0;
-        unsigned long long t0 = 0;
+        uint32_t polls = 0, idle_since = 0;
         // the next S has its operands
         auto s_ready = [&]() {
             return snv && (sv || warp_try(q_full + 8 * qs.stage, qs.parity)) && warp_try(k_full + 8 * ks.stage, ks.parity);
@@ -422,11 +429,10 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             if (lead == 2 || !do_s) {
                 do_o = lead > 0 && warp_try(p_full + 8 * go, np >> go & 1) && warp_try(v_full + 8 * vs.stage, vs.parity);
                 if (!do_o) {
-                    bool late = *dead;
-                    if ((++spins & 255) == 0) {
-                        if (spins == 256) t0 = now_ns();
-                        else late |= now_ns() - t0 > WAIT_NS;
-                    }
+                    if (++polls & 255) continue;
+                    const uint32_t now = now_ns32() | 1;
+                    if (!idle_since) idle_since = now;
+                    const bool late = *dead || now - idle_since > WAIT_NS;
                     if (__any_sync(0xffffffffu, late)) {
                         *dead = 1;
                         ok = false;
@@ -435,7 +441,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 }
                 if (!do_s) do_s = s_ready();
             }
-            spins = 0;
+            idle_since = 0;
             tc_fence_after();
             const bool last_use = !otwo || (ov & 1);
             if (leader) {
@@ -488,8 +494,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         }
         if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
             if (leader) mma_commit(drained);
-            const unsigned long long t0 = now_ns();
-            while (!mbar_try(drained, 0) && now_ns() - t0 < WAIT_NS) {}
+            const uint32_t t0 = now_ns32();
+            while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
         }
         __syncwarp();
     } else {
@@ -528,8 +534,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 s.ns = __shfl_sync(0xffffffffu, r.ns, i), s.nt = __shfl_sync(0xffffffffu, r.nt, i);
                 const int mt = __shfl_sync(0xffffffffu, r.mt, i), per = s.nt + OVERHEAD, all = mt * C.heads;
                 if (s.nt) {
-                    const int u0 = (int)((pos - pre) / per);
-                    const int u1 = min(min(all, u0 + 16), (int)min((long long)all, (hi - pre + per - 1) / per));
+                    const int u0 = (int)quotient(pos - pre, per);
+                    const int u1 = min(min(all, u0 + 16), (int)min((long long)all, quotient(hi - pre + per - 1, per)));
                     const int u = u0 + lane;
                     const long long first = pre + (long long)u * per;   // the row tile's first unit
                     s.b = b;
@@ -790,9 +796,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                             if (c < D) *reinterpret_cast<uint4 *>(to) = pack8<E>(o);
                             if (c + 8 < D) *reinterpret_cast<uint4 *>(to + 8) = pack8<E>(o + 8);
                         } else {
-                            float4 *to = reinterpret_cast<float4 *>(P.part_o) + ((int64_t)slot * (DP / 4) + c / 4) * PART_ROWS + rt;
+                            float4 *to = reinterpret_cast<float4 *>(P.part_o + ((int64_t)slot * PART_ROWS + rt) * DP + c);
 #pragma unroll
-                            for (int i = 0; i < 4; i++) to[i * PART_ROWS] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < 4; i++) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                     }
                     __syncwarp();
@@ -803,7 +809,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                             E &y = static_cast<E *>(P.out)[orow * D + d];
                             y = (E)((float)y + x);
                         } else {
-                            P.part_o[(((int64_t)slot * (DP / 4) + d / 4) * PART_ROWS + rt) * 4 + d % 4] += x;
+                            P.part_o[((int64_t)slot * PART_ROWS + rt) * DP + d] += x;
                         }
                     });
                 }
@@ -829,54 +835,105 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     }
 }
 
+// Four columns (from 4 sub on) of a joined row, and its lse.
+template <typename E>
+__device__ __forceinline__ void store_joined(const AttnArgs &P, const Cache &C, const Req &s, int4 d, int rt, int sub, float4 o,
+                                             float sum, float top) {
+    if (sub * 4 >= C.D) return;
+    const float inv = 1.f / sum;
+    const int rr = d.z * 2 * TILE + rt, tok = rr / P.G;
+    const int64_t orow = (int64_t)(s.row0 + tok) * P.Hq + d.y * P.G + rr - tok * P.G;
+    *reinterpret_cast<uint2 *>(static_cast<E *>(P.out) + orow * C.D + sub * 4) =
+        make_uint2(Num<E>::down(o.x * inv, o.y * inv), Num<E>::down(o.z * inv, o.w * inv));
+    if (P.lse && sub == 0) P.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 // Joins the parts of the row tiles that several CTAs hold, in order of the CTAs, and sets the rows
-// that no request uses.  Block (c, y): rows [32 y, 32 y + 32) of the row tile that begins in CTA c.
+// that no request uses.  Blocks (c, y): rows y, y + gridDim.y, ... of the row tile that begins in CTA c.
+// Many rows of few parts (long draft chains): a row per DP / 4 lanes.  Else a row's parts are spread over
+// the block, 16 bytes of a part per thread, and the thread groups' sums are added in shared memory: one
+// long request's parts (19 for 131 072 keys) then come in one round trip.
 template <typename E, int DP>
 __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C, const AttnArgs P) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int TPP = DP / 4, LANES = 256 / TPP;   // threads per part, parts at a time
+    __shared__ float weight[MAX_CTAS];
+    __shared__ float4 sums[LANES][TPP];
+    __shared__ float red[2][8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nblocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
     grid_wait();
     const int4 d = P.desc[blockIdx.x];
     if (d.x >= 0) {
         const Req s = req_of(A, C, P, d.x);
-        const int rows = min(s.M - d.z * 2 * TILE, 2 * TILE);
-        const int rt = blockIdx.y * 32 + lane;
-        if (rt < rows) {
-            const int first = blockIdx.x, last = d.w;
-            float top = -INFINITY;
-            bool nan = false;
-            for (int c = first; c <= last; c++) {
-                const float v = P.part_lse[(2 * c + (c == first)) * PART_ROWS + rt];
-                nan |= v != v;
-                top = fmaxf(top, v);
+        const int rows = min(s.M - d.z * 2 * TILE, 2 * TILE), first = blockIdx.x, parts = d.w - first + 1;
+        auto slot = [&](int p) { return 2 * (first + p) + (p == 0); };
+        if (parts <= TPP && rows > 2 * (int)gridDim.y) {
+            const int sub = lane % TPP;
+            for (int r0 = blockIdx.y * LANES; r0 < rows; r0 += gridDim.y * LANES) {   // (the whole warp)
+                const int rt = r0 + tid / TPP;
+                const bool on = rt < rows;
+                const float v = on && sub < parts ? P.part_lse[slot(sub) * PART_ROWS + rt] : -INFINITY;
+                float top = v;
+#pragma unroll
+                for (int o = TPP / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float f = v == -INFINITY ? 0.f : ex2(v - top);
+                float sum = f;
+#pragma unroll
+                for (int o = TPP / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int p = 0; p < parts; p++) {
+                    const float w = __shfl_sync(0xffffffffu, f, lane - sub + p);
+                    const float4 x = on ? *reinterpret_cast<const float4 *>(P.part_o + ((int64_t)slot(p) * PART_ROWS + rt) * DP + sub * 4)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+                }
+                if (on) store_joined<E>(P, C, s, d, rt, sub, o, sum, top);
             }
+        } else for (int rt = blockIdx.y; rt < rows; rt += gridDim.y) {
+            const float *lse = P.part_lse + rt;
+            const float v = tid < parts ? lse[slot(tid) * PART_ROWS] : -INFINITY;   // (parts <= MAX_CTAS < 256)
+            const float *from = P.part_o + (int64_t)rt * DP + (tid % TPP) * 4;
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {   // the first parts' values, under way while the weights come together
+                const int p = tid / TPP + i * LANES;
+                x[i] = p < parts ? *reinterpret_cast<const float4 *>(from + (int64_t)slot(p) * PART_ROWS * DP) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = v;
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) red[0][warp] = top;
+            __syncthreads();
+            top = red[0][0];
+            for (int i = 1; i < 8; i++) top = fmaxf(top, red[0][i]);
+            float f = v == -INFINITY ? 0.f : ex2(v - top);   // (NaN where a part is)
+            if (tid < parts) weight[tid] = f;
+            for (int o = 16; o; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+            if (lane == 0) red[1][warp] = f;
+            __syncthreads();
             float sum = 0.f;
-            float4 o[DP / 32];
+            for (int i = 0; i < 8; i++) sum += red[1][i];
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p0 = tid / TPP; p0 < parts; p0 += 4 * LANES) {
 #pragma unroll
-            for (int i = 0; i < DP / 32; i++) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = first; c <= last; c++) {
-                const int slot = 2 * c + (c == first);
-                const float f = ex2(P.part_lse[slot * PART_ROWS + rt] - top);
-                sum += f;
-                const float4 *from = reinterpret_cast<const float4 *>(P.part_o) + ((int64_t)slot * (DP / 4) + warp) * PART_ROWS + rt;
-#pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    const float4 x = from[(int64_t)i * 8 * PART_ROWS];
-                    o[i].x += f * x.x, o[i].y += f * x.y, o[i].z += f * x.z, o[i].w += f * x.w;
+                for (int i = 0; i < 4; i++) {
+                    const int p = p0 + i * LANES;
+                    if (p >= parts) break;
+                    if (p0 >= LANES) x[i] = *reinterpret_cast<const float4 *>(from + (int64_t)slot(p) * PART_ROWS * DP);
+                    const float w = weight[p];
+                    o.x += w * x[i].x, o.y += w * x[i].y, o.z += w * x[i].z, o.w += w * x[i].w;
                 }
             }
-            if (nan) sum = NAN;
-            const float inv = 1.f / sum;
-            const int rr = d.z * 2 * TILE + rt, tok = rr / P.G;
-            const int64_t orow = (int64_t)(s.row0 + tok) * P.Hq + d.y * P.G + rr - tok * P.G;
-#pragma unroll
-            for (int i = 0; i < DP / 32; i++) {
-                const int col = (i * 8 + warp) * 4;
-                if (col < C.D)
-                    *reinterpret_cast<uint2 *>(static_cast<E *>(P.out) + orow * C.D + col) =
-                        make_uint2(Num<E>::down(o[i].x * inv, o[i].y * inv), Num<E>::down(o[i].z * inv, o[i].w * inv));
+            sums[tid / TPP][tid % TPP] = o;
+            __syncthreads();
+            if (tid < TPP && tid * 4 < C.D) {
+                for (int i = 1; i < LANES; i++) {
+                    const float4 y = sums[i][tid];
+                    o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+                }
+                store_joined<E>(P, C, s, d, rt, tid, o, sum, top);
             }
-            if (P.lse && warp == 0) P.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+            __syncthreads();
         }
     }
     // unused rows: zeros; the rows of a request in error: NaN
@@ -987,7 +1044,7 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attention_kernel<E, DP>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
-    cfg.gridDim = dim3(ctas, (min(most_rows, PART_ROWS) + 31) / 32);
+    cfg.gridDim = dim3(ctas, most_rows < 16 ? most_rows : 16);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<E, DP>, A, C, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;

@@ -12,6 +12,7 @@
 #include <limits.h>
 
 #include "sv_cache.cuh"
+#include "sv_tc.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -196,6 +197,8 @@ __device__ __forceinline__ Want want_of(const PageState &S, const int32_t *nd, i
 __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const int32_t *nd) {
     __shared__ int counts[PW + 1];
     __shared__ long long tmp[PW + 1];
+    grid_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     long long sum = 0, want = 0;
     for (int b = threadIdx.x; b < S.B; b += PT) sum += want_of(S, nd, b).need;
@@ -275,6 +278,8 @@ __device__ __forceinline__ int fork_check(const PageState &S, const ForkArgs &K,
 __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkArgs K) {
     __shared__ int counts[PW + 1];
     __shared__ long long tmp[PW + 1];
+    grid_wait();
+    grid_launch_dependents();
     const int free = list_free(S, K.F, counts);
     if (cg::this_cluster().block_rank() != 0) return;
     for (int f = threadIdx.x; f < K.F; f += PT) {
@@ -326,6 +331,8 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
 constexpr int ST = 256, SPT = 4;   // threads per CTA, table entries per thread
 
 __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkArgs K) {
+    grid_wait();
+    grid_launch_dependents();
     const int f = blockIdx.x;
     const int n = S.result[f];
     if (n < 0) return;
@@ -377,6 +384,8 @@ __device__ __forceinline__ bool give_back(const PageState &S, int32_t *e, int b)
 // One CTA per request and direction (y = 0: past the length, upward; 1: before the window,
 // downward), RELEASE_CHUNK entries at a time until a chunk holds nothing.
 __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int window, int sinks) {
+    grid_wait();
+    grid_launch_dependents();
     const int b = blockIdx.x;
     const int len = S.len[b];
     if (len < 0) return;
@@ -421,6 +430,8 @@ __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int wind
 // are equally many.  S.list becomes the map from page to page for ids >= U.
 __global__ void __launch_bounds__(PT) compact_kernel(const PageState S, int32_t *src, int32_t *dst, int cap) {
     __shared__ int counts[3][PW + 1];
+    grid_wait();
+    grid_launch_dependents();
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31;
     const Slice sl = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
@@ -482,6 +493,8 @@ __global__ void __launch_bounds__(PT) compact_kernel(const PageState S, int32_t 
 }
 
 __global__ void __launch_bounds__(ST) remap_kernel(const PageState S) {
+    grid_wait();
+    grid_launch_dependents();
     const int U = *S.used;
     const long long total = (long long)S.B * S.max_pages;
     for (long long j = (long long)blockIdx.x * ST + threadIdx.x; j < total; j += (long long)gridDim.x * ST) {
@@ -505,34 +518,49 @@ struct CopyArgs {
     int num_pages, layers, n;
 };
 
-constexpr int CT = 256, CU = 8;   // threads per CTA, 16-byte loads in flight per thread
+constexpr int CT = 256, CU = 4;   // threads per CTA, 16-byte loads in flight per thread
 
+// An item is one pair in one layer's keys or values; a CTA takes every gridDim.x-th, and looks up 256 of
+// them at once, so that the pairs' latency is paid once and an absent pair costs next to nothing.
+// Bound by the memory: 16 KB pages move at 6.2 TB/s read and write together, 8 CTAs an SM.
 __global__ void __launch_bounds__(CT) copy_kernel(const CopyArgs A) {
-    const long long per_pair = (long long)A.layers * (A.v ? 2 : 1);
-    const long long items = per_pair * A.n;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int i = (int)(it / per_pair), part = (int)(it % per_pair);
-        const int s = __ldg(A.src + i), d = __ldg(A.dst + i);
-        if (s < 0 || d < 0) continue;
-        if (s >= A.num_pages || d >= A.num_pages) {
-            if (part == 0 && threadIdx.x == 0) record_error(A.hdr, SV_DEV_BAD_PAGE, i);
-            continue;
-        }
-        char *base = (part >= A.layers ? A.v : A.k) + (part % A.layers) * A.layer_stride;
-        const uint4 *from = reinterpret_cast<const uint4 *>(base + s * A.page_stride);
-        uint4 *to = reinterpret_cast<uint4 *>(base + d * A.page_stride);
-        const long long words = A.page_bytes / 16;
-        for (long long w0 = 0; w0 < words; w0 += CT * CU) {
-            uint4 x[CU];
-#pragma unroll
-            for (int u = 0; u < CU; u++) {
-                const long long w = w0 + u * CT + threadIdx.x;
-                if (w < words) x[u] = __ldcs(from + w);
+    __shared__ int2 pairs[CT];
+    grid_wait();
+    grid_launch_dependents();
+    const long long per_pair = (long long)A.layers * (A.v ? 2 : 1), items = per_pair * A.n;
+    const int words = (int)(A.page_bytes / 16);
+    for (long long base = blockIdx.x; base < items; base += (long long)CT * gridDim.x) {
+        const long long mine = base + (long long)threadIdx.x * gridDim.x;
+        int2 x = make_int2(-1, -1);
+        if (mine < items) {
+            const int i = (int)(mine / per_pair);
+            x = make_int2(__ldg(A.src + i), __ldg(A.dst + i));
+            if (x.x < 0 || x.y < 0) {
+                x.x = -1;
+            } else if (x.x >= A.num_pages || x.y >= A.num_pages) {
+                record_error(A.hdr, SV_DEV_BAD_PAGE, i);
+                x.x = -1;
             }
+        }
+        __syncthreads();
+        pairs[threadIdx.x] = x;
+        __syncthreads();
+        const int count = (int)min((long long)CT, (items - base + gridDim.x - 1) / gridDim.x);
+        for (int j = 0; j < count; j++) {
+            const int2 p = pairs[j];
+            if (p.x < 0) continue;
+            const int part = (int)((base + (long long)j * gridDim.x) % per_pair);
+            char *at = (part >= A.layers ? A.v : A.k) + (part >= A.layers ? part - A.layers : part) * A.layer_stride;
+            const uint4 *from = reinterpret_cast<const uint4 *>(at + p.x * A.page_stride);
+            uint4 *to = reinterpret_cast<uint4 *>(at + p.y * A.page_stride);
+            for (int w0 = threadIdx.x; w0 < words; w0 += CT * CU) {
+                uint4 v[CU];
 #pragma unroll
-            for (int u = 0; u < CU; u++) {
-                const long long w = w0 + u * CT + threadIdx.x;
-                if (w < words) __stcs(to + w, x[u]);
+                for (int u = 0; u < CU; u++)
+                    if (w0 + u * CT < words) v[u] = __ldcs(from + w0 + u * CT);
+#pragma unroll
+                for (int u = 0; u < CU; u++)
+                    if (w0 + u * CT < words) __stcs(to + w0 + u * CT, v[u]);
             }
         }
     }
@@ -561,22 +589,12 @@ static PageState page_state(int32_t *len, int32_t B, int32_t *table, int32_t max
                      reinterpret_cast<int32_t *>(w + L.used)};
 }
 
-// Launches a bookkeeping kernel as one cluster.
+// A bookkeeping kernel as one cluster.
 template <typename... P, typename... A>
 static cudaError_t launch_cluster(void (*kernel)(P...), int num_pages, cudaStream_t st, A... args) {
     int ctas = 1;
     while (ctas < 8 && (long long)ctas * PAGES_PER_CTA < num_pages) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(PT);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return launch_dependent(kernel, dim3(ctas), dim3(PT), ctas, st, args...);
 }
 
 }  // namespace svc
@@ -614,8 +632,8 @@ extern "C" sv_status spec_page_fork(const int32_t *parents, const int32_t *child
     const ForkArgs K{parents, children, fork_len, copy_src, copy_dst, num_forks};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (launch_cluster(fork_kernel, num_pages, st, S, K) != cudaSuccess) return SV_ERR_CUDA;
-    fork_share<<<dim3(num_forks, (max_pages + RELEASE_CHUNK - 1) / RELEASE_CHUNK), ST, 0, st>>>(S, K);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_dependent(fork_share, dim3(num_forks, (max_pages + RELEASE_CHUNK - 1) / RELEASE_CHUNK), dim3(ST), 1, st, S, K) ==
+                   cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status spec_page_release(const int32_t *kv_seq_len, int32_t B, int32_t *block_table, int32_t max_pages,
@@ -626,8 +644,8 @@ extern "C" sv_status spec_page_release(const int32_t *kv_seq_len, int32_t B, int
     if (!kv_seq_len || window < 0 || sinks < 0) return SV_ERR_INVALID_ARG;
     const PageState S = page_state(const_cast<int32_t *>(kv_seq_len), B, block_table, max_pages, ref_count, num_pages,
                                    page_size, workspace);
-    release_kernel<<<dim3(B, window ? 2 : 1), ST, 0, static_cast<cudaStream_t>(stream)>>>(S, window, sinks);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_dependent(release_kernel, dim3(B, window ? 2 : 1), dim3(ST), 1, static_cast<cudaStream_t>(stream), S, window,
+                            sinks) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status spec_page_compact(int32_t B, int32_t *block_table, int32_t max_pages, int32_t *ref_count,
@@ -642,8 +660,8 @@ extern "C" sv_status spec_page_compact(int32_t B, int32_t *block_table, int32_t 
     if (launch_cluster(compact_kernel, num_pages, st, S, copy_src, copy_dst, capacity) != cudaSuccess)
         return SV_ERR_CUDA;
     const long long blocks = ((long long)B * max_pages + ST * 4 - 1) / (ST * 4);
-    remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), ST, 0, st>>>(S);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_dependent(remap_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(ST), 1, st, S) == cudaSuccess
+               ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status spec_page_copy(void *k, void *v, int64_t page_bytes, int64_t page_stride, int32_t num_layers,
@@ -652,11 +670,12 @@ extern "C" sv_status spec_page_copy(void *k, void *v, int64_t page_bytes, int64_
     if (!k || !copy_src || !copy_dst || !workspace || n < 1 || num_pages < 1 || num_layers < 1 || page_bytes < 1 ||
         page_stride < page_bytes || layer_stride < 0 || (num_layers > 1 && layer_stride == 0))
         return SV_ERR_INVALID_ARG;
-    if (!aligned16(k) || !aligned16(v) || (page_bytes | page_stride | layer_stride) % 16) return SV_ERR_UNSUPPORTED;
+    if (!aligned16(k) || !aligned16(v) || (page_bytes | page_stride | layer_stride) % 16 || page_bytes > (1ll << 34))
+        return SV_ERR_UNSUPPORTED;
     if ((uintptr_t)workspace & 255) return SV_ERR_WORKSPACE;
     const CopyArgs A{static_cast<char *>(k), static_cast<char *>(v), copy_src, copy_dst, page_bytes, page_stride,
                      layer_stride, static_cast<int32_t *>(workspace), num_pages, num_layers, n};
     const long long items = (long long)n * num_layers * (v ? 2 : 1);
-    copy_kernel<<<(unsigned)(items < 1216 ? items : 1216), CT, 0, static_cast<cudaStream_t>(stream)>>>(A);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_dependent(copy_kernel, dim3((unsigned)(items < 1216 ? items : 1216)), dim3(CT), 1,
+                            static_cast<cudaStream_t>(stream), A) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

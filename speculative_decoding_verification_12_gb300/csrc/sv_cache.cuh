@@ -64,10 +64,9 @@ __device__ __forceinline__ Span span_of(const Batch &A, int max_tokens, int b) {
     return s;
 }
 
-// The request that owns row r (ragged layout): the largest b with row_off[b] <= r; -1 when the
-// row belongs to none.  One thread, binary search.
-__device__ __forceinline__ int request_of(const Batch &A, int r) {
-    if (!A.row_off) return r / (A.k_max + 1);
+// The request that owns row r of a ragged layout: the last b with row_off[b] <= r; -1 when the row
+// belongs to none.  One thread, binary search.
+static __device__ __noinline__ int request_of(const Batch &A, int r) {
     int lo = 0, hi = A.B;   // row_off[lo] <= r < row_off[hi], if the offsets are sound
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -75,6 +74,34 @@ __device__ __forceinline__ int request_of(const Batch &A, int r) {
         else hi = mid;
     }
     return (__ldg(A.row_off + lo) <= r && r < __ldg(A.row_off + lo + 1)) ? lo : -1;
+}
+
+// The request that owns row first + lane, for lanes below `rows` <= 32; -1 for a row that belongs to
+// none.  One warp: a 32-way search for the request of `first`, then the rows after it count the
+// offsets up to them among the next 32; where more than that many requests own no row, or `first` lies
+// before them all, each lane searches for itself.
+__device__ __forceinline__ int request_of_rows(const Batch &A, int first, int rows) {
+    const int lane = threadIdx.x & 31;
+    if (!A.row_off) return (first + lane) / (A.k_max + 1);
+    int lo = 0, hi = A.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = min(lo + lane * step, hi - 1);
+        const uint32_t m = __ballot_sync(0xffffffffu, __ldg(A.row_off + i) <= first);
+        lo = min(lo + (m ? 31 - __clz(m) : 0) * step, hi - 1);
+        hi = min(hi, lo + step);
+    }
+    const int next = lo + 1 + lane <= A.B ? __ldg(A.row_off + lo + 1 + lane) : 0x7fffffff;
+    bool search = __ldg(A.row_off + lo) > first;
+    int mine = -1;
+    for (int i = 0; i < rows; i++) {
+        const int later = __popc(__ballot_sync(0xffffffffu, next <= first + i));
+        if (lane == i) {
+            mine = lo + later < A.B ? lo + later : -1;
+            search |= later == 32;
+        }
+    }
+    if (search && lane < rows) mine = request_of(A, first + lane);
+    return mine;
 }
 
 // Reports the requests whose rows, length or drafts are out of range: a request with unsound
@@ -131,6 +158,25 @@ __device__ __forceinline__ uint4 pack8(const float x[8]) {
 }
 
 // --- host side ---
+
+// Launches a kernel as a programmatic dependent of the work before it on the stream: its CTAs may be
+// resident before that work ends, and wait for it (grid_wait) before their first access.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, int cluster, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 

@@ -9,13 +9,14 @@
 
 namespace svc {
 
-constexpr unsigned long long WAIT_NS = 2000000000ull;   // give up on an mbarrier after 2 s
+constexpr uint32_t WAIT_NS = 2000000000u;   // give up on an mbarrier after 2 s
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+// Low half of the nanosecond timer (differences up to 4.2 s).
+__device__ __forceinline__ uint32_t now_ns32() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
     return t;
 }
 
@@ -39,23 +40,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Waits for the phase of the given parity; false once the wait has run out, here or in another
-// warp of the CTA (*dead is then set).  The clock is read only now and then: reading the timer
-// takes longer than most of these waits.
-static __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *dead) {
-    unsigned long long t0 = 0;
+// warp of the CTA (*dead is then set).  Small, because it is inlined at every wait (a call would
+// cost the softmax warps their registers); the timer is read once in 256 polls, since ten warps
+// that read it at every poll slowed the others by 15 %.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
+    uint32_t t0 = 0;
     for (uint32_t n = 1; !mbar_try(bar, parity); n++) {
-        if (*dead) return false;
         if (n & 255) continue;
-        if (t0 == 0) t0 = now_ns();
-        else if (now_ns() - t0 > WAIT_NS) {
+        const uint32_t now = now_ns32() | 1;
+        if (!t0) t0 = now;
+        if (*dead || now - t0 > WAIT_NS) {
             *dead = 1;
             return false;
         }
     }
     return true;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, dead);
 }
 
 // The same for a whole warp, with one answer.

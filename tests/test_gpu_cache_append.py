@@ -122,6 +122,30 @@ def test_rows_of_both_layouts(sv, ragged):
     run_and_check(sv, s)
 
 
+def test_idle_requests_that_own_no_row(sv):
+    """Runs of more than 32 of them between, before and after the others."""
+    drafts = [-1] * 40 + [2, -1, 0] + [-1] * 100 + [3] + [-1] * 33 + [1] + [-1] * 50
+    lens = [9 + b % 40 for b in range(len(drafts))]
+    s = make(12, lens, drafts, 3, 4, 2, 64, 16, "bf16", 64)
+    rows = [k + 1 for k in drafts]
+    off = [sum(rows[:b]) for b in range(len(rows) + 1)]
+    s["R"] = off[-1] + 2              # and two rows after the last request
+    s["ro"] = torch.tensor(off, dtype=torch.int32)
+    for n in ("q", "k", "v", "qkv"):
+        s[n] = s[n][:s["R"]]
+    run_and_check(sv, s)
+
+
+def test_rows_before_the_first_request(sv):
+    s = make(13, [30, 40], [2, 1], 2, 4, 2, 64, 16, "bf16", 64)
+    s["ro"] = torch.tensor([3, 4, 6], dtype=torch.int32)
+    s["nd"] = torch.tensor([0, 1], dtype=torch.int32)
+    s["R"] = 6
+    for n in ("q", "k", "v", "qkv"):
+        s[n] = torch.cat([s[n], s[n]])[:6]
+    run_and_check(sv, s)
+
+
 def test_one_row(sv):
     run_and_check(sv, make(4, [777], [0], 0, 32, 8, 128, 16, "bf16", 128, ragged=False))
 

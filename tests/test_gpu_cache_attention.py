@@ -259,6 +259,17 @@ def test_offsets_out_of_order(sv):
     assert e == (1, 1)
 
 
+def test_idle_requests_that_own_no_row(sv):
+    drafts = [-1] * 40 + [2, -1, 0] + [-1] * 500 + [3] + [-1] * 33 + [1] + [-1] * 50
+    lens = [9 + b % 300 for b in range(len(drafts))]
+    s = make(36, lens, drafts, 3, 4, 2, 64, 16, "bf16")
+    rows = [k + 1 for k in drafts]
+    off = [sum(rows[:b]) for b in range(len(rows) + 1)]
+    s["ro"] = torch.tensor(off, dtype=torch.int32)
+    s["q"] = s["q"][:off[-1] + 2]      # and two rows after the last request
+    run_and_check(sv, s)
+
+
 def test_page_table_of_pages_never_seen(sv):
     """Entries past the length, and out of the window, are not looked at."""
     s = make(30, [300, 40], [4, 4], 4, 4, 2, 64, 16, "bf16", window=40, sinks=2)
