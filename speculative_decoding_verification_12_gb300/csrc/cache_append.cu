@@ -44,11 +44,13 @@ constexpr int AT = 256;   // threads per CTA
 constexpr int AU = 4;     // heads per thread and pass, all loaded before the first is used
 constexpr int ROWS = 32;  // rows per CTA at most
 
-// How the two elements of a pair come together.
-enum { PAIR_NEXT, PAIR_LANES, PAIR_ANY };   // neighbours; whole lanes apart (shuffle); any distance
+// How the two elements of a pair come together: as neighbours; in one thread, which holds 4 elements
+// of each half (rotary_dim a multiple of 8); or through shared memory, at any distance.
+enum { PAIR_NEXT, PAIR_HALVES, PAIR_ANY };
 
 // Each CTA takes a few rows in a row.  LPH lanes hold one head, 8 elements each (a power of two >=
-// head_dim / 8), so a thread's elements are the same in every head it meets.
+// head_dim / 8), so a thread's elements are the same in every head it meets, and its weights and
+// rotations stay in registers.
 //
 // What bounds it: 24 KB of a row in and out at the memory's rate is 4 ns, but each row waits for the
 // chain offsets -> length -> page.  So a CTA walks that chain once, a lane of one warp per row, while
@@ -65,7 +67,25 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     const int D = C.D, Hq = P.Hq, Hk = C.heads, heads = Hq + 2 * Hk, max_tokens = C.max_pages << C.page_shift;
     constexpr int HPC = AT / LPH;     // heads per CTA and step
     const int sub = tid % LPH, h_first = tid / LPH;
+    const int rot = 2 * P.half;
+    // this thread's elements: [d0, d0 + 4) and [d1, d1 + 4)
+    const bool turns = PAIR == PAIR_HALVES ? sub * 4 < P.half : sub * 8 < rot;
+    const int d0 = PAIR != PAIR_HALVES ? sub * 8 : turns ? sub * 4 : rot + (sub - P.half / 4) * 8;
+    const int d1 = PAIR == PAIR_HALVES && turns ? P.half + sub * 4 : d0 + 4;
     const bool in = sub * 8 < D;
+    auto take = [&](const E *at) {
+        if (PAIR != PAIR_HALVES) return *reinterpret_cast<const uint4 *>(at + d0);
+        const uint2 a = *reinterpret_cast<const uint2 *>(at + d0), b = *reinterpret_cast<const uint2 *>(at + d1);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    };
+    auto put = [&](E *at, uint4 w) {
+        if (PAIR != PAIR_HALVES) {
+            *reinterpret_cast<uint4 *>(at + d0) = w;
+        } else {
+            *reinterpret_cast<uint2 *>(at + d0) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2 *>(at + d1) = make_uint2(w.z, w.w);
+        }
+    };
 
     grid_wait();
     grid_launch_dependents();
@@ -78,7 +98,7 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
             if (h >= Hq) src = static_cast<const E *>(P.k) + r * P.k_stride + (int64_t)(h - Hq) * D;
             if (h >= Hq + Hk) src = static_cast<const E *>(P.v) + r * P.v_stride + (int64_t)(h - Hq - Hk) * D;
             raw[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (in && h < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + sub * 8);
+            if (in && h < heads) raw[u] = take(src);
         }
     };
     if (tid >= AT - 32) {
@@ -108,13 +128,10 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     }
     load(first, 0);
     uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
-    if (in && P.qw) qw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.qw) + sub * 8);
-    if (in && P.kw) kw = *reinterpret_cast<const uint4 *>(static_cast<const E *>(P.kw) + sub * 8);
+    if (in && P.qw) qw = take(static_cast<const E *>(P.qw));
+    if (in && P.kw) kw = take(static_cast<const E *>(P.kw));
     const float f = tid < P.half ? __ldg(P.inv_freq + tid) : 0.f;
     const uint64_t t = turns_of(f);
-    const int rot = 2 * P.half;
-    const bool low = sub * 8 < P.half;
-    const int partner = PAIR == PAIR_LANES && sub * 8 < rot ? lane + (low ? P.half / 8 : -(P.half / 8)) : lane;
     __syncthreads();
 
 #pragma unroll 1
@@ -134,19 +151,15 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
             if (i + 1 < rows) load(r + 1, 0);
             continue;
         }
-        // this thread's rotations: element e turns by (c, s) to x c + partner s (s signed)
-        float c[8], s[8];
+        // this thread's rotations: of its four pairs, or (any distance) of its eight elements
+        constexpr int NR = PAIR == PAIR_ANY ? 8 : 4;
+        float2 cs[NR];
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int d = sub * 8 + e;
-            c[e] = 1.f;
-            s[e] = 0.f;
-            if (d < rot) {
-                const bool head = PAIR == PAIR_NEXT ? e % 2 == 0 : d < P.half;
-                const float2 cs = turn[i & 1][PAIR == PAIR_NEXT ? d / 2 : (head ? d : d - P.half)];
-                c[e] = cs.x;
-                s[e] = head ? -cs.y : cs.y;
-            }
+        for (int e = 0; e < NR; e++) {
+            const int j = PAIR == PAIR_HALVES ? sub * 4 + e : PAIR == PAIR_NEXT ? sub * 4 + e
+                          : d0 + e < P.half ? d0 + e : d0 + e - P.half;
+            const bool on = PAIR == PAIR_ANY ? d0 + e < rot : j < P.half;
+            cs[e] = on ? turn[i & 1][j] : make_float2(1.f, 0.f);
         }
         const int64_t at = slot[i];
 #pragma unroll 1
@@ -174,29 +187,28 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
 #pragma unroll
                     for (int e = 0; e < 8; e++) x[e] *= inv * g[e];
                 }
-                __syncwarp();
-                float y[8];
-                if (PAIR == PAIR_NEXT) {
-#pragma unroll
-                    for (int e = 0; e < 8; e++) y[e] = x[e ^ 1];
-                } else if (PAIR == PAIR_LANES) {
-#pragma unroll
-                    for (int e = 0; e < 8; e++) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
-                } else {
+                if (PAIR == PAIR_ANY) {
                     float *mine = ex + (tid - sub) * 8;
+                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 8; e++) mine[sub * 8 + e] = x[e];
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const int d = sub * 8 + e;
-                        y[e] = d < rot ? mine[d < P.half ? d + P.half : d - P.half] : 0.f;
+                        const int d = d0 + e;
+                        if (d < P.half) x[e] = x[e] * cs[e % NR].x - mine[d + P.half] * cs[e % NR].y;
+                        else if (d < rot) x[e] = x[e] * cs[e % NR].x + mine[d - P.half] * cs[e % NR].y;
                     }
-                    __syncwarp();
-                }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; e++) x[e] = sub * 8 + e < rot ? fmaf(y[e], s[e], x[e] * c[e]) : x[e];
-                if (in && h < heads) *reinterpret_cast<uint4 *>(dst + sub * 8) = is_v ? raw[u] : pack8<E>(x);
+                    for (int e = 0; e < 4; e++) {
+                        float &a = x[PAIR == PAIR_NEXT ? 2 * e : e], &z = x[PAIR == PAIR_NEXT ? 2 * e + 1 : e + 4];
+                        const float a0 = a, z0 = z;
+                        a = a0 * cs[e % NR].x - z0 * cs[e % NR].y;
+                        z = a0 * cs[e % NR].y + z0 * cs[e % NR].x;
+                    }
+                }
+                if (in && h < heads) put(dst, is_v ? raw[u] : pack8<E>(x));
             }
         }
         if (i + 1 < rows) load(r + 1, 0);
@@ -214,7 +226,7 @@ static cudaError_t launch_heads(const Batch &A, const Cache &C, const AppendArgs
     if (per > ROWS) per = ROWS;
     const int grid = (A.R + per - 1) / per;
     if (P.interleaved || P.half == 0) return launch_dependent(append_kernel<E, LPH, PAIR_NEXT>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
-    if (P.half % 8 == 0) return launch_dependent(append_kernel<E, LPH, PAIR_LANES>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
+    if (P.half % 4 == 0) return launch_dependent(append_kernel<E, LPH, PAIR_HALVES>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
     return launch_dependent(append_kernel<E, LPH, PAIR_ANY>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
 }
 template <typename E>

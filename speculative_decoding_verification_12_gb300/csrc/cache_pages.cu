@@ -20,7 +20,7 @@ namespace svc {
 
 constexpr int PT = 1024;              // threads per bookkeeping CTA
 constexpr int PW = PT / 32;
-constexpr int PAGES_PER_CTA = 8192;   // cluster CTAs: one per so many pages, at most 8
+constexpr int PAGES_PER_CTA = 4096;   // cluster CTAs: one per so many pages, at most 8
 
 struct PageState {
     int32_t *len, *table, *ref;
@@ -105,24 +105,49 @@ __device__ __forceinline__ int used4(const int32_t *ref, int i, int hi, int &hav
     return m;
 }
 
+// Which pages of a warp's slice are in use: 4 bits a lane for each 128 pages.  The first 1024 pages of
+// a slice stay in a register (a pool of 262 144 pages in a cluster of 8), the rest are read again.
+struct Used {
+    const int32_t *ref;
+    Slice s;
+    uint32_t head;
+    __device__ __forceinline__ void read() {
+        head = 0;
+        for (int k = 0; k < 8 && s.lo + 128 * k < s.hi; k++) {
+            int have;
+            head |= (uint32_t)used4(ref, s.lo + 128 * k + 4 * (int)(threadIdx.x & 31), s.hi, have) << (4 * k);
+        }
+    }
+    __device__ __forceinline__ int groups() const { return (s.hi - s.lo + 127) / 128; }
+    __device__ __forceinline__ int page(int k) const { return s.lo + 128 * k + 4 * (int)(threadIdx.x & 31); }
+    // the lane's four pages of group k: in use, and existing
+    __device__ __forceinline__ int get(int k, int &have) const {
+        const int left = s.hi - page(k);
+        have = left >= 4 ? 15 : left > 0 ? (1 << left) - 1 : 0;
+        if (k < 8) return head >> (4 * k) & 15;
+        return used4(ref, page(k), s.hi, have);
+    }
+};
+
 // Exclusive prefix of this warp's count over all warps of the cluster, and the total.
 // counts: this CTA's PW + 1 shared words.  Contains cluster barriers.
-__device__ __forceinline__ int cluster_prefix(int count, int *counts, int *total) {
+template <typename T>
+__device__ __forceinline__ T cluster_prefix(T count, T *counts, T *total) {
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) counts[warp] = count;
     __syncthreads();
     if (warp == 0) {
-        const int c = counts[lane];
-        const int s = warp_scan(c);
+        const T c = counts[lane];
+        const T s = warp_scan(c);
         __syncwarp();
         counts[lane] = s - c;
         if (lane == 31) counts[PW] = s;
     }
     cl.sync();
-    int before = 0, all = 0;
+    T before = 0, all = 0;
     for (unsigned r = 0; r < cl.num_blocks(); r++) {
-        const int c = cl.map_shared_rank(counts, r)[PW];
+        const T c = cl.map_shared_rank(counts, r)[PW];
         all += c;
         if (r < cl.block_rank()) before += c;
     }
@@ -132,35 +157,30 @@ __device__ __forceinline__ int cluster_prefix(int count, int *counts, int *total
 
 // Writes the lowest `want` free pages to S.list in ascending order and returns how many free
 // pages there are; the list is visible to the whole cluster on return.
-__device__ __forceinline__ int list_free(const PageState &S, long long want, int *counts) {
-    cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31;
-    const Slice sl = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
-    int count = 0;
-    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
-        int have;
-        const int m = used4(S.ref, i, sl.hi, have);
+__device__ __forceinline__ int list_free(const PageState &S, const Used &U, long long want, int *counts) {
+    const int groups = U.groups();
+    int count = 0, have;
+    for (int k = 0; k < groups; k++) {
+        const int m = U.get(k, have);
         count += __popc(have & ~m);
     }
-    count = warp_sum(count);
     int total;
-    int at = cluster_prefix(count, counts, &total);
-    for (int base = sl.lo; base < sl.hi && at < want; base += 128) {
-        const int i = base + 4 * lane;
-        int have;
-        const int m = used4(S.ref, i, sl.hi, have);
+    int at = cluster_prefix(warp_sum(count), counts, &total);
+    for (int k = 0; k < groups && at < want; k++) {
+        const int m = U.get(k, have);
         const int f = have & ~m, c = __popc(f);
         const int inc = warp_scan(c);
         int r = at + inc - c;
+#pragma unroll
         for (int t = 0; t < 4; t++)
             if (f >> t & 1) {
-                if (r < want) S.list[r] = i + t;
+                if (r < want) S.list[r] = U.page(k) + t;
                 r++;
             }
         at += __shfl_sync(0xffffffffu, inc, 31);
     }
     __threadfence();
-    cl.sync();
+    cg::this_cluster().sync();
     return total;
 }
 
@@ -200,21 +220,34 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
     grid_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    long long sum = 0, want = 0;
-    for (int b = threadIdx.x; b < S.B; b += PT) sum += want_of(S, nd, b).need;
-    cta_scan(sum, tmp, &want);
+    Used U;
+    U.ref = S.ref;
+    U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
+    U.read();
+    // the first PT requests are looked at once
+    Want w0 = {0, 0, 0, 0};
+    if ((int)threadIdx.x < S.B) w0 = want_of(S, nd, threadIdx.x);
+    long long sum = w0.need, want = 0;
+    for (int b = threadIdx.x + PT; b < S.B; b += PT) sum += want_of(S, nd, b).need;
+    const long long at0 = cta_scan(sum, tmp, &want);   // (of PT requests at most: their places too)
     // (never past the list, whatever the counts say on the second look)
-    const long long free = min((long long)list_free(S, want, counts), want);
+    const long long free = min((long long)list_free(S, U, want, counts), want);
     if (cg::this_cluster().block_rank() != 0) return;
     long long before = 0;
     for (int b0 = 0; b0 < S.B; b0 += PT) {
         const int b = b0 + (int)threadIdx.x;
         const bool in = b < S.B;
-        Want w = {0, 0, 0, 0};
-        if (in) w = want_of(S, nd, b);
-        long long all;
-        const long long at = before + cta_scan(w.need, tmp, &all);
-        before += all;
+        Want w = w0;
+        long long at = at0;
+        if (b0) {
+            w = {0, 0, 0, 0};
+            if (in) w = want_of(S, nd, b);
+        }
+        if (S.B > PT) {
+            long long all;
+            at = before + cta_scan(w.need, tmp, &all);
+            before += all;
+        }
         if (w.need > 0 && at + w.need > free) {
             w.err = SV_DEV_NO_PAGES;
             w.need = 0;
@@ -280,18 +313,22 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
     __shared__ long long tmp[PW + 1];
     grid_wait();
     grid_launch_dependents();
-    const int free = list_free(S, K.F, counts);
+    Used U;
+    U.ref = S.ref;
+    U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
+    U.read();
+    if (cg::this_cluster().block_rank() == 0)
+        for (int f = threadIdx.x; f < K.F; f += PT) {
+            int n, tail;
+            const int err = fork_check(S, K, f, n, tail);
+            const int c = K.children[f];
+            const bool claims = c >= 0 && c < S.B && S.len[c] == 0;
+            S.result[f] = err ? -err : n;
+            K.src[f] = tail;
+            K.dst[f] = claims ? 1 : 0;
+        }
+    const int free = list_free(S, U, K.F, counts);   // (and a barrier: every length is read before one changes)
     if (cg::this_cluster().block_rank() != 0) return;
-    for (int f = threadIdx.x; f < K.F; f += PT) {
-        int n, tail;
-        const int err = fork_check(S, K, f, n, tail);
-        const int c = K.children[f];
-        const bool claims = c >= 0 && c < S.B && S.len[c] == 0;
-        S.result[f] = err ? -err : n;
-        K.src[f] = tail;
-        K.dst[f] = claims ? 1 : 0;
-    }
-    __syncthreads();
     for (int f = threadIdx.x; f < K.F; f += PT)
         if (K.dst[f]) atomicMin(S.len + K.children[f], INT_MIN + f);
     __syncthreads();
@@ -339,25 +376,28 @@ __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkAr
     const int32_t *from = S.table + (int64_t)K.parents[f] * S.max_pages;
     int32_t *to = S.table + (int64_t)K.children[f] * S.max_pages;
     const int full = n / S.page_size, fresh = K.dst[f];
+    int p[SPT], count[SPT];
+    const int j0 = blockIdx.y * SPT * ST + threadIdx.x;
 #pragma unroll
     for (int t = 0; t < SPT; t++) {
-        const int j = (blockIdx.y * SPT + t) * ST + threadIdx.x;
+        const int j = j0 + t * ST;
+        p[t] = j < full ? from[j] : -1;
+    }
+#pragma unroll
+    for (int t = 0; t < SPT; t++) {
+        const bool is = p[t] >= 0 && p[t] < S.num_pages;
+        count[t] = is ? atomicAdd(S.ref + p[t], 1) : p[t] == -1 ? 1 : 0;
+    }
+#pragma unroll
+    for (int t = 0; t < SPT; t++) {
+        const int j = j0 + t * ST;
         if (j >= S.max_pages) break;
-        int p = -1;
-        if (j < full) {
-            p = from[j];
-            if (p >= S.num_pages || p < -1) {
-                record_error(S.hdr, SV_DEV_BAD_PAGE, f);
-                p = -1;
-            } else if (p >= 0 && atomicAdd(S.ref + p, 1) < 1) {
-                atomicSub(S.ref + p, 1);
-                record_error(S.hdr, SV_DEV_BAD_PAGE, f);
-                p = -1;
-            }
-        } else if (j == full) {
-            p = fresh;
+        if (count[t] < 1) {   // not a page, or one that no request holds
+            if (p[t] >= 0 && p[t] < S.num_pages) atomicSub(S.ref + p[t], 1);
+            record_error(S.hdr, SV_DEV_BAD_PAGE, f);
+            p[t] = -1;
         }
-        to[j] = p;
+        to[j] = j == full ? fresh : p[t];
     }
 }
 
@@ -367,18 +407,31 @@ __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkAr
 
 constexpr int RELEASE_CHUNK = ST * SPT;
 
-// Gives one entry back; returns whether it held anything.
-__device__ __forceinline__ bool give_back(const PageState &S, int32_t *e, int b) {
-    const int p = *e;
-    if (p == -1) return false;
-    *e = -1;
-    if (p < 0 || p >= S.num_pages) {
-        record_error(S.hdr, SV_DEV_BAD_PAGE, b);
-    } else if (atomicSub(S.ref + p, 1) < 1) {
-        atomicAdd(S.ref + p, 1);
-        record_error(S.hdr, SV_DEV_BAD_PAGE, b);
+// Gives back the SPT entries that `entry(t)` points at (NULL: none); returns whether they held anything.
+template <typename F>
+__device__ __forceinline__ bool give_back(const PageState &S, int b, F entry) {
+    int p[SPT], count[SPT];
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < SPT; t++) {
+        const int32_t *e = entry(t);
+        p[t] = e ? *e : -1;
     }
-    return true;
+#pragma unroll
+    for (int t = 0; t < SPT; t++) {
+        count[t] = 1;
+        if (p[t] == -1) continue;
+        any = true;
+        *entry(t) = -1;
+        count[t] = p[t] >= 0 && p[t] < S.num_pages ? atomicSub(S.ref + p[t], 1) : 0;
+    }
+#pragma unroll
+    for (int t = 0; t < SPT; t++)
+        if (count[t] < 1) {   // not a page, or one that no request holds
+            if (p[t] >= 0 && p[t] < S.num_pages) atomicAdd(S.ref + p[t], 1);
+            record_error(S.hdr, SV_DEV_BAD_PAGE, b);
+        }
+    return any;
 }
 
 // One CTA per request and direction (y = 0: past the length, upward; 1: before the window,
@@ -395,30 +448,19 @@ __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int wind
         if (threadIdx.x == 0) record_error(S.hdr, SV_DEV_BAD_LAYOUT, b);
         return;
     }
-    if (blockIdx.y == 0) {
-        for (int base = keep; base < S.max_pages; base += RELEASE_CHUNK) {
-            bool any = false;
-#pragma unroll
-            for (int t = 0; t < SPT; t++) {
-                const int j = base + t * ST + threadIdx.x;
-                if (j < S.max_pages) any |= give_back(S, row + j, b);
-            }
-            if (!__syncthreads_or(any)) break;
-        }
-    } else {
-        // pages [first, last): all tokens >= sinks, all tokens <= len - window
-        const int first = sinks / S.page_size + (sinks % S.page_size != 0);
+    // pages [first, last): past the length, or with all tokens >= sinks and <= len - window
+    int first = keep, last = S.max_pages;
+    if (blockIdx.y) {
         const long long gone = (long long)len - window + 1;
-        const int last = gone > 0 ? (int)(gone / S.page_size) : 0;
-        for (int top = last; top > first; top -= RELEASE_CHUNK) {
-            bool any = false;
-#pragma unroll
-            for (int t = 0; t < SPT; t++) {
-                const int j = top - 1 - t * ST - (int)threadIdx.x;
-                if (j >= first) any |= give_back(S, row + j, b);
-            }
-            if (!__syncthreads_or(any)) break;
-        }
+        first = sinks / S.page_size + (sinks % S.page_size != 0);
+        last = gone > 0 ? (int)(gone / S.page_size) : 0;
+    }
+    for (int done = 0; done < last - first; done += RELEASE_CHUNK) {
+        const bool any = give_back(S, b, [&](int t) {
+            const int i = done + t * ST + (int)threadIdx.x;
+            return i < last - first ? row + (blockIdx.y ? last - 1 - i : first + i) : nullptr;
+        });
+        if (!__syncthreads_or(any)) break;
     }
 }
 
@@ -429,37 +471,36 @@ __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int wind
 // The r-th used page at or above U (pages in use) pairs with the r-th free page below U; there
 // are equally many.  S.list becomes the map from page to page for ids >= U.
 __global__ void __launch_bounds__(PT) compact_kernel(const PageState S, int32_t *src, int32_t *dst, int cap) {
-    __shared__ int counts[3][PW + 1];
+    __shared__ int counts[PW + 1];
+    __shared__ long long counts2[PW + 1];
     grid_wait();
     grid_launch_dependents();
     cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31;
-    const Slice sl = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
-    int count = 0;
-    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
-        int have;
-        count += __popc(used4(S.ref, i, sl.hi, have));
-    }
-    int U, moves, holes;
-    cluster_prefix(warp_sum(count), counts[0], &U);
+    Used P;
+    P.ref = S.ref;
+    P.s = slice_of(S.num_pages, cl.block_rank(), cl.num_blocks());
+    P.read();
+    const int groups = P.groups();
+    int count = 0, have, U;
+    for (int k = 0; k < groups; k++) count += __popc(P.get(k, have));
+    cluster_prefix(warp_sum(count), counts, &U);
+    auto below = [&](int i) { return U <= i ? 0 : (U >= i + 4 ? 15 : (1 << (U - i)) - 1); };   // ids < U of i .. i + 3
     int up = 0, down = 0;
-    for (int i = sl.lo + 4 * lane; i < sl.hi; i += 128) {
-        int have;
-        const int m = used4(S.ref, i, sl.hi, have);
-        const int below = U <= i ? 0 : (U >= i + 4 ? 15 : (1 << (U - i)) - 1);   // ids < U
-        up += __popc(m & ~below);
-        down += __popc(have & ~m & below);
+    for (int k = 0; k < groups; k++) {
+        const int m = P.get(k, have), lo = below(P.page(k));
+        up += __popc(m & ~lo);
+        down += __popc(have & ~m & lo);
     }
-    int at_up = cluster_prefix(warp_sum(up), counts[1], &moves);
-    int at_down = cluster_prefix(warp_sum(down), counts[2], &holes);
-    for (int base = sl.lo; base < sl.hi; base += 128) {
-        const int i = base + 4 * lane;
-        int have;
-        const int m = used4(S.ref, i, sl.hi, have);
-        const int below = U <= i ? 0 : (U >= i + 4 ? 15 : (1 << (U - i)) - 1);
-        const int fu = m & ~below, fd = have & ~m & below, free_above = have & ~m & ~below;
+    long long both;   // movers in the low half, holes in the high half
+    const long long at = cluster_prefix((long long)warp_sum(up) | (long long)warp_sum(down) << 32, counts2, &both);
+    int at_up = (int)at, at_down = (int)(at >> 32);
+    const int moves = (int)both;
+    for (int k = 0; k < groups; k++) {
+        const int i = P.page(k), m = P.get(k, have), lo = below(i);
+        const int fu = m & ~lo, fd = have & ~m & lo, free_above = have & ~m & ~lo;
         const int iu = warp_scan(__popc(fu)), id = warp_scan(__popc(fd));
         int ru = at_up + iu - __popc(fu), rd = at_down + id - __popc(fd);
+#pragma unroll
         for (int t = 0; t < 4; t++) {
             if (fu >> t & 1) {
                 if (ru < cap) src[ru] = i + t;
