@@ -37,9 +37,8 @@ constexpr int NTHREADS = 384;            // 2 x 4 softmax warps, then one warp f
 constexpr int W_K = 8, W_MMA = 9, W_V = 10;   // keys, matrix instructions, values, and the front warp
 constexpr int MAX_CTAS = 160;
 constexpr int PART_ROWS = 256;           // rows of a part
-constexpr int P_COL = TILE / 2;          // weights lie over the upper half of their scores
 constexpr int MAX_STAGES = 7;            // of each of the two rings
-constexpr int OVERHEAD = 1;              // cost of a row tile beside its key tiles, in key tiles
+constexpr int MAX_QBUFS = 4;
 
 struct AttnArgs {
     const void *q;
@@ -51,12 +50,12 @@ struct AttnArgs {
     float *part_lse;   // workspace, [2 * MAX_CTAS][PART_ROWS]: log2 of the part's sum
     float *part_o;     // workspace, [2 * MAX_CTAS][PART_ROWS][DP]
     float c;           // |scale| log2(e)
-    uint32_t qflip;    // sign flip of two queries (scale < 0)
-    int qzero;         // scale == 0
+    int negative, zero;   // scale < 0, scale == 0
     int Hq, G, window, sinks;
     int k_stages, v_stages;
+    int overhead;      // cost of a row tile beside its key tiles, in key tiles
     int q_tiles;       // row tiles of 128 that a request may have at a time: 1 or 2
-    int q_rows;        // rows of a query buffer (a multiple of 8); two buffers if q_tiles == 1
+    int q_rows, q_bufs;   // rows of a query buffer (a multiple of 8), and how many there are
 };
 
 struct AttnWs {
@@ -98,8 +97,8 @@ __device__ __forceinline__ Req req_of(const Batch &A, const Cache &C, const Attn
     return r;
 }
 // A request's cost, in units of a key tile.
-__device__ __forceinline__ long long units_of(const Req &r, int heads) {
-    return r.nt ? (long long)(r.nt + OVERHEAD) * r.mt * heads : 0;
+__device__ __forceinline__ long long units_of(const Req &r, int heads, int overhead) {
+    return r.nt ? (long long)(r.nt + overhead) * r.mt * heads : 0;
 }
 
 // A segment, as the front warp hands it out (64 bytes): key tiles [t0, t1) of the nt of row tile m of
@@ -224,13 +223,17 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     // the running maximum may lag by this many powers of two before O is scaled down
     constexpr float LAG = Num<E>::BF16 ? 8.f : 6.f;
     constexpr int NW = NTHREADS / 32;
+    // With narrow heads O leaves room for P beside it, so that a group's next S can be made as soon as
+    // its scores are in registers; with wide ones P lies over S, and S waits for P V.
+    constexpr bool APART = DP == 64;
+    constexpr int P_COL = APART ? 2 * TILE + 64 : TILE / 2;   // P of group g at column g * 128 + P_COL
     extern __shared__ __align__(1024) char smem[];
-    // [barriers and small state][two query buffers][ring of K tiles][ring of V tiles]; the matrix
+    // [barriers and small state][query buffers][ring of K tiles][ring of V tiles]; the matrix
     // instruction reads 128 rows from a query buffer whatever it holds: the rows past it are other
     // bytes of this memory, and reach only rows of S, P and O that nothing uses
     const int q_block = P.q_rows * 128, q_buffer = NB * q_block;
     char *const q_p = smem + SMALL;
-    char *const k_p = q_p + 2 * q_buffer, *const v_p = k_p + P.k_stages * STAGE;
+    char *const k_p = q_p + P.q_bufs * P.q_tiles * q_buffer, *const v_p = k_p + P.k_stages * STAGE;
     int *const ctl = reinterpret_cast<int *>(smem + 384);                    // dead, tmem, -, -, patched[2][4], bad[16]
     float2 *const ex = reinterpret_cast<float2 *>(smem + 512);               // [2][128] (m, l)
     long long *const scan = reinterpret_cast<long long *>(ex);               // the set-up's scratch, before ex is used
@@ -238,17 +241,17 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const uint32_t seg_full = smem_addr(smem + 4608), seg_empty = seg_full + 8 * SEGS;
     const uint32_t k_full = smem_addr(smem), k_empty = k_full + 8 * MAX_STAGES, v_full = k_empty + 8 * MAX_STAGES,
                    v_empty = v_full + 8 * MAX_STAGES, s_full = v_empty + 8 * MAX_STAGES, p_full = s_full + 16,
-                   o_done = p_full + 16, q_full = o_done + 16, q_empty = q_full + 16, both = q_empty + 16,
-                   drained = both + 16;
+                   o_done = p_full + 16, both = o_done + 16, s_free = both + 16, drained = s_free + 16, q_full = drained + 8, q_empty = q_full + 8 * MAX_QBUFS;
     volatile int *const dead = ctl, *const patched = ctl + 4, *const bad = ctl + 12;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_tiles == 1 ? 2 : 1;
+    const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_bufs;
 
     // one thread per barrier: the rings and pairs in a row from k_full, then the segments'
-    constexpr int NBARS = 4 * MAX_STAGES + 13;
+    constexpr int NBARS = 4 * MAX_STAGES + 11 + 2 * MAX_QBUFS;
     if (tid < NBARS) {
-        const int p = tid - 4 * MAX_STAGES;   // s_full, p_full, o_done, q_full, q_empty, both: two each; drained
-        mbar_init(k_full + 8 * tid, p < 0 ? 1 : p / 2 == 1 ? 4 : p / 2 == 5 ? 8 : 1);
+        // pairs: s_full, p_full (4 warps), o_done, both (8 warps), s_free (4 warps); then the rest
+        const int p = (tid - 4 * MAX_STAGES) >> 1;
+        mbar_init(k_full + 8 * tid, p == 1 || p == 4 ? 4 : p == 3 ? 8 : 1);
     } else if (tid >= 128 && tid < 128 + 2 * SEGS) {
         mbar_init(seg_full + 8 * (tid - 128), tid < 128 + SEGS ? 1 : SEG_READERS);
     } else if (tid >= 256 && tid < 256 + 28 && tid != 257) {   // (1 is the tensor memory's address)
@@ -271,7 +274,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 #pragma unroll 1
         for (int b0 = 0; b0 < A.B; b0 += NTHREADS) {
             const int b = b0 + tid;
-            const long long w = b < A.B ? units_of(req_of(A, C, P, b), C.heads) : 0;
+            const long long w = b < A.B ? units_of(req_of(A, C, P, b), C.heads, P.overhead) : 0;
             long long inc = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -396,8 +399,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         // that S are issued together, the commits after both, and whether K is there is asked before.
         // A commit costs the issuing lane some 140 cycles: there are two a product, S is there (the
         // softmax group then frees the K tile) and the V tile is free.  A group learns of its last
-        // product of a segment by o_done; earlier ones are complete when a later S is.
-        constexpr uint32_t idesc_s = mma_idesc(Num<E>::BF16, TILE, TILE, false);
+        // product of a segment by o_done; earlier ones are complete when a later S is.  (With P apart
+        // o_done follows every product, and the group frees the V tile.)
+        const uint32_t idesc_s = mma_idesc(Num<E>::BF16, TILE, TILE, false) | (uint32_t)P.negative << 13;
         const int steps = (C.D + 15) / 16;                              // of 16 columns: nothing past head_dim
         const uint32_t idesc_o = mma_idesc(Num<E>::BF16, TILE, 0, true) | (uint32_t)(steps * 2) << 17;
         const bool leader = elect();
@@ -416,30 +420,34 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         open(sseg, sv, snv, stwo, false);
         if (ok) open(oseg, ov, onv, otwo, true);
         Place ks{0, 0}, vs{0, 0}, qs{0, 0};
-        uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each group's next P
-        int lead = 0;                      // products whose S, but not P V, is issued: at most 2
+        uint32_t gs = 0, go = 0, np = 0, nf = 3;   // groups whose turn it is; parities of each one's next P and free S
+        int lead = 0;                      // products whose S, but not P V, is issued: at most 2, or 4 with P apart
         uint32_t polls = 0, idle_since = 0;
-        // the next S has its operands
-        auto s_ready = [&]() {
-            return snv && (sv || warp_try(q_full + 8 * qs.stage, qs.parity)) && warp_try(k_full + 8 * ks.stage, ks.parity);
-        };
 #pragma unroll 1
         while (ok && onv) {
-            bool do_s = s_ready(), do_o = false;
-            if (lead == 2 || !do_s) {
-                do_o = lead > 0 && warp_try(p_full + 8 * go, np >> go & 1) && warp_try(v_full + 8 * vs.stage, vs.parity);
-                if (!do_o) {
-                    if (++polls & 255) continue;
-                    const uint32_t now = now_ns32() | 1;
-                    if (!idle_since) idle_since = now;
-                    const bool late = *dead || now - idle_since > WAIT_NS;
-                    if (__any_sync(0xffffffffu, late)) {
-                        *dead = 1;
-                        ok = false;
-                    }
-                    continue;
+            // all that may be waited for is asked at once; every lane has to have seen it
+            uint32_t there = 0;
+            if (snv) {   // the next S: its place (with P apart), its queries and its keys
+                there |= !APART || mbar_test(s_free + 8 * gs, nf >> gs & 1);
+                there |= (uint32_t)(sv || mbar_test(q_full + 8 * qs.stage, qs.parity)) << 1;
+                there |= (uint32_t)mbar_test(k_full + 8 * ks.stage, ks.parity) << 2;
+            }
+            if (lead) {
+                there |= (uint32_t)mbar_test(p_full + 8 * go, np >> go & 1) << 3;
+                there |= (uint32_t)mbar_test(v_full + 8 * vs.stage, vs.parity) << 4;
+            }
+            there = __reduce_and_sync(0xffffffffu, there);
+            const bool do_o = there >> 3 == 3, do_s = (there & 7) == 7 && (APART || lead < 2 || do_o);
+            if (!do_o && !do_s) {
+                if (++polls & 255) continue;
+                const uint32_t now = now_ns32() | 1;
+                if (!idle_since) idle_since = now;
+                const bool late = *dead || now - idle_since > WAIT_NS;
+                if (__any_sync(0xffffffffu, late)) {
+                    *dead = 1;
+                    ok = false;
                 }
-                if (!do_s) do_s = s_ready();
+                continue;
             }
             idle_since = 0;
             tc_fence_after();
@@ -470,8 +478,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     if (sv == snv - 1) mma_commit(q_empty + 8 * qs.stage);
                 }
                 if (do_o) {
-                    if (last_use) mma_commit(v_empty + 8 * vs.stage);
-                    if (ov >= onv - 2) mma_commit(o_done + 8 * go);
+                    if (!APART && last_use) mma_commit(v_empty + 8 * vs.stage);
+                    if (APART || ov >= onv - 2) mma_commit(o_done + 8 * go);
                 }
             }
             __syncwarp();
@@ -484,6 +492,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             }
             if (do_s && ok) {
                 if (!stwo || (sv & 1)) ks.advance(k_stages);
+                nf ^= 1u << gs;
                 gs ^= 1;
                 lead++;
                 if (++sv == snv) {
@@ -501,11 +510,11 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     } else {
         // Front: the segments of this CTA's range, in order, and their queries, swizzled as the matrix
         // instruction reads them.  Requests are looked at 32 at a time, row tiles of one 16 at a time.
-        uint32_t pushed = 0, loaded = 0;
+        uint32_t pushed = 0, issued = 0, done = 0;   // segments handed out, their queries' copies begun, and there
         long long pos = lo, pre = lo < hi ? start_pre : 0;
         int b = lo < hi ? (int)start_b : 0, b_base = -32;
         Req r = {};
-        Place at{0, 1};
+        Place at{0, 1}, out{0, 0};   // query buffers to fill, and filling
         if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
         __syncwarp();
         auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
@@ -520,7 +529,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 #pragma unroll 1
         for (bool more = lo < hi, ended = false; ok;) {
 #pragma unroll 1
-            while (ok && more && pushed - loaded < 12) {
+            while (ok && more && pushed - done < 12) {
                 if (b - b_base >= 32) {
                     b_base = b;
                     r.nt = 0;
@@ -532,7 +541,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 s.len = __shfl_sync(0xffffffffu, r.len, i), s.M = __shfl_sync(0xffffffffu, r.M, i);
                 s.lo = __shfl_sync(0xffffffffu, r.lo, i), s.w0 = __shfl_sync(0xffffffffu, r.w0, i);
                 s.ns = __shfl_sync(0xffffffffu, r.ns, i), s.nt = __shfl_sync(0xffffffffu, r.nt, i);
-                const int mt = __shfl_sync(0xffffffffu, r.mt, i), per = s.nt + OVERHEAD, all = mt * C.heads;
+                const int mt = __shfl_sync(0xffffffffu, r.mt, i), per = s.nt + P.overhead, all = mt * C.heads;
                 if (s.nt) {
                     const int u0 = (int)quotient(pos - pre, per);
                     const int u1 = min(min(all, u0 + 16), (int)min((long long)all, quotient(hi - pre + per - 1, per)));
@@ -541,14 +550,14 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     s.b = b;
                     s.kvh = u / mt;
                     s.m = u - s.kvh * mt;
-                    s.t0 = (int)max(lo - first - OVERHEAD, 0ll);
-                    s.t1 = (int)min((long long)per, hi - first) - OVERHEAD;
+                    s.t0 = (int)max(lo - first - P.overhead, 0ll);
+                    s.t1 = (int)min((long long)per, hi - first) - P.overhead;
                     const bool any = u < u1 && s.t1 > s.t0;   // (else nothing, or the overhead alone)
                     const uint32_t mask = __ballot_sync(0xffffffffu, any);
                     if (any) {
                         ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
                         if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
-                            const long long last = first + OVERHEAD + s.nt;
+                            const long long last = first + P.overhead + s.nt;
                             P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
                         }
                     }
@@ -570,43 +579,44 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 ok = __all_sync(0xffffffffu, ok);
                 ended = true;
             }
-            if (!ok || loaded == pushed) break;
-            const Seg &s = segs[loaded & (SEGS - 1)];   // (not written again before it is loaded)
-            const int row0 = s.m * 2 * TILE, rows = min(s.M - row0, 2 * TILE);
-            const bool two = s.two();
-            const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D;
-            constexpr int CH = DP / 8, U = 8;
-            const int total = rows * CH;
-#pragma unroll 1
-            for (int i0 = lane; i0 < total + 32; i0 += 32 * U) {
-                uint4 w[U];
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int i = i0 + 32 * u, row = i / CH, ch = i % CH, rr = row0 + row, tok = rr / P.G;
-                    w[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (i < total && ch * 8 < C.D && !P.qzero)
-                        w[u] = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)(rr - tok * P.G) * C.D + ch * 8);
+            if (!ok) break;
+            // two segments' copies under way where there are buffers; else finish the older one first
+            const bool room = issued < pushed && issued - done < min(q_bufs, 2u);
+            if (room && (done == issued ? warp_wait(q_empty + 8 * at.stage, at.parity, dead)
+                                        : warp_try(q_empty + 8 * at.stage, at.parity))) {
+                const Seg &s = segs[issued & (SEGS - 1)];   // (not written again before its queries are there)
+                const int row0 = s.m * 2 * TILE, rows = min(s.M - row0, 2 * TILE);
+                const bool two = s.two();
+                constexpr int CH = DP / 8, RPW = 32 / CH;   // 16-byte pieces of a row, rows per warp step
+                const int ch = lane % CH;
+                int row = lane / CH, tok = (row0 + row) / P.G, head = row0 + row - tok * P.G;
+                const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + (ch * 8 < C.D ? ch * 8 : 0);
+                const uint32_t bytes = ch * 8 < C.D && !P.zero ? 16 : 0;
+                const uint32_t base = smem_addr(q_p) + (two ? 0 : at.stage) * q_buffer + (ch >> 3) * q_block;
+#pragma unroll 2
+                for (; row < rows; row += RPW) {
+                    copy16(base + (row >> 7) * q_buffer + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                           q + tok * P.q_stride + (int64_t)head * C.D, bytes);
+                    head += RPW;
+                    while (head >= P.G) head -= P.G, tok++;
                 }
-                if (i0 < 32) {   // the buffer's last user is through
-                    ok = warp_wait(q_empty + 8 * at.stage, at.parity, dead);
-                    if (!ok) break;
-                }
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int i = i0 + 32 * u, row = i / CH, ch = i % CH;
-                    if (i >= total) continue;
-                    w[u].x ^= P.qflip, w[u].y ^= P.qflip, w[u].z ^= P.qflip, w[u].w ^= P.qflip;
-                    char *to = q_p + (two ? row >> 7 : at.stage) * q_buffer + (ch >> 3) * q_block + (row & 127) * 128 +
-                               (((ch & 7) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(to) = w[u];
-                }
+                copies_commit();
+                issued++;
+                at.advance(q_bufs);
+            } else if (done < issued) {
+                if (issued - done == 2) copies_wait<1>();
+                else copies_wait<0>();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + 8 * out.stage);
+                done++;
+                out.advance(q_bufs);
+            } else {
+                if (room) ok = false;   // the wait ran out
+                break;                  // (nothing is left)
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(q_full + 8 * at.stage);
-            loaded++;
-            at.advance(q_bufs);
         }
+        copies_wait<0>();
     }
     } else {
         regs_up<208>();
@@ -656,39 +666,45 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     __syncwarp();
                 }
                 if (warp_on) {
-                    // 128 scores a thread in four times 32 columns; three of the four stay in registers
-                    // from the maximum to the weights, the first is loaded again in their shadow
-                    uint32_t x[3][32];
-                    auto masked = [&](uint32_t *v, int i) {
-                        if (whole) return;
-                        const uint32_t see = seen_mask(P, pos, base + 32 * i);
+                    uint32_t x[4][32];   // a thread's 128 scores
+                    if (!whole) {   // hide what this row does not see, in place: one copy of the code, off the main path
+#pragma unroll 1
+                        for (int i = 0; i < TILE; i += 32) {
+                            const uint32_t see = seen_mask(P, pos, base + i);
+                            tmem_ld32(t_s + i, x[0]);
+                            tmem_wait_ld();
+                            after_wait32(x[0]);
 #pragma unroll
-                        for (int k = 0; k < 32; k++) v[k] = (see >> k & 1) ? v[k] : 0xff800000u;   // -inf
-                    };
+                            for (int k = 0; k < 32; k++) x[0][k] = (see >> k & 1) ? x[0][k] : 0xff800000u;   // -inf
+                            tmem_st32(t_s + i, x[0]);
+                        }
+                        tmem_wait_st();
+                    }
                     float top[4] = {m, m, m, m};
                     auto largest = [&](const uint32_t *v) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 2)
                             top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
                     };
-                    tmem_ld32(t_s, x[0]);
-                    tmem_ld32(t_s + 32, x[1]);
-                    tmem_ld32(t_s + 64, x[2]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) tmem_ld32(t_s + 32 * i, x[i]);
                     tmem_wait_ld();
-                    after_wait32(x[0]);
-                    after_wait32(x[1]);
-                    after_wait32(x[2]);
-                    masked(x[0], 0);
-                    largest(x[0]);
-                    tmem_ld32(t_s + 96, x[0]);
-                    masked(x[1], 1);
-                    largest(x[1]);
-                    masked(x[2], 2);
-                    largest(x[2]);
-                    tmem_wait_ld();
-                    after_wait32(x[0]);
-                    masked(x[0], 3);
-                    largest(x[0]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) after_wait32(x[i]);
+                    if (APART) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free + 8 * g);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) largest(x[i]);
+                    if (APART && any_tile) {
+                        if (!warp_wait(o_done + 8 * g, ns_ & 1, dead)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
                     const float new_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // lift the running maximum, and scale O and l down, only where it lags too far
                     const bool lift = active && (m == -INFINITY ? new_m > m : (new_m - m) * P.c > LAG);
@@ -697,7 +713,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                         if (lift) m = new_m;
                         if (any_tile) {
                             l *= f;
-                            // (the group's last product is complete: it was issued before this S)
+                            // (the group's last product is complete: with P apart waited for above,
+                            // else issued before this S)
 #pragma unroll 1
                             for (int i = 0; i < D; i += 32) {
                                 uint32_t o[32];
@@ -724,27 +741,38 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                             sum[k / 2 & 1] = add2(sum[k / 2 & 1], pair_of(a, b));
                             w[k / 2] = Num<E>::down(a, b);
                         }
-                        tmem_st16(t_s + P_COL + 16 * i, w);   // over columns 64.. of S, which are all in registers
+                        tmem_st16(t_s + P_COL + 16 * i, w);
                     };
-                    weights(x[2], 2);
-                    tmem_ld32(t_s, x[2]);
-                    weights(x[0], 3);
-                    weights(x[1], 1);
-                    tmem_wait_ld();
-                    after_wait32(x[2]);
-                    masked(x[2], 0);
-                    weights(x[2], 0);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) weights(x[i], i);
                     float s0, s1;
                     split(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
                     tmem_wait_st();
                 }
+                if (APART && !warp_on) {
+                    // a warp without rows keeps step: a second arrival while another warp still owes its
+                    // first would pass for that one's
+                    if (lane == 0) mbar_arrive(s_free + 8 * g);
+                    if (any_tile && !warp_wait(o_done + 8 * g, ns_ & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                // the group's last product is through with its weights, which these replace, and its V tile
+                if (APART && any_tile && (warp & 3) == 0 && lane == 0 && (!two || mine))
+                    mbar_arrive(v_empty + 8 * ((tile0 + t - (two ? 1 : 2)) % v_stages));
                 any_tile = true;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * g);
             }
-            if (ok) ok = warp_wait(o_done + 8 * g, parts++ & 1, dead);
+            if (ok) ok = warp_wait(o_done + 8 * g, APART ? (ns_ - 1) & 1 : parts & 1, dead);
+            parts++;
+            if (APART && ok && (warp & 3) == 0 && lane == 0 && (!two || mine)) {
+                const int last = two ? nt - 1 : nt - 1 - ((nt - 1 - mine) & 1);   // this group's last key tile
+                mbar_arrive(v_empty + 8 * ((tile0 + last) % v_stages));
+            }
             if (ok && pair) {   // the other group's maxima, sums and O
                 ex[g * TILE + row] = make_float2(m, l);
                 tc_fence_before();
@@ -767,10 +795,10 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     l = a.y * f0 + b.y * f1;
                 }
                 if (broken) l = NAN;
-                const float inv = (l == 0.f && !direct) ? 0.f : 1.f / l;
+                const float inv = (l == 0.f && !direct) ? 0.f : rcp(l);
                 f0 *= inv;
                 f1 *= inv;
-                const float lse2 = l == 0.f ? -INFINITY : m * P.c + log2f(l) - BIAS;
+                const float lse2 = l == 0.f ? -INFINITY : m * P.c + lg2(l) - BIAS;
                 const int slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
                 const int head = s.kvh * P.G + rr - tok * P.G;
                 const int64_t orow = (int64_t)(s.row0 + tok) * Hq + head;
@@ -1019,15 +1047,20 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
         return SV_ERR_CUDA;
     P.q_tiles = (A.k_max + 1) * P.G > TILE ? 2 : 1;
     P.q_rows = P.q_tiles == 2 ? TILE : ((A.k_max + 1) * P.G + 7) / 8 * 8;
-    const int q_bytes = 2 * P.q_rows * DP * 2;
+    P.q_bufs = P.q_tiles == 2 ? 1 : P.q_rows <= 32 ? MAX_QBUFS : 2;
+    const int q_bytes = P.q_bufs * P.q_tiles * P.q_rows * DP * 2;
     // values wait longer than keys for their use: the odd stage is theirs
     const int stages = (SMEM_MAX - SMALL - q_bytes) / STAGE;
+    // A row tile costs about 4 us beside its key tiles (a first tile's latency, the epilogue, the join),
+    // and a key tile 1.0 us at 64 columns, 1.6 at 128.  Ragged 96 requests at 64 columns: 93, 78, 72, 68 us
+    // with 1, 2, 3, 4; ragged 64 at 128 columns, full and windowed: 69 and 46, 61 and 42, 60 and 44, 63 and 46.
+    P.overhead = DP == 64 ? 4 : 2;
     P.k_stages = stages / 2 < MAX_STAGES ? stages / 2 : MAX_STAGES;
     P.v_stages = stages - P.k_stages < MAX_STAGES ? stages - P.k_stages : MAX_STAGES;
     const int smem = SMALL + q_bytes + (P.k_stages + P.v_stages) * STAGE;
     // no more CTAs than the batch can have units
     const long long most = (long long)A.B * C.heads * (((long long)(A.k_max + 1) * P.G + 2 * TILE - 1) / (2 * TILE)) *
-                           ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + OVERHEAD);
+                           ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + P.overhead);
     int ctas = nsm < MAX_CTAS ? nsm : MAX_CTAS;
     if (most < ctas) ctas = (int)most;
     if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -1085,8 +1118,8 @@ extern "C" sv_status spec_attention(const void *q, int64_t q_stride, int32_t num
     P.part_lse = reinterpret_cast<float *>(w + L.lse);
     P.part_o = reinterpret_cast<float *>(w + L.o);
     P.c = (scale == 0.f ? 1.f : fabsf(scale)) * 1.4426950408889634f;
-    P.qflip = scale < 0.f ? 0x80008000u : 0u;
-    P.qzero = scale == 0.f;
+    P.negative = scale < 0.f;
+    P.zero = scale == 0.f;
     P.Hq = num_q_heads;
     P.G = num_q_heads / cache.num_heads;
     P.window = window;

@@ -39,6 +39,17 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same without suspending the thread, for polling one barrier among several.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Waits for the phase of the given parity; false once the wait has run out, here or in another
 // warp of the CTA (*dead is then set).  Small, because it is inlined at every wait (a call would
 // cost the softmax warps their registers); the timer is read once in 256 polls, since ten warps
@@ -63,10 +74,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 __device__ __forceinline__ bool warp_try(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try(bar, parity));
+    return __all_sync(0xffffffffu, mbar_test(bar, parity));
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 bytes from global to shared memory in the background; `bytes` 0 writes zeros instead.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {
     asm volatile(
@@ -116,7 +135,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // Instruction descriptor: fp32 sums, A and B both bf16 or both fp16, M x N; `tb`: B is given with
-// N contiguous.
+// N contiguous.  Bit 13 negates A.
 __host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int M, int N, bool tb) {
     return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | (uint32_t)tb << 16 | (uint32_t)(N >> 3) << 17 |
            (uint32_t)(M >> 4) << 24;
@@ -216,6 +235,19 @@ template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Approximate reciprocal and binary logarithm (2 ulp), where 1.f / x and log2f took longer than the rest
+// of an epilogue's scalars.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
