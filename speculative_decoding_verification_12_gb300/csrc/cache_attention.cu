@@ -274,7 +274,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 #pragma unroll 1
         for (int b0 = 0; b0 < A.B; b0 += NTHREADS) {
             const int b = b0 + tid;
-            const long long w = b < A.B ? units_of(req_of(A, C, P, b), C.heads, P.overhead) : 0;
+            Req r = {};
+            if (b < A.B) r = req_of(A, C, P, b);
+            const long long w = units_of(r, C.heads, P.overhead);
             long long inc = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -285,7 +287,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             if (lane == 31) scan[warp] = inc;
             __syncthreads();
             long long pre = before + inc - w, all = 0;
-#pragma unroll 1
+#pragma unroll
             for (int i = 0; i < NW; i++) {
                 const long long x = scan[i];
                 if (i < warp) pre += x;
@@ -805,28 +807,30 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 const uint32_t t0_ = pair ? t_o : t_o + g * TILE;
                 const int c0 = pair ? g * (DP / 2) : 0, c1 = min(D, pair ? c0 + DP / 2 : DP);
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 16) {
-                    uint32_t a[16], b[16];
-                    float o[16];
-                    tmem_ld16(t0_ + c, a);
-                    if (pair) tmem_ld16(t0_ + TILE + c, b);
+                for (int c = c0; c < c1; c += 32) {
+                    uint32_t a[32], b[32];
+                    tmem_ld32(t0_ + c, a);
+                    if (pair) tmem_ld32(t0_ + TILE + c, b);
                     tmem_wait_ld();
-                    after_wait16(a);
-                    after_wait16(b);
+                    after_wait32(a);
+                    after_wait32(b);
+                    float o[32];
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        o[i] = __uint_as_float(a[i]) * f0;
-                        if (pair) o[i] += __uint_as_float(b[i]) * f1;
-                    }
+                    for (int i = 0; i < 32; i++) o[i] = __uint_as_float(a[i]) * f0;
+                    if (pair)
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] = fmaf(__uint_as_float(b[i]), f1, o[i]);
                     if (active) {
                         if (direct) {
                             E *to = static_cast<E *>(P.out) + orow * D + c;
-                            if (c < D) *reinterpret_cast<uint4 *>(to) = pack8<E>(o);
-                            if (c + 8 < D) *reinterpret_cast<uint4 *>(to + 8) = pack8<E>(o + 8);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                if (c + i < c1) *reinterpret_cast<uint4 *>(to + i) = pack8<E>(o + i);
                         } else {
                             float4 *to = reinterpret_cast<float4 *>(P.part_o + ((int64_t)slot * PART_ROWS + rt) * DP + c);
 #pragma unroll
-                            for (int i = 0; i < 4; i++) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < 8; i++)
+                                if (c + i * 4 < c1) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                     }
                     __syncwarp();
