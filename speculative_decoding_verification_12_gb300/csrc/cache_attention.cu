@@ -34,7 +34,7 @@ namespace svc {
 constexpr int TILE = 128;                // tokens per key tile, rows per row tile
 constexpr int BLK = TILE * 128;          // bytes of 128 rows x 64 elements
 constexpr int NTHREADS = 384;            // 2 x 4 softmax warps, then one warp for each of:
-constexpr int W_K = 8, W_MMA = 9, W_V = 10;   // keys, matrix instructions, values, and the front warp
+constexpr int W_K = 9, W_V = 10, W_MMA = 11;   // keys, values, matrix instructions; 8 is the front warp
 constexpr int MAX_CTAS = 160;
 constexpr int PART_ROWS = 256;           // rows of a part
 constexpr int MAX_STAGES = 7;            // of each of the two rings
@@ -212,6 +212,11 @@ __device__ __forceinline__ void add_non_finite(const Cache &C, const AttnArgs &P
 
 // Barriers, flags and the groups' exchange, at the start of shared memory.
 constexpr int SMALL = 5120;
+// Narrow heads, up to 32 rows: group 1 takes its rows to the third quarter of tensor memory, so that the
+// groups' one busy warp each sits on a scheduler of its own, and hands its O to group 0 through shared
+// memory.
+constexpr int FEW_ROWS = 32, DOWN = 64;   // rows, and how far down group 1 has them
+__host__ __device__ constexpr int hand_over(int DP) { return DP == 64 ? FEW_ROWS * (64 + 4) * 4 + 512 : 0; }   // (9216: 1024-byte steps)
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -228,30 +233,32 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     constexpr bool APART = DP == 64;
     constexpr int P_COL = APART ? 2 * TILE + 64 : TILE / 2;   // P of group g at column g * 128 + P_COL
     extern __shared__ __align__(1024) char smem[];
-    // [barriers and small state][query buffers][ring of K tiles][ring of V tiles]; the matrix
-    // instruction reads 128 rows from a query buffer whatever it holds: the rows past it are other
+    // [barriers and small state][group 1's O][ring of K tiles][query buffers][ring of V tiles]; the matrix
+    // instruction reads 128 rows around a query buffer whatever they hold: the rows outside it are other
     // bytes of this memory, and reach only rows of S, P and O that nothing uses
     const int q_block = P.q_rows * 128, q_buffer = NB * q_block;
-    char *const q_p = smem + SMALL;
-    char *const k_p = q_p + P.q_bufs * P.q_tiles * q_buffer, *const v_p = k_p + P.k_stages * STAGE;
-    int *const ctl = reinterpret_cast<int *>(smem + 384);                    // dead, tmem, -, -, patched[2][4], bad[16]
+    float *const handed = reinterpret_cast<float *>(smem + SMALL);           // [FEW_ROWS][DP + 4]
+    char *const k_p = smem + SMALL + hand_over(DP), *const q_p = k_p + P.k_stages * STAGE;
+    char *const v_p = q_p + P.q_bufs * P.q_tiles * q_buffer;
+    int *const ctl = reinterpret_cast<int *>(smem + 400);                    // dead, tmem, -, -, patched[2][4], bad[16]
     float2 *const ex = reinterpret_cast<float2 *>(smem + 512);               // [2][128] (m, l)
     long long *const scan = reinterpret_cast<long long *>(ex);               // the set-up's scratch, before ex is used
     Seg *const segs = reinterpret_cast<Seg *>(smem + 2560);                  // [SEGS]
     const uint32_t seg_full = smem_addr(smem + 4608), seg_empty = seg_full + 8 * SEGS;
     const uint32_t k_full = smem_addr(smem), k_empty = k_full + 8 * MAX_STAGES, v_full = k_empty + 8 * MAX_STAGES,
                    v_empty = v_full + 8 * MAX_STAGES, s_full = v_empty + 8 * MAX_STAGES, p_full = s_full + 16,
-                   o_done = p_full + 16, both = o_done + 16, s_free = both + 16, drained = s_free + 16, q_full = drained + 8, q_empty = q_full + 8 * MAX_QBUFS;
+                   o_done = p_full + 16, both = o_done + 16, s_free = both + 16, drained = s_free + 16, q_full = drained + 24, q_empty = q_full + 8 * MAX_QBUFS;
     volatile int *const dead = ctl, *const patched = ctl + 4, *const bad = ctl + 12;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_bufs;
 
     // one thread per barrier: the rings and pairs in a row from k_full, then the segments'
-    constexpr int NBARS = 4 * MAX_STAGES + 11 + 2 * MAX_QBUFS;
+    constexpr int NBARS = 4 * MAX_STAGES + 13 + 2 * MAX_QBUFS;
     if (tid < NBARS) {
         // pairs: s_full, p_full (4 warps), o_done, both (8 warps), s_free (4 warps); then the rest
         const int p = (tid - 4 * MAX_STAGES) >> 1;
-        mbar_init(k_full + 8 * tid, p == 1 || p == 4 ? 4 : p == 3 ? 8 : 1);
+        const bool frees_v = tid >= 3 * MAX_STAGES && tid < 4 * MAX_STAGES;
+        mbar_init(k_full + 8 * tid, p == 1 || p == 4 ? 4 : p == 3 ? 8 : APART && frees_v ? 2 : 1);
     } else if (tid >= 128 && tid < 128 + 2 * SEGS) {
         mbar_init(seg_full + 8 * (tid - 128), tid < 128 + SEGS ? 1 : SEG_READERS);
     } else if (tid >= 256 && tid < 256 + 28 && tid != 257) {   // (1 is the tensor memory's address)
@@ -318,7 +325,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 
     // Takes segment k into registers; false at the end of the list, or when a wait ran out (ok).
     bool ok = true;
-    auto take = [&](int k, Seg &s, bool release) {
+    auto take = [&](int k, Seg &s, bool release_now) {
         const int slot = k & (SEGS - 1);
         ok = warp_wait(seg_full + 8 * slot, k / SEGS & 1, dead);
         if (!ok) return false;
@@ -327,8 +334,38 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 #pragma unroll
         for (int i = 0; i < 4; i++) to[i] = from[i];
         __syncwarp();
-        if (release && lane == 0) mbar_arrive(seg_empty + 8 * slot);
+        if (release_now && lane == 0) mbar_arrive(seg_empty + 8 * slot);
         return s.nt > 0;
+    };
+    auto release = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + 8 * (k & (SEGS - 1)));
+    };
+
+    // S of group g from the queries and keys at the given places, and P V into the group's O (one lane each)
+    const int steps = (C.D + 15) / 16;                              // of 16 columns: nothing past head_dim
+    auto issue_s = [&](uint32_t g, uint32_t q_at, uint32_t k_stage, bool down) {
+        const uint32_t idesc = mma_idesc(Num<E>::BF16, TILE, TILE, false) | (uint32_t)P.negative << 13;
+        const uint64_t qd = smem_desc(smem_addr(q_p) + q_at * q_buffer - (down ? DOWN * 128 : 0), 16), kd = smem_desc(smem_addr(k_p) + k_stage * STAGE, 16);
+        const uint32_t q_step = q_block >> 4;
+        auto run = [&](auto n) {
+#pragma unroll
+            for (int k = 0; k < decltype(n)::N; k++)
+                mma_ss(tmem + g * TILE, qd + (uint64_t)((k >> 2) * q_step + (k & 3) * 2),
+                       kd + (uint64_t)((k >> 2) * (BLK >> 4) + (k & 3) * 2), idesc, k > 0);
+        };
+        if (DP == 64) run(Const<4>());
+        else if (steps == 8) run(Const<8>());
+        else if (steps == 5) run(Const<5>());
+        else if (steps == 6) run(Const<6>());
+        else run(Const<7>());
+    };
+    auto issue_o = [&](uint32_t g, uint32_t v_stage, bool add) {
+        const uint32_t idesc = mma_idesc(Num<E>::BF16, TILE, 0, true) | (uint32_t)(steps * 2) << 17;
+        const uint64_t vd = smem_desc(smem_addr(v_p) + v_stage * STAGE, BLK);
+#pragma unroll
+        for (int k = 0; k < TILE / 16; k++)
+            mma_ts(tmem + 2 * TILE + g * TILE, tmem + g * TILE + P_COL + k * 8, vd + (uint64_t)(k * 2048 >> 4), idesc, add || k > 0);
     };
 
     if (warp >= 8) {
@@ -392,24 +429,49 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
                 while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
         }
-    } else if (warp == W_MMA) {
-        // Matrix instructions.  Over all segments the row tiles' products come in one sequence: tile v
-        // of a segment, or, with two row tiles, row tile v & 1 of key tile v >> 1.  The groups take it
-        // in turn, S runs two ahead of P V, and so the next segment's scores are ready while this
-        // one's last tiles are still with the groups.  The whole warp runs this; one lane issues.
-        // The path from a group's weights to its next scores is the kernel's longest chain, so P V and
-        // that S are issued together, the commits after both, and whether K is there is asked before.
-        // A commit costs the issuing lane some 140 cycles: there are two a product, S is there (the
-        // softmax group then frees the K tile) and the V tile is free.  A group learns of its last
-        // product of a segment by o_done; earlier ones are complete when a later S is.  (With P apart
-        // o_done follows every product, and the group frees the V tile.)
-        const uint32_t idesc_s = mma_idesc(Num<E>::BF16, TILE, TILE, false) | (uint32_t)P.negative << 13;
-        const int steps = (C.D + 15) / 16;                              // of 16 columns: nothing past head_dim
-        const uint32_t idesc_o = mma_idesc(Num<E>::BF16, TILE, 0, true) | (uint32_t)(steps * 2) << 17;
+    } else if (APART && warp == W_MMA) {
+        // Scores, with P apart: each as soon as its group has the last ones in registers.
         const bool leader = elect();
-        const uint64_t k_desc = smem_desc(smem_addr(k_p), 16), v_desc = smem_desc(smem_addr(v_p), BLK),
-                       q_desc = smem_desc(smem_addr(q_p), 16);
-        const uint32_t q_step = q_block >> 4;
+        Place ks{0, 0}, qs{0, 0};
+        uint32_t g = 0, nf = 3;   // the group whose turn it is; parities of each one's free S
+        Seg s;
+        for (int seg = 0; ok && take(seg, s, true); seg++) {
+            const int two = s.two(), nv = (s.t1 - s.t0) << two;
+            ok = warp_wait(q_full + 8 * qs.stage, qs.parity, dead);
+#pragma unroll 1
+            for (int v = 0; ok && v < nv; v++) {
+                ok = warp_wait(s_free + 8 * g, nf >> g & 1, dead) && warp_wait(k_full + 8 * ks.stage, ks.parity, dead);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    issue_s(g, two ? v & 1 : qs.stage, ks.stage, g && s.M <= FEW_ROWS);
+                    mma_commit(s_full + 8 * g);
+                    if (v == nv - 1) mma_commit(q_empty + 8 * qs.stage);
+                }
+                __syncwarp();
+                nf ^= 1u << g;
+                g ^= 1;
+                if (!two || (v & 1)) ks.advance(k_stages);
+            }
+            qs.advance(q_bufs);
+        }
+        if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
+            if (leader) mma_commit(drained);
+            const uint32_t t0 = now_ns32();
+            while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
+        }
+        __syncwarp();
+    } else if (warp == W_MMA) {
+        // Matrix instructions, with P over S.  Over all segments the row tiles' products come in one
+        // sequence: tile v of a segment, or, with two row tiles, row tile v & 1 of key tile v >> 1.  The
+        // groups take it in turn, S runs two ahead of P V, and so the next segment's scores are ready
+        // while this one's last tiles are still with the groups.  The whole warp runs this; one lane
+        // issues.  The path from a group's weights to its next scores is the kernel's longest chain, so
+        // P V and that S are issued together, the commits after both.  A commit costs the issuing lane
+        // 70 to 140 cycles: there are two a product, S is there (the softmax group then frees the K tile)
+        // and the V tile is free.  A group learns of its last product of a segment by o_done; earlier
+        // ones are complete when a later S is.
+        const bool leader = elect();
         int sseg = 0, oseg = 0;                                     // segments opened
         int sv = 0, snv = 0, stwo = 0, ov = 0, onv = 0, otwo = 0;   // product, products and kind of the current ones
         auto open = [&](int &k, int &v, int &nv, int &two, bool release) {
@@ -422,24 +484,23 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         open(sseg, sv, snv, stwo, false);
         if (ok) open(oseg, ov, onv, otwo, true);
         Place ks{0, 0}, vs{0, 0}, qs{0, 0};
-        uint32_t gs = 0, go = 0, np = 0, nf = 3;   // groups whose turn it is; parities of each one's next P and free S
-        int lead = 0;                      // products whose S, but not P V, is issued: at most 2, or 4 with P apart
+        uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each one's next P
+        int lead = 0;                      // products whose S, but not P V, is issued: at most 2
         uint32_t polls = 0, idle_since = 0;
 #pragma unroll 1
         while (ok && onv) {
             // all that may be waited for is asked at once; every lane has to have seen it
             uint32_t there = 0;
-            if (snv) {   // the next S: its place (with P apart), its queries and its keys
-                there |= !APART || mbar_test(s_free + 8 * gs, nf >> gs & 1);
-                there |= (uint32_t)(sv || mbar_test(q_full + 8 * qs.stage, qs.parity)) << 1;
-                there |= (uint32_t)mbar_test(k_full + 8 * ks.stage, ks.parity) << 2;
+            if (snv) {   // the next S: its queries and its keys
+                there = sv || mbar_test(q_full + 8 * qs.stage, qs.parity);
+                there |= (uint32_t)mbar_test(k_full + 8 * ks.stage, ks.parity) << 1;
             }
             if (lead) {
-                there |= (uint32_t)mbar_test(p_full + 8 * go, np >> go & 1) << 3;
-                there |= (uint32_t)mbar_test(v_full + 8 * vs.stage, vs.parity) << 4;
+                there |= (uint32_t)mbar_test(p_full + 8 * go, np >> go & 1) << 2;
+                there |= (uint32_t)mbar_test(v_full + 8 * vs.stage, vs.parity) << 3;
             }
             there = __reduce_and_sync(0xffffffffu, there);
-            const bool do_o = there >> 3 == 3, do_s = (there & 7) == 7 && (APART || lead < 2 || do_o);
+            const bool do_o = there >> 2 == 3, do_s = (there & 3) == 3 && (lead < 2 || do_o);
             if (!do_o && !do_s) {
                 if (++polls & 255) continue;
                 const uint32_t now = now_ns32() | 1;
@@ -455,33 +516,15 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             tc_fence_after();
             const bool last_use = !otwo || (ov & 1);
             if (leader) {
-                if (do_o) {
-                    const uint64_t vd = v_desc + (uint64_t)(vs.stage * STAGE >> 4);
-#pragma unroll
-                    for (int k = 0; k < TILE / 16; k++)
-                        mma_ts(tmem + 2 * TILE + go * TILE, tmem + go * TILE + P_COL + k * 8, vd + (uint64_t)(k * 2048 >> 4),
-                               idesc_o, ov >= 2 || k > 0);
-                }
+                if (do_o) issue_o(go, vs.stage, ov >= 2);
                 if (do_s) {
-                    const uint64_t kd = k_desc + (uint64_t)(ks.stage * STAGE >> 4);
-                    const uint64_t qd = q_desc + (uint64_t)((stwo ? sv & 1 : qs.stage) * q_buffer >> 4);
-                    auto issue = [&](auto n) {
-#pragma unroll
-                        for (int k = 0; k < decltype(n)::N; k++)
-                            mma_ss(tmem + gs * TILE, qd + (uint64_t)((k >> 2) * q_step + (k & 3) * 2),
-                                   kd + (uint64_t)((k >> 2) * (BLK >> 4) + (k & 3) * 2), idesc_s, k > 0);
-                    };
-                    if (DP == 64) issue(Const<4>());
-                    else if (steps == 8) issue(Const<8>());
-                    else if (steps == 5) issue(Const<5>());
-                    else if (steps == 6) issue(Const<6>());
-                    else issue(Const<7>());
+                    issue_s(gs, stwo ? sv & 1 : qs.stage, ks.stage, false);
                     mma_commit(s_full + 8 * gs);
                     if (sv == snv - 1) mma_commit(q_empty + 8 * qs.stage);
                 }
                 if (do_o) {
-                    if (!APART && last_use) mma_commit(v_empty + 8 * vs.stage);
-                    if (APART || ov >= onv - 2) mma_commit(o_done + 8 * go);
+                    if (last_use) mma_commit(v_empty + 8 * vs.stage);
+                    if (ov >= onv - 2) mma_commit(o_done + 8 * go);
                 }
             }
             __syncwarp();
@@ -494,7 +537,6 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             }
             if (do_s && ok) {
                 if (!stwo || (sv & 1)) ks.advance(k_stages);
-                nf ^= 1u << gs;
                 gs ^= 1;
                 lead++;
                 if (++sv == snv) {
@@ -624,13 +666,15 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         regs_up<208>();
         // Softmax and epilogue: group g, a thread per row.
         Seg s;
-        const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int g = warp >> 2, lane_row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
         const uint32_t t_s = tmem + g * TILE + lanes, t_o = tmem + 2 * TILE + lanes;
         const int D = C.D, Hq = P.Hq;
-        uint32_t ns_ = 0, turn = 0, tiles = 0, parts = 0, pairs = 0;   // S tiles taken; products, key tiles, epilogues, joint ones
+        const bool leader = elect();
+        uint32_t ns_ = 0, turn = 0, tiles = 0, parts = 0, joint = 0, pairs = 0;   // S tiles taken; products, key tiles, epilogues; barriers of both groups
 #pragma unroll 1
-        for (int seg = 0; ok && take(seg, s, true); seg++) {
+        for (int seg = 0; ok && take(seg, s, false); release(seg++)) {
+            const Seg &all = segs[seg & (SEGS - 1)];   // what only the ends of a segment need stays there
             const int nt = s.t1 - s.t0;
             const bool two = s.two();
             const int mine = (g ^ turn) & 1;      // this group's row tile, or its first key tile
@@ -639,12 +683,13 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             tiles += nt;
             if (!two && mine >= nt) continue;     // a single key tile, and the other group's turn
             const bool pair = !two && nt > 1;     // both groups hold a part of every row
+            const bool few = APART && s.M <= FEW_ROWS;
+            const int row = lane_row ^ (few && g ? DOWN : 0);
             const int rows = min(s.M - s.m * 2 * TILE, 2 * TILE);   // of this row tile
             const int rt = two ? mine * TILE + row : row;           // this thread's row of it
             const bool active = rt < rows;
-            const bool warp_on = (two ? mine * TILE : 0) + (warp & 3) * 32 < rows;
-            const int rr = s.m * 2 * TILE + rt, tok = rr / P.G;
-            const int pos = s.len - s.n + tok;
+            const bool warp_on = (two ? mine * TILE : 0) + (((warp & 3) * 32) ^ (few && g ? DOWN : 0)) < rows;
+            const int pos = s.len - s.n + (s.m * 2 * TILE + rt) / P.G;
             float m = -INFINITY, l = 0.f;
             bool any_tile = false;
 #pragma unroll 1
@@ -666,6 +711,13 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     if (clean_values<E, DP>(P, s, base, row, v_p + stage * STAGE)) patched[4 * g + (seg & 3)] = seg;
                     fence_proxy_async();
                     __syncwarp();
+                }
+                if (APART && two && !whole) {   // the other group's product reads this V tile too
+                    if (lane == 0) mbar_arrive(both);
+                    if (!warp_wait(both, joint++ & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 if (warp_on) {
                     uint32_t x[4][32];   // a thread's 128 scores
@@ -762,30 +814,69 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     }
                 }
                 // the group's last product is through with its weights, which these replace, and its V tile
-                if (APART && any_tile && (warp & 3) == 0 && lane == 0 && (!two || mine))
-                    mbar_arrive(v_empty + 8 * ((tile0 + t - (two ? 1 : 2)) % v_stages));
-                any_tile = true;
+                // (two arrivals free a tile: one of each group, or both of the one that used it)
+                if (APART && any_tile && (warp & 3) == 0 && lane == 0)
+                    mbar_arrive(v_empty + 8 * ((tile0 + t - (two ? 1 : 2)) % v_stages), two ? 1 : 2);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * g);
+                // with P apart the group issues its P V itself: its last warp, which has no rows of its own
+                // unless the row tile has more than 96
+                if (APART && (warp & 3) == 3) {
+                    const uint32_t round = (tile0 + t) / v_stages, stage = tile0 + t - round * v_stages;
+                    ok = warp_wait(p_full + 8 * g, (ns_ - 1) & 1, dead) && warp_wait(v_full + 8 * stage, round & 1, dead);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        issue_o(g, stage, any_tile);
+                        mma_commit(o_done + 8 * g);
+                    }
+                    __syncwarp();
+                }
+                any_tile = true;
             }
             if (ok) ok = warp_wait(o_done + 8 * g, APART ? (ns_ - 1) & 1 : parts & 1, dead);
             parts++;
-            if (APART && ok && (warp & 3) == 0 && lane == 0 && (!two || mine)) {
+            if (APART && ok && (warp & 3) == 0 && lane == 0) {
                 const int last = two ? nt - 1 : nt - 1 - ((nt - 1 - mine) & 1);   // this group's last key tile
-                mbar_arrive(v_empty + 8 * ((tile0 + last) % v_stages));
+                mbar_arrive(v_empty + 8 * ((tile0 + last) % v_stages), two ? 1 : 2);
             }
             if (ok && pair) {   // the other group's maxima, sums and O
                 ex[g * TILE + row] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(both);
-                ok = warp_wait(both, pairs & 1, dead);
+                ok = warp_wait(both, joint++ & 1, dead);
             }
             if (!ok) break;
             tc_fence_after();
+            if (pair && few) {   // (the barrier that ends a pair: group 1's part is handed over before it)
+                if (g && warp_on) {
+                    const float2 a = ex[row], b = ex[TILE + row];
+                    const float f = b.x == fmaxf(a.x, b.x) ? 1.f : ex2((b.x - a.x) * P.c);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + TILE + c, o);
+                        tmem_wait_ld();
+                        after_wait32(o);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(handed + row * (DP + 4) + c + i) =
+                                make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
+                                            __uint_as_float(o[i + 3]) * f);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(both + 8);
+                ok = warp_wait(both + 8, pairs++ & 1, dead);
+                if (!ok) break;
+                if (g) continue;
+            }
+            const int rr = all.m * 2 * TILE + rt, tok = pos - all.len + all.n;
             const bool patch = patched[seg & 3] == seg || patched[4 + (seg & 3)] == seg, broken = bad[seg & 15] == seg + 1;
-            const bool direct = s.t0 == 0 && s.t1 == s.nt;
+            const bool direct = all.t0 == 0 && all.t1 == all.nt;
             if (warp_on) {
                 // the part's maximum and sum, and the factors of the (up to) two sums O
                 float f0 = 1.f, f1 = 0.f;
@@ -801,25 +892,33 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 f0 *= inv;
                 f1 *= inv;
                 const float lse2 = l == 0.f ? -INFINITY : m * P.c + lg2(l) - BIAS;
-                const int slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
-                const int head = s.kvh * P.G + rr - tok * P.G;
-                const int64_t orow = (int64_t)(s.row0 + tok) * Hq + head;
+                const int slot = 2 * cta + (all.t0 > 0 ? 0 : 1);
+                const int head = all.kvh * P.G + rr - tok * P.G;
+                const int64_t orow = (int64_t)(all.row0 + tok) * Hq + head;
                 const uint32_t t0_ = pair ? t_o : t_o + g * TILE;
-                const int c0 = pair ? g * (DP / 2) : 0, c1 = min(D, pair ? c0 + DP / 2 : DP);
+                const bool halves = pair && !few;
+                const int c0 = halves ? g * (DP / 2) : 0, c1 = min(D, halves ? c0 + DP / 2 : DP);
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
                     uint32_t a[32], b[32];
                     tmem_ld32(t0_ + c, a);
-                    if (pair) tmem_ld32(t0_ + TILE + c, b);
+                    if (halves) tmem_ld32(t0_ + TILE + c, b);
                     tmem_wait_ld();
                     after_wait32(a);
                     after_wait32(b);
                     float o[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) o[i] = __uint_as_float(a[i]) * f0;
-                    if (pair)
+                    if (halves) {
 #pragma unroll
                         for (int i = 0; i < 32; i++) o[i] = fmaf(__uint_as_float(b[i]), f1, o[i]);
+                    } else if (pair) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(handed + row * (DP + 4) + c + i);
+                            o[i] += x.x * inv, o[i + 1] += x.y * inv, o[i + 2] += x.z * inv, o[i + 3] += x.w * inv;
+                        }
+                    }
                     if (active) {
                         if (direct) {
                             E *to = static_cast<E *>(P.out) + orow * D + c;
@@ -836,7 +935,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     __syncwarp();
                 }
                 if (patch && active) {
-                    add_non_finite<E>(C, P, s, pos, c0, c1, [&](int d, float x) {
+                    add_non_finite<E>(C, P, all, pos, c0, c1, [&](int d, float x) {
                         if (direct) {
                             E &y = static_cast<E *>(P.out)[orow * D + d];
                             y = (E)((float)y + x);
@@ -851,11 +950,16 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 }
             }
             tc_fence_before();
-            if (pair) {   // neither group's next product may overwrite an O that the other still reads
+            if (pair && !few) {   // neither group's next product may overwrite an O that the other still reads
                 __syncwarp();
                 if (lane == 0) mbar_arrive(both + 8);
                 ok = warp_wait(both + 8, pairs++ & 1, dead);
             }
+        }
+        if (APART && !ok && (warp & 3) == 3) {   // as the matrix warp does
+            if (leader) mma_commit(drained + 8 + 8 * g);
+            const uint32_t t0 = now_ns32();
+            while (!mbar_try(drained + 8 + 8 * g, 0) && now_ns32() - t0 < WAIT_NS) {}
         }
     }
     tc_fence_before();
@@ -1054,14 +1158,14 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     P.q_bufs = P.q_tiles == 2 ? 1 : P.q_rows <= 32 ? MAX_QBUFS : 2;
     const int q_bytes = P.q_bufs * P.q_tiles * P.q_rows * DP * 2;
     // values wait longer than keys for their use: the odd stage is theirs
-    const int stages = (SMEM_MAX - SMALL - q_bytes) / STAGE;
+    const int stages = (SMEM_MAX - SMALL - hand_over(DP) - q_bytes) / STAGE;
     // A row tile costs about 4 us beside its key tiles (a first tile's latency, the epilogue, the join),
     // and a key tile 1.0 us at 64 columns, 1.6 at 128.  Ragged 96 requests at 64 columns: 93, 78, 72, 68 us
     // with 1, 2, 3, 4; ragged 64 at 128 columns, full and windowed: 69 and 46, 61 and 42, 60 and 44, 63 and 46.
     P.overhead = DP == 64 ? 4 : 2;
     P.k_stages = stages / 2 < MAX_STAGES ? stages / 2 : MAX_STAGES;
     P.v_stages = stages - P.k_stages < MAX_STAGES ? stages - P.k_stages : MAX_STAGES;
-    const int smem = SMALL + q_bytes + (P.k_stages + P.v_stages) * STAGE;
+    const int smem = SMALL + hand_over(DP) + q_bytes + (P.k_stages + P.v_stages) * STAGE;
     // no more CTAs than the batch can have units
     const long long most = (long long)A.B * C.heads * (((long long)(A.k_max + 1) * P.G + 2 * TILE - 1) / (2 * TILE)) *
                            ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + P.overhead);
