@@ -123,6 +123,8 @@ sv_status spec_append(const void *q, const void *k, const void *v, int64_t q_str
  *   out          device [total_rows, num_q_heads, head_dim], contiguous, 16-byte aligned.
  *   out_lse      optional device fp32 [total_rows, num_q_heads].
  *   workspace    sv_attention_workspace_bytes() bytes, 256-byte aligned.
+ * Every wait inside the kernel is bounded (2 s): one that runs out ends the call with
+ * SV_DEV_TIMEOUT in the error word and unspecified outputs, and the device stays usable.
  * Sizes as spec_append, and head_dim <= 128.  Results are the same from call to call: the split
  * of the work over the chip depends on the lengths alone, and parts are joined in a fixed order.
  */

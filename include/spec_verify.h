@@ -289,7 +289,8 @@ sv_status sv_set_phase_events(void *stream_kernel_start, void *stream_kernel_end
 /* Testing aid for the failure path: while `on` is nonzero, the streaming kernel of every
  * spec_verify / spec_verify_onehot / spec_verify_lazy call that takes the streaming path
  * (16-byte aligned rows) withholds one work unit from its copy and reduction warps, as a
- * stalled scheduler would.  Their bounded waits run out after 2 s; the call then completes
+ * stalled scheduler would, and the attention kernel of spec_attention (spec_cache.h) one tile of
+ * keys.  Their bounded waits run out after 2 s; the call then completes
  * with -1 outputs for the requests SV_DEV_TIMEOUT describes, that code in the workspace's
  * error word, and the device stays usable.  No page has a counterpart: it exists so that the
  * timeout path can be tested without a GPU fault.  Process-wide, for every device; returns

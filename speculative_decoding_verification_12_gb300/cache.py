@@ -154,3 +154,67 @@ def spec_page_copy(k_cache, v_cache, copy_src, copy_dst, workspace, stream=None)
     st = (_native or _load()).copy(k_cache, v_cache, copy_src, copy_dst, workspace, stream)
     if st != SV_OK:
         raise SvError(st, "spec_page_copy")
+
+
+class PagedCache:
+    """The paged KV cache of `slots` requests over `layers` layers, resident on a CUDA device, with
+    one method per step of the header's sequence.  Plumbing only, like batch.DeviceBatch: it holds
+    the tensors and the workspace, and every method is one or two of the calls above.
+
+    k, v [layers, pages, page_size, heads, head_dim]; kv_seq_len [slots], block_table [slots,
+    max_pages], ref_count [pages]: the state that spec_page_* work on.  All requests start empty.
+    """
+
+    def __init__(self, layers: int, slots: int, pages: int, page_size: int, max_pages: int, heads: int, head_dim: int,
+                 dtype=torch.bfloat16, device="cuda"):
+        shape = (layers, pages, page_size, heads, head_dim)
+        self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        ints = dict(dtype=torch.int32, device=device)
+        self.kv_seq_len = torch.zeros(slots, **ints)
+        self.block_table = torch.full((slots, max_pages), -1, **ints)
+        self.ref_count = torch.zeros(pages, **ints)
+        self.page_size = page_size
+        need = max(sv_attention_workspace_bytes(head_dim), sv_page_workspace_bytes(slots, pages))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+
+    def reserve(self, num_drafts, stream=None) -> None:
+        """Room for num_drafts[b] + 1 new tokens of every request (-1: idle)."""
+        spec_page_reserve(num_drafts, self.kv_seq_len, self.block_table, self.ref_count, self.page_size,
+                          self.workspace, stream)
+
+    def append(self, layer: int, q, k, v, q_weight, k_weight, eps, inv_freq, num_drafts, row_offsets, k_max, out_q,
+               interleaved=False, rope_scale=1.0, stream=None) -> None:
+        spec_append(q, k, v, q_weight, k_weight, eps, inv_freq, self.k[layer], self.v[layer], self.block_table,
+                    self.kv_seq_len, num_drafts, row_offsets, k_max, out_q, self.workspace, interleaved, rope_scale,
+                    stream)
+
+    def attend(self, layer: int, q, num_drafts, row_offsets, k_max, scale, out, window=0, sinks=0, out_lse=None,
+               stream=None) -> None:
+        spec_attention(q, self.k[layer], self.v[layer], self.block_table, self.kv_seq_len, num_drafts, row_offsets,
+                       k_max, scale, window, sinks, out, out_lse, self.workspace, stream)
+
+    def commit(self, accept_len, num_drafts, window=0, sinks=0, stream=None) -> None:
+        """Rolls every request back to its accepted drafts and gives the pages past them back."""
+        st = rollback(self.kv_seq_len, accept_len, num_drafts, self.workspace, stream)
+        if st != SV_OK:
+            raise SvError(st, "spec_rollback")
+        self.release(window, sinks, stream)
+
+    def release(self, window=0, sinks=0, stream=None) -> None:
+        spec_page_release(self.kv_seq_len, self.block_table, self.ref_count, self.page_size, window, sinks,
+                          self.workspace, stream)
+
+    def fork(self, parents, children, fork_len=None, stream=None) -> None:
+        """Empty slots children[f] continue from (the first fork_len[f] tokens of) parents[f]."""
+        src, dst = torch.empty_like(parents), torch.empty_like(parents)
+        spec_page_fork(parents, children, fork_len, self.kv_seq_len, self.block_table, self.ref_count, self.page_size,
+                       src, dst, self.workspace, stream)
+        spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)
+
+    def compact(self, capacity: int, stream=None) -> None:
+        """Moves up to `capacity` used pages down into the free ones below them."""
+        src = torch.empty(capacity, dtype=torch.int32, device=self.k.device)
+        dst = torch.empty_like(src)
+        spec_page_compact(self.block_table, self.ref_count, src, dst, self.workspace, stream)
+        spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)

@@ -27,6 +27,7 @@
 #include <atomic>
 
 #include "sv_cache.cuh"
+#include "sv_launch.h"
 #include "sv_tc.cuh"
 
 namespace svc {
@@ -51,6 +52,7 @@ struct AttnArgs {
     float *part_o;     // workspace, [2 * MAX_CTAS][PART_ROWS][DP]
     float c;           // |scale| log2(e)
     int negative, zero;   // scale < 0, scale == 0
+    int withhold;         // testing aid: the last CTA never loads its first K tile
     int Hq, G, window, sinks;
     int k_stages, v_stages;
     int overhead;      // cost of a row tile beside its key tiles, in key tiles
@@ -411,6 +413,10 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
                 ok = warp_wait(empty + 8 * at.stage, at.parity, dead);
                 if (!ok) break;
+                if (P.withhold && cta == nc - 1 && !is_v && loads == 0) {   // (its waits then run out, as they are meant to)
+                    ok = false;
+                    break;
+                }
                 loads++;
                 if (lane == 0) mbar_expect(full + 8 * at.stage, bytes);
                 __syncwarp();
@@ -1228,6 +1234,7 @@ extern "C" sv_status spec_attention(const void *q, int64_t q_stride, int32_t num
     P.c = (scale == 0.f ? 1.f : fabsf(scale)) * 1.4426950408889634f;
     P.negative = scale < 0.f;
     P.zero = scale == 0.f;
+    P.withhold = sv::withholding();
     P.Hq = num_q_heads;
     P.G = num_q_heads / cache.num_heads;
     P.window = window;

@@ -142,6 +142,7 @@ static std::atomic<cudaEvent_t> g_phase_start{nullptr}, g_phase_end{nullptr};
 // Testing aid (sv_set_test_withhold): process-wide; while set, every stream kernel withholds
 // one work unit so that its bounded waits run out.
 static std::atomic<bool> g_withhold{false};
+bool withholding() { return g_withhold.load(); }
 
 }  // namespace sv
 

@@ -16,6 +16,9 @@ struct LaunchOpts {
     cudaEvent_t ph0, ph1;    // measurement aid: recorded around the stream kernel when set
 };
 
+// Testing aid (sv_set_test_withhold): kernels with bounded waits withhold one unit while it is set.
+bool withholding();
+
 // The one-pass call: the stream and select kernels for 16-byte aligned rows (vec) that they can
 // hold, else the row kernel.  Returns the launch status.
 cudaError_t launch_onepass_bf16(const Args &A, cudaStream_t stream, const LaunchOpts &o, bool vec, bool qvec);
