@@ -11,9 +11,11 @@
 // and the products run on the tensor cores whatever M is: the padded rows cost nothing that the
 // load of a key tile (64 KB, 1.5 us of one SM's share of the memory) does not hide.
 //
-// Work.  The unit of work is one key tile of one (request, key head, row tile).  All units of the
+// Work.  The unit of work is one key tile of one (key head, request, row tile).  All units of the
 // batch, in that order, are cut into one equal range per CTA, from the lengths on the device: ragged
-// batches, one long request and windows need no other schedule.  A row tile whose keys lie in several
+// batches, one long request and windows need no other schedule.  Heads come first so that the heads of
+// a request run at the same time, CTAs / heads apart: where they lie beside each other in a token's
+// row and are not whole 128-byte lines wide, the lines that two of them share are then read once.  A row tile whose keys lie in several
 // CTAs' ranges leaves a part per CTA in the workspace, and the second kernel joins them in order.
 //
 // A CTA: a front warp that turns the CTA's range into segments (a row tile and its key tiles here) and
@@ -98,9 +100,9 @@ __device__ __forceinline__ Req req_of(const Batch &A, const Cache &C, const Attn
     r.nt = s.n ? r.ns + (s.len + TILE - 1) / TILE - r.w0 : 0;
     return r;
 }
-// A request's cost, in units of a key tile.
-__device__ __forceinline__ long long units_of(const Req &r, int heads, int overhead) {
-    return r.nt ? (long long)(r.nt + overhead) * r.mt * heads : 0;
+// A request's cost per key head, in units of a key tile.
+__device__ __forceinline__ long long units_of(const Req &r, int overhead) {
+    return r.nt ? (long long)(r.nt + overhead) * r.mt : 0;
 }
 
 // A segment, as the front warp hands it out (64 bytes): key tiles [t0, t1) of the nt of row tile m of
@@ -117,6 +119,10 @@ constexpr int SEG_READERS = 11;          // warps that take each of them
 // a / b for a >= 0, b > 0: nearly always in 32 bits, where it takes a tenth of the time.
 __device__ __forceinline__ long long quotient(long long a, int b) {
     return (a >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+__device__ __forceinline__ long long quotient64(long long a, long long b) {
+    return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
 // Whether the row at position pos sees token j.
@@ -273,8 +279,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     // the batch's units, and where this CTA's range begins: prefix sums over the requests, NTHREADS at a
     // time (a batch of up to that many is looked at once)
     long long &start_pre = scan[NW], &start_b = scan[NW + 1];
-    long long T = 0, lo = 0, hi = 0, before = 0;
-    int nc = 0;
+    long long W = 0, T = 0, lo = 0, hi = 0, before = 0;   // units of one key head, of all, and this CTA's range
+    int nc = 0, kvh0 = 0;
     const int cta = blockIdx.x;
     __syncthreads();   // (barriers and flags are set)
 #pragma unroll 1
@@ -285,7 +291,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             const int b = b0 + tid;
             Req r = {};
             if (b < A.B) r = req_of(A, C, P, b);
-            const long long w = units_of(r, C.heads, P.overhead);
+            const long long w = units_of(r, P.overhead);
             long long inc = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -305,18 +311,21 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             before += all;
             if (pass == 0) continue;
             if (b0 == 0) {
-                if (A.B <= NTHREADS) T = all;
+                if (A.B <= NTHREADS) W = all;
+                T = W * C.heads;
                 nc = (int)min((long long)gridDim.x, T);
                 if (cta < nc) {   // [T cta / nc, T (cta + 1) / nc)
                     const long long q = quotient(T, nc);
                     const int rest = (int)(T - q * nc);
                     lo = q * cta + rest * cta / nc;
                     hi = q * (cta + 1) + rest * (cta + 1) / nc;
+                    if (lo < hi) kvh0 = (int)quotient64(lo, W);
                 }
             }
-            if (lo < hi && pre <= lo && lo < pre + w) start_b = b, start_pre = pre;
+            const long long at = lo - kvh0 * W;
+            if (lo < hi && pre <= at && at < pre + w) start_b = b, start_pre = pre;
         }
-        if (pass == 0) T = before;
+        if (pass == 0) W = before;
         __syncthreads();
     }
     tc_fence_before();
@@ -559,11 +568,13 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         __syncwarp();
     } else {
         // Front: the segments of this CTA's range, in order, and their queries, swizzled as the matrix
-        // instruction reads them.  Requests are looked at 32 at a time, row tiles of one 16 at a time.
+        // instruction reads them.  A lane looks at one of 16 requests at a time.
         uint32_t pushed = 0, issued = 0, done = 0;   // segments handed out, their queries' copies begun, and there
-        long long pos = lo, pre = lo < hi ? start_pre : 0;
-        int b = lo < hi ? (int)start_b : 0, b_base = -32;
+        int kvh = kvh0, b_base = lo < hi ? (int)start_b : 0, m = 0;
+        long long pre = lo < hi ? start_pre : 0;     // units of this head before request b_base
         Req r = {};
+        long long first = 0, sum = 0;                // this lane's request's first unit, all 16's units
+        bool fresh = true;
         Place at{0, 1}, out{0, 0};   // query buffers to fill, and filling
         if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
         __syncwarp();
@@ -580,48 +591,53 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         for (bool more = lo < hi, ended = false; ok;) {
 #pragma unroll 1
             while (ok && more && pushed - done < 12) {
-                if (b - b_base >= 32) {
-                    b_base = b;
-                    r.nt = 0;
-                    if (b + lane < A.B) r = req_of(A, C, P, b + lane);
+                if (fresh) {
+                    r.nt = r.mt = 0;
+                    if (lane < 16 && b_base + lane < A.B) r = req_of(A, C, P, b_base + lane);
+                    const long long w = units_of(r, P.overhead);
+                    sum = w;
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) {
+                        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                        if (lane >= o) sum += y;
+                    }
+                    first = kvh * W + pre + sum - w;
+                    sum = __shfl_sync(0xffffffffu, sum, 15);
+                    m = 0;
+                    fresh = false;
                 }
-                const int i = b - b_base;
+                // row tile m of each of them, as far as it lies in [lo, hi)
+                const int per = r.nt + P.overhead;
+                const long long mine = first + (long long)m * per;
                 Seg s;
-                s.row0 = __shfl_sync(0xffffffffu, r.row0, i), s.n = __shfl_sync(0xffffffffu, r.n, i);
-                s.len = __shfl_sync(0xffffffffu, r.len, i), s.M = __shfl_sync(0xffffffffu, r.M, i);
-                s.lo = __shfl_sync(0xffffffffu, r.lo, i), s.w0 = __shfl_sync(0xffffffffu, r.w0, i);
-                s.ns = __shfl_sync(0xffffffffu, r.ns, i), s.nt = __shfl_sync(0xffffffffu, r.nt, i);
-                const int mt = __shfl_sync(0xffffffffu, r.mt, i), per = s.nt + P.overhead, all = mt * C.heads;
-                if (s.nt) {
-                    const int u0 = (int)quotient(pos - pre, per);
-                    const int u1 = min(min(all, u0 + 16), (int)min((long long)all, quotient(hi - pre + per - 1, per)));
-                    const int u = u0 + lane;
-                    const long long first = pre + (long long)u * per;   // the row tile's first unit
-                    s.b = b;
-                    s.kvh = u / mt;
-                    s.m = u - s.kvh * mt;
-                    s.t0 = (int)max(lo - first - P.overhead, 0ll);
-                    s.t1 = (int)min((long long)per, hi - first) - P.overhead;
-                    const bool any = u < u1 && s.t1 > s.t0;   // (else nothing, or the overhead alone)
-                    const uint32_t mask = __ballot_sync(0xffffffffu, any);
-                    if (any) {
-                        ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
-                        if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
-                            const long long last = first + P.overhead + s.nt;
-                            P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
-                        }
+                s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
+                s.b = b_base + lane;
+                s.kvh = kvh;
+                s.m = m;
+                s.t0 = (int)max(lo - mine - P.overhead, 0ll);
+                s.t1 = (int)min((long long)per, hi - mine) - P.overhead;
+                const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
+                const uint32_t mask = __ballot_sync(0xffffffffu, any);
+                if (any) {
+                    ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
+                    if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
+                        const long long last = mine + per;
+                        P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
                     }
-                    ok = __all_sync(0xffffffffu, ok);
-                    pushed += __popc(mask);
-                    pos = pre + (long long)u1 * per;
-                    if (u1 < all) {
-                        more = pos < hi;
-                        continue;
-                    }
-                    pre = pos;
                 }
-                b++;
-                more = pos < hi && b < A.B;
+                ok = __all_sync(0xffffffffu, ok);
+                pushed += __popc(mask);
+                if (__any_sync(0xffffffffu, ++m < r.mt)) continue;
+                fresh = true;
+                pre += sum;
+                b_base += 16;
+                more = kvh * W + pre < hi;
+                if (b_base >= A.B) {
+                    kvh++;
+                    b_base = 0;
+                    pre = 0;
+                    more = kvh * W < hi;
+                }
             }
             if (!more && !ended && ok) {
                 Seg s = {};
@@ -1176,6 +1192,8 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     const long long most = (long long)A.B * C.heads * (((long long)(A.k_max + 1) * P.G + 2 * TILE - 1) / (2 * TILE)) *
                            ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + P.overhead);
     int ctas = nsm < MAX_CTAS ? nsm : MAX_CTAS;
+    // heads that share lines keep step only if each has a whole number of CTAs: worth up to 5 % of them
+    if (C.D * 2 % 128 && cache.head_stride * 2 % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas) ctas -= ctas % C.heads;
     if (most < ctas) ctas = (int)most;
     if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SV_ERR_CUDA;
