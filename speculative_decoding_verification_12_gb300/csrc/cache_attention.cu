@@ -857,6 +857,11 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 }
                 any_tile = true;
             }
+            // (what the epilogue needs of the segment, while the last product runs)
+            const int rr = all.m * 2 * TILE + rt, tok = pos - all.len + all.n;
+            const bool direct = all.t0 == 0 && all.t1 == all.nt;
+            const int slot = 2 * cta + (all.t0 > 0 ? 0 : 1);
+            const int64_t orow = (int64_t)(all.row0 + tok) * Hq + all.kvh * P.G + rr - tok * P.G;
             if (ok) ok = warp_wait(o_done + 8 * g, APART ? (ns_ - 1) & 1 : parts & 1, dead);
             parts++;
             if (APART && ok && (warp & 3) == 0 && lane == 0) {
@@ -896,9 +901,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 if (!ok) break;
                 if (g) continue;
             }
-            const int rr = all.m * 2 * TILE + rt, tok = pos - all.len + all.n;
             const bool patch = patched[seg & 3] == seg || patched[4 + (seg & 3)] == seg, broken = bad[seg & 15] == seg + 1;
-            const bool direct = all.t0 == 0 && all.t1 == all.nt;
             if (warp_on) {
                 // the part's maximum and sum, and the factors of the (up to) two sums O
                 float f0 = 1.f, f1 = 0.f;
@@ -914,9 +917,6 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 f0 *= inv;
                 f1 *= inv;
                 const float lse2 = l == 0.f ? -INFINITY : m * P.c + lg2(l) - BIAS;
-                const int slot = 2 * cta + (all.t0 > 0 ? 0 : 1);
-                const int head = all.kvh * P.G + rr - tok * P.G;
-                const int64_t orow = (int64_t)(all.row0 + tok) * Hq + head;
                 const uint32_t t0_ = pair ? t_o : t_o + g * TILE;
                 const bool halves = pair && !few;
                 const int c0 = halves ? g * (DP / 2) : 0, c1 = min(D, halves ? c0 + DP / 2 : DP);
