@@ -54,7 +54,7 @@ struct AttnArgs {
     float *part_o;     // workspace, [2 * MAX_CTAS][PART_ROWS][DP]
     float c;           // |scale| log2(e)
     int negative, zero;   // scale < 0, scale == 0
-    int withhold;         // testing aid: the last CTA never loads its first K tile
+    int withhold;         // testing aid: no CTA loads its first K tile
     int Hq, G, window, sinks;
     int k_stages, v_stages;
     int overhead;      // cost of a row tile beside its key tiles, in key tiles
@@ -114,6 +114,7 @@ struct __align__(16) Seg {
     __device__ __forceinline__ bool two() const { return M > TILE; }
 };
 constexpr int SEGS = 32;                 // segments in flight between the front warp and the others
+constexpr int SMALL_BATCH = 16;          // requests that the front warp looks at together
 constexpr int SEG_READERS = 11;          // warps that take each of them
 
 // a / b for a >= 0, b > 0: nearly always in 32 bits, where it takes a tenth of the time.
@@ -276,57 +277,63 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     if (warp == W_MMA) tmem_alloc(smem_addr(ctl + 1), 512);
     grid_wait();   // the work before this on the stream may still be writing what follows
 
-    // the batch's units, and where this CTA's range begins: prefix sums over the requests, NTHREADS at a
-    // time (a batch of up to that many is looked at once)
+    // The batch's units, and where this CTA's range begins: prefix sums over the requests, NTHREADS at a
+    // time (a batch of up to that many is looked at once).  Only the front warp needs them, and finds those
+    // of a small batch by itself, a request a lane.
     long long &start_pre = scan[NW], &start_b = scan[NW + 1];
     long long W = 0, T = 0, lo = 0, hi = 0, before = 0;   // units of one key head, of all, and this CTA's range
     int nc = 0, kvh0 = 0;
     const int cta = blockIdx.x;
-    __syncthreads();   // (barriers and flags are set)
-#pragma unroll 1
-    for (int pass = A.B <= NTHREADS; pass < 2; pass++) {   // pass 0 sums, pass 1 finds
-        before = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < A.B; b0 += NTHREADS) {
-            const int b = b0 + tid;
-            Req r = {};
-            if (b < A.B) r = req_of(A, C, P, b);
-            const long long w = units_of(r, P.overhead);
-            long long inc = w;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            if (b0) __syncthreads();
-            if (lane == 31) scan[warp] = inc;
-            __syncthreads();
-            long long pre = before + inc - w, all = 0;
-#pragma unroll
-            for (int i = 0; i < NW; i++) {
-                const long long x = scan[i];
-                if (i < warp) pre += x;
-                all += x;
-            }
-            before += all;
-            if (pass == 0) continue;
-            if (b0 == 0) {
-                if (A.B <= NTHREADS) W = all;
-                T = W * C.heads;
-                nc = (int)min((long long)gridDim.x, T);
-                if (cta < nc) {   // [T cta / nc, T (cta + 1) / nc)
-                    const long long q = quotient(T, nc);
-                    const int rest = (int)(T - q * nc);
-                    lo = q * cta + rest * cta / nc;
-                    hi = q * (cta + 1) + rest * (cta + 1) / nc;
-                    if (lo < hi) kvh0 = (int)quotient64(lo, W);
-                }
-            }
-            const long long at = lo - kvh0 * W;
-            if (lo < hi && pre <= at && at < pre + w) start_b = b, start_pre = pre;
+    auto range = [&]() {   // [T cta / nc, T (cta + 1) / nc), and the head that it begins in
+        T = W * C.heads;
+        nc = (int)min((long long)gridDim.x, T);
+        if (cta < nc) {
+            const long long q = quotient(T, nc);
+            const int rest = (int)(T - q * nc);
+            lo = q * cta + rest * cta / nc;
+            hi = q * (cta + 1) + rest * (cta + 1) / nc;
+            if (lo < hi) kvh0 = (int)quotient64(lo, W);
         }
-        if (pass == 0) W = before;
-        __syncthreads();
+    };
+    if (A.B > SMALL_BATCH) {
+        __syncthreads();   // (barriers and flags are set)
+#pragma unroll 1
+        for (int pass = A.B <= NTHREADS; pass < 2; pass++) {   // pass 0 sums, pass 1 finds
+            before = 0;
+#pragma unroll 1
+            for (int b0 = 0; b0 < A.B; b0 += NTHREADS) {
+                const int b = b0 + tid;
+                Req r = {};
+                if (b < A.B) r = req_of(A, C, P, b);
+                const long long w = units_of(r, P.overhead);
+                long long inc = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                if (b0) __syncthreads();
+                if (lane == 31) scan[warp] = inc;
+                __syncthreads();
+                long long pre = before + inc - w, all = 0;
+#pragma unroll
+                for (int i = 0; i < NW; i++) {
+                    const long long x = scan[i];
+                    if (i < warp) pre += x;
+                    all += x;
+                }
+                before += all;
+                if (pass == 0) continue;
+                if (b0 == 0) {
+                    if (A.B <= NTHREADS) W = all;
+                    range();
+                }
+                const long long at = lo - kvh0 * W;
+                if (lo < hi && pre <= at && at < pre + w) start_b = b, start_pre = pre;
+            }
+            if (pass == 0) W = before;
+            __syncthreads();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -380,310 +387,318 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     };
 
     if (warp >= 8) {
-    regs_down<88>();   // to the softmax warps: 2 x 208 + 88 = 3 x 168
-    if (warp == W_K || warp == W_V) {
-        // Keys, or values, of each segment's tiles.
-        const bool is_v = warp == W_V;
-        const CUtensorMap *const map = is_v ? &map_v : &map_k;
-        const uint32_t ring = smem_addr(is_v ? v_p : k_p), full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty,
-                       stages = is_v ? v_stages : k_stages;
-        Seg s;
-        const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
-        const int sub = lane & (npg - 1), lane_tile = lane / npg;
-        Place at{0, 1};   // the first round finds every stage empty
-        uint32_t loads = 0;
-        for (int seg = 0; ok && take(seg, s, true); seg++) {
-            // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
-            // serves several tiles, and is issued that many tiles ahead of its use
-            const int32_t *table = C.table + (int64_t)s.b * C.max_pages;
-            auto fetch = [&](int t) {
-                t += lane_tile;
-                const int j = s.base(t) + sub * box;
-                if (t >= s.t1 || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
-                return (int)min((uint32_t)__ldg(table + (j >> C.page_shift)), (uint32_t)C.num_pages);   // (num_pages: not a page)
-            };
-            int ids = -1, ahead = fetch(s.t0), t_ids = s.t0 - tpl;
-#pragma unroll 1
-            for (int t = s.t0; t < s.t1; t++) {
-                if (t == t_ids + tpl) {
-                    ids = ahead;
-                    t_ids = t;
-                    ahead = fetch(t + tpl);
-                }
-                // this lane's page of tile t (lanes below npg), or -1
-                int id = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
-                if (lane >= npg) id = -1;
-                if (id == C.num_pages) {
-                    bad[seg & 15] = seg + 1;
-                    record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
-                    id = -1;
-                }
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128 * NB;
-                __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
-                ok = warp_wait(empty + 8 * at.stage, at.parity, dead);
-                if (!ok) break;
-                if (P.withhold && cta == nc - 1 && !is_v && loads == 0) {   // (its waits then run out, as they are meant to)
-                    ok = false;
-                    break;
-                }
-                loads++;
-                if (lane == 0) mbar_expect(full + 8 * at.stage, bytes);
-                __syncwarp();
-                if (id >= 0) {
-                    const uint32_t dst = ring + at.stage * STAGE + sub * box * 128;
-                    for (int blk = 0; blk < NB; blk++)
-                        tma_load_4d(dst + blk * BLK, map, full + 8 * at.stage, blk * 64, s.base(t) & (P_ - 1) & ~(box - 1),
-                                    s.kvh, id);
-                }
-                __syncwarp();
-                at.advance(stages);
-            }
-        }
-        if (!ok) {   // let the copies in flight land before the CTA may end
-            const uint32_t t0 = now_ns32();
-            for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
-                while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
-        }
-    } else if (APART && warp == W_MMA) {
-        // Scores, with P apart: each as soon as its group has the last ones in registers.
-        const bool leader = elect();
-        Place ks{0, 0}, qs{0, 0};
-        uint32_t g = 0, nf = 3;   // the group whose turn it is; parities of each one's free S
-        Seg s;
-        for (int seg = 0; ok && take(seg, s, true); seg++) {
-            const int two = s.two(), nv = (s.t1 - s.t0) << two;
-            ok = warp_wait(q_full + 8 * qs.stage, qs.parity, dead);
-#pragma unroll 1
-            for (int v = 0; ok && v < nv; v++) {
-                ok = warp_wait(s_free + 8 * g, nf >> g & 1, dead) && warp_wait(k_full + 8 * ks.stage, ks.parity, dead);
-                if (!ok) break;
-                tc_fence_after();
-                if (leader) {
-                    issue_s(g, two ? v & 1 : qs.stage, ks.stage, g && s.M <= FEW_ROWS);
-                    mma_commit(s_full + 8 * g);
-                    if (v == nv - 1) mma_commit(q_empty + 8 * qs.stage);
-                }
-                __syncwarp();
-                nf ^= 1u << g;
-                g ^= 1;
-                if (!two || (v & 1)) ks.advance(k_stages);
-            }
-            qs.advance(q_bufs);
-        }
-        if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
-            if (leader) mma_commit(drained);
-            const uint32_t t0 = now_ns32();
-            while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
-        }
-        __syncwarp();
-    } else if (warp == W_MMA) {
-        // Matrix instructions, with P over S.  Over all segments the row tiles' products come in one
-        // sequence: tile v of a segment, or, with two row tiles, row tile v & 1 of key tile v >> 1.  The
-        // groups take it in turn, S runs two ahead of P V, and so the next segment's scores are ready
-        // while this one's last tiles are still with the groups.  The whole warp runs this; one lane
-        // issues.  The path from a group's weights to its next scores is the kernel's longest chain, so
-        // P V and that S are issued together, the commits after both.  A commit costs the issuing lane
-        // 70 to 140 cycles: there are two a product, S is there (the softmax group then frees the K tile)
-        // and the V tile is free.  A group learns of its last product of a segment by o_done; earlier
-        // ones are complete when a later S is.
-        const bool leader = elect();
-        int sseg = 0, oseg = 0;                                     // segments opened
-        int sv = 0, snv = 0, stwo = 0, ov = 0, onv = 0, otwo = 0;   // product, products and kind of the current ones
-        auto open = [&](int &k, int &v, int &nv, int &two, bool release) {
+        regs_down<88>();   // to the softmax warps: 2 x 208 + 88 = 3 x 168
+        if (warp == W_K || warp == W_V) {
+            // Keys, or values, of each segment's tiles.
+            const bool is_v = warp == W_V;
+            const CUtensorMap *const map = is_v ? &map_v : &map_k;
+            const uint32_t ring = smem_addr(is_v ? v_p : k_p), full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty,
+                           stages = is_v ? v_stages : k_stages;
             Seg s;
-            v = nv = 0;
-            if (!take(k++, s, release)) return;
-            two = s.two();
-            nv = (s.t1 - s.t0) << two;
-        };
-        open(sseg, sv, snv, stwo, false);
-        if (ok) open(oseg, ov, onv, otwo, true);
-        Place ks{0, 0}, vs{0, 0}, qs{0, 0};
-        uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each one's next P
-        int lead = 0;                      // products whose S, but not P V, is issued: at most 2
-        uint32_t polls = 0, idle_since = 0;
+            const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
+            const int sub = lane & (npg - 1), lane_tile = lane / npg;
+            Place at{0, 1};   // the first round finds every stage empty
+            uint32_t loads = 0;
+            for (int seg = 0; ok && take(seg, s, true); seg++) {
+                // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
+                // serves several tiles, and is issued that many tiles ahead of its use
+                const int32_t *table = C.table + (int64_t)s.b * C.max_pages;
+                auto fetch = [&](int t) {
+                    t += lane_tile;
+                    const int j = s.base(t) + sub * box;
+                    if (t >= s.t1 || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
+                    return (int)min((uint32_t)__ldg(table + (j >> C.page_shift)), (uint32_t)C.num_pages);   // (num_pages: not a page)
+                };
+                int ids = -1, ahead = fetch(s.t0), t_ids = s.t0 - tpl;
 #pragma unroll 1
-        while (ok && onv) {
-            // all that may be waited for is asked at once; every lane has to have seen it
-            uint32_t there = 0;
-            if (snv) {   // the next S: its queries and its keys
-                there = sv || mbar_test(q_full + 8 * qs.stage, qs.parity);
-                there |= (uint32_t)mbar_test(k_full + 8 * ks.stage, ks.parity) << 1;
-            }
-            if (lead) {
-                there |= (uint32_t)mbar_test(p_full + 8 * go, np >> go & 1) << 2;
-                there |= (uint32_t)mbar_test(v_full + 8 * vs.stage, vs.parity) << 3;
-            }
-            there = __reduce_and_sync(0xffffffffu, there);
-            const bool do_o = there >> 2 == 3, do_s = (there & 3) == 3 && (lead < 2 || do_o);
-            if (!do_o && !do_s) {
-                if (++polls & 255) continue;
-                const uint32_t now = now_ns32() | 1;
-                if (!idle_since) idle_since = now;
-                const bool late = *dead || now - idle_since > WAIT_NS;
-                if (__any_sync(0xffffffffu, late)) {
-                    *dead = 1;
-                    ok = false;
+                for (int t = s.t0; t < s.t1; t++) {
+                    if (t == t_ids + tpl) {
+                        ids = ahead;
+                        t_ids = t;
+                        ahead = fetch(t + tpl);
+                    }
+                    // this lane's page of tile t (lanes below npg), or -1
+                    int id = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
+                    if (lane >= npg) id = -1;
+                    if (id == C.num_pages) {
+                        bad[seg & 15] = seg + 1;
+                        record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
+                        id = -1;
+                    }
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128 * NB;
+                    __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
+                    ok = warp_wait(empty + 8 * at.stage, at.parity, dead);
+                    if (!ok) break;
+                    if (P.withhold && !is_v && loads == 0) {   // (its waits then run out, as they are meant to)
+                        ok = false;
+                        break;
+                    }
+                    loads++;
+                    if (lane == 0) mbar_expect(full + 8 * at.stage, bytes);
+                    __syncwarp();
+                    if (id >= 0) {
+                        const uint32_t dst = ring + at.stage * STAGE + sub * box * 128;
+                        for (int blk = 0; blk < NB; blk++)
+                            tma_load_4d(dst + blk * BLK, map, full + 8 * at.stage, blk * 64, s.base(t) & (P_ - 1) & ~(box - 1),
+                                        s.kvh, id);
+                    }
+                    __syncwarp();
+                    at.advance(stages);
                 }
-                continue;
             }
-            idle_since = 0;
-            tc_fence_after();
-            const bool last_use = !otwo || (ov & 1);
-            if (leader) {
-                if (do_o) issue_o(go, vs.stage, ov >= 2);
-                if (do_s) {
-                    issue_s(gs, stwo ? sv & 1 : qs.stage, ks.stage, false);
-                    mma_commit(s_full + 8 * gs);
-                    if (sv == snv - 1) mma_commit(q_empty + 8 * qs.stage);
+            if (!ok) {   // let the copies in flight land before the CTA may end
+                const uint32_t t0 = now_ns32();
+                for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
+                    while (!mbar_try(full + 8 * (i % stages), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+            }
+        } else if (APART && warp == W_MMA) {
+            // Scores, with P apart: each as soon as its group has the last ones in registers.
+            const bool leader = elect();
+            Place ks{0, 0}, qs{0, 0};
+            uint32_t g = 0, nf = 3;   // the group whose turn it is; parities of each one's free S
+            Seg s;
+            for (int seg = 0; ok && take(seg, s, true); seg++) {
+                const int two = s.two(), nv = (s.t1 - s.t0) << two;
+                ok = warp_wait(q_full + 8 * qs.stage, qs.parity, dead);
+#pragma unroll 1
+                for (int v = 0; ok && v < nv; v++) {
+                    ok = warp_wait(s_free + 8 * g, nf >> g & 1, dead) && warp_wait(k_full + 8 * ks.stage, ks.parity, dead);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        issue_s(g, two ? v & 1 : qs.stage, ks.stage, g && s.M <= FEW_ROWS);
+                        mma_commit(s_full + 8 * g);
+                        if (v == nv - 1) mma_commit(q_empty + 8 * qs.stage);
+                    }
+                    __syncwarp();
+                    nf ^= 1u << g;
+                    g ^= 1;
+                    if (!two || (v & 1)) ks.advance(k_stages);
                 }
-                if (do_o) {
-                    if (last_use) mma_commit(v_empty + 8 * vs.stage);
-                    if (ov >= onv - 2) mma_commit(o_done + 8 * go);
-                }
+                qs.advance(q_bufs);
+            }
+            if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
+                if (leader) mma_commit(drained);
+                const uint32_t t0 = now_ns32();
+                while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
             }
             __syncwarp();
-            if (do_o) {
-                if (last_use) vs.advance(v_stages);
-                np ^= 1u << go;
-                go ^= 1;
-                lead--;
-                if (++ov == onv) open(oseg, ov, onv, otwo, true);
-            }
-            if (do_s && ok) {
-                if (!stwo || (sv & 1)) ks.advance(k_stages);
-                gs ^= 1;
-                lead++;
-                if (++sv == snv) {
-                    qs.advance(q_bufs);
-                    open(sseg, sv, snv, stwo, false);
-                }
-            }
-        }
-        if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
-            if (leader) mma_commit(drained);
-            const uint32_t t0 = now_ns32();
-            while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
-        }
-        __syncwarp();
-    } else {
-        // Front: the segments of this CTA's range, in order, and their queries, swizzled as the matrix
-        // instruction reads them.  A lane looks at one of 16 requests at a time.
-        uint32_t pushed = 0, issued = 0, done = 0;   // segments handed out, their queries' copies begun, and there
-        int kvh = kvh0, b_base = lo < hi ? (int)start_b : 0, m = 0;
-        long long pre = lo < hi ? start_pre : 0;     // units of this head before request b_base
-        Req r = {};
-        long long first = 0, sum = 0;                // this lane's request's first unit, all 16's units
-        bool fresh = true;
-        Place at{0, 1}, out{0, 0};   // query buffers to fill, and filling
-        if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
-        __syncwarp();
-        auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
-            const uint32_t slot = k & (SEGS - 1);
-            const bool free = mbar_wait(seg_empty + 8 * slot, (k / SEGS & 1) ^ 1, dead);
-            if (free) {
-                segs[slot] = s;
-                mbar_arrive(seg_full + 8 * slot);
-            }
-            return free;
-        };
-#pragma unroll 1
-        for (bool more = lo < hi, ended = false; ok;) {
-#pragma unroll 1
-            while (ok && more && pushed - done < 12) {
-                if (fresh) {
-                    r.nt = r.mt = 0;
-                    if (lane < 16 && b_base + lane < A.B) r = req_of(A, C, P, b_base + lane);
-                    const long long w = units_of(r, P.overhead);
-                    sum = w;
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) {
-                        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-                        if (lane >= o) sum += y;
-                    }
-                    first = kvh * W + pre + sum - w;
-                    sum = __shfl_sync(0xffffffffu, sum, 15);
-                    m = 0;
-                    fresh = false;
-                }
-                // row tile m of each of them, as far as it lies in [lo, hi)
-                const int per = r.nt + P.overhead;
-                const long long mine = first + (long long)m * per;
+        } else if (warp == W_MMA) {
+            // Matrix instructions, with P over S.  Over all segments the row tiles' products come in one
+            // sequence: tile v of a segment, or, with two row tiles, row tile v & 1 of key tile v >> 1.  The
+            // groups take it in turn, S runs two ahead of P V, and so the next segment's scores are ready
+            // while this one's last tiles are still with the groups.  The whole warp runs this; one lane
+            // issues.  The path from a group's weights to its next scores is the kernel's longest chain, so
+            // P V and that S are issued together, the commits after both.  A commit costs the issuing lane
+            // 70 to 140 cycles: there are two a product, S is there (the softmax group then frees the K tile)
+            // and the V tile is free.  A group learns of its last product of a segment by o_done; earlier
+            // ones are complete when a later S is.
+            const bool leader = elect();
+            int sseg = 0, oseg = 0;                                     // segments opened
+            int sv = 0, snv = 0, stwo = 0, ov = 0, onv = 0, otwo = 0;   // product, products and kind of the current ones
+            auto open = [&](int &k, int &v, int &nv, int &two, bool release) {
                 Seg s;
-                s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
-                s.b = b_base + lane;
-                s.kvh = kvh;
-                s.m = m;
-                s.t0 = (int)max(lo - mine - P.overhead, 0ll);
-                s.t1 = (int)min((long long)per, hi - mine) - P.overhead;
-                const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
-                const uint32_t mask = __ballot_sync(0xffffffffu, any);
-                if (any) {
-                    ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
-                    if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
-                        const long long last = mine + per;
-                        P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
+                v = nv = 0;
+                if (!take(k++, s, release)) return;
+                two = s.two();
+                nv = (s.t1 - s.t0) << two;
+            };
+            open(sseg, sv, snv, stwo, false);
+            if (ok) open(oseg, ov, onv, otwo, true);
+            Place ks{0, 0}, vs{0, 0}, qs{0, 0};
+            uint32_t gs = 0, go = 0, np = 0;   // groups whose turn it is; parity of each one's next P
+            int lead = 0;                      // products whose S, but not P V, is issued: at most 2
+            uint32_t polls = 0, idle_since = 0;
+#pragma unroll 1
+            while (ok && onv) {
+                // all that may be waited for is asked at once; every lane has to have seen it
+                uint32_t there = 0;
+                if (snv) {   // the next S: its queries and its keys
+                    there = sv || mbar_test(q_full + 8 * qs.stage, qs.parity);
+                    there |= (uint32_t)mbar_test(k_full + 8 * ks.stage, ks.parity) << 1;
+                }
+                if (lead) {
+                    there |= (uint32_t)mbar_test(p_full + 8 * go, np >> go & 1) << 2;
+                    there |= (uint32_t)mbar_test(v_full + 8 * vs.stage, vs.parity) << 3;
+                }
+                there = __reduce_and_sync(0xffffffffu, there);
+                const bool do_o = there >> 2 == 3, do_s = (there & 3) == 3 && (lead < 2 || do_o);
+                if (!do_o && !do_s) {
+                    if (++polls & 255) continue;
+                    const uint32_t now = now_ns32() | 1;
+                    if (!idle_since) idle_since = now;
+                    const bool late = *dead || now - idle_since > WAIT_NS;
+                    if (__any_sync(0xffffffffu, late)) {
+                        *dead = 1;
+                        ok = false;
+                    }
+                    continue;
+                }
+                idle_since = 0;
+                tc_fence_after();
+                const bool last_use = !otwo || (ov & 1);
+                if (leader) {
+                    if (do_o) issue_o(go, vs.stage, ov >= 2);
+                    if (do_s) {
+                        issue_s(gs, stwo ? sv & 1 : qs.stage, ks.stage, false);
+                        mma_commit(s_full + 8 * gs);
+                        if (sv == snv - 1) mma_commit(q_empty + 8 * qs.stage);
+                    }
+                    if (do_o) {
+                        if (last_use) mma_commit(v_empty + 8 * vs.stage);
+                        if (ov >= onv - 2) mma_commit(o_done + 8 * go);
                     }
                 }
-                ok = __all_sync(0xffffffffu, ok);
-                pushed += __popc(mask);
-                if (__any_sync(0xffffffffu, ++m < r.mt)) continue;
-                fresh = true;
-                pre += sum;
-                b_base += 16;
-                more = kvh * W + pre < hi;
-                if (b_base >= A.B) {
-                    kvh++;
-                    b_base = 0;
-                    pre = 0;
-                    more = kvh * W < hi;
-                }
-            }
-            if (!more && !ended && ok) {
-                Seg s = {};
-                if (lane == 0) ok = push(pushed, s);
-                ok = __all_sync(0xffffffffu, ok);
-                ended = true;
-            }
-            if (!ok) break;
-            // two segments' copies under way where there are buffers; else finish the older one first
-            const bool room = issued < pushed && issued - done < min(q_bufs, 2u);
-            if (room && (done == issued ? warp_wait(q_empty + 8 * at.stage, at.parity, dead)
-                                        : warp_try(q_empty + 8 * at.stage, at.parity))) {
-                const Seg &s = segs[issued & (SEGS - 1)];   // (not written again before its queries are there)
-                const int row0 = s.m * 2 * TILE, rows = min(s.M - row0, 2 * TILE);
-                const bool two = s.two();
-                constexpr int CH = DP / 8, RPW = 32 / CH;   // 16-byte pieces of a row, rows per warp step
-                const int ch = lane % CH;
-                int row = lane / CH, tok = (row0 + row) / P.G, head = row0 + row - tok * P.G;
-                const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + (ch * 8 < C.D ? ch * 8 : 0);
-                const uint32_t bytes = ch * 8 < C.D && !P.zero ? 16 : 0;
-                const uint32_t base = smem_addr(q_p) + (two ? 0 : at.stage) * q_buffer + (ch >> 3) * q_block;
-#pragma unroll 2
-                for (; row < rows; row += RPW) {
-                    copy16(base + (row >> 7) * q_buffer + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                           q + tok * P.q_stride + (int64_t)head * C.D, bytes);
-                    head += RPW;
-                    while (head >= P.G) head -= P.G, tok++;
-                }
-                copies_commit();
-                issued++;
-                at.advance(q_bufs);
-            } else if (done < issued) {
-                if (issued - done == 2) copies_wait<1>();
-                else copies_wait<0>();
-                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full + 8 * out.stage);
-                done++;
-                out.advance(q_bufs);
-            } else {
-                if (room) ok = false;   // the wait ran out
-                break;                  // (nothing is left)
+                if (do_o) {
+                    if (last_use) vs.advance(v_stages);
+                    np ^= 1u << go;
+                    go ^= 1;
+                    lead--;
+                    if (++ov == onv) open(oseg, ov, onv, otwo, true);
+                }
+                if (do_s && ok) {
+                    if (!stwo || (sv & 1)) ks.advance(k_stages);
+                    gs ^= 1;
+                    lead++;
+                    if (++sv == snv) {
+                        qs.advance(q_bufs);
+                        open(sseg, sv, snv, stwo, false);
+                    }
+                }
             }
+            if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
+                if (leader) mma_commit(drained);
+                const uint32_t t0 = now_ns32();
+                while (!mbar_try(drained, 0) && now_ns32() - t0 < WAIT_NS) {}
+            }
+            __syncwarp();
+        } else {
+            // Front: the segments of this CTA's range, in order, and their queries, swizzled as the matrix
+            // instruction reads them.  A lane looks at one of 16 requests at a time.
+            uint32_t pushed = 0, issued = 0, done = 0;   // segments handed out, their queries' copies begun, and there
+            Req r = {};
+            long long first = 0, sum = 0;                // this lane's request's first unit, all 16's units
+            bool fresh = true;
+            auto look = [&](int b) {                     // at requests b .. b + 15: first and sum from this head's start
+                r.nt = r.mt = 0;
+                if (lane < SMALL_BATCH && b + lane < A.B) r = req_of(A, C, P, b + lane);
+                const long long w = units_of(r, P.overhead);
+                sum = w;
+#pragma unroll
+                for (int o = 1; o < SMALL_BATCH; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                first = sum - w;
+                sum = __shfl_sync(0xffffffffu, sum, SMALL_BATCH - 1);
+            };
+            if (A.B <= SMALL_BATCH) {
+                look(0);
+                W = sum;
+                range();
+            }
+            int kvh = kvh0, b_base = A.B > SMALL_BATCH && lo < hi ? (int)start_b : 0, m = 0;
+            long long pre = A.B > SMALL_BATCH && lo < hi ? start_pre : 0;   // units of this head before request b_base
+            Place at{0, 1}, out{0, 0};   // query buffers to fill, and filling
+            if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
+            __syncwarp();
+            auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
+                const uint32_t slot = k & (SEGS - 1);
+                const bool free = mbar_wait(seg_empty + 8 * slot, (k / SEGS & 1) ^ 1, dead);
+                if (free) {
+                    segs[slot] = s;
+                    mbar_arrive(seg_full + 8 * slot);
+                }
+                return free;
+            };
+#pragma unroll 1
+            for (bool more = lo < hi, ended = false; ok;) {
+#pragma unroll 1
+                while (ok && more && pushed - done < 12) {
+                    if (fresh) {
+                        if (A.B > SMALL_BATCH) look(b_base);
+                        m = 0;
+                        fresh = false;
+                    }
+                    // row tile m of each of them, as far as it lies in [lo, hi)
+                    const int per = r.nt + P.overhead;
+                    const long long mine = kvh * W + pre + first + (long long)m * per;
+                    Seg s;
+                    s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
+                    s.b = b_base + lane;
+                    s.kvh = kvh;
+                    s.m = m;
+                    s.t0 = (int)max(lo - mine - P.overhead, 0ll);
+                    s.t1 = (int)min((long long)per, hi - mine) - P.overhead;
+                    const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
+                    const uint32_t mask = __ballot_sync(0xffffffffu, any);
+                    if (any) {
+                        ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
+                        if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
+                            const long long last = mine + per;
+                            P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    pushed += __popc(mask);
+                    if (__any_sync(0xffffffffu, ++m < r.mt)) continue;
+                    fresh = true;
+                    pre += sum;
+                    b_base += SMALL_BATCH;
+                    more = kvh * W + pre < hi;
+                    if (b_base >= A.B) {
+                        kvh++;
+                        b_base = 0;
+                        pre = 0;
+                        more = kvh * W < hi;
+                    }
+                }
+                if (!more && !ended && ok) {
+                    Seg s = {};
+                    if (lane == 0) ok = push(pushed, s);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ended = true;
+                }
+                if (!ok) break;
+                // two segments' copies under way where there are buffers; else finish the older one first
+                const bool room = issued < pushed && issued - done < min(q_bufs, 2u);
+                if (room && (done == issued ? warp_wait(q_empty + 8 * at.stage, at.parity, dead)
+                                            : warp_try(q_empty + 8 * at.stage, at.parity))) {
+                    const Seg &s = segs[issued & (SEGS - 1)];   // (not written again before its queries are there)
+                    const int row0 = s.m * 2 * TILE, rows = min(s.M - row0, 2 * TILE);
+                    const bool two = s.two();
+                    constexpr int CH = DP / 8, RPW = 32 / CH;   // 16-byte pieces of a row, rows per warp step
+                    const int ch = lane % CH;
+                    int row = lane / CH, tok = (row0 + row) / P.G, head = row0 + row - tok * P.G;
+                    const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + (ch * 8 < C.D ? ch * 8 : 0);
+                    const uint32_t bytes = ch * 8 < C.D && !P.zero ? 16 : 0;
+                    const uint32_t base = smem_addr(q_p) + (two ? 0 : at.stage) * q_buffer + (ch >> 3) * q_block;
+#pragma unroll 2
+                    for (; row < rows; row += RPW) {
+                        copy16(base + (row >> 7) * q_buffer + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                               q + tok * P.q_stride + (int64_t)head * C.D, bytes);
+                        head += RPW;
+                        while (head >= P.G) head -= P.G, tok++;
+                    }
+                    copies_commit();
+                    issued++;
+                    at.advance(q_bufs);
+                } else if (done < issued) {
+                    if (issued - done == 2) copies_wait<1>();
+                    else copies_wait<0>();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full + 8 * out.stage);
+                    done++;
+                    out.advance(q_bufs);
+                } else {
+                    if (room) ok = false;   // the wait ran out
+                    break;                  // (nothing is left)
+                }
+            }
+            copies_wait<0>();
         }
-        copies_wait<0>();
-    }
     } else {
         regs_up<208>();
         // Softmax and epilogue: group g, a thread per row.
