@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
             else if (r >= s.row0 && r - s.row0 < s.n) {
                 st = 1;
                 p = s.len - s.n + (r - s.row0);
-                page = __ldg(C.table + (int64_t)b * C.max_pages + (p >> C.page_shift));
+                page = C.table[(int64_t)b * C.max_pages + (p >> C.page_shift)];
                 if (page < 0 || page >= C.num_pages) {
                     record_error(P.hdr, SV_DEV_BAD_PAGE, b);
                     st = 2;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
     if (in && P.qw) qw = take(static_cast<const E *>(P.qw));
     if (in && P.kw) kw = take(static_cast<const E *>(P.kw));
-    const float f = tid < P.half ? __ldg(P.inv_freq + tid) : 0.f;
+    const float f = tid < P.half ? P.inv_freq[tid] : 0.f;
     const uint64_t t = turns_of(f);
     __syncthreads();
 

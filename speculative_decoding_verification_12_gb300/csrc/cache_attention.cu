@@ -15,8 +15,10 @@
 // batch, in that order, are cut into one equal range per CTA, from the lengths on the device: ragged
 // batches, one long request and windows need no other schedule.  Heads come first so that the heads of
 // a request run at the same time, CTAs / heads apart: where they lie beside each other in a token's
-// row and are not whole 128-byte lines wide, the lines that two of them share are then read once.  A row tile whose keys lie in several
-// CTAs' ranges leaves a part per CTA in the workspace, and the second kernel joins them in order.
+// row and are not whole 128-byte lines wide, the lines that two of them share are then read once
+// (64 requests of 4096 keys, 8 heads of 80 columns: 178 us request by request, 123 us).  A row tile
+// whose keys lie in several CTAs' ranges leaves a part per CTA in the workspace, and the second kernel
+// joins them in order.
 //
 // A CTA: a front warp that turns the CTA's range into segments (a row tile and its key tiles here) and
 // loads their queries, a warp for K and one for V (tensor copies of pages into two rings of tiles),
@@ -109,11 +111,14 @@ __device__ __forceinline__ long long units_of(const Req &r, int overhead) {
 // key head kvh of request b.  nt == 0 ends the list.
 struct __align__(16) Seg {
     int row0, n, len, M, lo, w0, ns, nt;   // as in Req
-    int b, kvh, m, t0, t1, pad[3];
+    int b, kvh, m, t0, t1, solo, pad[2];   // solo: one group takes all its tiles
     __device__ __forceinline__ int base(int t) const { return (t < ns ? t : w0 + t - ns) * TILE; }
     __device__ __forceinline__ bool two() const { return M > TILE; }
 };
 constexpr int SEGS = 32;                 // segments in flight between the front warp and the others
+// Narrow heads: key tiles of a segment that one group takes alone.  512 x 8 segments of 3 tiles take 150 us
+// shared and 129 alone; 1024 x 8 of 8 tiles 422 shared and 440 alone (the last one leaves a group idle).
+constexpr int SOLO_TILES = 4;
 constexpr int SMALL_BATCH = 16;          // requests that the front warp looks at together
 constexpr int SEG_READERS = 11;          // warps that take each of them
 
@@ -206,7 +211,7 @@ __device__ __forceinline__ void add_non_finite(const Cache &C, const AttnArgs &P
             if (side && (!P.window || j > s.len - s.n)) break;   // (the causal side has it)
             const int tile = j / TILE, t = tile >= s.w0 ? tile - s.w0 + s.ns : tile;
             if (t < s.t0 || t >= s.t1 || seen_by_all(P, s, j) || !sees(P, pos, j)) continue;
-            const int page = __ldg(C.table + (int64_t)s.b * C.max_pages + (j >> C.page_shift));
+            const int page = C.table[(int64_t)s.b * C.max_pages + (j >> C.page_shift)];
             if (page < 0 || page >= C.num_pages) continue;
             const E *v = static_cast<const E *>(C.v) + page * C.page_stride +
                          (j & ((1 << C.page_shift) - 1)) * C.token_stride + s.kvh * C.head_stride;
@@ -407,7 +412,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     t += lane_tile;
                     const int j = s.base(t) + sub * box;
                     if (t >= s.t1 || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
-                    return (int)min((uint32_t)__ldg(table + (j >> C.page_shift)), (uint32_t)C.num_pages);   // (num_pages: not a page)
+                    return (int)min((uint32_t)table[j >> C.page_shift], (uint32_t)C.num_pages);   // (num_pages: not a page)
                 };
                 int ids = -1, ahead = fetch(s.t0), t_ids = s.t0 - tpl;
 #pragma unroll 1
@@ -472,7 +477,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     }
                     __syncwarp();
                     nf ^= 1u << g;
-                    g ^= 1;
+                    if (!s.solo || v == nv - 1) g ^= 1;
                     if (!two || (v & 1)) ks.advance(k_stages);
                 }
                 qs.advance(q_bufs);
@@ -631,6 +636,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     s.m = m;
                     s.t0 = (int)max(lo - mine - P.overhead, 0ll);
                     s.t1 = (int)min((long long)per, hi - mine) - P.overhead;
+                    // a short segment among others is one group's alone: the groups then work on two segments at
+                    // a time, and neither waits for the other at the end
+                    s.solo = APART && s.M <= TILE && s.t1 - s.t0 <= SOLO_TILES && hi - lo >= 4 * per;
                     const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
                     const uint32_t mask = __ballot_sync(0xffffffffu, any);
                     if (any) {
@@ -716,10 +724,11 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             const bool two = s.two();
             const int mine = (g ^ turn) & 1;      // this group's row tile, or its first key tile
             const uint32_t tile0 = tiles;
-            turn += nt << two;
+            turn += s.solo ? 1 : nt << two;
             tiles += nt;
-            if (!two && mine >= nt) continue;     // a single key tile, and the other group's turn
-            const bool pair = !two && nt > 1;     // both groups hold a part of every row
+            const bool alone = two || s.solo;     // this group's rows are its own
+            if (!two && mine >= (s.solo ? 1 : nt)) continue;   // the other group's turn
+            const bool pair = !alone && nt > 1;   // both groups hold a part of every row
             const bool few = APART && s.M <= FEW_ROWS;
             const int row = lane_row ^ (few && g ? DOWN : 0);
             const int rows = min(s.M - s.m * 2 * TILE, 2 * TILE);   // of this row tile
@@ -730,7 +739,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             float m = -INFINITY, l = 0.f;
             bool any_tile = false;
 #pragma unroll 1
-            for (int t = two ? 0 : mine; t < nt; t += two ? 1 : 2) {
+            for (int t = alone ? 0 : mine; t < nt; t += alone ? 1 : 2) {
                 if (!warp_wait(s_full + 8 * g, ns_++ & 1, dead)) {
                     ok = false;
                     break;
@@ -853,7 +862,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 // the group's last product is through with its weights, which these replace, and its V tile
                 // (two arrivals free a tile: one of each group, or both of the one that used it)
                 if (APART && any_tile && (warp & 3) == 0 && lane == 0)
-                    mbar_arrive(v_empty + 8 * ((tile0 + t - (two ? 1 : 2)) % v_stages), two ? 1 : 2);
+                    mbar_arrive(v_empty + 8 * ((tile0 + t - (alone ? 1 : 2)) % v_stages), two ? 1 : 2);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * g);
@@ -880,7 +889,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             if (ok) ok = warp_wait(o_done + 8 * g, APART ? (ns_ - 1) & 1 : parts & 1, dead);
             parts++;
             if (APART && ok && (warp & 3) == 0 && lane == 0) {
-                const int last = two ? nt - 1 : nt - 1 - ((nt - 1 - mine) & 1);   // this group's last key tile
+                const int last = alone ? nt - 1 : nt - 1 - ((nt - 1 - mine) & 1);   // this group's last key tile
                 mbar_arrive(v_empty + 8 * ((tile0 + last) % v_stages), two ? 1 : 2);
             }
             if (ok && pair) {   // the other group's maxima, sums and O
@@ -1119,7 +1128,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
             if (err) record_error(P.hdr, err, b);
             int end = s.row0 + A.k_max + 1;
             if (A.row_off) {
-                end = __ldg(A.row_off + b + 1);
+                end = A.row_off[b + 1];
                 if (b == 0) head = min(max(s.row0, 0), A.R);                       // rows before the first request
                 if (b == A.B - 1) tail = A.R - min(max(end, 0), A.R);              // and after the last
             }
@@ -1270,7 +1279,8 @@ extern "C" sv_status spec_attention(const void *q, int64_t q_stride, int32_t num
     P.withhold = sv::withholding();
     P.Hq = num_q_heads;
     P.G = num_q_heads / cache.num_heads;
-    P.window = window;
+    // (a window that holds every length is none: differences of positions stay in 32 bits)
+    P.window = window < (cache.max_pages << C.page_shift) ? window : 0;
     P.sinks = sinks;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wide = cache.head_dim > 64;

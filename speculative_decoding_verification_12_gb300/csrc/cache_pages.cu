@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(CT) copy_kernel(const CopyArgs A) {
         int2 x = make_int2(-1, -1);
         if (mine < items) {
             const int i = (int)(mine / per_pair);
-            x = make_int2(__ldg(A.src + i), __ldg(A.dst + i));
+            x = make_int2(A.src[i], A.dst[i]);
             if (x.x < 0 || x.y < 0) {
                 x.x = -1;
             } else if (x.x >= A.num_pages || x.y >= A.num_pages) {

@@ -22,6 +22,8 @@ __device__ __forceinline__ void record_error(int32_t *hdr, int code, int b) {
     atomicMax(hdr + 1, 0x7fffffff - b);
 }
 
+// Everything here is read with plain loads: under a programmatic launch the work before may still be
+// writing it while this grid is already resident, which the read-only path does not allow for.
 struct Batch {
     const int32_t *nd;        // num_drafts
     const int32_t *row_off;   // NULL: uniform layout
@@ -45,15 +47,15 @@ __device__ __forceinline__ Span span_of(const Batch &A, int max_tokens, int b) {
     Span s;
     int owned;
     if (A.row_off) {
-        s.row0 = __ldg(A.row_off + b);
-        const int end = __ldg(A.row_off + b + 1);
+        s.row0 = A.row_off[b];
+        const int end = A.row_off[b + 1];
         owned = (s.row0 >= 0 && end >= s.row0 && end <= A.R) ? end - s.row0 : -1;
     } else {
         s.row0 = b * (A.k_max + 1);
         owned = A.k_max + 1;
     }
-    const int k = __ldg(A.nd + b);
-    s.len = __ldg(A.len + b);
+    const int k = A.nd[b];
+    s.len = A.len[b];
     s.n = k + 1;
     s.err = 0;
     if (k == -1 && owned >= 0) return s;   // idle
@@ -70,10 +72,10 @@ static __device__ __noinline__ int request_of(const Batch &A, int r) {
     int lo = 0, hi = A.B;   // row_off[lo] <= r < row_off[hi], if the offsets are sound
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(A.row_off + mid) <= r) lo = mid;
+        if (A.row_off[mid] <= r) lo = mid;
         else hi = mid;
     }
-    return (__ldg(A.row_off + lo) <= r && r < __ldg(A.row_off + lo + 1)) ? lo : -1;
+    return (A.row_off[lo] <= r && r < A.row_off[lo + 1]) ? lo : -1;
 }
 
 // The request that owns row first + lane, for lanes below `rows` <= 32; -1 for a row that belongs to
@@ -86,12 +88,12 @@ __device__ __forceinline__ int request_of_rows(const Batch &A, int first, int ro
     int lo = 0, hi = A.B;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, i = min(lo + lane * step, hi - 1);
-        const uint32_t m = __ballot_sync(0xffffffffu, __ldg(A.row_off + i) <= first);
+        const uint32_t m = __ballot_sync(0xffffffffu, A.row_off[i] <= first);
         lo = min(lo + (m ? 31 - __clz(m) : 0) * step, hi - 1);
         hi = min(hi, lo + step);
     }
-    const int next = lo + 1 + lane <= A.B ? __ldg(A.row_off + lo + 1 + lane) : 0x7fffffff;
-    bool search = __ldg(A.row_off + lo) > first;
+    const int next = lo + 1 + lane <= A.B ? A.row_off[lo + 1 + lane] : 0x7fffffff;
+    bool search = A.row_off[lo] > first;
     int mine = -1;
     for (int i = 0; i < rows; i++) {
         const int later = __popc(__ballot_sync(0xffffffffu, next <= first + i));
@@ -196,7 +198,9 @@ inline sv_status check_batch(const int32_t *num_drafts, const int32_t *row_offse
     if (c.page_size < 8 || c.page_size > 256 || (c.page_size & (c.page_size - 1))) return SV_ERR_UNSUPPORTED;
     if (c.page_stride % 8 || c.token_stride % 8 || c.head_stride % 8 || !aligned16(c.k) || !aligned16(c.v))
         return SV_ERR_UNSUPPORTED;
-    if ((long long)c.max_pages * c.page_size > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
+    // (a tile past the last token must not overflow; a tensor map's strides have 40 bits)
+    if ((long long)c.max_pages * c.page_size > 0x7ffffe00ll) return SV_ERR_UNSUPPORTED;
+    if ((c.page_stride | c.token_stride | c.head_stride) >> 38) return SV_ERR_UNSUPPORTED;
     batch = Batch{num_drafts, row_offsets, kv_seq_len, B, k_max, total_rows};
     cache.k = c.k;
     cache.v = c.v;

@@ -121,7 +121,7 @@ HEADS = [
     (3, 1, 8, 8, "bf16", "nhd"), (5, 5, 16, 16, "fp16", "both"), (48, 1, 128, 16, "fp16", "nhd"),
     (2, 2, 72, 16, "bf16", "hnd"), (130, 1, 64, 16, "bf16", "nhd"), (1, 1, 128, 8, "bf16", "nhd"),
 ]
-MASKS = [(0, 0), (1, 0), (7, 3), (100, 4), (128, 128), (200, 0), (1 << 30, 5)]
+MASKS = [(0, 0), (1, 0), (7, 3), (100, 4), (128, 128), (200, 0), (1 << 30, 5), (2 ** 31 - 1, 2 ** 31 - 1)]
 
 
 @pytest.mark.parametrize("Hq,Hk,D,page,dtype,layout", HEADS)
@@ -155,6 +155,16 @@ def test_many_rows_with_a_window(sv):
 @pytest.mark.parametrize("L", [4096, 20011, 70001])
 def test_long_contexts(sv, L):
     run_and_check(sv, make(L, [L, 3], [3, 0], 3, 8, 2, 128 if L < 50000 else 64, 16, "bf16" if L < 50000 else "fp16"))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_requests(sv, D):
+    """More requests than one look at the batch takes, of one to five key tiles: segments of one
+    group, of both, and cut between CTAs."""
+    r = random.Random(D)
+    drafts = [r.randint(0, 3) for _ in range(450)]
+    lens = [r.randint(k + 1, 600) for k in drafts]
+    run_and_check(sv, make(37, lens, drafts, 3, 4, 2, D, 32, "bf16"))
 
 
 def test_uneven_batch(sv):
