@@ -113,9 +113,20 @@ struct Used {
     uint32_t head;
     __device__ __forceinline__ void read() {
         head = 0;
-        for (int k = 0; k < 8 && s.lo + 128 * k < s.hi; k++) {
+        if (((uintptr_t)ref & 15) == 0) {   // (slices begin at multiples of 128: the eight loads go out together)
+            int4 w[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                w[k] = page(k) + 4 <= s.hi ? *reinterpret_cast<const int4 *>(ref + page(k)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                head |= (uint32_t)((w[k].x != 0) | (w[k].y != 0) << 1 | (w[k].z != 0) << 2 | (w[k].w != 0) << 3) << (4 * k);
+        }
+#pragma unroll 1
+        for (int k = 0; k < 8 && s.lo + 128 * k < s.hi; k++) {   // the pool's last few pages, or an odd base
             int have;
-            head |= (uint32_t)used4(ref, s.lo + 128 * k + 4 * (int)(threadIdx.x & 31), s.hi, have) << (4 * k);
+            if (((uintptr_t)ref & 15) || (page(k) < s.hi && page(k) + 4 > s.hi))
+                head |= (uint32_t)used4(ref, page(k), s.hi, have) << (4 * k);
         }
     }
     __device__ __forceinline__ int groups() const { return (s.hi - s.lo + 127) / 128; }
@@ -155,9 +166,13 @@ __device__ __forceinline__ T cluster_prefix(T count, T *counts, T *total) {
     return before + counts[warp];
 }
 
-// Writes the lowest `want` free pages to S.list in ascending order and returns how many free
-// pages there are; the list is visible to the whole cluster on return.
-__device__ __forceinline__ int list_free(const PageState &S, const Used &U, long long want, int *counts) {
+constexpr int NEAR = 2048;   // lists up to this stay in the first CTA's shared memory
+
+// Lists the lowest `want` free pages in ascending order -- in the cluster's first CTA's `near` (NEAR
+// entries) if they fit, which saves the fence and the round trip of S.list -- and returns how many free
+// pages there are; the list is there for the first CTA on return.
+__device__ __forceinline__ int list_free(const PageState &S, const Used &U, long long want, int *counts, int *near) {
+    int *const first = cg::this_cluster().map_shared_rank(near, 0);
     const int groups = U.groups();
     int count = 0, have;
     for (int k = 0; k < groups; k++) {
@@ -174,12 +189,12 @@ __device__ __forceinline__ int list_free(const PageState &S, const Used &U, long
 #pragma unroll
         for (int t = 0; t < 4; t++)
             if (f >> t & 1) {
-                if (r < want) S.list[r] = U.page(k) + t;
+                if (r < want) (want <= NEAR ? first : S.list)[r] = U.page(k) + t;
                 r++;
             }
         at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    __threadfence();
+    if (want > NEAR) __threadfence();
     cg::this_cluster().sync();
     return total;
 }
@@ -215,7 +230,7 @@ __device__ __forceinline__ Want want_of(const PageState &S, const int32_t *nd, i
 }
 
 __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const int32_t *nd) {
-    __shared__ int counts[PW + 1];
+    __shared__ int counts[PW + 1], near[NEAR];
     __shared__ long long tmp[PW + 1];
     grid_wait();
     grid_launch_dependents();
@@ -231,8 +246,9 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
     for (int b = threadIdx.x + PT; b < S.B; b += PT) sum += want_of(S, nd, b).need;
     const long long at0 = cta_scan(sum, tmp, &want);   // (of PT requests at most: their places too)
     // (never past the list, whatever the counts say on the second look)
-    const long long free = min((long long)list_free(S, U, want, counts), want);
+    const long long free = min((long long)list_free(S, U, want, counts, near), want);
     if (cg::this_cluster().block_rank() != 0) return;
+    const int32_t *list = want <= NEAR ? near : S.list;
     long long before = 0;
     for (int b0 = 0; b0 < S.B; b0 += PT) {
         const int b = b0 + (int)threadIdx.x;
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
         int32_t *row = S.table + (int64_t)b * S.max_pages + w.have;
         const int small = w.need <= 4 ? (int)w.need : 0;
         for (int i = 0; i < small; i++) {
-            const int p = S.list[at + i];
+            const int p = list[at + i];
             row[i] = p;
             S.ref[p] = 1;
         }
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
             const long long n = __shfl_sync(0xffffffffu, w.need, l), a = __shfl_sync(0xffffffffu, at, l);
             int32_t *to = reinterpret_cast<int32_t *>(__shfl_sync(0xffffffffu, (unsigned long long)row, l));
             for (long long i = lane; i < n; i += 32) {
-                const int p = S.list[a + i];
+                const int p = list[a + i];
                 to[i] = p;
                 S.ref[p] = 1;
             }
@@ -309,7 +325,7 @@ __device__ __forceinline__ int fork_check(const PageState &S, const ForkArgs &K,
 // tables).  An empty child goes to the lowest f that names it: that f's claim is the smallest
 // value INT_MIN + f left in its length.
 __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkArgs K) {
-    __shared__ int counts[PW + 1];
+    __shared__ int counts[PW + 1], near[NEAR];
     __shared__ long long tmp[PW + 1];
     grid_wait();
     grid_launch_dependents();
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
     U.ref = S.ref;
     U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
     U.read();
-    if (cg::this_cluster().block_rank() == 0)
+    if (cg::this_cluster().block_rank() == 0) {
         for (int f = threadIdx.x; f < K.F; f += PT) {
             int n, tail;
             const int err = fork_check(S, K, f, n, tail);
@@ -327,11 +343,13 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
             K.src[f] = tail;
             K.dst[f] = claims ? 1 : 0;
         }
-    const int free = list_free(S, U, K.F, counts);   // (and a barrier: every length is read before one changes)
+        __syncthreads();   // every length is read before one changes
+        for (int f = threadIdx.x; f < K.F; f += PT)
+            if (K.dst[f]) atomicMin(S.len + K.children[f], INT_MIN + f);
+    }
+    const int free = list_free(S, U, K.F, counts, near);   // (and a barrier: every claim is made)
     if (cg::this_cluster().block_rank() != 0) return;
-    for (int f = threadIdx.x; f < K.F; f += PT)
-        if (K.dst[f]) atomicMin(S.len + K.children[f], INT_MIN + f);
-    __syncthreads();
+    const int32_t *list = K.F <= NEAR ? near : S.list;
     long long before = 0;
     for (int f0 = 0; f0 < K.F; f0 += PT) {
         const int f = f0 + (int)threadIdx.x;
@@ -352,7 +370,7 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
         int fresh = -1;
         if (need) {
             if (at >= free) err = SV_DEV_NO_PAGES;
-            else fresh = S.list[at];
+            else fresh = list[at];
         }
         if (in) {
             if (err) record_error(S.hdr, err, f);
@@ -407,11 +425,10 @@ __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkAr
 
 constexpr int RELEASE_CHUNK = ST * SPT;
 
-// Gives back the SPT entries that `entry(t)` points at (NULL: none); returns whether they held anything.
+// Gives back the SPT entries that `entry(t)` points at (NULL: none); returns whether the last held anything.
 template <typename F>
 __device__ __forceinline__ bool give_back(const PageState &S, int b, F entry) {
     int p[SPT], count[SPT];
-    bool any = false;
 #pragma unroll
     for (int t = 0; t < SPT; t++) {
         const int32_t *e = entry(t);
@@ -421,7 +438,6 @@ __device__ __forceinline__ bool give_back(const PageState &S, int b, F entry) {
     for (int t = 0; t < SPT; t++) {
         count[t] = 1;
         if (p[t] == -1) continue;
-        any = true;
         *entry(t) = -1;
         count[t] = p[t] >= 0 && p[t] < S.num_pages ? atomicSub(S.ref + p[t], 1) : 0;
     }
@@ -431,11 +447,11 @@ __device__ __forceinline__ bool give_back(const PageState &S, int b, F entry) {
             if (p[t] >= 0 && p[t] < S.num_pages) atomicAdd(S.ref + p[t], 1);
             record_error(S.hdr, SV_DEV_BAD_PAGE, b);
         }
-    return any;
+    return p[SPT - 1] != -1;
 }
 
 // One CTA per request and direction (y = 0: past the length, upward; 1: before the window,
-// downward), RELEASE_CHUNK entries at a time until a chunk holds nothing.
+// downward), RELEASE_CHUNK entries at a time until the far end of a chunk is empty.
 __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int window, int sinks) {
     grid_wait();
     grid_launch_dependents();
@@ -456,11 +472,11 @@ __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int wind
         last = gone > 0 ? (int)(gone / S.page_size) : 0;
     }
     for (int done = 0; done < last - first; done += RELEASE_CHUNK) {
-        const bool any = give_back(S, b, [&](int t) {
+        const bool far = give_back(S, b, [&](int t) {
             const int i = done + t * ST + (int)threadIdx.x;
             return i < last - first ? row + (blockIdx.y ? last - 1 - i : first + i) : nullptr;
         });
-        if (!__syncthreads_or(any)) break;
+        if (!__syncthreads_or(far)) break;   // (any of the chunk's last ST entries)
     }
 }
 
