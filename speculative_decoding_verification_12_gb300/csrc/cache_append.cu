@@ -40,6 +40,22 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
     return (u >> 31) ? 0 - t : t;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
 constexpr int AT = 256;   // threads per CTA
 constexpr int AU = 4;     // heads per thread and pass, all loaded before the first is used
 constexpr int ROWS = 32;  // rows per CTA at most
@@ -68,6 +84,7 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     constexpr int HPC = AT / LPH;     // heads per CTA and step
     const int sub = tid % LPH, h_first = tid / LPH;
     const int rot = 2 * P.half;
+    const float inv_d = 1.f / (float)D;
     // this thread's elements: [d0, d0 + 4) and [d1, d1 + 4)
     const bool turns = PAIR == PAIR_HALVES ? sub * 4 < P.half : sub * 8 < rot;
     const int d0 = PAIR != PAIR_HALVES ? sub * 8 : turns ? sub * 4 : rot + (sub - P.half / 4) * 8;
@@ -173,42 +190,54 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
                 E *dst = out + (int64_t)h * D;
                 if (is_k) dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
                 if (is_v) dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
-                float x[8];
-                unpack8<E>(raw[u], x);
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (h0 + u * HPC + (tid & ~31) / LPH >= Hq + Hk) {   // (the whole warp)
+                    if (in && h < heads) put(dst, raw[u]);
+                    continue;
+                }
+                float2 x[4];
+                unpack8<E>(raw[u], reinterpret_cast<float *>(x));
                 if (is_k ? P.kw != nullptr : P.qw != nullptr) {
-                    float g[8];
-                    unpack8<E>(is_k ? kw : qw, g);
-                    const float inv = 1.f / sqrtf(ss / (float)D + P.eps);
+                    float2 s2 = make_float2(0.f, 0.f), g[4];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] *= inv * g[e];
+                    for (int e = 0; e < 4; e++) s2 = fma2(x[e], x[e], s2);
+                    float ss = s2.x + s2.y;
+#pragma unroll
+                    for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    unpack8<E>(is_k ? kw : qw, reinterpret_cast<float *>(g));
+                    const float inv = rsqrtf(fmaf(ss, inv_d, P.eps));
+#pragma unroll
+                    for (int e = 0; e < 4; e++) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
                 }
                 if (PAIR == PAIR_ANY) {
-                    float *mine = ex + (tid - sub) * 8;
+                    float2 *mine = reinterpret_cast<float2 *>(ex + (tid - sub) * 8);
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; e++) mine[sub * 8 + e] = x[e];
+                    for (int e = 0; e < 4; e++) mine[sub * 4 + e] = x[e];
                     __syncwarp();
+                    const float *all = ex + (tid - sub) * 8;
+                    float *y = reinterpret_cast<float *>(x);
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const int d = d0 + e;
-                        if (d < P.half) x[e] = x[e] * cs[e % NR].x - mine[d + P.half] * cs[e % NR].y;
-                        else if (d < rot) x[e] = x[e] * cs[e % NR].x + mine[d - P.half] * cs[e % NR].y;
+                        if (d < P.half) y[e] = y[e] * cs[e % NR].x - all[d + P.half] * cs[e % NR].y;
+                        else if (d < rot) y[e] = y[e] * cs[e % NR].x + all[d - P.half] * cs[e % NR].y;
+                    }
+                } else if (PAIR == PAIR_NEXT) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 c = cs[e % NR];
+                        x[e] = fma2(x[e], make_float2(c.x, c.x), mul2(make_float2(x[e].y, x[e].x), make_float2(-c.y, c.y)));
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        float &a = x[PAIR == PAIR_NEXT ? 2 * e : e], &z = x[PAIR == PAIR_NEXT ? 2 * e + 1 : e + 4];
-                        const float a0 = a, z0 = z;
-                        a = a0 * cs[e % NR].x - z0 * cs[e % NR].y;
-                        z = a0 * cs[e % NR].y + z0 * cs[e % NR].x;
+                    for (int e = 0; e < 2; e++) {
+                        const float2 a = x[e], z = x[e + 2], c = make_float2(cs[2 * e].x, cs[2 * e + 1].x),
+                                     n = make_float2(cs[2 * e].y, cs[2 * e + 1].y);
+                        x[e] = fma2(a, c, mul2(z, make_float2(-n.x, -n.y)));
+                        x[e + 2] = fma2(z, c, mul2(a, n));
                     }
                 }
-                if (in && h < heads) put(dst, is_v ? raw[u] : pack8<E>(x));
+                if (in && h < heads) put(dst, is_v ? raw[u] : pack8<E>(reinterpret_cast<const float *>(x)));
             }
         }
         if (i + 1 < rows) load(r + 1, 0);
