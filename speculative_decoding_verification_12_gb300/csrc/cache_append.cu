@@ -57,8 +57,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 
 constexpr int AT = 256;   // threads per CTA
-constexpr int AU = 4;     // heads per thread and pass, all loaded before the first is used
-constexpr int ROWS = 32;  // rows per CTA at most
+constexpr int AU = 3;     // heads per thread and pass, all loaded before the first is used (4: 9.4 us, 2: 9.9)
+constexpr int OCC = 3;    // CTAs per SM (2: 10.4 us; 4 spill: 12.5)
+constexpr int ROWS = 16;  // rows per CTA at most: 16 KB of rotations
 
 // How the two elements of a pair come together: as neighbours; in one thread, which holds 4 elements
 // of each half (rotary_dim a multiple of 8); or through shared memory, at any distance.
@@ -66,15 +67,19 @@ enum { PAIR_NEXT, PAIR_HALVES, PAIR_ANY };
 
 // Each CTA takes a few rows in a row.  LPH lanes hold one head, 8 elements each (a power of two >=
 // head_dim / 8), so a thread's elements are the same in every head it meets, and its weights and
-// rotations stay in registers.
+// rotations serve all of them.
 //
-// What bounds it: 24 KB of a row in and out at the memory's rate is 4 ns, but each row waits for the
-// chain offsets -> length -> page.  So a CTA walks that chain once, a lane of one warp per row, while
-// the first row's data, the weights and the turns of the frequencies are under way, and asks for the
-// next row's data before it turns to the next row.
+// What bounds it: a row of 48 heads of 128 is 24 KB in and out, 4 ns at the memory's rate, and about
+// 250 instructions per warp; a call's few rows per CTA also wait once for the chain offsets -> length
+// -> page.  So a CTA walks that chain once, a lane of one warp per row, while the first row's data, the
+// weights and the turns of the frequencies are under way, and then turns all its rows' pairs at once:
+// two barriers in all, and a warp asks for its next row's data before it works on this one's.  1280
+// rows of 48 heads take 9.0 us (3.5 TB/s read and written; with the rotations per row behind a barrier
+// each 10.4, and with one fp32 operation per instruction 10.9); one row takes 3.4 us, the launch.
+// Background copies of the next rows to shared memory: 12.0 before those two steps, no gain.
 template <typename E, int LPH, int PAIR>
-__global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cache C, const AppendArgs P, int per_cta) {
-    __shared__ float2 turn[2][128];   // (cos, sin) * rope_scale of each pair, of even and odd rows
+__global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Cache C, const AppendArgs P, int per_cta) {
+    __shared__ float2 turn[ROWS][128];   // (cos, sin) * rope_scale of each row's pairs
     __shared__ float ex[PAIR == PAIR_ANY ? AT * 8 : 1];
     __shared__ int64_t slot[ROWS];    // the tokens' offsets in the cache
     __shared__ int state[ROWS], pos[ROWS];   // state: 0: unused row, 1: used, 2: in error
@@ -88,36 +93,46 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     // this thread's elements: [d0, d0 + 4) and [d1, d1 + 4)
     const bool turns = PAIR == PAIR_HALVES ? sub * 4 < P.half : sub * 8 < rot;
     const int d0 = PAIR != PAIR_HALVES ? sub * 8 : turns ? sub * 4 : rot + (sub - P.half / 4) * 8;
-    const int d1 = PAIR == PAIR_HALVES && turns ? P.half + sub * 4 : d0 + 4;
+    const int d1 = (PAIR == PAIR_HALVES && turns ? P.half + sub * 4 : d0 + 4) - d0;   // (from d0)
     const bool in = sub * 8 < D;
     auto take = [&](const E *at) {
-        if (PAIR != PAIR_HALVES) return *reinterpret_cast<const uint4 *>(at + d0);
-        const uint2 a = *reinterpret_cast<const uint2 *>(at + d0), b = *reinterpret_cast<const uint2 *>(at + d1);
+        if (PAIR != PAIR_HALVES) return *reinterpret_cast<const uint4 *>(at);
+        const uint2 a = *reinterpret_cast<const uint2 *>(at), b = *reinterpret_cast<const uint2 *>(at + d1);
         return make_uint4(a.x, a.y, b.x, b.y);
     };
     auto put = [&](E *at, uint4 w) {
         if (PAIR != PAIR_HALVES) {
-            *reinterpret_cast<uint4 *>(at + d0) = w;
+            *reinterpret_cast<uint4 *>(at) = w;
         } else {
-            *reinterpret_cast<uint2 *>(at + d0) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2 *>(at) = make_uint2(w.x, w.y);
             *reinterpret_cast<uint2 *>(at + d1) = make_uint2(w.z, w.w);
         }
     };
 
     grid_wait();
     grid_launch_dependents();
-    uint4 raw[AU];
-    auto load = [&](int r, int h0) {
+    uint4 raw[AU], qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
+    // Row i's elements of head h.
+    auto source = [&](int h, int i) {
+        const int64_t r = first + i;
+        if (h >= Hq + Hk) return static_cast<const E *>(P.v) + r * P.v_stride + ((h - Hq - Hk) * D + d0);
+        if (h >= Hq) return static_cast<const E *>(P.k) + r * P.k_stride + ((h - Hq) * D + d0);
+        return static_cast<const E *>(P.q) + r * P.q_stride + (h * D + d0);
+    };
+    auto begin = [&](int h0) {
 #pragma unroll
         for (int u = 0; u < AU; u++) {
             const int h = h0 + u * HPC + h_first;
-            const E *src = static_cast<const E *>(P.q) + r * P.q_stride + (int64_t)h * D;
-            if (h >= Hq) src = static_cast<const E *>(P.k) + r * P.k_stride + (int64_t)(h - Hq) * D;
-            if (h >= Hq + Hk) src = static_cast<const E *>(P.v) + r * P.v_stride + (int64_t)(h - Hq - Hk) * D;
             raw[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (in && h < heads) raw[u] = take(src);
+            if (in && h < heads) raw[u] = take(source(h, 0));
         }
     };
+    begin(0);
+    const int hp = P.half > 64 ? 128 : P.half > 32 ? 64 : 32;   // threads per row for the turns
+    const int pair = tid & (hp - 1);
+    const float f = pair < P.half ? P.inv_freq[pair] : 0.f;
+    if (in && P.qw) qw = take(static_cast<const E *>(P.qw) + d0);
+    if (in && P.kw) kw = take(static_cast<const E *>(P.kw) + d0);
     if (tid >= AT - 32) {
         const int r = first + lane;
         const int b = request_of_rows(A, first, rows);   // (each lane its row's)
@@ -143,59 +158,54 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
     } else if (tid >= AT - 64) {
         check_requests(A, max_tokens, P.hdr, blockIdx.x * 32 + lane, gridDim.x * 32);
     }
-    load(first, 0);
-    uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
-    if (in && P.qw) qw = take(static_cast<const E *>(P.qw));
-    if (in && P.kw) kw = take(static_cast<const E *>(P.kw));
-    const float f = tid < P.half ? P.inv_freq[tid] : 0.f;
     const uint64_t t = turns_of(f);
     __syncthreads();
-
-#pragma unroll 1
-    for (int i = 0; i < rows; i++) {
-        const int r = first + i, st = state[i];
-        if (tid < P.half) {
+    if (pair < P.half)
+        for (int i = tid / hp; i < rows; i += AT / hp) {
             float sn, cs;
             sincospif((float)(int32_t)(uint32_t)(t * (uint64_t)(uint32_t)pos[i] >> 32) * 0x1p-31f, &sn, &cs);
             if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
-            turn[i & 1][tid] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
+            turn[i][pair] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
         }
-        __syncthreads();   // (and no one is still at the row before the last, whose turns these were)
-        E *out = static_cast<E *>(P.out) + r * P.out_stride;
-        if (st != 1) {
-            const uint32_t w = st == 2 ? Num<E>::NAN2 : 0u;
-            for (int j = tid; j < Hq * D / 8; j += AT) reinterpret_cast<uint4 *>(out)[j] = make_uint4(w, w, w, w);
-            if (i + 1 < rows) load(r + 1, 0);
-            continue;
-        }
-        // this thread's rotations: of its four pairs, or (any distance) of its eight elements
-        constexpr int NR = PAIR == PAIR_ANY ? 8 : 4;
-        float2 cs[NR];
-#pragma unroll
-        for (int e = 0; e < NR; e++) {
-            const int j = PAIR == PAIR_HALVES ? sub * 4 + e : PAIR == PAIR_NEXT ? sub * 4 + e
-                          : d0 + e < P.half ? d0 + e : d0 + e - P.half;
-            const bool on = PAIR == PAIR_ANY ? d0 + e < rot : j < P.half;
-            cs[e] = on ? turn[i & 1][j] : make_float2(1.f, 0.f);
-        }
-        const int64_t at = slot[i];
+    __syncthreads();
+
 #pragma unroll 1
-        for (int h0 = 0; h0 < heads; h0 += AU * HPC) {
-            if (h0) load(r, h0);
+    for (int h0 = 0; h0 < heads; h0 += AU * HPC) {
+        if (h0) begin(h0);
+#pragma unroll 1
+        for (int i = 0; i < rows; i++) {
+            const int st = state[i];
+            const int64_t at_q = (first + i) * P.out_stride, at_kv = slot[i];
+            // this thread's rotations: of its four pairs, or (any distance) of its eight elements
+            constexpr int NR = PAIR == PAIR_ANY ? 8 : 4;
+            float2 cs[NR];
+#pragma unroll
+            for (int e = 0; e < NR; e++) {
+                const int j = PAIR != PAIR_ANY ? sub * 4 + e : d0 + e < P.half ? d0 + e : d0 + e - P.half;
+                const bool on = PAIR == PAIR_ANY ? d0 + e < rot : j < P.half;
+                cs[e] = on ? turn[i][j] : make_float2(1.f, 0.f);
+            }
 #pragma unroll
             for (int u = 0; u < AU; u++) {
                 const int h = h0 + u * HPC + h_first;
                 if (h0 + u * HPC >= heads) break;   // (the whole CTA)
-                const bool is_v = h >= Hq + Hk, is_k = h >= Hq;
-                E *dst = out + (int64_t)h * D;
-                if (is_k) dst = static_cast<E *>(C.k) + at + (h - Hq) * C.head_stride;
-                if (is_v) dst = static_cast<E *>(C.v) + at + (h - Hq - Hk) * C.head_stride;
+                const bool is_v = h >= Hq + Hk, is_k = h >= Hq, on = in && h < heads;
+                const uint4 mine = raw[u];
+                if (on && i + 1 < rows) raw[u] = take(source(h, i + 1));
+                E *to = is_v   ? static_cast<E *>(C.v) + at_kv + (h - Hq - Hk) * C.head_stride + d0
+                        : is_k ? static_cast<E *>(C.k) + at_kv + (h - Hq) * C.head_stride + d0
+                               : static_cast<E *>(P.out) + at_q + (h * D + d0);
+                if (st != 1) {
+                    const uint32_t w = st == 2 ? Num<E>::NAN2 : 0u;
+                    if (on && !is_k) put(to, make_uint4(w, w, w, w));
+                    continue;
+                }
                 if (h0 + u * HPC + (tid & ~31) / LPH >= Hq + Hk) {   // (the whole warp)
-                    if (in && h < heads) put(dst, raw[u]);
+                    if (on) put(to, mine);
                     continue;
                 }
                 float2 x[4];
-                unpack8<E>(raw[u], reinterpret_cast<float *>(x));
+                unpack8<E>(mine, reinterpret_cast<float *>(x));
                 if (is_k ? P.kw != nullptr : P.qw != nullptr) {
                     float2 s2 = make_float2(0.f, 0.f), g[4];
 #pragma unroll
@@ -209,10 +219,10 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
                     for (int e = 0; e < 4; e++) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
                 }
                 if (PAIR == PAIR_ANY) {
-                    float2 *mine = reinterpret_cast<float2 *>(ex + (tid - sub) * 8);
+                    float2 *own = reinterpret_cast<float2 *>(ex + (tid - sub) * 8);
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 4; e++) mine[sub * 4 + e] = x[e];
+                    for (int e = 0; e < 4; e++) own[sub * 4 + e] = x[e];
                     __syncwarp();
                     const float *all = ex + (tid - sub) * 8;
                     float *y = reinterpret_cast<float *>(x);
@@ -237,10 +247,9 @@ __global__ void __launch_bounds__(AT, 3) append_kernel(const Batch A, const Cach
                         x[e + 2] = fma2(z, c, mul2(a, n));
                     }
                 }
-                if (in && h < heads) put(dst, is_v ? raw[u] : pack8<E>(reinterpret_cast<const float *>(x)));
+                if (on) put(to, is_v ? mine : pack8<E>(reinterpret_cast<const float *>(x)));
             }
         }
-        if (i + 1 < rows) load(r + 1, 0);
     }
 }
 
@@ -251,7 +260,7 @@ static cudaError_t launch_heads(const Batch &A, const Cache &C, const AppendArgs
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // one wave of resident CTAs where the rows allow
-    int per = (A.R + 3 * nsm - 1) / (3 * nsm);
+    int per = (A.R + OCC * nsm - 1) / (OCC * nsm);
     if (per > ROWS) per = ROWS;
     const int grid = (A.R + per - 1) / per;
     if (P.interleaved || P.half == 0) return launch_dependent(append_kernel<E, LPH, PAIR_NEXT>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
