@@ -23,7 +23,11 @@
  *
  * Shared conventions are those of spec_verify.h: device pointers, no allocation, no host copy,
  * no synchronisation, host-visible errors returned with nothing enqueued, device-data errors
- * in the workspace's sticky error word (sv_read_device_error), no trap or assert.
+ * in the workspace's sticky error word (sv_read_device_error), no trap or assert.  Every kernel
+ * is a programmatic dependent of the work before it on its stream and waits for that work before
+ * it touches a caller's buffer; a kernel of the caller's that is launched with programmatic stream
+ * serialization behind one of these must wait for its prerequisite grid likewise.  A call may be
+ * captured into a graph.  Calls on several streams need a workspace each.
  *
  *  - The workspace's first 256 bytes are its header.  These calls add to the error word and do
  *    not clear it (spec_verify does): zero the header once before the first call.
@@ -121,7 +125,7 @@ sv_status spec_append(const void *q, const void *k, const void *v, int64_t q_str
  *                apart (a multiple of 8), 16-byte aligned.
  *   window       >= 0; 0: no window.   sinks  >= 0 (no effect without a window).
  *   out          device [total_rows, num_q_heads, head_dim], contiguous, 16-byte aligned.
- *   out_lse      optional device fp32 [total_rows, num_q_heads].
+ *   out_lse      optional device fp32 [total_rows, num_q_heads] (unused rows: 0).
  *   workspace    sv_attention_workspace_bytes() bytes, 256-byte aligned.
  * Every wait inside the kernel is bounded (2 s): one that runs out ends the call with
  * SV_DEV_TIMEOUT in the error word and unspecified outputs, and the device stays usable.
@@ -182,8 +186,9 @@ sv_status spec_page_fork(const int32_t *parents, const int32_t *children, const 
  * after `sinks`.  A released entry becomes -1 and its page's count falls by one.  A request that
  * ends has its length set to 0 before the call.  Negative lengths are left alone.  The pages of a
  * request reach without a gap from its length (or from the window's start, downward) to the last
- * one held; the search in a direction ends, in steps of 1024 entries, where the last 256 are -1.  SV_DEV_BAD_LAYOUT: a length
- * past max_pages; SV_DEV_BAD_PAGE: an entry that is not a page in use (it becomes -1).
+ * one held; the search in a direction ends, in steps of 1024 entries, where the last 256 are -1.
+ * SV_DEV_BAD_LAYOUT: a length past max_pages; SV_DEV_BAD_PAGE: an entry that is not a page in use
+ * (it becomes -1).
  *   workspace  its header only (256 bytes).
  */
 sv_status spec_page_release(const int32_t *kv_seq_len, int32_t B, int32_t *block_table, int32_t max_pages,

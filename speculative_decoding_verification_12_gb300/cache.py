@@ -174,6 +174,8 @@ class PagedCache:
         self.block_table = torch.full((slots, max_pages), -1, **ints)
         self.ref_count = torch.zeros(pages, **ints)
         self.page_size = page_size
+        # pages to copy, kept: a tensor of one call would belong to the current stream alone
+        self._pairs = torch.empty((2, max(slots, pages)), **ints)
         need = max(sv_attention_workspace_bytes(head_dim), sv_page_workspace_bytes(slots, pages))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
         self.workspace[:256].zero_()
@@ -207,14 +209,13 @@ class PagedCache:
 
     def fork(self, parents, children, fork_len=None, stream=None) -> None:
         """Empty slots children[f] continue from (the first fork_len[f] tokens of) parents[f]."""
-        src, dst = torch.empty_like(parents), torch.empty_like(parents)
+        src, dst = self._pairs[:, :parents.numel()]
         spec_page_fork(parents, children, fork_len, self.kv_seq_len, self.block_table, self.ref_count, self.page_size,
                        src, dst, self.workspace, stream)
         spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)
 
     def compact(self, capacity: int, stream=None) -> None:
         """Moves up to `capacity` used pages down into the free ones below them."""
-        src = torch.empty(capacity, dtype=torch.int32, device=self.k.device)
-        dst = torch.empty_like(src)
+        src, dst = self._pairs[:, :capacity]
         spec_page_compact(self.block_table, self.ref_count, src, dst, self.workspace, stream)
         spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)
