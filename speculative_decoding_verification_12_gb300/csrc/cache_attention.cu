@@ -60,6 +60,7 @@ struct AttnArgs {
     int Hq, G, window, sinks;
     int k_stages, v_stages;
     int overhead;      // cost of a row tile beside its key tiles, in key tiles
+    int weighted;      // whether a key tile costs more for more than 128 rows
     int q_tiles;       // row tiles of 128 that a request may have at a time: 1 or 2
     int q_rows, q_bufs;   // rows of a query buffer (a multiple of 8), and how many there are
 };
@@ -102,9 +103,20 @@ __device__ __forceinline__ Req req_of(const Batch &A, const Cache &C, const Attn
     r.nt = s.n ? r.ns + (s.len + TILE - 1) / TILE - r.w0 : 0;
     return r;
 }
-// A request's cost per key head, in units of a key tile.
-__device__ __forceinline__ long long units_of(const Req &r, int overhead) {
-    return r.nt ? (long long)(r.nt + overhead) * r.mt : 0;
+// What a key tile costs for up to 128 rows, and for more.  16 requests of 65 rows on 8192 keys, 8 query heads
+// per key head, whose third row tile has the last 8 of 520 rows: 180 us at 1 to 1, 168 at 3 to 4, 166 at
+// 2 to 3, 175 at 1 to 2; 64 ragged requests of up to 17 rows: 185, 175, 175 and 175 us.
+constexpr int W_ONE = 2, W_TWO = 3;
+__device__ __forceinline__ uint32_t over_weight(uint32_t x, int w) {
+    return w == 1 ? x : w == W_ONE ? x / W_ONE : x / W_TWO;
+}
+
+// The cost of a key tile for row tile m of a request, and the request's cost per key head.
+__device__ __forceinline__ int weight_of(const AttnArgs &P, const Req &r, int m) {
+    return !P.weighted ? 1 : r.M - m * 2 * TILE > TILE ? W_TWO : W_ONE;
+}
+__device__ __forceinline__ long long units_of(const AttnArgs &P, const Req &r) {
+    return r.nt ? (long long)(r.nt + P.overhead) * ((r.mt - 1) * (P.weighted ? W_TWO : 1) + weight_of(P, r, r.mt - 1)) : 0;
 }
 
 // A segment, as the front warp hands it out (64 bytes): key tiles [t0, t1) of the nt of row tile m of
@@ -113,7 +125,7 @@ struct __align__(16) Seg {
     int row0, n, len, M, lo, w0, ns, nt;   // as in Req
     int b, kvh, m, t0, t1, solo, pad[2];   // solo: one group takes all its tiles
     __device__ __forceinline__ int base(int t) const { return (t < ns ? t : w0 + t - ns) * TILE; }
-    __device__ __forceinline__ bool two() const { return M > TILE; }
+    __device__ __forceinline__ bool two() const { return M - m * 2 * TILE > TILE; }
 };
 constexpr int SEGS = 32;                 // segments in flight between the front warp and the others
 // Narrow heads: key tiles of a segment that one group takes alone.  512 x 8 segments of 3 tiles take 150 us
@@ -291,7 +303,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const int cta = blockIdx.x;
     auto range = [&]() {   // [T cta / nc, T (cta + 1) / nc), and the head that it begins in
         T = W * C.heads;
-        nc = (int)min((long long)gridDim.x, T);
+        nc = (int)min((long long)gridDim.x, P.weighted ? T / W_TWO : T);   // (a key tile at least for each)
+        if (T && !nc) nc = 1;
         if (cta < nc) {
             const long long q = quotient(T, nc);
             const int rest = (int)(T - q * nc);
@@ -310,7 +323,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 const int b = b0 + tid;
                 Req r = {};
                 if (b < A.B) r = req_of(A, C, P, b);
-                const long long w = units_of(r, P.overhead);
+                const long long w = units_of(P, r);
                 long long inc = w;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -588,7 +601,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             auto look = [&](int b) {                     // at requests b .. b + 15: first and sum from this head's start
                 r.nt = r.mt = 0;
                 if (lane < SMALL_BATCH && b + lane < A.B) r = req_of(A, C, P, b + lane);
-                const long long w = units_of(r, P.overhead);
+                const long long w = units_of(P, r);
                 sum = w;
 #pragma unroll
                 for (int o = 1; o < SMALL_BATCH; o <<= 1) {
@@ -627,15 +640,17 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                         fresh = false;
                     }
                     // row tile m of each of them, as far as it lies in [lo, hi)
-                    const int per = r.nt + P.overhead;
-                    const long long mine = kvh * W + pre + first + (long long)m * per;
+                    const int w = weight_of(P, r, m);
+                    const int per = (r.nt + P.overhead) * w;
+                    const long long mine = kvh * W + pre + first + (long long)m * (r.nt + P.overhead) * (P.weighted ? W_TWO : 1);
                     Seg s;
                     s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
                     s.b = b_base + lane;
                     s.kvh = kvh;
                     s.m = m;
-                    s.t0 = (int)max(lo - mine - P.overhead, 0ll);
-                    s.t1 = (int)min((long long)per, hi - mine) - P.overhead;
+                    // (a key tile is its last unit's: the CTA of the row tile's last unit has its last key tile)
+                    s.t0 = max((int)over_weight((uint32_t)min(max(lo - mine, 0ll), (long long)per), w) - P.overhead, 0);
+                    s.t1 = (int)over_weight((uint32_t)min(max(hi - mine, 0ll), (long long)per), w) - P.overhead;
                     // a short segment among others is one group's alone: the groups then work on two segments at
                     // a time, and neither waits for the other at the end
                     s.solo = APART && s.M <= TILE && s.t1 - s.t0 <= SOLO_TILES && hi - lo >= 4 * per;
@@ -1031,7 +1046,8 @@ __device__ __forceinline__ void store_joined(const AttnArgs &P, const Cache &C, 
 }
 
 // Joins the parts of the row tiles that several CTAs hold, in order of the CTAs, and sets the rows
-// that no request uses.  Blocks (c, y): rows y, y + gridDim.y, ... of the row tile that begins in CTA c.
+// that no request uses.  Blocks (c, y): rows y, y + ny, ... of the row tile that begins in CTA c; the last y
+// has the rows that no request uses.
 // Many rows of few parts (long draft chains): a row per DP / 4 lanes.  Else a row's parts are spread over
 // the block, 16 bytes of a part per thread, and the thread groups' sums are added in shared memory: one
 // long request's parts (19 for 131 072 keys) then come in one round trip.
@@ -1042,16 +1058,17 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
     __shared__ float4 sums[LANES][TPP];
     __shared__ float red[2][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nblocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
+    const int ny = gridDim.y - 1;
     grid_wait();
-    const int4 d = P.desc[blockIdx.x];
-    if (d.x >= 0) {
+    if ((int)blockIdx.y < ny) {
+        const int4 d = P.desc[blockIdx.x];
+        if (d.x < 0) return;
         const Req s = req_of(A, C, P, d.x);
         const int rows = min(s.M - d.z * 2 * TILE, 2 * TILE), first = blockIdx.x, parts = d.w - first + 1;
         auto slot = [&](int p) { return 2 * (first + p) + (p == 0); };
-        if (parts <= TPP && rows > 2 * (int)gridDim.y) {
+        if (parts <= TPP && rows > 2 * ny) {
             const int sub = lane % TPP;
-            for (int r0 = blockIdx.y * LANES; r0 < rows; r0 += gridDim.y * LANES) {   // (the whole warp)
+            for (int r0 = blockIdx.y * LANES; r0 < rows; r0 += ny * LANES) {   // (the whole warp)
                 const int rt = r0 + tid / TPP;
                 const bool on = rt < rows;
                 const float v = on && sub < parts ? P.part_lse[slot(sub) * PART_ROWS + rt] : -INFINITY;
@@ -1072,7 +1089,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
                 }
                 if (on) store_joined<E>(P, C, s, d, rt, sub, o, sum, top);
             }
-        } else for (int rt = blockIdx.y; rt < rows; rt += gridDim.y) {
+        } else for (int rt = blockIdx.y; rt < rows; rt += ny) {
             const float *lse = P.part_lse + rt;
             const float v = tid < parts ? lse[slot(tid) * PART_ROWS] : -INFINITY;   // (parts <= MAX_CTAS < 256)
             const float *from = P.part_o + (int64_t)rt * DP + (tid % TPP) * 4;
@@ -1117,15 +1134,19 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
             }
             __syncthreads();
         }
+        return;
     }
-    // unused rows: zeros; the rows of a request in error: NaN
-    for (int b0 = (me * 8 + warp) * 32; b0 < A.B; b0 += nblocks * 256) {
-        const int b = b0 + lane;
+    // unused rows: zeros; the rows of a request in error: NaN.  A warp looks at 32 requests, and up to 64
+    // warps share what there is to fill in them: the half of 16 requests of 65 rows that is unused took one
+    // warp per 32 requests 150 us.
+    const int nb = gridDim.x, groups = (A.B + 31) / 32, shares = max(1, min(64, nb * 8 / groups));
+    for (int i = warp * nb + blockIdx.x; i < groups * shares; i += nb * 8) {
+        const int share = i / groups, b = (i - share * groups) * 32 + lane;
         int from = 0, to = 0, err = 0, head = 0, tail = 0;
         if (b < A.B) {
             const Span s = span_of(A, C.max_pages << C.page_shift, b);
             err = s.err;
-            if (err) record_error(P.hdr, err, b);
+            if (err && share == 0) record_error(P.hdr, err, b);
             int end = s.row0 + A.k_max + 1;
             if (A.row_off) {
                 end = A.row_off[b + 1];
@@ -1149,10 +1170,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
                 const int64_t n = (int64_t)(r1 - r0) * P.Hq * C.D / 8, hn = (int64_t)(r1 - r0) * P.Hq;
                 uint4 *o = reinterpret_cast<uint4 *>(static_cast<E *>(P.out) + (int64_t)r0 * P.Hq * C.D);
 #pragma unroll 1
-                for (int64_t i = lane; i < n; i += 32) o[i] = make_uint4(w, w, w, w);
+                for (int64_t j = share * 32 + lane; j < n; j += shares * 32) o[j] = make_uint4(w, w, w, w);
                 if (P.lse)
 #pragma unroll 1
-                    for (int64_t i = lane; i < hn; i += 32) P.lse[(int64_t)r0 * P.Hq + i] = nan ? NAN : 0.f;
+                    for (int64_t j = share * 32 + lane; j < hn; j += shares * 32)
+                        P.lse[(int64_t)r0 * P.Hq + j] = nan ? NAN : 0.f;
             }
         }
     }
@@ -1209,6 +1231,7 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     // and a key tile 1.0 us at 64 columns, 1.6 at 128.  Ragged 96 requests at 64 columns: 93, 78, 72, 68 us
     // with 1, 2, 3, 4; ragged 64 at 128 columns, full and windowed: 69 and 46, 61 and 42, 60 and 44, 63 and 46.
     P.overhead = DP == 64 ? 4 : 2;
+    P.weighted = P.q_tiles == 2;
     P.k_stages = stages / 2 < MAX_STAGES ? stages / 2 : MAX_STAGES;
     P.v_stages = stages - P.k_stages < MAX_STAGES ? stages - P.k_stages : MAX_STAGES;
     const int smem = SMALL + hand_over(DP) + q_bytes + (P.k_stages + P.v_stages) * STAGE;
@@ -1233,7 +1256,7 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attention_kernel<E, DP>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
-    cfg.gridDim = dim3(ctas, most_rows < 16 ? most_rows : 16);
+    cfg.gridDim = dim3(ctas, (most_rows < 16 ? most_rows : 16) + 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<E, DP>, A, C, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;

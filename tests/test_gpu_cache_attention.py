@@ -148,6 +148,19 @@ def test_many_rows_per_request(sv, ragged, Hq, Hk):
     run_and_check(sv, s)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(8, 1), (8, 2), (10, 2)])
+@pytest.mark.parametrize("ragged", [True, False])
+def test_last_row_tiles_of_any_height(sv, D, Hq, Hk, ragged):
+    """520, 260 and 325 rows per key head, and all the smaller counts beside them, over one and many CTAs."""
+    rng = random.Random(Hq * 10 + Hk)
+    run_and_check(sv, make(31, [65], [64], 64, Hq, Hk, D, 16, "bf16", ragged=ragged))
+    run_and_check(sv, make(32, [2900, 700], [64, 31], 64, Hq, Hk, D, 64, "fp16", ragged=ragged))
+    drafts = [rng.choice([-1, 0, 1, 15, 25, 31, 32, 50, 63, 64]) for _ in range(21)]
+    lens = [k + 1 + rng.choice([0, 1, 127, 600]) for k in drafts]
+    run_and_check(sv, make(33, lens, drafts, 64, Hq, Hk, D, 32, "bf16", ragged=ragged))
+
+
 def test_many_rows_with_a_window(sv):
     run_and_check(sv, make(22, [300, 70, 513, 65], [64, 64, 40, 64], 64, 8, 1, 64, 32, "fp16", window=50, sinks=20))
 
