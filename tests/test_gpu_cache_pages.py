@@ -169,6 +169,24 @@ def test_fork_shares_a_page_that_is_none(sv):
     assert sv.sv_read_device_error(p.ws) == (9, 0)
 
 
+@pytest.mark.parametrize("B,M,forks", [(40, 400, 20), (40, 1024, 20), (40, 1025, 20), (300, 1100, 150), (1300, 7, 1200)])
+def test_many_forks(sv, B, M, forks):
+    """Forks of several chunks of a table row and of one short of it; more forks than threads."""
+    r = random.Random(B + M)
+    parents = B - forks
+    page, lens, ids = 4, [], list(range(parents * M + forks))
+    r.shuffle(ids)
+    table, ref = [[-1] * M for _ in range(B)], [0] * len(ids)
+    for b in range(B):
+        lens.append(r.randint(1, M * page) if b < parents else 0)
+        for x in range(-(-lens[b] // page)):
+            table[b][x] = p = ids.pop()
+            ref[p] = 1
+    p = Pool(sv, lens, table, ref, page)
+    pa = [r.randrange(parents) for _ in range(forks)]
+    p.fork(pa, r.sample(range(parents, B), forks), [r.randint(1, lens[b]) for b in pa])
+
+
 def test_release_errors_and_windows(sv):
     p = Pool(sv, [4, 13, -5, 0], [[0, 7, 1], [2, 3, 4], [5, -1, -1], [-3, 6, -1]], [1, 0, 1, 1, 1, 1, 0], 4)
     sv.spec_page_release(p.len, p.table, p.ref, 4, 0, 0, p.ws)
