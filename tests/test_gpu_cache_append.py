@@ -150,6 +150,16 @@ def test_one_row(sv):
     run_and_check(sv, make(4, [777], [0], 0, 32, 8, 128, 16, "bf16", 128, ragged=False))
 
 
+@pytest.mark.parametrize("B,Hq,Hk,D,rotary,il,ragged", [(125, 2, 1, 16, 16, False, False), (130, 1, 1, 24, 20, False, True),
+                                                       (30, 112, 8, 64, 64, False, True), (12, 60, 2, 128, 128, True, False),
+                                                       (12, 60, 2, 128, 36, False, True)])
+def test_many_rows(sv, B, Hq, Hk, D, rotary, il, ragged):
+    """More rows than one wave of CTAs takes, and several rows per CTA of more heads than it holds at a time."""
+    lens = [65 + 7 * b % 200 for b in range(B)]
+    drafts = [64 if not ragged or b % 3 else 63 - b % 11 for b in range(B)]
+    run_and_check(sv, make(6, lens, drafts, 64, Hq, Hk, D, 16, "bf16", rotary, ragged=ragged), il, inplace=bool(B % 2))
+
+
 def test_padded_rows_and_in_place(sv):
     s = make(5, [12, 90], [4, 2], 4, 6, 3, 80, 16, "fp16", 80, packed=False)
     run_and_check(sv, s, inplace=True)
