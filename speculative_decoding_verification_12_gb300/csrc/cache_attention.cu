@@ -51,7 +51,8 @@ struct AttnArgs {
     void *out;
     float *lse;
     int32_t *hdr;
-    int4 *desc;        // workspace, per CTA: the row tile whose first part, but not last, it holds
+    int4 *desc;        // workspace, per CTA: the row tile whose first part, but not last, it holds (its request's
+                       // first row, or -1: none; key head; number; last part's CTA and 256 M)
     float *part_lse;   // workspace, [2 * MAX_CTAS][PART_ROWS]: log2 of the part's sum
     float *part_o;     // workspace, [2 * MAX_CTAS][PART_ROWS][DP]
     float c;           // |scale| log2(e)
@@ -660,7 +661,7 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                         ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
                         if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
                             const long long last = mine + per;
-                            P.desc[cta] = make_int4(s.b, s.kvh, s.m, (int)((last * nc + T - 1) / T) - 1);
+                            P.desc[cta] = make_int4(s.row0, s.kvh, s.m, s.M << 8 | ((int)((last * nc + T - 1) / T) - 1));
                         }
                     }
                     ok = __all_sync(0xffffffffu, ok);
@@ -1034,12 +1035,12 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
 
 // Four columns (from 4 sub on) of a joined row, and its lse.
 template <typename E>
-__device__ __forceinline__ void store_joined(const AttnArgs &P, const Cache &C, const Req &s, int4 d, int rt, int sub, float4 o,
-                                             float sum, float top) {
+__device__ __forceinline__ void store_joined(const AttnArgs &P, const Cache &C, int4 d, int rt, int sub, float4 o, float sum,
+                                             float top) {
     if (sub * 4 >= C.D) return;
     const float inv = 1.f / sum;
     const int rr = d.z * 2 * TILE + rt, tok = rr / P.G;
-    const int64_t orow = (int64_t)(s.row0 + tok) * P.Hq + d.y * P.G + rr - tok * P.G;
+    const int64_t orow = (int64_t)(d.x + tok) * P.Hq + d.y * P.G + rr - tok * P.G;
     *reinterpret_cast<uint2 *>(static_cast<E *>(P.out) + orow * C.D + sub * 4) =
         make_uint2(Num<E>::down(o.x * inv, o.y * inv), Num<E>::down(o.z * inv, o.w * inv));
     if (P.lse && sub == 0) P.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
@@ -1063,8 +1064,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
     if ((int)blockIdx.y < ny) {
         const int4 d = P.desc[blockIdx.x];
         if (d.x < 0) return;
-        const Req s = req_of(A, C, P, d.x);
-        const int rows = min(s.M - d.z * 2 * TILE, 2 * TILE), first = blockIdx.x, parts = d.w - first + 1;
+        const int rows = min((d.w >> 8) - d.z * 2 * TILE, 2 * TILE), first = blockIdx.x, parts = (d.w & 255) - first + 1;
         auto slot = [&](int p) { return 2 * (first + p) + (p == 0); };
         if (parts <= TPP && rows > 2 * ny) {
             const int sub = lane % TPP;
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                     o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
                 }
-                if (on) store_joined<E>(P, C, s, d, rt, sub, o, sum, top);
+                if (on) store_joined<E>(P, C, d, rt, sub, o, sum, top);
             }
         } else for (int rt = blockIdx.y; rt < rows; rt += ny) {
             const float *lse = P.part_lse + rt;
@@ -1130,7 +1130,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
                     const float4 y = sums[i][tid];
                     o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
                 }
-                store_joined<E>(P, C, s, d, rt, tid, o, sum, top);
+                store_joined<E>(P, C, d, rt, tid, o, sum, top);
             }
             __syncthreads();
         }
