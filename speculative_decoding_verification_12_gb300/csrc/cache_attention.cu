@@ -1072,6 +1072,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
                 const int rt = r0 + tid / TPP;
                 const bool on = rt < rows;
                 const float v = on && sub < parts ? P.part_lse[slot(sub) * PART_ROWS + rt] : -INFINITY;
+                const float4 *from = reinterpret_cast<const float4 *>(P.part_o + (int64_t)rt * DP) + sub;
+                auto part = [&](int p) {
+                    return on ? from[(int64_t)slot(p) * PART_ROWS * (DP / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+                const float4 x0 = part(0), x1 = part(1);   // (there are two at least: under way with the weights)
                 float top = v;
 #pragma unroll
                 for (int o = TPP / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1080,13 +1085,14 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
 #pragma unroll
                 for (int o = TPP / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int p = 0; p < parts; p++) {
+                auto add = [&](int p, float4 x) {
                     const float w = __shfl_sync(0xffffffffu, f, lane - sub + p);
-                    const float4 x = on ? *reinterpret_cast<const float4 *>(P.part_o + ((int64_t)slot(p) * PART_ROWS + rt) * DP + sub * 4)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
                     o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
-                }
+                };
+                add(0, x0);
+                add(1, x1);
+#pragma unroll 2
+                for (int p = 2; p < parts; p++) add(p, part(p));
                 if (on) store_joined<E>(P, C, d, rt, sub, o, sum, top);
             }
         } else for (int rt = blockIdx.y; rt < rows; rt += ny) {
