@@ -263,9 +263,10 @@ static cudaError_t launch_heads(const Batch &A, const Cache &C, const AppendArgs
     int per = (A.R + OCC * nsm - 1) / (OCC * nsm);
     if (per > ROWS) per = ROWS;
     const int grid = (A.R + per - 1) / per;
-    if (P.interleaved || P.half == 0) return launch_dependent(append_kernel<E, LPH, PAIR_NEXT>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
-    if (P.half % 4 == 0) return launch_dependent(append_kernel<E, LPH, PAIR_HALVES>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
-    return launch_dependent(append_kernel<E, LPH, PAIR_ANY>, dim3(grid), dim3(AT), 1, st, A, C, P, per);
+    auto *const kernel = P.interleaved || P.half == 0 ? append_kernel<E, LPH, PAIR_NEXT>
+                         : P.half % 4 == 0            ? append_kernel<E, LPH, PAIR_HALVES>
+                                                      : append_kernel<E, LPH, PAIR_ANY>;
+    return launch_dependent(kernel, dim3(grid), dim3(AT), 1, st, A, C, P, per);
 }
 template <typename E>
 static cudaError_t launch_append(const Batch &A, const Cache &C, const AppendArgs &P, cudaStream_t st) {

@@ -26,6 +26,13 @@
 // operand), and two groups of 4 warps, a thread per row, for softmax and epilogue.  With one row tile
 // the groups take alternate key tiles, each with its own m, l and O, joined at the end; with two, each
 // has its own.
+//
+// What bounds it.  Few rows per key (a verify step): the cache's bytes; 256 requests of 5 rows over up to
+// 4096 keys of 8 heads of 128 read 4.3 GB in 645 us, 6.7 TB/s, one request over 131 071 keys 0.54 GB in
+// 90 us.  Many rows (16 requests of 65 rows, 8 query heads per key head, 8192 keys): the chain of a
+// product, its softmax and the next product on the 512 columns of tensor memory; 161 us, 860 TFLOP/s.
+// Small calls: the chain of launch, lengths, table, first tile, epilogue and join, 11.4 us for one request
+// of 2049 keys; short and narrow segments: about 2 us each to change from one to the next.
 #include <math.h>
 
 #include <atomic>
@@ -117,7 +124,8 @@ __device__ __forceinline__ int weight_of(const AttnArgs &P, const Req &r, int m)
     return !P.weighted ? 1 : r.M - m * 2 * TILE > TILE ? W_TWO : W_ONE;
 }
 __device__ __forceinline__ long long units_of(const AttnArgs &P, const Req &r) {
-    return r.nt ? (long long)(r.nt + P.overhead) * ((r.mt - 1) * (P.weighted ? W_TWO : 1) + weight_of(P, r, r.mt - 1)) : 0;
+    const int weight = (r.mt - 1) * (P.weighted ? W_TWO : 1) + weight_of(P, r, r.mt - 1);
+    return r.nt ? (long long)(r.nt + P.overhead) * weight : 0;
 }
 
 // A segment, as the front warp hands it out (64 bytes): key tiles [t0, t1) of the nt of row tile m of
@@ -215,7 +223,8 @@ __device__ __forceinline__ bool clean_values(const AttnArgs &P, const Seg &s, in
 // The non-finite elements that clean_values took, for the row at position pos, added to its result
 // after it was stored: `put(d, x)` adds x to element d, for d in [c0, c1).
 template <typename E, typename F>
-__device__ __forceinline__ void add_non_finite(const Cache &C, const AttnArgs &P, const Seg &s, int pos, int c0, int c1, F put) {
+__device__ __forceinline__ void add_non_finite(const Cache &C, const AttnArgs &P, const Seg &s, int pos, int c0, int c1,
+                                               F put) {
 #pragma unroll 1
     for (int side = 0; side < 2; side++) {
         const int from = side ? s.lo : s.len - s.n + 1, to = side ? min(s.len, s.lo + s.n - 1) : s.len;
@@ -243,7 +252,9 @@ constexpr int SMALL = 5120;
 // groups' one busy warp each sits on a scheduler of its own, and hands its O to group 0 through shared
 // memory.
 constexpr int FEW_ROWS = 32, DOWN = 64;   // rows, and how far down group 1 has them
-__host__ __device__ constexpr int hand_over(int DP) { return DP == 64 ? FEW_ROWS * (64 + 4) * 4 + 512 : 0; }   // (9216: 1024-byte steps)
+__host__ __device__ constexpr int hand_over(int DP) {   // (9216: 1024-byte steps)
+    return DP == 64 ? FEW_ROWS * (64 + 4) * 4 + 512 : 0;
+}
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -274,7 +285,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const uint32_t seg_full = smem_addr(smem + 4608), seg_empty = seg_full + 8 * SEGS;
     const uint32_t k_full = smem_addr(smem), k_empty = k_full + 8 * MAX_STAGES, v_full = k_empty + 8 * MAX_STAGES,
                    v_empty = v_full + 8 * MAX_STAGES, s_full = v_empty + 8 * MAX_STAGES, p_full = s_full + 16,
-                   o_done = p_full + 16, both = o_done + 16, s_free = both + 16, drained = s_free + 16, q_full = drained + 24, q_empty = q_full + 8 * MAX_QBUFS;
+                   o_done = p_full + 16, both = o_done + 16, s_free = both + 16, drained = s_free + 16,
+                   q_full = drained + 24, q_empty = q_full + 8 * MAX_QBUFS;
     volatile int *const dead = ctl, *const patched = ctl + 4, *const bad = ctl + 12;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_bufs;
@@ -383,7 +395,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
     const int steps = (C.D + 15) / 16;                              // of 16 columns: nothing past head_dim
     auto issue_s = [&](uint32_t g, uint32_t q_at, uint32_t k_stage, bool down) {
         const uint32_t idesc = mma_idesc(Num<E>::BF16, TILE, TILE, false) | (uint32_t)P.negative << 13;
-        const uint64_t qd = smem_desc(smem_addr(q_p) + q_at * q_buffer - (down ? DOWN * 128 : 0), 16), kd = smem_desc(smem_addr(k_p) + k_stage * STAGE, 16);
+        const uint64_t qd = smem_desc(smem_addr(q_p) + q_at * q_buffer - (down ? DOWN * 128 : 0), 16);
+        const uint64_t kd = smem_desc(smem_addr(k_p) + k_stage * STAGE, 16);
         const uint32_t q_step = q_block >> 4;
         auto run = [&](auto n) {
 #pragma unroll
@@ -402,7 +415,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         const uint64_t vd = smem_desc(smem_addr(v_p) + v_stage * STAGE, BLK);
 #pragma unroll
         for (int k = 0; k < TILE / 16; k++)
-            mma_ts(tmem + 2 * TILE + g * TILE, tmem + g * TILE + P_COL + k * 8, vd + (uint64_t)(k * 2048 >> 4), idesc, add || k > 0);
+            mma_ts(tmem + 2 * TILE + g * TILE, tmem + g * TILE + P_COL + k * 8, vd + (uint64_t)(k * 2048 >> 4), idesc,
+                   add || k > 0);
     };
 
     if (warp >= 8) {
@@ -643,7 +657,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     // row tile m of each of them, as far as it lies in [lo, hi)
                     const int w = weight_of(P, r, m);
                     const int per = (r.nt + P.overhead) * w;
-                    const long long mine = kvh * W + pre + first + (long long)m * (r.nt + P.overhead) * (P.weighted ? W_TWO : 1);
+                    const long long mine =
+                        kvh * W + pre + first + (long long)m * (r.nt + P.overhead) * (P.weighted ? W_TWO : 1);
                     Seg s;
                     s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
                     s.b = b_base + lane;
@@ -695,7 +710,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     constexpr int CH = DP / 8, RPW = 32 / CH;   // 16-byte pieces of a row, rows per warp step
                     const int ch = lane % CH;
                     int row = lane / CH, tok = (row0 + row) / P.G, head = row0 + row - tok * P.G;
-                    const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + (ch * 8 < C.D ? ch * 8 : 0);
+                    const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D +
+                                 (ch * 8 < C.D ? ch * 8 : 0);
                     const uint32_t bytes = ch * 8 < C.D && !P.zero ? 16 : 0;
                     const uint32_t base = smem_addr(q_p) + (two ? 0 : at.stage) * q_buffer + (ch >> 3) * q_block;
 #pragma unroll 2
@@ -732,7 +748,8 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
         const uint32_t t_s = tmem + g * TILE + lanes, t_o = tmem + 2 * TILE + lanes;
         const int D = C.D, Hq = P.Hq;
         const bool leader = elect();
-        uint32_t ns_ = 0, turn = 0, tiles = 0, parts = 0, joint = 0, pairs = 0;   // S tiles taken; products, key tiles, epilogues; barriers of both groups
+        // S tiles taken; products, key tiles, epilogues; barriers of both groups
+        uint32_t ns_ = 0, turn = 0, tiles = 0, parts = 0, joint = 0, pairs = 0;
 #pragma unroll 1
         for (int seg = 0; ok && take(seg, s, false); release(seg++)) {
             const Seg &all = segs[seg & (SEGS - 1)];   // what only the ends of a segment need stays there
@@ -1103,7 +1120,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const Cache C,
 #pragma unroll
             for (int i = 0; i < 4; i++) {   // the first parts' values, under way while the weights come together
                 const int p = tid / TPP + i * LANES;
-                x[i] = p < parts ? *reinterpret_cast<const float4 *>(from + (int64_t)slot(p) * PART_ROWS * DP) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[i] = p < parts ? *reinterpret_cast<const float4 *>(from + (int64_t)slot(p) * PART_ROWS * DP)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float top = v;
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1208,11 +1226,14 @@ static EncodeFn encode_fn() {
 static bool encode(CUtensorMap *map, const sv_kv_cache &c, void *ptr) {
     EncodeFn f = encode_fn();
     if (!f) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2, (cuuint64_t)c.page_stride * 2};
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
+                                (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
+                                   (cuuint64_t)c.page_stride * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)(c.page_size < TILE ? c.page_size : TILE), 1, 1}, one[4] = {1, 1, 1, 1};
     return f(map, c.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, ptr, dims,
-             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, c.head_dim % 64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             c.head_dim % 64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1246,7 +1267,8 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
                            ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + P.overhead);
     int ctas = nsm < MAX_CTAS ? nsm : MAX_CTAS;
     // heads that share lines keep step only if each has a whole number of CTAs: worth up to 5 % of them
-    if (C.D * 2 % 128 && cache.head_stride * 2 % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas) ctas -= ctas % C.heads;
+    if (C.D * 2 % 128 && cache.head_stride * 2 % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas)
+        ctas -= ctas % C.heads;
     if (most < ctas) ctas = (int)most;
     if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SV_ERR_CUDA;
@@ -1261,8 +1283,9 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attention_kernel<E, DP>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
+    // 8 blocks a row tile: 64 windows of 4096 keys take 61 us, 63 with 16; 16 x 65 rows 161 us, 163 with 4
     const int most_rows = (A.k_max + 1) * P.G;
-    cfg.gridDim = dim3(ctas, (most_rows < 16 ? most_rows : 16) + 1);
+    cfg.gridDim = dim3(ctas, (most_rows < 8 ? most_rows : 8) + 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<E, DP>, A, C, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
@@ -1314,6 +1337,7 @@ extern "C" sv_status spec_attention(const void *q, int64_t q_stride, int32_t num
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wide = cache.head_dim > 64;
     if (cache.dtype == SV_BF16)
-        return wide ? launch_attention<__nv_bfloat16, 128>(A, C, P, cache, st) : launch_attention<__nv_bfloat16, 64>(A, C, P, cache, st);
+        return wide ? launch_attention<__nv_bfloat16, 128>(A, C, P, cache, st)
+                    : launch_attention<__nv_bfloat16, 64>(A, C, P, cache, st);
     return wide ? launch_attention<__half, 128>(A, C, P, cache, st) : launch_attention<__half, 64>(A, C, P, cache, st);
 }
