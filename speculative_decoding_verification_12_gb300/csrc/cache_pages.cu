@@ -8,9 +8,9 @@
 // depends on the order of atomics, and no free list has to be kept consistent between calls.
 // These kernels move a few hundred KB at most and are bound by latency (launch, two dependent
 // passes over the counts, one cluster barrier): fork, copy, reserve, rollback and release together take
-// 18 us on the GPU for 8 requests and 30 for 512 with 81 920 pages, 2 to 4 us a kernel; a caller that
+// 17.6 us on the GPU for 8 requests and 30 for 512 with 81 920 pages, 2 to 4 us a kernel; a caller that
 // issues them one by one waits longer for its own launches (3 us each).  Doing the children's tables
-// inside the fork's cluster instead of in a second launch gained nothing (18.0, and 31.4).  Only
+// inside the fork's cluster instead of in a second launch gained nothing (18.0 of then 18.0, and 31.4 of 30.5).  Only
 // spec_page_copy is bound by bandwidth.
 #include <cooperative_groups.h>
 #include <limits.h>
@@ -212,9 +212,9 @@ struct Want {
     long long need;
 };
 
-__device__ __forceinline__ Want want_of(const PageState &S, const int32_t *nd, int b) {
+// Of request b with k drafts and length len.
+__device__ __forceinline__ Want want_of(const PageState &S, int b, int k, int len) {
     Want w = {0, 0, 0, 0};
-    const int k = nd[b], len = S.len[b];
     if (k == -1) return w;
     const long long grown = (long long)len + k + 1;
     if (k < -1 || len < 0 || grown > (long long)S.max_pages * S.page_size) {
@@ -242,12 +242,13 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
     Used U;
     U.ref = S.ref;
     U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
+    // the first PT requests are looked at once, their first loads together with the pool's
+    const bool in0 = (int)threadIdx.x < S.B;
+    const int k0 = in0 ? nd[threadIdx.x] : -1, len0 = in0 ? S.len[threadIdx.x] : 0;
     U.read();
-    // the first PT requests are looked at once
-    Want w0 = {0, 0, 0, 0};
-    if ((int)threadIdx.x < S.B) w0 = want_of(S, nd, threadIdx.x);
+    const Want w0 = want_of(S, threadIdx.x, k0, len0);
     long long sum = w0.need, want = 0;
-    for (int b = threadIdx.x + PT; b < S.B; b += PT) sum += want_of(S, nd, b).need;
+    for (int b = threadIdx.x + PT; b < S.B; b += PT) sum += want_of(S, b, nd[b], S.len[b]).need;
     const long long at0 = cta_scan(sum, tmp, &want);   // (of PT requests at most: their places too)
     // (never past the list, whatever the counts say on the second look)
     const long long free = min((long long)list_free(S, U, want, counts, near), want);
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
         long long at = at0;
         if (b0) {
             w = {0, 0, 0, 0};
-            if (in) w = want_of(S, nd, b);
+            if (in) w = want_of(S, b, nd[b], S.len[b]);
         }
         if (S.B > PT) {
             long long all;
@@ -309,14 +310,13 @@ struct ForkArgs {
     int F;
 };
 
-// The error of fork f as the state was before the call, its length and its partly filled page.
-__device__ __forceinline__ int fork_check(const PageState &S, const ForkArgs &K, int f, int &n, int &tail) {
-    const int p = K.parents[f], c = K.children[f];
-    n = 0;
+// The error of a fork of n tokens of p (or all) to c as the state was before the call, its length and its
+// partly filled page.
+__device__ __forceinline__ int fork_check(const PageState &S, int p, int c, bool all, int &n, int &tail) {
     tail = -1;
     if (p < 0 || p >= S.B || c < 0 || c >= S.B || S.len[c] != 0) return SV_DEV_BAD_LAYOUT;
     const int len = S.len[p];
-    n = K.fork_len ? K.fork_len[f] : len;
+    if (all) n = len;
     if (n < 1 || n > len || (long long)n > (long long)S.max_pages * S.page_size) return SV_DEV_BAD_LAYOUT;
     if (n % S.page_size) {
         tail = S.table[(int64_t)p * S.max_pages + n / S.page_size];
@@ -336,12 +336,17 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
     Used U;
     U.ref = S.ref;
     U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
+    // the first PT forks' first loads go out together with the pool's
+    int p = -1, c = -1, len = 0;
+    auto load = [&](int f) { p = K.parents[f], c = K.children[f], len = K.fork_len ? K.fork_len[f] : 0; };
+    const bool decides = cg::this_cluster().block_rank() == 0;
+    if (decides && (int)threadIdx.x < K.F) load(threadIdx.x);
     U.read();
-    if (cg::this_cluster().block_rank() == 0) {
+    if (decides) {
         for (int f = threadIdx.x; f < K.F; f += PT) {
-            int n, tail;
-            const int err = fork_check(S, K, f, n, tail);
-            const int c = K.children[f];
+            if (f >= PT) load(f);
+            int n = len, tail;
+            const int err = fork_check(S, p, c, !K.fork_len, n, tail);
             const bool claims = c >= 0 && c < S.B && S.len[c] == 0;
             S.result[f] = err ? -err : n;
             K.src[f] = tail;
