@@ -69,14 +69,15 @@ enum { PAIR_NEXT, PAIR_HALVES, PAIR_ANY };
 // head_dim / 8), so a thread's elements are the same in every head it meets, and its weights and
 // rotations serve all of them.
 //
-// What bounds it: a row of 48 heads of 128 is 24 KB in and out, 4 ns at the memory's rate, and about
-// 250 instructions per warp; a call's few rows per CTA also wait once for the chain offsets -> length
-// -> page.  So a CTA walks that chain once, a lane of one warp per row, while the first row's data, the
+// What bounds it: a row of 48 heads of 128 is 24 KB in and out, 4 ns at the memory's rate, but its
+// arithmetic and addresses keep the schedulers busy for half of the time (an instruction in 54 % of the
+// cycles), and a call's few rows per CTA wait once for the chain offsets -> length -> page.  So a CTA walks that chain once, a lane of one warp per row, while the first row's data, the
 // weights and the turns of the frequencies are under way, and then turns all its rows' pairs at once:
 // two barriers in all, and a warp asks for its next row's data before it works on this one's.  1280
 // rows of 48 heads take 9.0 us (3.5 TB/s read and written; with the rotations per row behind a barrier
 // each 10.4, and with one fp32 operation per instruction 10.9); one row takes 3.4 us, the launch.
-// Background copies of the next rows to shared memory: 12.0 before those two steps, no gain.
+// Background copies of the next rows to shared memory: 12.0 before those two steps, no gain; a row's
+// addresses kept per thread and stepped instead of made anew: 9.5.
 template <typename E, int LPH, int PAIR>
 __global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Cache C, const AppendArgs P, int per_cta) {
     __shared__ float2 turn[ROWS][128];   // (cos, sin) * rope_scale of each row's pairs
