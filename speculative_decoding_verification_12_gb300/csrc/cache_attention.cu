@@ -196,26 +196,29 @@ template <typename E, int DP>
 __device__ __forceinline__ bool clean_values(const AttnArgs &P, const Seg &s, int base, int tok, char *tile) {
     const int j = base + tok;
     if (seen_by_all(P, s, j)) return false;
-    const bool any = seen_by_any(P, s, j);
+    // (a different 16 bytes of the row per lane: no two of 8 lanes share a bank)
+    auto at = [&](int i) {
+        return reinterpret_cast<uint4 *>(tile + (i >> 3) * BLK + tok * 128 + (((i ^ tok) & 7) << 4));
+    };
+    if (!seen_by_any(P, s, j)) {
+#pragma unroll 8
+        for (int i = 0; i < DP / 8; i++) *at(i) = make_uint4(0u, 0u, 0u, 0u);
+        return false;
+    }
     bool took = false;
 #pragma unroll 1
     for (int i = 0; i < DP / 8; i++) {
-        // (a different 16 bytes of the row per lane: no two of 8 lanes share a bank)
-        uint4 *at = reinterpret_cast<uint4 *>(tile + (i >> 3) * BLK + tok * 128 + (((i ^ tok) & 7) << 4));
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (any) {
-            w = *at;
-            uint32_t *p = &w.x;
-            bool hit = false;
+        uint4 w = *at(i);
+        uint32_t *p = &w.x;
+        bool hit = false;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                if (!finite16<E>(p[e] & 0xffffu)) p[e] &= 0xffff0000u, hit = true;
-                if (!finite16<E>(p[e] >> 16)) p[e] &= 0xffffu, hit = true;
-            }
-            if (!hit) continue;
-            took = true;
+        for (int e = 0; e < 4; e++) {
+            if (!finite16<E>(p[e] & 0xffffu)) p[e] &= 0xffff0000u, hit = true;
+            if (!finite16<E>(p[e] >> 16)) p[e] &= 0xffffu, hit = true;
         }
-        *at = w;
+        if (!hit) continue;
+        took = true;
+        *at(i) = w;
     }
     return took;
 }
@@ -773,15 +776,9 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             bool any_tile = false;
 #pragma unroll 1
             for (int t = alone ? 0 : mine; t < nt; t += alone ? 1 : 2) {
-                if (!warp_wait(s_full + 8 * g, ns_++ & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if ((warp & 3) == 0 && lane == 0 && (!two || mine)) mbar_arrive(k_empty + 8 * ((tile0 + t) % k_stages));
                 const int base = s.base(s.t0 + t);
                 const bool whole = whole_tile(P, s, base);
-                if (!whole && (!two || mine == 0)) {
+                if (!whole && (!two || mine == 0)) {   // (while this tile's scores are made)
                     const uint32_t round = (tile0 + t) / v_stages, stage = tile0 + t - round * v_stages;
                     if (!warp_wait(v_full + 8 * stage, round & 1, dead)) {
                         ok = false;
@@ -791,6 +788,12 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     fence_proxy_async();
                     __syncwarp();
                 }
+                if (!warp_wait(s_full + 8 * g, ns_++ & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if ((warp & 3) == 0 && lane == 0 && (!two || mine)) mbar_arrive(k_empty + 8 * ((tile0 + t) % k_stages));
                 if (APART && two && !whole) {   // the other group's product reads this V tile too
                     if (lane == 0) mbar_arrive(both);
                     if (!warp_wait(both, joint++ & 1, dead)) {
