@@ -234,11 +234,11 @@ __device__ __forceinline__ Want want_of(const PageState &S, int b, int k, int le
 }
 
 __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const int32_t *nd) {
+    __shared__ int places[PT], rows[PT];   // of the requests looked at: their first page in the list and the table
     __shared__ int counts[PW + 1], near[NEAR];
     __shared__ long long tmp[PW + 1];
     grid_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
     Used U;
     U.ref = S.ref;
     U.s = slice_of(S.num_pages, cg::this_cluster().block_rank(), cg::this_cluster().num_blocks());
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
         const int b = b0 + (int)threadIdx.x;
         const bool in = b < S.B;
         Want w = w0;
-        long long at = at0;
+        long long at = at0, base = before, total = want;
         if (b0) {
             w = {0, 0, 0, 0};
             if (in) w = want_of(S, b, nd[b], S.len[b]);
@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
             long long all;
             at = before + cta_scan(w.need, tmp, &all);
             before += all;
+            total = all;
         }
         if (w.need > 0 && at + w.need > free) {
             w.err = SV_DEV_NO_PAGES;
@@ -286,16 +287,24 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
             row[i] = p;
             S.ref[p] = 1;
         }
-        // longer ones (a prompt's pages) by the whole warp
-        for (unsigned m = __ballot_sync(0xffffffffu, w.need > 4); m; m &= m - 1) {
-            const int l = __ffs(m) - 1;
-            const long long n = __shfl_sync(0xffffffffu, w.need, l), a = __shfl_sync(0xffffffffu, at, l);
-            int32_t *to = reinterpret_cast<int32_t *>(__shfl_sync(0xffffffffu, (unsigned long long)row, l));
-            for (long long i = lane; i < n; i += 32) {
-                const int p = list[a + i];
-                to[i] = p;
+        // longer ones (a prompt's pages) by the whole CTA, a page a thread: the list's i-th page is the last
+        // request's whose place is at or before i (8 prompts of 8192 pages by a warp each: 530 us)
+        places[threadIdx.x] = (int)(at - base);
+        rows[threadIdx.x] = w.need > 4 ? w.have : -1;
+        const int end = (int)max(min(total, free - base), 0ll);   // (what is granted ends before the free pages do)
+        if (__syncthreads_or(w.need > 4)) {
+#pragma unroll 2
+            for (int i = threadIdx.x; i < end; i += PT) {
+                int r = 0;
+#pragma unroll
+                for (int step = PT / 2; step; step >>= 1)
+                    if (places[r + step] <= i) r += step;
+                if (rows[r] < 0) continue;
+                const int p = list[base + i];
+                S.table[(int64_t)(b0 + r) * S.max_pages + rows[r] + (i - places[r])] = p;
                 S.ref[p] = 1;
             }
+            __syncthreads();
         }
     }
 }

@@ -169,6 +169,17 @@ def test_fork_shares_a_page_that_is_none(sv):
     assert sv.sv_read_device_error(p.ws) == (9, 0)
 
 
+@pytest.mark.parametrize("B,M,N,long", [(3, 5000, 15000, 3), (40, 300, 9000, 30), (1500, 40, 30000, 700), (1500, 40, 9000, 900),
+                                        (1024, 9, 5000, 1024)])
+def test_prompts_among_steps(sv, B, M, N, long):
+    """Many pages for some requests and few or none for the others, with enough and too few in the pool."""
+    r = random.Random(B + N)
+    p = Pool(sv, [0] * B, [[-1] * M for _ in range(B)], [int(r.random() < 0.1) for _ in range(N)], 4)
+    want = [r.randint(16, M * 4 - 1) if b < long else r.choice([-1, 0, 3, 4, 15]) for b in range(B)]
+    r.shuffle(want)
+    p.reserve(want)
+
+
 @pytest.mark.parametrize("B,M,forks", [(40, 400, 20), (40, 1024, 20), (40, 1025, 20), (300, 1100, 150), (1300, 7, 1200)])
 def test_many_forks(sv, B, M, forks):
     """Forks of several chunks of a table row and of one short of it; more forks than threads."""
