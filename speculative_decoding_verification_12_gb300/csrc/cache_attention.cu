@@ -31,7 +31,7 @@
 // 4096 keys of 8 heads of 128 read 4.3 GB in 645 us, 6.7 TB/s, one request over 131 071 keys 0.54 GB in
 // 90 us.  Many rows (16 requests of 65 rows, 8 query heads per key head, 8192 keys): the chain of a
 // product, its softmax and the next product on the 512 columns of tensor memory; 161 us, 860 TFLOP/s.
-// Small calls: the chain of launch, lengths, table, first tile, epilogue and join, 11.4 us for one request
+// Small calls: the chain of launch, lengths, table, first tile, epilogue and join, 10.9 us for one request
 // of 2049 keys; short and narrow segments: about 2 us each to change from one to the next.
 #include <math.h>
 
@@ -1286,7 +1286,7 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attention_kernel<E, DP>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
-    // 8 blocks a row tile: 64 windows of 4096 keys take 61 us, 63 with 16; 16 x 65 rows 161 us, 163 with 4
+    // 8 blocks a row tile: 64 windows of 4096 keys took 61 us, 63 with 16; 16 x 65 rows 161 us, 163 with 4
     const int most_rows = (A.k_max + 1) * P.G;
     cfg.gridDim = dim3(ctas, (most_rows < 8 ? most_rows : 8) + 1);
     cfg.blockDim = dim3(256);
