@@ -184,9 +184,8 @@ sv_status spec_page_fork(const int32_t *parents, const int32_t *children, const 
  * spec_page_release -- pages past each request's length go back, and with window > 0 those that
  * no later row can see: pages whose tokens all lie at or before kv_seq_len[b] - window and at or
  * after `sinks`.  A released entry becomes -1 and its page's count falls by one.  A request that
- * ends has its length set to 0 before the call.  Negative lengths are left alone.  The pages of a
- * request reach without a gap from its length (or from the window's start, downward) to the last
- * one held; the search in a direction ends, in steps of 1024 entries, where the last 256 are -1.
+ * ends has its length set to 0 before the call: all that it holds goes back, whatever a window left
+ * of it.  Negative lengths are left alone.
  * SV_DEV_BAD_LAYOUT: a length past max_pages; SV_DEV_BAD_PAGE: an entry that is not a page in use
  * (it becomes -1).
  *   workspace  its header only (256 bytes).

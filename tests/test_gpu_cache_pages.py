@@ -286,3 +286,54 @@ def test_graph_of_a_step(sv):
         p.model.len = [n - 2 for n in p.model.len]
         p.model.release()
         p.same()
+
+
+@pytest.mark.parametrize("L,sinks,window", [(20479, 0, 4096), (20479, 4, 4096), (50000, 0, 4096), (50000, 4, 4096),
+                                            (65536, 5000, 64), (16500, 16384, 1)])
+def test_a_windowed_request_that_ends_gives_every_page_back(sv, L, sinks, window):
+    """A long request whose middle pages went back under its window ends: its table row empties and every
+    count returns to 0, and so again for the slot's next owner."""
+    page, M = 16, 4096
+    r = random.Random(L + sinks)
+    need = -(-L // page)
+    ids = list(range(need + 40))
+    r.shuffle(ids)
+    other = ids[need:need + 5]
+    ref = [0] * len(ids)
+    for p in ids[:need + 5]:
+        ref[p] = 1
+    p = Pool(sv, [L, 5 * page], [ids[:need] + [-1] * (M - need), other + [-1] * (M - 5)], ref, page)
+    for n in (L, 3):
+        p.release(window, sinks)
+        p.set_len(0, 0)
+        p.release(0 if n == 3 else window, sinks)
+        assert p.table[0].tolist() == [-1] * M and int(p.ref.sum()) == 5
+        p.reserve([n - 1, -1])
+    p.release()
+
+
+@pytest.mark.parametrize("L,window,keep", [(50000, 4096, 4), (50000, 4096, 16), (40000, 100, 33)])
+def test_a_windowed_request_cut_to_its_first_tokens(sv, L, window, keep):
+    """Whatever length a caller sets, the pages past it go back, also behind a gap."""
+    page, M, need = 16, 3200, -(-L // 16)
+    p = Pool(sv, [L], [list(range(need)) + [-1] * (M - need)], [1] * need + [0] * 8, page)
+    p.release(window, 33)
+    p.set_len(0, keep)
+    p.release(window, 33)
+    assert int(p.ref.sum()) == -(-keep // page)
+
+
+def test_release_of_rows_of_every_length(sv):
+    """Rows shorter and longer than one CTA's entries, at odd lengths and starts."""
+    for M in (1, 2, 255, 257, 1023, 1024, 1025, 5001):
+        r = random.Random(M)
+        lens, table, ref, n = [], [], [], 0
+        for b in range(5):
+            held = r.randint(0, M)
+            table.append(list(range(n, n + held)) + [-1] * (M - held))
+            ref += [1] * held
+            n += held
+            lens.append(r.choice([0, -3, r.randint(0, held * 8), held * 8]))
+        p = Pool(sv, lens, table, ref + [0], 8)
+        p.release(r.choice([0, 1, 77, 5000]), r.choice([0, 9, 4000]))
+        p.release()
