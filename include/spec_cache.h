@@ -16,7 +16,7 @@
  *     per layer: spec_append     norm and rotate q and k, append k and v to the layer's cache
  *                spec_attention  the rows attend over the layer's cache
  *     spec_verify                (spec_verify.h) the logits' verdict: accept_len
- *     spec_rollback              (spec_verify.h) kv_seq_len[b] <- kv_seq_len[b] - k_b + a_b
+ *     spec_cache_rollback        kv_seq_len[b] <- kv_seq_len[b] - k_b + a_b, the accepted drafts kept
  *     spec_page_release          pages past the new length, or out of the window, go back
  * and between steps spec_page_fork (a new request continues from another's tokens) and
  * spec_page_compact, each followed by spec_page_copy.
@@ -33,8 +33,9 @@
  *    not clear it (spec_verify does): zero the header once before the first call.
  *  - Rows.  Request b owns rows [row_offsets[b], row_offsets[b+1]) (row_offsets == NULL:
  *    [b (k_max+1), (b+1) (k_max+1))) and uses its first num_drafts[b] + 1, as in spec_verify.
- *    num_drafts[b] == -1 marks an idle request: it has no new tokens.  Rows that no request
- *    uses get zero outputs.
+ *    num_drafts[b] == -1 marks an idle request: it has no new tokens, and every call here leaves
+ *    it as it is.  (spec_verify knows no idle requests: give it 0 drafts for one and ignore its
+ *    token.)  Rows that no request uses get zero outputs.
  *  - Lengths.  kv_seq_len[b] counts the new tokens: used row i of request b is the token at
  *    position kv_seq_len[b] - (num_drafts[b] + 1) + i.  A negative length marks a request whose
  *    reservation or fork failed; spec_append and spec_attention treat it as a layout error.
@@ -162,6 +163,17 @@ size_t sv_attention_workspace_bytes(int32_t head_dim);
 sv_status spec_page_reserve(const int32_t *num_drafts, int32_t *kv_seq_len, int32_t B, int32_t *block_table,
                             int32_t max_pages, int32_t *ref_count, int32_t num_pages, int32_t page_size,
                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * spec_cache_rollback -- commits the verdict to the lengths: spec_rollback (spec_verify.h) for a
+ * batch with idle requests.  kv_seq_len[b] <- kv_seq_len[b] - num_drafts[b] + accept_len[b]; an idle
+ * request (num_drafts -1) keeps its length, and its accept_len is not looked at.  num_drafts < -1, an
+ * accept_len outside [0, num_drafts], a negative length or a result outside [0, kv_seq_len]: the
+ * request keeps its length, SV_DEV_BAD_LAYOUT.
+ *   workspace  its header only (256 bytes).
+ */
+sv_status spec_cache_rollback(int32_t *kv_seq_len, const int32_t *accept_len, const int32_t *num_drafts, int32_t B,
+                              void *workspace, void *stream);
 
 /*
  * spec_page_fork -- requests children[f] (empty) continue from the first fork_len[f] tokens of

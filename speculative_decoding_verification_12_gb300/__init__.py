@@ -237,8 +237,8 @@ def sv_read_device_error(workspace):
 
 def __getattr__(name):
     """The cache-side calls (cache.py, which imports torch) by the package's name."""
-    if name in ("spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
-                "spec_page_compact", "spec_page_copy", "sv_attention_workspace_bytes", "sv_page_workspace_bytes",
+    if name in ("spec_append", "spec_attention", "spec_cache_rollback", "spec_page_reserve", "spec_page_fork",
+                "spec_page_release", "spec_page_compact", "spec_page_copy", "sv_attention_workspace_bytes", "sv_page_workspace_bytes",
                 "SvKvCache", "SV_F16", "PagedCache"):
         from . import cache
         globals()[name] = f = getattr(cache, name)

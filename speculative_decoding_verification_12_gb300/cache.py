@@ -36,6 +36,7 @@ def _lib():
                 ("spec_append", [P, P, P, L, L, L, I, P, P, F, P, I, I, F, P, P, P, I, I, I, SvKvCache, P, L, P, P]),
                 ("spec_attention", [P, L, I, P, P, P, I, I, I, SvKvCache, F, I, I, P, P, P, Z, P]),
                 ("spec_page_reserve", [P, P, I, P, I, P, I, I, P, Z, P]),
+                ("spec_cache_rollback", [P, P, P, I, P, P]),
                 ("spec_page_fork", [P, P, P, I, P, I, P, I, P, I, I, P, P, P, Z, P]),
                 ("spec_page_release", [P, I, P, I, P, I, I, I, I, P, P]),
                 ("spec_page_compact", [I, P, I, P, I, P, P, I, P, Z, P]),
@@ -58,6 +59,9 @@ def sv_page_workspace_bytes(B: int, num_pages: int) -> int:
     return int(_lib().sv_page_workspace_bytes(B, num_pages))
 
 
+# the entry points that the compiled binding calls, in its order
+ENTRIES = ("spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
+           "spec_page_compact", "spec_page_copy", "spec_rollback", "spec_cache_rollback")
 _native = None
 
 
@@ -70,9 +74,7 @@ def _load():
         raise RuntimeError("the compiled binding is missing: build it first "
                            "(python -c 'import __graft_entry__ as g; g.build()')") from e
     l = _lib()
-    _binding.init(*(C.cast(getattr(l, name), C.c_void_p).value for name in (
-        "spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
-        "spec_page_compact", "spec_page_copy", "spec_rollback")), torch._C._cuda_getCurrentRawStream)
+    _binding.init(*(C.cast(getattr(l, name), C.c_void_p).value for name in ENTRIES), torch._C._cuda_getCurrentRawStream)
     _native = _binding
     return _binding
 
@@ -120,6 +122,13 @@ def spec_page_reserve(num_drafts, kv_seq_len, block_table, ref_count, page_size:
     st = (_native or _load()).reserve(num_drafts, kv_seq_len, block_table, ref_count, page_size, workspace, stream)
     if st != SV_OK:
         raise SvError(st, "spec_page_reserve")
+
+
+def spec_cache_rollback(kv_seq_len, accept_len, num_drafts, workspace, stream=None) -> None:
+    """kv_seq_len[b] <- kv_seq_len[b] - num_drafts[b] + accept_len[b] (-1 drafts: an idle request, unchanged)."""
+    st = (_native or _load()).commit(kv_seq_len, accept_len, num_drafts, workspace, stream)
+    if st != SV_OK:
+        raise SvError(st, "spec_cache_rollback")
 
 
 def spec_page_fork(parents, children, fork_len, kv_seq_len, block_table, ref_count, page_size: int, copy_src,
@@ -197,10 +206,9 @@ class PagedCache:
                        k_max, scale, window, sinks, out, out_lse, self.workspace, stream)
 
     def commit(self, accept_len, num_drafts, window=0, sinks=0, stream=None) -> None:
-        """Rolls every request back to its accepted drafts and gives the pages past them back."""
-        st = rollback(self.kv_seq_len, accept_len, num_drafts, self.workspace, stream)
-        if st != SV_OK:
-            raise SvError(st, "spec_rollback")
+        """Rolls every request back to its accepted drafts (idle ones, -1 drafts, stay) and gives the
+        pages past them back."""
+        spec_cache_rollback(self.kv_seq_len, accept_len, num_drafts, self.workspace, stream)
         self.release(window, sinks, stream)
 
     def release(self, window=0, sinks=0, stream=None) -> None:

@@ -24,6 +24,7 @@ struct Entry {
     decltype(&spec_page_compact) compact;
     decltype(&spec_page_copy) copy;
     decltype(&spec_rollback) rollback;
+    decltype(&spec_cache_rollback) commit;
     PyObject *raw_stream;   // torch._C._cuda_getCurrentRawStream
 } lib;
 
@@ -309,6 +310,16 @@ sv_status rollback(Args a) {
     return lib.rollback(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
 }
 
+// The same for spec_cache_rollback.
+sv_status commit(Args a) {
+    int64_t n;
+    size_t bytes;
+    int32_t *ln = static_cast<int32_t *>(a.data(0, "kv_seq_len", I32, -1, &n));
+    const int32_t *acc = ints(a.data(1, "accept_len", I32, n)), *nd = ints(a.data(2, "num_drafts", I32, n));
+    void *ws = a.workspace(3, &bytes);
+    return lib.commit(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
+}
+
 template <sv_status (*F)(Args), int N>
 PyObject *call(PyObject *, PyObject *const *v, Py_ssize_t n) {
     if (n != N) {
@@ -331,12 +342,12 @@ PyObject *call(PyObject *, PyObject *const *v, Py_ssize_t n) {
 
 // Addresses of the entry points in the order of Entry, then the raw-stream function.
 PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    if (n != 9) {
-        PyErr_SetString(PyExc_TypeError, "expected 9 arguments");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "expected 10 arguments");
         return nullptr;
     }
-    void *p[8];
-    for (int i = 0; i < 8; i++) {
+    void *p[9];
+    for (int i = 0; i < 9; i++) {
         p[i] = PyLong_AsVoidPtr(v[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -351,8 +362,9 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
     lib.compact = reinterpret_cast<decltype(lib.compact)>(p[5]);
     lib.copy = reinterpret_cast<decltype(lib.copy)>(p[6]);
     lib.rollback = reinterpret_cast<decltype(lib.rollback)>(p[7]);
-    Py_INCREF(v[8]);
-    lib.raw_stream = v[8];
+    lib.commit = reinterpret_cast<decltype(lib.commit)>(p[8]);
+    Py_INCREF(v[9]);
+    lib.raw_stream = v[9];
     Py_RETURN_NONE;
 }
 
@@ -366,6 +378,7 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("compact", (call<compact, 6>)),
                          FAST("copy", (call<copy, 6>)),
                          FAST("rollback", (call<rollback, 5>)),
+                         FAST("commit", (call<commit, 5>)),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Checks of tensors before the cache-side calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,4 +1,4 @@
-// cache_pages.cu -- page bookkeeping of the paged KV cache: reserve, fork, release, compact, copy.
+// cache_pages.cu -- page bookkeeping of the paged KV cache: reserve, rollback, fork, release, compact, copy.
 //
 // The only record of what is free is ref_count itself (0: free), and pages are taken lowest id
 // first, in request order: rank r of the free pages goes to the r-th page asked for.  Both ranks
@@ -307,6 +307,26 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
             __syncthreads();
         }
     }
+}
+
+// ---------------------------------------------------------------------------------------------
+// rollback
+// ---------------------------------------------------------------------------------------------
+
+constexpr int BT = 256;
+
+// One pass over three words a request: bound by the launch.
+__global__ void __launch_bounds__(BT) rollback_kernel(int32_t *len, const int32_t *accept, const int32_t *nd, int B,
+                                                      int32_t *hdr) {
+    grid_wait();
+    grid_launch_dependents();
+    const int b = blockIdx.x * BT + (int)threadIdx.x;
+    if (b >= B) return;
+    const int k = nd[b], a = accept[b], L = len[b];
+    if (k == -1) return;
+    const long long kept = (long long)L - k + a;
+    if (k < 0 || a < 0 || a > k || kept < 0) record_error(hdr, SV_DEV_BAD_LAYOUT, b);   // (kept <= L: a <= k)
+    else len[b] = (int)kept;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -697,6 +717,16 @@ extern "C" sv_status spec_page_reserve(const int32_t *num_drafts, int32_t *kv_se
     if (workspace_bytes < page_ws(B, num_pages).total) return SV_ERR_WORKSPACE;
     const PageState S = page_state(kv_seq_len, B, block_table, max_pages, ref_count, num_pages, page_size, workspace);
     return launch_cluster(reserve_kernel, num_pages, static_cast<cudaStream_t>(stream), S, num_drafts) == cudaSuccess
+               ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status spec_cache_rollback(int32_t *kv_seq_len, const int32_t *accept_len, const int32_t *num_drafts,
+                                         int32_t B, void *workspace, void *stream) {
+    if (B < 1 || !kv_seq_len || !accept_len || !num_drafts || !workspace) return SV_ERR_INVALID_ARG;
+    if (B >= MAXB) return SV_ERR_UNSUPPORTED;
+    if ((uintptr_t)workspace & 255) return SV_ERR_WORKSPACE;
+    return launch_dependent(rollback_kernel, dim3((B + BT - 1) / BT), dim3(BT), 1, static_cast<cudaStream_t>(stream), kv_seq_len,
+                            accept_len, num_drafts, (int)B, static_cast<int32_t *>(workspace)) == cudaSuccess
                ? SV_OK : SV_ERR_CUDA;
 }
 

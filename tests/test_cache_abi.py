@@ -147,3 +147,15 @@ def test_binding_refuses_wrong_tensors(sv):
         sv.spec_page_compact(tab, i, i, i, ws)
     with pytest.raises(ValueError):
         sv.spec_page_copy(c, c, i, i, ws)
+
+
+def test_cache_rollback_refusals(sv):
+    def call(ln=PTR, acc=PTR, nd=PTR, B=2, ws=PTR):
+        return sv.lib().spec_cache_rollback(ln, acc, nd, B, ws, None)
+
+    for bad, want in [(dict(ln=None), INV), (dict(acc=None), INV), (dict(nd=None), INV), (dict(B=0), INV),
+                      (dict(ws=None), INV), (dict(ws=128), WS), (dict(B=1 << 25), UNS)]:
+        assert call(**bad) == want, bad
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        sv.spec_cache_rollback(i, i, i, torch.zeros(256, dtype=torch.uint8))

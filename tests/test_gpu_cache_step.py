@@ -59,3 +59,44 @@ def test_bounded_waits_run_out(sv):
         ws[:256] = 0
         call(again)
         assert sv.sv_read_device_error(ws) == (0, -1) and torch.equal(out, again)
+
+
+def test_idle_slots_in_a_whole_step(sv):
+    """Slots without a request (num_drafts -1), empty and resting ones, from the reservation to the commit: no
+    length, page or error word of theirs changes, whatever accept_len holds for them."""
+    c = sv.PagedCache(1, 6, 40, 8, 8, 1, 64)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    c.reserve(ints(9, -1, 20, 3, -1, 0))
+    before = c.block_table[2].tolist()
+    x = torch.randn(6 * 5, 1, 64, device="cuda").bfloat16()
+    for nd, acc in [(ints(4, -1, -1, 0, -1, 2), ints(2, -1, 99, 0, -1, 2)), (ints(-1, -1, -1, 4, -1, -1), ints(0, 5, 1, 0, 0, 7))]:
+        out, again = torch.empty_like(x), torch.empty_like(x)
+        lens = c.kv_seq_len.tolist()
+        c.reserve(nd)
+        c.append(0, x, x, x, None, None, 0.0, None, nd, None, 4, out)
+        c.attend(0, out, nd, None, 4, 0.125, again)
+        c.commit(acc, nd)
+        want = [n + 1 + a if k >= 0 else n for n, k, a in zip(lens, nd.tolist(), acc.tolist())]
+        assert c.kv_seq_len.tolist() == want
+        assert sv.sv_read_device_error(c.workspace) == (0, -1)
+    assert c.block_table[2].tolist() == before and c.kv_seq_len[2] == 21
+    assert int(c.ref_count.sum()) == sum(-(-n // 8) for n in c.kv_seq_len.tolist())
+
+
+def test_commit_still_reports_what_is_wrong(sv):
+    """Drafts below -1, accepted drafts below 0 or above the drafts, and failed reservations keep their length."""
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for nd, acc, length in [(-2, 0, 9), (2, -1, 9), (2, 3, 9), (2, 1, -10), (8, 0, 7)]:
+        c = sv.PagedCache(1, 2, 10, 8, 4, 1, 64)
+        c.reserve(ints(8, 4))
+        c.kv_seq_len[0] = length
+        c.commit(ints(acc, 1), ints(nd, 4))
+        assert c.kv_seq_len.tolist() == [length, 2] and sv.sv_read_device_error(c.workspace) == (1, 0)
+
+
+def test_rollback_itself_takes_no_idle_requests(sv):
+    """spec_rollback's own rule is unchanged: drafts below 0 are an error."""
+    kv, acc, nd = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([9, 9], [0, 1], [-1, 3]))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sv.spec_rollback(kv, acc, nd, ws)
+    assert kv.tolist() == [9, 7] and sv.sv_read_device_error(ws) == (1, 0)
