@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Ca
     const int sub = tid % LPH, h_first = tid / LPH;
     const int rot = 2 * P.half;
     const float inv_d = 1.f / (float)D;
+    // one weight alone: a warp then holds heads with and without a norm
+    const bool q_alone = P.kw == nullptr, one_alone = q_alone != (P.qw == nullptr);
     // this thread's elements: [d0, d0 + 4) and [d1, d1 + 4)
     const bool turns = PAIR == PAIR_HALVES ? sub * 4 < P.half : sub * 8 < rot;
     const int d0 = PAIR != PAIR_HALVES ? sub * 8 : turns ? sub * 4 : rot + (sub - P.half / 4) * 8;
@@ -112,7 +114,8 @@ __global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Ca
 
     grid_wait();
     grid_launch_dependents();
-    uint4 raw[AU], qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
+    constexpr uint32_t ONE2 = Num<E>::ONE2;
+    uint4 raw[AU], qw = make_uint4(ONE2, ONE2, ONE2, ONE2), kw = qw;   // (no weight: ones)
     // Row i's elements of head h.
     auto source = [&](int h, int i) {
         const int64_t r = first + i;
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Ca
                 }
                 float2 x[4];
                 unpack8<E>(mine, reinterpret_cast<float *>(x));
-                if (is_k ? P.kw != nullptr : P.qw != nullptr) {
+                if (P.qw || P.kw) {   // (the whole grid, so that a warp's shuffles are together)
                     float2 s2 = make_float2(0.f, 0.f), g[4];
 #pragma unroll
                     for (int e = 0; e < 4; e++) s2 = fma2(x[e], x[e], s2);
@@ -215,7 +218,8 @@ __global__ void __launch_bounds__(AT, OCC) append_kernel(const Batch A, const Ca
 #pragma unroll
                     for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                     unpack8<E>(is_k ? kw : qw, reinterpret_cast<float *>(g));
-                    const float inv = rsqrtf(fmaf(ss, inv_d, P.eps));
+                    float inv = rsqrtf(fmaf(ss, inv_d, P.eps));
+                    if (one_alone && is_k == q_alone) inv = 1.f;   // (and its weights are ones)
 #pragma unroll
                     for (int e = 0; e < 4; e++) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
                 }

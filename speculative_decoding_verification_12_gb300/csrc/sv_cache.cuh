@@ -126,7 +126,7 @@ struct Num<__nv_bfloat16> {
         const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&r);
     }
-    static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr uint32_t NAN2 = 0x7fff7fffu, ONE2 = 0x3f803f80u;
     static constexpr bool BF16 = true;
 };
 template <>
@@ -138,7 +138,7 @@ struct Num<__half> {
         const __half2 r = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&r);
     }
-    static constexpr uint32_t NAN2 = 0x7fff7fffu;
+    static constexpr uint32_t NAN2 = 0x7fff7fffu, ONE2 = 0x3c003c00u;
     static constexpr bool BF16 = false;
 };
 

@@ -254,3 +254,14 @@ def test_another_stream_and_graph(sv):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), ref[0]) and torch.equal(dev["kc"].cpu(), ref[1])
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("D,rotary,il", [(64, 64, False), (64, 64, True), (64, 20, False), (16, 0, False), (128, 128, False),
+                                         (128, 64, True), (128, 70, False), (256, 256, False), (136, 36, False)])
+def test_one_weight_alone(sv, which, D, rotary, il):
+    """A norm of the queries or of the keys alone, with query, key and value heads of all counts in one warp."""
+    for Hq, Hk in [(7, 7), (7, 1), (3, 3), (1, 1), (5, 5), (33, 11)]:
+        s = make(D + Hq, [1, 9, 40], [0, 3, 4], 4, Hq, Hk, D, 16, "bf16", rotary)
+        s["w"] = (s["w"][0], None) if which == 0 else (None, s["w"][1])
+        run_and_check(sv, s, il)
