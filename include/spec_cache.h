@@ -154,9 +154,10 @@ size_t sv_attention_workspace_bytes(int32_t head_dim);
  * the pages that this needs.  Requests are served in order; one for which the free pages do not
  * suffice, counting those asked for before it, is SV_DEV_NO_PAGES.  Also SV_DEV_BAD_LAYOUT
  * (num_drafts < -1, a negative length, more than max_pages), SV_DEV_SHARED_PAGE and
- * SV_DEV_BAD_PAGE (the partly filled last page is shared, or not a page).  A request that fails
- * takes no page, and its length becomes -1 - length until the caller repairs it, so that the
- * step's other calls leave it alone.
+ * SV_DEV_BAD_PAGE (the partly filled last page is shared, or not a page in use before the call).
+ * Table entries past a request's length are overwritten, not given back: release them first.
+ * A request that fails takes no page, and its length becomes -1 - length until the caller repairs
+ * it, so that the step's other calls leave it alone.
  *   workspace  sv_page_workspace_bytes(B, num_pages) bytes, 256-byte aligned.
  *   B < 2^25, max_pages <= 2^20, num_pages < 2^28, B * max_pages < 2^40.
  */

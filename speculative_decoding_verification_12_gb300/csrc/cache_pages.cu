@@ -31,7 +31,7 @@ struct PageState {
     int B, max_pages, num_pages, page_size;
     int32_t *hdr;
     int32_t *list;      // workspace: num_pages entries
-    int32_t *result;    // workspace: B entries (fork: the child's length, or -1)
+    int32_t *result;    // workspace: B entries (reserve: pages asked for; fork: the child's length, or -1; < 0: an error)
     int32_t *used;      // workspace: pages in use (compact)
 };
 
@@ -207,6 +207,11 @@ __device__ __forceinline__ int list_free(const PageState &S, const Used &U, long
 // reserve
 // ---------------------------------------------------------------------------------------------
 
+// Pages that hold len >= 0 tokens.
+__device__ __forceinline__ int pages_of(const PageState &S, int len) {
+    return len / S.page_size + (len % S.page_size != 0);
+}
+
 struct Want {
     int err, have, grown;
     long long need;
@@ -221,7 +226,7 @@ __device__ __forceinline__ Want want_of(const PageState &S, int b, int k, int le
         w.err = SV_DEV_BAD_LAYOUT;
         return w;
     }
-    w.have = len / S.page_size + (len % S.page_size != 0);
+    w.have = pages_of(S, len);
     w.grown = (int)grown;
     w.need = (grown + S.page_size - 1) / S.page_size - w.have;
     if (len % S.page_size) {   // the partly filled page: this request's alone
@@ -248,11 +253,15 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
     U.read();
     const Want w0 = want_of(S, threadIdx.x, k0, len0);
     long long sum = w0.need, want = 0;
-    for (int b = threadIdx.x + PT; b < S.B; b += PT) sum += want_of(S, b, nd[b], S.len[b]).need;
+    const bool decides = cg::this_cluster().block_rank() == 0;
+    for (int b = threadIdx.x + PT; b < S.B; b += PT) {
+        const Want w = want_of(S, b, nd[b], S.len[b]);
+        sum += w.need;
+        if (decides) S.result[b] = w.err ? -w.err : (int)w.need;   // (kept: a later look would see pages that this call grants)
+    }
     const long long at0 = cta_scan(sum, tmp, &want);   // (of PT requests at most: their places too)
-    // (never past the list, whatever the counts say on the second look)
-    const long long free = min((long long)list_free(S, U, want, counts, near), want);
-    if (cg::this_cluster().block_rank() != 0) return;
+    const long long free = list_free(S, U, want, counts, near);
+    if (!decides) return;
     const int32_t *list = want <= NEAR ? near : S.list;
     long long before = 0;
     for (int b0 = 0; b0 < S.B; b0 += PT) {
@@ -262,7 +271,11 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const PageState S, const in
         long long at = at0, base = before, total = want;
         if (b0) {
             w = {0, 0, 0, 0};
-            if (in) w = want_of(S, b, nd[b], S.len[b]);
+            if (in && nd[b] != -1) {
+                const int r = S.result[b], len = S.len[b];
+                if (r < 0) w.err = -r;
+                else w = {0, pages_of(S, len), len + nd[b] + 1, r};
+            }
         }
         if (S.B > PT) {
             long long all;
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(ST) release_kernel(const PageState S, int wind
     const int len = S.len[b];
     if (len < 0) return;
     int32_t *row = S.table + (int64_t)b * S.max_pages;
-    const int keep = len / S.page_size + (len % S.page_size != 0);
+    const int keep = pages_of(S, len);
     if (keep > S.max_pages) {
         if (threadIdx.x == 0 && blockIdx.y == 0) record_error(S.hdr, SV_DEV_BAD_LAYOUT, b);
         return;

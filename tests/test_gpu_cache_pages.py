@@ -337,3 +337,57 @@ def test_release_of_rows_of_every_length(sv):
         p = Pool(sv, lens, table, ref + [0], 8)
         p.release(r.choice([0, 1, 77, 5000]), r.choice([0, 9, 4000]))
         p.release()
+
+
+def reserve_by_the_state_before(p, drafts):
+    """p.reserve, where the model's counts are read as they were before the call: a partly filled page without
+    a request is none, also once another request has been granted it."""
+    m, hidden = p.model, {}
+    for b, L in enumerate(m.len):
+        if L > 0 and L % m.P:
+            x = m.table[b][L // m.P]
+            if 0 <= x < len(m.ref) and m.ref[x] < 1:
+                hidden[b, L // m.P], m.table[b][L // m.P] = x, -1
+    m.reserve(ints(drafts))
+    for (b, i), x in hidden.items():
+        m.table[b][i] = x
+    p.sv.spec_page_reserve(ints(drafts).cuda(), p.len, p.table, p.ref, p.page, p.ws)
+    p.same()
+
+
+@pytest.mark.parametrize("B", [1023, 1024, 1025, 2100, 3000])
+def test_reserve_judges_every_request_by_the_state_before_the_call(sv, B):
+    """The last request's partly filled page is a free one, which the same call grants to the first request:
+    still no page in use, however many requests lie between; and the requests behind it are served."""
+    page, N = 4, B + 8
+    lens = [0] * (B - 2) + [2, 0]
+    table = [[-1, -1] for _ in range(B)]
+    table[B - 2][0] = 0
+    p = Pool(sv, lens, table, [0] * N, page)
+    reserve_by_the_state_before(p, [0] * (B - 2) + [4, 7])
+    assert p.model.errors == [(9, B - 2)]
+
+
+def test_reserve_of_many_requests_with_errors_among_them(sv):
+    r = random.Random(77)
+    for N in (6000, 2200):
+        B, M, page = 2600, 4, 8
+        lens, table, ref, n = [], [], [0] * N, 0
+        for b in range(B):
+            L = r.choice([0, 0, r.randint(1, 2 * page)]) if n < 1500 else 0
+            row = [-1] * M
+            for x in range(-(-L // page)):
+                row[x] = n
+                ref[n] = 1
+                n += 1
+            what = r.random()
+            if L % page and what < 0.1:
+                row[L // page] = r.choice([-1, N, r.randrange(1600, 1700)])
+            elif L % page and what < 0.2:
+                ref[row[L // page]] = r.choice([0, 2])
+            elif what < 0.22:
+                L = -5
+            lens.append(L)
+            table.append(row)
+        p = Pool(sv, lens, table, ref, page)
+        reserve_by_the_state_before(p, [r.choice([-2, -1, 0, 1, 8, 15, 31]) for _ in range(B)])
