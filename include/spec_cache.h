@@ -181,8 +181,8 @@ sv_status spec_cache_rollback(int32_t *kv_seq_len, const int32_t *accept_len, co
  * requests parents[f] (fork_len NULL: from all).  The parent's full pages are shared; a partly
  * filled last page becomes a fresh page of the child, and (copy_src[f], copy_dst[f]) is the pair
  * to copy in every layer (spec_page_copy), or (-1, -1).  Entries of -1 (out of a window) stay -1.
- * Lengths and tables are read as they were before the call.  SV_DEV_BAD_LAYOUT: an index outside
- * [0, B), a child that is not empty or already taken by a lower f, fork_len outside
+ * Lengths, tables and counts are read as they were before the call.  SV_DEV_BAD_LAYOUT: an index
+ * outside [0, B), a child that is not empty or already taken by a lower f, fork_len outside
  * [1, kv_seq_len[parent]]; SV_DEV_BAD_PAGE: the partly filled page is not a page in use, or a
  * shared one is not (its entry becomes -1); SV_DEV_NO_PAGES as above, in order of f.  The error's
  * request is f.  A fork that fails shares nothing, its pair is (-1, -1), and a child that was empty

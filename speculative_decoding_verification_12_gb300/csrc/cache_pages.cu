@@ -432,10 +432,18 @@ __global__ void __launch_bounds__(PT) fork_kernel(const PageState S, const ForkA
             K.dst[f] = fresh;
         }
     }
+    __syncthreads();   // (the list has been read)
+    for (int f = threadIdx.x; f < K.F; f += PT) {   // list[page taken] = the fork that took it, for fork_share
+        const int fresh = K.dst[f];
+        if (fresh >= 0) S.list[fresh] = f;
+    }
 }
 
 constexpr int ST = 256, SPT = 4;   // threads per CTA, table entries per thread
 
+// The children's tables, and a count more for each shared page.  A page that no request held before the
+// call is not shared: its count is 0, which nothing here changes, or 1 because fork_kernel took it, which
+// its entry of the list tells (whatever else the list holds there names no fork that took it).
 __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkArgs K) {
     grid_wait();
     grid_launch_dependents();
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkAr
     const int32_t *from = S.table + (int64_t)K.parents[f] * S.max_pages;
     int32_t *to = S.table + (int64_t)K.children[f] * S.max_pages;
     const int full = n / S.page_size, fresh = K.dst[f];
-    int p[SPT], count[SPT];
+    int p[SPT], count[SPT], taker[SPT];
     const int j0 = blockIdx.y * SPT * ST + threadIdx.x;
 #pragma unroll
     for (int t = 0; t < SPT; t++) {
@@ -455,14 +463,16 @@ __global__ void __launch_bounds__(ST) fork_share(const PageState S, const ForkAr
 #pragma unroll
     for (int t = 0; t < SPT; t++) {
         const bool is = p[t] >= 0 && p[t] < S.num_pages;
-        count[t] = is ? atomicAdd(S.ref + p[t], 1) : p[t] == -1 ? 1 : 0;
+        count[t] = is ? __ldcg(S.ref + p[t]) : 0;
+        taker[t] = is ? S.list[p[t]] : -1;
     }
 #pragma unroll
     for (int t = 0; t < SPT; t++) {
         const int j = j0 + t * ST;
         if (j >= S.max_pages) break;
-        if (count[t] < 1) {   // not a page, or one that no request holds
-            if (p[t] >= 0 && p[t] < S.num_pages) atomicSub(S.ref + p[t], 1);
+        if (count[t] > 0 && !(taker[t] >= 0 && taker[t] < K.F && K.dst[taker[t]] == p[t])) {
+            atomicAdd(S.ref + p[t], 1);
+        } else if (p[t] != -1) {   // not a page, or one that no request holds
             record_error(S.hdr, SV_DEV_BAD_PAGE, f);
             p[t] = -1;
         }

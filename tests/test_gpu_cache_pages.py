@@ -391,3 +391,39 @@ def test_reserve_of_many_requests_with_errors_among_them(sv):
             table.append(row)
         p = Pool(sv, lens, table, ref, page)
         reserve_by_the_state_before(p, [r.choice([-2, -1, 0, 1, 8, 15, 31]) for _ in range(B)])
+
+
+@pytest.mark.parametrize("extra", [0, 2100])
+def test_fork_shares_no_page_that_was_free_before_the_call(sv, extra):
+    """Full pages of a parent that no request holds are no pages in use, for each of several children,
+    also where the same call takes them as fresh pages, and with more forks than a CTA's list holds."""
+    B, N, page = 8 + extra, 60 + 2 * extra, 4
+    # parent 0: 6 tokens, pages 40 and 41; parent 1: 12 tokens, pages 0 and 5 free, 42 in use; parent 2: as parent 0
+    table = [[-1] * 3 for _ in range(B)]
+    table[0][:2], table[1][:], table[2][:2] = [40, 41], [0, 5, 42], [43, 44]
+    ref = [0] * N
+    for p in range(40, 45):
+        ref[p] = 1
+    lens = [6, 12, 6] + [0] * (B - 3)
+    pa = [0, 1, 1, 2, 1] + [0] * extra
+    ch = [3, 4, 5, 6, 7] + list(range(8, B))
+    t, n, c = ints(table).cuda(), ints(lens).cuda(), ints(ref).cuda()
+    F = len(pa)
+    src, dst = torch.full((2, F), 55, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(sv.sv_page_workspace_bytes(B, N), dtype=torch.uint8, device="cuda")
+    ws[256:] = 171
+    sv.spec_page_fork(ints(pa).cuda(), ints(ch).cuda(), None, n, t, c, page, src, dst, ws)
+    assert sv.sv_read_device_error(ws) == (9, 1)
+    fresh = [p for p in range(N) if ref[p] == 0][:2 + extra]
+    assert t[3].tolist() == [40, fresh[0], -1] and t[6].tolist() == [43, fresh[1], -1]
+    for child in (4, 5, 7):
+        assert t[child].tolist() == [-1, -1, 42]
+    want = list(ref)
+    for p in fresh:
+        want[p] = 1
+    want[40] += 1 + extra
+    want[43] += 1
+    want[42] += 3
+    assert c.tolist() == want
+    assert dst.tolist() == [fresh[0], -1, -1, fresh[1], -1] + fresh[2:]
+    assert n.tolist()[:8] == [6, 12, 6, 6, 12, 12, 6, 12]
