@@ -1245,8 +1245,6 @@ constexpr int SMEM_MAX = 232448;
 template <typename E, int DP>
 static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, const sv_kv_cache &cache, cudaStream_t st) {
     constexpr int STAGE = DP / 64 * BLK;
-    CUtensorMap mk, mv;
-    if (!encode(&mk, cache, cache.k) || !encode(&mv, cache, cache.v)) return SV_ERR_CUDA;
     int dev = 0, nsm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -1275,6 +1273,9 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     if (most < ctas) ctas = (int)most;
     if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SV_ERR_CUDA;
+    // (after a runtime call that brings this host thread to the device: encoding alone does not, and fails in a new thread)
+    CUtensorMap mk, mv;
+    if (!encode(&mk, cache, cache.k) || !encode(&mv, cache, cache.v)) return SV_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(NTHREADS);

@@ -363,3 +363,28 @@ def test_pool_past_32_bits(sv):
     x.call()
     got = x.results()
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_first_call_of_a_host_thread(sv):
+    """A thread whose first CUDA call of all is this one: the library itself brings it to the device."""
+    import threading
+
+    s = make(48, [300], [2], 2, 4, 2, 64, 16, "bf16", ragged=False)
+    x = OnGpu(sv, s)
+    x.call()
+    want = x.results()
+    x.out.fill_(7.0)
+    stream, failed = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+
+    def run():
+        try:
+            x.call(stream.cuda_stream)
+        except Exception as e:
+            failed.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert not failed
+    assert torch.equal(x.results()[0], want[0])
