@@ -1271,7 +1271,8 @@ static sv_status launch_attention(const Batch &A, const Cache &C, AttnArgs P, co
     if (C.D * 2 % 128 && cache.head_stride * 2 % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas)
         ctas -= ctas % C.heads;
     if (most < ctas) ctas = (int)most;
-    if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // (one limit for every call: another thread's call may come between this and the launch)
+    if (cudaFuncSetAttribute(attention_kernel<E, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
         return SV_ERR_CUDA;
     // (after a runtime call that brings this host thread to the device: encoding alone does not, and fails in a new thread)
     CUtensorMap mk, mv;

@@ -388,3 +388,40 @@ def test_first_call_of_a_host_thread(sv):
     t.join()
     assert not failed
     assert torch.equal(x.results()[0], want[0])
+
+
+def test_threads_with_different_row_counts(sv):
+    """Two threads, a stream and a workspace each, whose calls need different amounts of shared memory: every
+    one is launched.  (The library is called without the interpreter's lock.)"""
+    import threading
+
+    from speculative_decoding_verification_12_gb300 import cache
+    lib, want, fails = cache._lib(), [], []
+
+    def prepare(G, k_max, D):
+        s = make(50 + G, [k_max + 90], [k_max], k_max, G, 1, D, 16, "bf16", ragged=False)
+        x = OnGpu(sv, s)
+        x.call()
+        want.append(x.results()[0])
+        x.out.fill_(7.0)
+        kc = x.kc
+        view = sv.SvKvCache(kc.data_ptr(), x.vc.data_ptr(), *kc.stride()[:3], kc.shape[0], 16, 1, D, 1, x.table.shape[1],
+                            x.table.data_ptr())
+        stream = torch.cuda.Stream()
+        args = (x.q.data_ptr(), x.q.stride(0), G, x.nd.data_ptr(), None, x.lens.data_ptr(), 1, k_max, k_max + 1, view,
+                s["scale"], 0, 0, x.out.data_ptr(), None, x.ws.data_ptr(), x.ws.numel(), stream.cuda_stream)
+        return x, args, stream
+
+    calls = [prepare(1, 0, 128), prepare(8, 64, 128)]
+    torch.cuda.synchronize()
+
+    def run(args):
+        fails.append([s for s in (lib.spec_attention(*args) for _ in range(4000)) if s])
+
+    threads = [threading.Thread(target=run, args=(c[1],)) for c in calls]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert fails == [[], []]
+    for (x, _, _), w in zip(calls, want):
+        assert torch.equal(x.results()[0], w)
