@@ -937,10 +937,11 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
             }
             if (!ok) break;
             tc_fence_after();
-            if (pair && few) {   // (the barrier that ends a pair: group 1's part is handed over before it)
+            float2 part0 = {}, part1 = {};   // the groups' (m, l) of this row
+            if (pair) part0 = ex[row], part1 = ex[TILE + row];
+            if (pair && few) {   // (the barrier that ends a pair: group 1's part is handed over, and both have read ex, before it)
                 if (g && warp_on) {
-                    const float2 a = ex[row], b = ex[TILE + row];
-                    const float f = b.x == fmaxf(a.x, b.x) ? 1.f : ex2((b.x - a.x) * P.c);
+                    const float f = part1.x == fmaxf(part0.x, part1.x) ? 1.f : ex2((part1.x - part0.x) * P.c);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
@@ -966,11 +967,10 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                 // the part's maximum and sum, and the factors of the (up to) two sums O
                 float f0 = 1.f, f1 = 0.f;
                 if (pair) {
-                    const float2 a = ex[row], b = ex[TILE + row];
-                    m = fmaxf(a.x, b.x);
-                    f0 = a.x == m ? 1.f : ex2((a.x - m) * P.c);
-                    f1 = b.x == m ? 1.f : ex2((b.x - m) * P.c);
-                    l = a.y * f0 + b.y * f1;
+                    m = fmaxf(part0.x, part1.x);
+                    f0 = part0.x == m ? 1.f : ex2((part0.x - m) * P.c);
+                    f1 = part1.x == m ? 1.f : ex2((part1.x - m) * P.c);
+                    l = part0.y * f0 + part1.y * f1;
                 }
                 if (broken) l = NAN;
                 const float inv = (l == 0.f && !direct) ? 0.f : rcp(l);

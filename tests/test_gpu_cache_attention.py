@@ -425,3 +425,23 @@ def test_threads_with_different_row_counts(sv):
     assert fails == [[], []]
     for (x, _, _), w in zip(calls, want):
         assert torch.equal(x.results()[0], w)
+
+
+@pytest.mark.parametrize("G,k_max", [(4, 4), (8, 3), (1, 0)])
+@pytest.mark.parametrize("tiles", [5, 6, 9])
+def test_short_segments_of_both_groups_in_a_row(sv, tiles, G, k_max):
+    """Narrow heads, up to 32 rows: segments that both groups share follow each other directly, each handing its
+    maxima and sums over at the same place.  A segment whose scores are far above the next one's would show in it."""
+    B = 120
+    r = random.Random(tiles)
+    lens = [tiles * 128 - r.randint(0, 100) for _ in range(B)]
+    s = make(70 + tiles, lens, [k_max] * B, k_max, 4 * G, 4, 64, 32, "bf16", ragged=False)
+    s["q"] *= torch.tensor([30.0, 0.02])[torch.arange(s["q"].shape[0]) // (k_max + 1) % 2][:, None, None].to(s["q"].dtype)
+    x = OnGpu(sv, s)
+    x.call()
+    out, lse, e = x.results()
+    assert e == (0, -1)
+    check(s, out, lse)
+    for _ in range(20):
+        x.call()
+        assert torch.equal(x.results()[0], out)
