@@ -37,10 +37,10 @@ def deps():
 
 
 def start_binding(tmp: str):
-    """The g++ process that compiles the binding to `tmp`."""
+    """The g++ process that compiles the binding to `tmp`; None without PyTorch, for whose users it is."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("the binding needs PyTorch's headers")
+        return None
     torch = list(spec.submodule_search_locations)[0]
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
@@ -54,9 +54,11 @@ def start_binding(tmp: str):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libspecverify.so and _binding.so unless they are newer than every source.  Each
     translation unit (one per logits dtype and scheme, the entry points, the cache-side kernels)
-    compiles in its own process, in parallel; one link makes the library."""
-    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
-        t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    compiles in its own process, in parallel; one link makes the library.  The library comes first:
+    it is there also where the binding is not (no PyTorch) or fails to compile (which raises)."""
+    made = [LIB] + ([BINDING] if importlib.util.find_spec("torch") else [])
+    if not force and all(os.path.exists(p) for p in made):
+        t = min(os.path.getmtime(p) for p in made)
         if all(os.path.getmtime(p) <= t for p in deps()):
             return LIB
     tag = f"{os.getpid()}"
@@ -69,24 +71,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     binding_tmp = BINDING + f".tmp{tag}"
-    procs.append(("binding.cpp", start_binding(binding_tmp)))
+    binding = start_binding(binding_tmp)
     failed = False
     for src, pr in procs:
         out, _ = pr.communicate()
         if pr.returncode != 0 or verbose:
             sys.stderr.write(out)
         failed = failed or pr.returncode != 0
+    binding_out = binding.communicate()[0] if binding else ""
     try:
         if failed:
-            raise RuntimeError("compiling libspecverify.so or _binding.so failed")
+            raise RuntimeError("nvcc failed building libspecverify.so")
         tmp = LIB + f".tmp{tag}"
         res = subprocess.run([nvcc(), *ARCH, "-shared", "-cudart", "shared", "-Xlinker",
                               "-rpath,/usr/local/cuda/lib64", "-o", tmp, *objs], capture_output=True, text=True)
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError("linking libspecverify.so failed")
-        os.replace(binding_tmp, BINDING)
         os.replace(tmp, LIB)
+        if binding is not None:
+            if binding.returncode != 0 or verbose:
+                sys.stderr.write(binding_out)
+            if binding.returncode != 0:
+                raise RuntimeError("compiling _binding.so failed")
+            os.replace(binding_tmp, BINDING)
     finally:
         for o in [*objs, binding_tmp]:
             if os.path.exists(o):

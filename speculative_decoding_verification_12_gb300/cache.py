@@ -79,9 +79,12 @@ def _load():
     return _binding
 
 
-def rollback(kv_seq_len, accept_len, num_drafts, workspace, stream) -> int:
-    """The status of spec_rollback (the package's call of that name raises on it)."""
-    return (_native or _load()).rollback(kv_seq_len, accept_len, num_drafts, workspace, stream)
+def binding():
+    """The compiled binding, or None where it was not built."""
+    try:
+        return _native or _load()
+    except RuntimeError:
+        return None
 
 
 def spec_append(q, k, v, q_weight, k_weight, eps: float, inv_freq, k_cache, v_cache, block_table, kv_seq_len,

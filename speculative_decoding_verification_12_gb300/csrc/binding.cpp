@@ -300,17 +300,27 @@ sv_status copy(Args a) {
                     count32(n, "copy_src"), ws, a.stream(5));
 }
 
-// kv_seq_len, accept_len, num_drafts, workspace, stream
+// kv_seq_len, accept_len, num_drafts, workspace, stream.  The package's spec_rollback, with the checks that it has in
+// Python: tensors may be on any device, a workspace of any size, and the library refuses what is None.
 sv_status rollback(Args a) {
     int64_t n;
-    size_t bytes;
     int32_t *ln = static_cast<int32_t *>(a.data(0, "kv_seq_len", I32, -1, &n));
-    const int32_t *acc = ints(a.data(1, "accept_len", I32, n)), *nd = ints(a.data(2, "num_drafts", I32, n));
-    void *ws = a.workspace(3, &bytes);
+    const int device = a.device;
+    auto any = [&](int i, const char *name, bool counted) -> void * {
+        a.device = -1;
+        if (a.none(i)) return nullptr;
+        if (counted) return a.data(i, name, I32, n);
+        const at::Tensor &t = a.tensor(i, name);
+        if (!t.is_contiguous()) fail(name, "contiguous");
+        return t.data_ptr();
+    };
+    const int32_t *acc = ints(any(1, "accept_len", true)), *nd = ints(any(2, "num_drafts", true));
+    void *ws = any(3, "workspace", false);
+    a.device = device;
     return lib.rollback(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
 }
 
-// The same for spec_cache_rollback.
+// kv_seq_len, accept_len, num_drafts, workspace, stream
 sv_status commit(Args a) {
     int64_t n;
     size_t bytes;

@@ -159,3 +159,59 @@ def test_cache_rollback_refusals(sv):
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         sv.spec_cache_rollback(i, i, i, torch.zeros(256, dtype=torch.uint8))
+
+
+def test_the_library_is_built_without_pytorch(tmp_path, monkeypatch):
+    """The binding is for PyTorch's users; the library needs neither it nor its headers."""
+    from speculative_decoding_verification_12_gb300 import build
+    (tmp_path / "one.cu").write_text('extern "C" int one() { return 1; }\n')
+    monkeypatch.setattr(build, "CSRC", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "binding.so"))
+    with monkeypatch.context() as m:
+        m.setattr(build.importlib.util, "find_spec", lambda name: None)
+        assert C.CDLL(build.build()).one() == 1
+        assert sorted(p.name for p in tmp_path.iterdir()) == ["lib.so", "one.cu"]
+    # and where the binding does not compile
+    (tmp_path / "lib.so").unlink()
+    (tmp_path / "binding.cpp").write_text("no C++\n")
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        build.build()
+    assert (tmp_path / "lib.so").exists() and not (tmp_path / "binding.so").exists()
+
+
+def test_rollback_without_the_compiled_binding(sv, monkeypatch):
+    """spec_rollback needs libspecverify.so alone: its own checks, then the library."""
+    import sys
+
+    from speculative_decoding_verification_12_gb300 import cache
+
+    class OnCuda:
+        is_cuda, dtype = True, torch.int32
+
+        def __init__(self, at, n=2):
+            self.at, self.n = at, n
+
+        def is_contiguous(self):
+            return True
+
+        def numel(self):
+            return self.n
+
+        def data_ptr(self):
+            return self.at
+
+    class Library:
+        def spec_rollback(self, *args):
+            self.args = args
+            return sv.SV_OK
+
+    monkeypatch.setattr(cache, "_native", None)
+    monkeypatch.delattr(sv, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, "speculative_decoding_verification_12_gb300._binding", None)
+    library = Library()
+    monkeypatch.setattr(sv, "lib", lambda: library)
+    sv.spec_rollback(OnCuda(256), OnCuda(512), OnCuda(768), OnCuda(1024, 2), stream=7)
+    assert library.args == (256, 512, 768, 2, 1024, 7)
+    with pytest.raises(ValueError, match="accept_len"):
+        sv.spec_rollback(OnCuda(256), OnCuda(512, 3), OnCuda(768), OnCuda(1024))

@@ -100,3 +100,24 @@ def test_rollback_itself_takes_no_idle_requests(sv):
     ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
     sv.spec_rollback(kv, acc, nd, ws)
     assert kv.tolist() == [9, 7] and sv.sv_read_device_error(ws) == (1, 0)
+
+
+def test_rollback_takes_what_it_always_took(sv):
+    """A workspace of a few words, and none at all refused by the library, with and without compiled checks."""
+    from speculative_decoding_verification_12_gb300 import cache
+    for native in (True, False):
+        kv, acc, nd = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([9, 9], [0, 1], [2, 3]))
+        ws = torch.zeros(8, dtype=torch.uint8, device="cuda")
+        if native:
+            sv.spec_rollback(kv, acc, nd, ws)
+        else:
+            with pytest.MonkeyPatch.context() as m:
+                m.setattr(cache, "_native", None)
+                m.delattr(sv, "_binding", raising=False)
+                m.setitem(sys.modules, "speculative_decoding_verification_12_gb300._binding", None)
+                sv.spec_rollback(kv, acc, nd, ws)
+        assert kv.tolist() == [7, 7]
+        with pytest.raises(sv.SvError):
+            sv.spec_rollback(kv, acc, nd, None)
+        with pytest.raises(ValueError):
+            sv.spec_rollback(kv, acc.long(), nd, ws)
