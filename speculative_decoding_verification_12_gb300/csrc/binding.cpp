@@ -28,6 +28,16 @@ struct Entry {
     PyObject *raw_stream;   // torch._C._cuda_getCurrentRawStream
 } lib;
 
+// The library's call without the interpreter's lock: a launch may wait for room in the stream's queue, and other
+// threads go on meanwhile.  (The caller's frame keeps the tensors.)
+template <typename F, typename... A>
+sv_status unlocked(F call, A... args) {
+    PyThreadState *const state = PyEval_SaveThread();
+    const sv_status status = call(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 struct Bad {};   // a Python error is set
 
 [[noreturn]] void fail(const char *name, const char *format, ...) {
@@ -179,7 +189,7 @@ sv_status append(Args a) {
     void *ws = a.workspace(15, &bytes);
     const int il = PyObject_IsTrue(a.v[16]);
     if (il < 0) throw Bad{};
-    return lib.append(pq, pk, pv, sq, sk, sv, count32(Hq, "q"), qw, kw, a.real(5), static_cast<const float *>(inv),
+    return unlocked(lib.append, pq, pk, pv, sq, sk, sv, count32(Hq, "q"), qw, kw, a.real(5), static_cast<const float *>(inv),
                       count32(2 * half, "inv_freq"), il, a.real(17), nd, ro, ln, count32(n, "num_drafts"),
                       a.i32(13, "k_max"), count32(R, "q"), c, po, so, ws, a.stream(18));
 }
@@ -199,7 +209,7 @@ sv_status attention(Args a) {
     const int32_t *ro = ints(a.optional(6, "row_offsets", I32, n + 1)), *ln = ints(a.data(4, "kv_seq_len", I32, n));
     void *out = a.data(11, "out", type, R * Hq * c.head_dim), *lse = a.optional(12, "out_lse", F32, R * Hq);
     void *ws = a.workspace(13, &bytes);
-    return lib.attention(pq, sq, count32(Hq, "q"), nd, ro, ln, count32(n, "num_drafts"), a.i32(7, "k_max"),
+    return unlocked(lib.attention, pq, sq, count32(Hq, "q"), nd, ro, ln, count32(n, "num_drafts"), a.i32(7, "k_max"),
                          count32(R, "q"), c, a.real(8), a.i32(9, "window"), a.i32(10, "sinks"), out,
                          static_cast<float *>(lse), ws, bytes, a.stream(14));
 }
@@ -229,7 +239,7 @@ sv_status reserve(Args a) {
     const State s = state(a, 2, true);
     const int32_t *nd = ints(a.data(0, "num_drafts", I32, s.B));
     void *ws = a.workspace(5, &bytes);
-    return lib.reserve(nd, s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages, a.i32(4, "page_size"), ws, bytes,
+    return unlocked(lib.reserve, nd, s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages, a.i32(4, "page_size"), ws, bytes,
                        a.stream(6));
 }
 
@@ -242,7 +252,7 @@ sv_status fork(Args a) {
                   *fl = ints(a.optional(2, "fork_len", I32, n));
     int32_t *src = static_cast<int32_t *>(a.data(7, "copy_src", I32, n)), *dst = static_cast<int32_t *>(a.data(8, "copy_dst", I32, n));
     void *ws = a.workspace(9, &bytes);
-    return lib.fork(pa, ch, fl, count32(n, "parents"), s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages,
+    return unlocked(lib.fork, pa, ch, fl, count32(n, "parents"), s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages,
                     a.i32(6, "page_size"), src, dst, ws, bytes, a.stream(10));
 }
 
@@ -251,7 +261,7 @@ sv_status release(Args a) {
     size_t bytes;
     const State s = state(a, 1, true);
     void *ws = a.workspace(6, &bytes);
-    return lib.release(s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages, a.i32(3, "page_size"), a.i32(4, "window"),
+    return unlocked(lib.release, s.len, s.B, s.table, s.max_pages, s.ref, s.num_pages, a.i32(3, "page_size"), a.i32(4, "window"),
                        a.i32(5, "sinks"), ws, a.stream(7));
 }
 
@@ -262,7 +272,7 @@ sv_status compact(Args a) {
     const State s = state(a, 0, false);
     int32_t *src = static_cast<int32_t *>(a.data(2, "copy_src", I32, -1, &cap)), *dst = static_cast<int32_t *>(a.data(3, "copy_dst", I32, cap));
     void *ws = a.workspace(4, &bytes);
-    return lib.compact(s.B, s.table, s.max_pages, s.ref, s.num_pages, src, dst, count32(cap, "copy_src"), ws, bytes,
+    return unlocked(lib.compact, s.B, s.table, s.max_pages, s.ref, s.num_pages, src, dst, count32(cap, "copy_src"), ws, bytes,
                        a.stream(5));
 }
 
@@ -295,7 +305,7 @@ sv_status copy(Args a) {
     size_t bytes;
     const int32_t *src = ints(a.data(2, "copy_src", I32, -1, &n)), *dst = ints(a.data(3, "copy_dst", I32, n));
     void *ws = a.workspace(4, &bytes);
-    return lib.copy(k.data_ptr(), pv, dense * size, k.stride(page_dim) * size, page_dim ? count32(k.size(0), "k_cache") : 1,
+    return unlocked(lib.copy, k.data_ptr(), pv, dense * size, k.stride(page_dim) * size, page_dim ? count32(k.size(0), "k_cache") : 1,
                     page_dim ? k.stride(0) * size : 0, count32(k.size(page_dim), "k_cache"), src, dst,
                     count32(n, "copy_src"), ws, a.stream(5));
 }
@@ -317,7 +327,7 @@ sv_status rollback(Args a) {
     const int32_t *acc = ints(any(1, "accept_len", true)), *nd = ints(any(2, "num_drafts", true));
     void *ws = any(3, "workspace", false);
     a.device = device;
-    return lib.rollback(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
+    return unlocked(lib.rollback, ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
 }
 
 // kv_seq_len, accept_len, num_drafts, workspace, stream
@@ -327,7 +337,7 @@ sv_status commit(Args a) {
     int32_t *ln = static_cast<int32_t *>(a.data(0, "kv_seq_len", I32, -1, &n));
     const int32_t *acc = ints(a.data(1, "accept_len", I32, n)), *nd = ints(a.data(2, "num_drafts", I32, n));
     void *ws = a.workspace(3, &bytes);
-    return lib.commit(ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
+    return unlocked(lib.commit, ln, acc, nd, count32(n, "kv_seq_len"), ws, a.stream(4));
 }
 
 template <sv_status (*F)(Args), int N>

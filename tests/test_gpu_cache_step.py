@@ -121,3 +121,38 @@ def test_rollback_takes_what_it_always_took(sv):
             sv.spec_rollback(kv, acc, nd, None)
         with pytest.raises(ValueError):
             sv.spec_rollback(kv, acc.long(), nd, ws)
+
+
+def test_calls_let_other_threads_run(sv, tmp_path):
+    """The compiled calls release the interpreter's lock while the library works: with a library that takes
+    0.3 s, another thread goes on.  In a process of its own, whose binding keeps the slow library."""
+    import subprocess
+    (tmp_path / "slow.c").write_text("#include <unistd.h>\nint slow(void) { usleep(300000); return 0; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(tmp_path / "slow.so"), str(tmp_path / "slow.c")], check=True)
+    code = f"""
+import ctypes, sys, threading, time
+sys.path.insert(0, {ROOT!r})
+import torch
+from speculative_decoding_verification_12_gb300 import cache
+binding = cache._load()
+slow = ctypes.CDLL({str(tmp_path / "slow.so")!r}).slow
+binding.init(*[ctypes.cast(slow, ctypes.c_void_p).value] * ENTRIES, torch._C._cuda_getCurrentRawStream)
+t = torch.zeros(256, dtype=torch.int32, device="cuda")
+ticks, stop = [0], []
+def tick():
+    while not stop:
+        time.sleep(0.001)
+        ticks[0] += 1
+thread = threading.Thread(target=tick)
+thread.start()
+time.sleep(0.05)
+before = ticks[0]
+assert binding.rollback(t, t, t, t, 0) == 0
+print(ticks[0] - before)
+stop.append(1)
+thread.join()
+"""
+    from speculative_decoding_verification_12_gb300 import cache
+    code = code.replace("ENTRIES", str(len(cache.ENTRIES)))
+    out = subprocess.run([sys.executable, "-c", code], check=True, capture_output=True, text=True).stdout
+    assert int(out) > 30
