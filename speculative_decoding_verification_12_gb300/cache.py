@@ -175,6 +175,10 @@ class PagedCache:
 
     k, v [layers, pages, page_size, heads, head_dim]; kv_seq_len [slots], block_table [slots,
     max_pages], ref_count [pages]: the state that spec_page_* work on.  All requests start empty.
+
+    The cache is ready when the constructor returns (it waits for its fills), so that every method may
+    be given any stream.  One cache's calls share its state and workspace: order those of different
+    streams as for any tensors, by events or synchronisation.
     """
 
     def __init__(self, layers: int, slots: int, pages: int, page_size: int, max_pages: int, heads: int, head_dim: int,
@@ -191,6 +195,8 @@ class PagedCache:
         need = max(sv_attention_workspace_bytes(head_dim), sv_page_workspace_bytes(slots, pages))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
         self.workspace[:256].zero_()
+        if self.k.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.k.device).synchronize()
 
     def reserve(self, num_drafts, stream=None) -> None:
         """Room for num_drafts[b] + 1 new tokens of every request (-1: idle)."""

@@ -156,3 +156,17 @@ thread.join()
     code = code.replace("ENTRIES", str(len(cache.ENTRIES)))
     out = subprocess.run([sys.executable, "-c", code], check=True, capture_output=True, text=True).stdout
     assert int(out) > 30
+
+
+def test_a_new_cache_is_ready_for_any_stream(sv):
+    """What the constructor fills is there when it returns, however busy the stream it was filled on."""
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    nd, other = ints(20, -1, 3), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)      # (about 0.1 s)
+    c = sv.PagedCache(1, 3, 30, 8, 8, 1, 64)
+    c.reserve(nd, other)
+    other.synchronize()
+    assert c.kv_seq_len.tolist() == [21, 0, 4]
+    assert c.block_table.tolist() == [[0, 1, 2] + [-1] * 5, [-1] * 8, [3] + [-1] * 7]
+    assert c.ref_count.tolist() == [1] * 4 + [0] * 26 and sv.sv_read_device_error(c.workspace) == (0, -1)
