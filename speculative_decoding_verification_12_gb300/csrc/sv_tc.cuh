@@ -173,27 +173,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
         "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(addr));
-}
-
 // Keeps uses of loaded registers behind the wait that completes their load.
 __device__ __forceinline__ void after_wait32(uint32_t *v) {
 #define SVC_IO(i) "+r"(v[i])
     asm volatile("" : SVC_R32(SVC_IO));
 #undef SVC_IO
 }
-__device__ __forceinline__ void after_wait16(uint32_t *v) {
-    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                      "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
-                      "+r"(v[15]));
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
