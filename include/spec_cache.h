@@ -119,7 +119,9 @@ sv_status spec_append(const void *q, const void *k, const void *v, int64_t q_str
  * S = the keys it sees, for each query head (its key/value head is head / (Hq / num_heads)):
  *     out = sum_{j in S} softmax_{j in S}(scale * q . k_j) v_j,   lse = log sum_{j in S} e^(scale q . k_j)
  * Every row sees at least its own token.  Scores, softmax and sums are fp32; the weights are
- * rounded to cache.dtype for the product with v, and the output once.
+ * rounded to cache.dtype for the product with v (off by up to eps / 2 of sum_j p_j |v_j|, as much
+ * again as the output's own rounding), and the output once.  The lse is good to
+ * (T + 16) 2^-23 + 2^-22 |lse| over T keys, beside the rounding of the fp32 scores.
  * A masked key has no influence, whatever its slot holds (an unwritten slot may hold NaN).
  *
  *   q            device [total_rows, num_q_heads, head_dim], cache.dtype, rows q_stride elements

@@ -69,13 +69,16 @@ enum { PAIR_NEXT, PAIR_HALVES, PAIR_ANY };
 // head_dim / 8), so a thread's elements are the same in every head it meets, and its weights and
 // rotations serve all of them.
 //
-// What bounds it: a row of 48 heads of 128 is 24 KB in and out, 4 ns at the memory's rate, but its
-// arithmetic and addresses keep the schedulers busy for half of the time (an instruction in 54 % of the
-// cycles), and a call's few rows per CTA wait once for the chain offsets -> length -> page.  So a CTA walks that chain once, a lane of one warp per row, while the first row's data, the
-// weights and the turns of the frequencies are under way, and then turns all its rows' pairs at once:
-// two barriers in all, and a warp asks for its next row's data before it works on this one's.  1280
-// rows of 48 heads take 9.0 us (3.5 TB/s read and written; with the rotations per row behind a barrier
-// each 10.4, and with one fp32 operation per instruction 10.9); one row takes 3.4 us, the launch.
+// What bounds it: latency, in a call that is one wave of CTAs.  A row of 48 heads of 128 is 24 KB in and
+// out, 4 ns at the memory's rate, and neither the memory nor the schedulers are full: an instruction is
+// issued in 56 % of the cycles in which a CTA is resident and in 39 % of the kernel's, 5.3 warps per
+// scheduler of which 1.3 could go on, and the others wait for arithmetic results (1.9 of 9.5 cycles per
+// instruction), global and shared memory (1.4 and 1.0) and barriers (0.9).  The few rows of a CTA wait once
+// for the chain offsets -> length -> page: one warp walks it, a lane per row, while the first row's data,
+// the weights and the turns of the frequencies are under way, and all the rows' pairs are then turned at
+// once: two barriers in all, and a warp asks for its next row's data before it works on this one's.  1280
+// rows of 48 heads take 9.2 us (3.4 TB/s read and written; with the rotations per row behind a barrier
+// each 10.4, and with one fp32 operation per instruction 10.9); one row takes 3.5 us, the launch.
 // Background copies of the next rows to shared memory: 12.0 before those two steps, no gain; a row's
 // addresses kept per thread and stepped instead of made anew: 9.5.
 template <typename E, int LPH, int PAIR>

@@ -27,12 +27,16 @@
 // the groups take alternate key tiles, each with its own m, l and O, joined at the end; with two, each
 // has its own.
 //
-// What bounds it.  Few rows per key (a verify step): the cache's bytes; 256 requests of 5 rows over up to
-// 4096 keys of 8 heads of 128 read 4.3 GB in 645 us, 6.7 TB/s, one request over 131 071 keys 0.54 GB in
-// 90 us.  Many rows (16 requests of 65 rows, 8 query heads per key head, 8192 keys): the chain of a
-// product, its softmax and the next product on the 512 columns of tensor memory; 161 us, 860 TFLOP/s.
-// Small calls: the chain of launch, lengths, table, first tile, epilogue and join, 10.9 us for one request
-// of 2049 keys; short and narrow segments: about 2 us each to change from one to the next.
+// What bounds it.  Few rows per key (a verify step): the cache's bytes; 256 requests of 5 rows over 4096
+// keys of 8 heads of 128 read 4.3 GB in 633 to 661 us by run, 6.5 to 6.8 TB/s, one request over 131 071
+// keys 0.54 GB in 90 us.  Many rows (16 requests of 65 rows, 8 query heads per key head, 8192 keys): the
+// chain of a product, its softmax and the next product on the 512 columns of tensor memory; 162 us in a
+// graph (166 issued), 860 TFLOP/s, the tensor pipe active in 50 % of the cycles.  Small calls: the chain of
+// launch, lengths, table, first tile, epilogue and join, 10.5 us for one request of 2049 keys.  Short
+// segments: the change from one to the next, about 2 us where both groups share them (512 one-row requests
+// of 8 heads under a window of 64 keys: 27 segments a CTA, 151 us).  Many rows of one request: one warp
+// loads up to 256 rows' queries, into one buffer where there are two row tiles (65 rows, 32 on 8 heads,
+// over 65 keys: 18.9 us).
 #include <math.h>
 
 #include <atomic>
@@ -865,6 +869,10 @@ attention_kernel(const Batch A, const Cache C, const AttnArgs P, const __grid_co
                     }
                     const float off = BIAS - (m == -INFINITY ? 0.f : m * P.c);
                     const uint64_t cc = pair_of(P.c, P.c), offs = pair_of(off, off);
+                    // (l is the fp32 weights' own sum; for the product with v they are rounded to the cache's
+                    // type, the only operand that the matrix instruction takes beside such a v.  The outputs'
+                    // error against 64 bits is then 0.0022 relative in bf16 and 0.00021 in fp16, where weights
+                    // of 32 bits, as a plain form has them, leave 0.0017 and 0.00018: the output's rounding.)
                     uint64_t sum[2] = {0, 0};
                     auto weights = [&](const uint32_t *v, int i) {
                         uint32_t w[16];

@@ -173,12 +173,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
         "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
         : "memory");
 }
+
 // Keeps uses of loaded registers behind the wait that completes their load.
 __device__ __forceinline__ void after_wait32(uint32_t *v) {
 #define SVC_IO(i) "+r"(v[i])
     asm volatile("" : SVC_R32(SVC_IO));
 #undef SVC_IO
 }
+
+// Approximate power of two (within 2^-22 of its value), results below 2^-126 as zero.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -224,8 +227,8 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Approximate reciprocal and binary logarithm (2 ulp), where 1.f / x and log2f took longer than the rest
-// of an epilogue's scalars.
+// Approximate reciprocal (1 ulp) and binary logarithm (2^-22, absolute between 1/2 and 2 and else relative),
+// where 1.f / x and log2f took longer than the rest of an epilogue's scalars.
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
