@@ -44,6 +44,8 @@
  *  - A request with a device-data error (SV_DEV_BAD_LAYOUT: num_drafts, offsets or length out of
  *    range; SV_DEV_BAD_PAGE: a page it needs is not in [0, num_pages)) has NaN outputs, and
  *    nothing of it is written to the cache by the rows in error.
+ *    row_offsets that do not ascend are reported too, but leave open which rows are whose: outputs
+ *    and appended rows of any request are then unspecified, within the arrays.
  */
 #ifndef SPEC_CACHE_H
 #define SPEC_CACHE_H
