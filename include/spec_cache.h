@@ -18,6 +18,7 @@
  *     spec_verify                (spec_verify.h) the logits' verdict: accept_len
  *     spec_cache_rollback        kv_seq_len[b] <- kv_seq_len[b] - k_b + a_b, the accepted drafts kept
  *     spec_page_release          pages past the new length, or out of the window, go back
+ * (spec_append8 and spec_attention8 for a cache in 8 bits; spec_logits.h between the model and the verdict)
  * and between steps spec_page_fork (a new request continues from another's tokens) and
  * spec_page_compact, each followed by spec_page_copy.
  *
@@ -237,6 +238,74 @@ size_t sv_page_workspace_bytes(int32_t B, int32_t num_pages);
 sv_status spec_page_copy(void *k, void *v, int64_t page_bytes, int64_t page_stride, int32_t num_layers,
                          int64_t layer_stride, int32_t num_pages, const int32_t *copy_src, const int32_t *copy_dst,
                          int32_t n, void *workspace, void *stream);
+
+/*
+ * A cache in 8 bits.  Keys and values are e4m3 numbers with one scale for each block of scale_tokens
+ * tokens and head, keys and values apart: token t's element is scale * e4m3.  Everything else is as
+ * above: rows, lengths, pages and their bookkeeping do not know how a page is written, and
+ * spec_page_copy moves scales with their page where both lie in the same page_bytes.
+ *
+ * Element [page, slot, head, d] of k and of v is the byte at page * page_stride + slot * token_stride +
+ * head * head_stride + d; the scale of [page, slot, head] is element page * scale_page_stride +
+ * (slot / scale_tokens) * scale_block_stride + head * scale_head_stride of k_scale and of v_scale.
+ * A scale below 2^-40, or not a number, counts as 2^-40, and one above 2^40 as 2^40.
+ */
+typedef struct sv_kv_cache8 {
+    void *k, *v;                    /* device, 16-byte aligned, e4m3                           */
+    float *k_scale, *v_scale;       /* device                                                  */
+    int64_t page_stride, token_stride, head_stride;   /* bytes; positive multiples of 16      */
+    int64_t scale_page_stride, scale_block_stride, scale_head_stride;   /* floats; positive  */
+    int32_t num_pages;              /* pages in the pool                                       */
+    int32_t page_size;              /* tokens per page: a power of two in [8, 256]             */
+    int32_t scale_tokens;           /* tokens per scale: a power of two in [8, page_size]      */
+    int32_t num_heads;              /* key/value heads                                         */
+    int32_t head_dim;               /* a multiple of 16, up to 128                             */
+    int32_t max_pages;              /* entries per request in block_table                      */
+    const int32_t *block_table;     /* device int32 [B, max_pages]                             */
+} sv_kv_cache8;
+
+/*
+ * spec_append8 -- spec_append to a cache in 8 bits.
+ *
+ * Queries, norms and rotations are spec_append's.  The rotated keys and the values are stored block
+ * by block.  A block's scale is the least power of two s in [2^-40, 2^40] with |x| <= 448 s for every new
+ * finite element x of it; a block that holds tokens of the request from before keeps its scale where that
+ * is larger, and where it is smaller the tokens from before are rewritten in the new one.  Each
+ * element is then the nearest e4m3 number to x / s (ties to even; |x| > 448 s, at the upper bound of s
+ * only, becomes 448 s); what is not finite becomes NaN.  Rewriting in a scale that is a larger power of two
+ * loses what falls below 2^-9 s and nothing else, so a block does not lose precision with every token
+ * that joins it.  Tokens that a rollback took back leave their scale: it falls when their block is begun anew.
+ * The appended tokens' blocks are the request's own (a shared page is always full).
+ *
+ *   dtype        of q, k, v, the weights and out_q: SV_BF16 or SV_F16.
+ * All other arguments, sizes and errors: spec_append, with cache.head_dim a multiple of 16 up to 128.
+ */
+sv_status spec_append8(const void *q, const void *k, const void *v, sv_dtype dtype, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, int32_t num_q_heads, const void *q_weight, const void *k_weight, float eps,
+                       const float *inv_freq, int32_t rotary_dim, int32_t interleaved, float rope_scale,
+                       const int32_t *num_drafts, const int32_t *row_offsets, const int32_t *kv_seq_len, int32_t B,
+                       int32_t k_max, int32_t total_rows, sv_kv_cache8 cache, void *out_q, int64_t out_q_stride,
+                       void *workspace, void *stream);
+
+/*
+ * spec_attention8 -- spec_attention over a cache in 8 bits.
+ *
+ * The same formula, with k_j and v_j the stored numbers times their scales.  Queries keep all their
+ * bits: a query row is a sum of e4m3 parts that are exact for elements down to 2^-14 of the row's largest,
+ * and off by at most 2^-21 of that below.  Scores, softmax and sums are fp32; the weights are rounded to
+ * 9 bits (SV_BF16) or 11 (SV_F16) for the product with v, and the output once.  A query row with an
+ * infinity or a NaN gives a NaN row.  The lse is as good as spec_attention's.
+ *
+ *   dtype        of q and out: SV_BF16 or SV_F16.
+ *   workspace    sv_attention_workspace_bytes() bytes, 256-byte aligned.
+ * All other arguments, sizes and errors, the bounded waits and the fixed order of the sums: spec_attention,
+ * with cache.head_dim a multiple of 16.
+ */
+sv_status spec_attention8(const void *q, sv_dtype dtype, int64_t q_stride, int32_t num_q_heads,
+                          const int32_t *num_drafts, const int32_t *row_offsets, const int32_t *kv_seq_len, int32_t B,
+                          int32_t k_max, int32_t total_rows, sv_kv_cache8 cache, float scale, int32_t window,
+                          int32_t sinks, void *out, float *out_lse, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,7 @@ SV_OK, SV_ERR_INVALID_ARG, SV_ERR_WORKSPACE, SV_ERR_CUDA, SV_ERR_UNSUPPORTED, SV
 SV_F32, SV_BF16 = 0, 1
 DEV_ERRORS = {0: "ok", 1: "bad layout", 2: "bad token", 3: "bad temperature", 4: "bad top_p",
               5: "bad uniform", 6: "bad penalty", 7: "timeout", 8: "bad history", 9: "bad page", 10: "no pages",
-              11: "shared page"}
+              11: "shared page", 12: "bad bias", 13: "bad mask"}
 
 
 class SvParams(C.Structure):
@@ -248,10 +248,10 @@ def sv_read_device_error(workspace):
 
 
 def __getattr__(name):
-    """The cache-side calls (cache.py, which imports torch) by the package's name."""
-    if name in ("spec_append", "spec_attention", "spec_cache_rollback", "spec_page_reserve", "spec_page_fork",
+    """The cache-side calls and spec_logits (cache.py, which imports torch) by the package's name."""
+    if name in ("spec_append", "spec_attention", "spec_append8", "spec_attention8", "spec_logits", "spec_cache_rollback", "spec_page_reserve", "spec_page_fork",
                 "spec_page_release", "spec_page_compact", "spec_page_copy", "sv_attention_workspace_bytes", "sv_page_workspace_bytes",
-                "SvKvCache", "SV_F16", "PagedCache"):
+                "SvKvCache", "SvKvCache8", "SvLogitRules", "SV_F16", "PagedCache"):
         from . import cache
         globals()[name] = f = getattr(cache, name)
         return f

@@ -1,6 +1,7 @@
-"""The cache side of a verify step: spec_append, spec_attention and the page bookkeeping calls.
+"""The cache side of a verify step: spec_append, spec_attention, their forms for a cache in 8 bits, the page
+bookkeeping calls, and spec_logits.
 
-The same thin binding as the package's verify calls, over include/spec_cache.h: checks of the
+The same thin binding as the package's verify calls, over include/spec_cache.h and include/spec_logits.h: checks of the
 tensors, then one call into libspecverify.so.  The checks are compiled (csrc/binding.cpp), since
 several of these kernels run for less time than Python needs to look at a dozen tensors.  Caches
 are torch tensors [pages, slots, heads, head_dim] of any strides whose last is 1, so a [pages,
@@ -24,6 +25,23 @@ class SvKvCache(C.Structure):
                 ("block_table", C.c_void_p)]
 
 
+class SvKvCache8(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("page_stride", C.c_int64), ("token_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("scale_page_stride", C.c_int64), ("scale_block_stride", C.c_int64), ("scale_head_stride", C.c_int64),
+                ("num_pages", C.c_int32), ("page_size", C.c_int32), ("scale_tokens", C.c_int32),
+                ("num_heads", C.c_int32), ("head_dim", C.c_int32), ("max_pages", C.c_int32),
+                ("block_table", C.c_void_p)]
+
+
+class SvLogitRules(C.Structure):
+    _fields_ = [("repetition", C.c_void_p), ("presence", C.c_void_p), ("frequency", C.c_void_p),
+                ("prior_offsets", C.c_void_p), ("prior_tokens", C.c_void_p), ("prior_counts", C.c_void_p),
+                ("prior_len", C.c_int32), ("bias_len", C.c_int32), ("bias_offsets", C.c_void_p),
+                ("bias_tokens", C.c_void_p), ("bias_values", C.c_void_p), ("masks", C.c_void_p),
+                ("mask_rows", C.c_void_p), ("num_masks", C.c_int32), ("mask_words", C.c_int32)]
+
+
 _calls = None
 
 
@@ -35,6 +53,9 @@ def _lib():
         for name, args in (
                 ("spec_append", [P, P, P, L, L, L, I, P, P, F, P, I, I, F, P, P, P, I, I, I, SvKvCache, P, L, P, P]),
                 ("spec_attention", [P, L, I, P, P, P, I, I, I, SvKvCache, F, I, I, P, P, P, Z, P]),
+                ("spec_append8", [P, P, P, I, L, L, L, I, P, P, F, P, I, I, F, P, P, P, I, I, I, SvKvCache8, P, L, P, P]),
+                ("spec_attention8", [P, I, L, I, P, P, P, I, I, I, SvKvCache8, F, I, I, P, P, P, Z, P]),
+                ("spec_logits", [P, I, P, P, P, I, I, I, I, SvLogitRules, P, P, P]),
                 ("spec_page_reserve", [P, P, I, P, I, P, I, I, P, Z, P]),
                 ("spec_cache_rollback", [P, P, P, I, P, P]),
                 ("spec_page_fork", [P, P, P, I, P, I, P, I, P, I, I, P, P, P, Z, P]),
@@ -61,7 +82,8 @@ def sv_page_workspace_bytes(B: int, num_pages: int) -> int:
 
 # the entry points that the compiled binding calls, in its order
 ENTRIES = ("spec_append", "spec_attention", "spec_page_reserve", "spec_page_fork", "spec_page_release",
-           "spec_page_compact", "spec_page_copy", "spec_rollback", "spec_cache_rollback")
+           "spec_page_compact", "spec_page_copy", "spec_rollback", "spec_cache_rollback", "spec_append8",
+           "spec_attention8", "spec_logits")
 _native = None
 
 
@@ -117,6 +139,47 @@ def spec_attention(q, k_cache, v_cache, block_table, kv_seq_len, num_drafts, row
                                         scale, window, sinks, out, out_lse, workspace, stream)
     if st != SV_OK:
         raise SvError(st, "spec_attention")
+
+
+def spec_append8(q, k, v, q_weight, k_weight, eps: float, inv_freq, k_cache, v_cache, k_scale, v_scale, block_table,
+                 kv_seq_len, num_drafts, row_offsets, k_max: int, out_q, workspace, interleaved: bool = False,
+                 rope_scale: float = 1.0, stream=None) -> None:
+    """spec_append to a cache in 8 bits: k_cache, v_cache float8_e4m3fn [pages, page_size, Hk, D],
+    k_scale, v_scale fp32 [pages, blocks, Hk], a scale for each page_size / blocks tokens of a head (see
+    include/spec_cache.h); the rest as spec_append, with q, k, v bfloat16 or float16.
+    """
+    st = (_native or _load()).append8(q, k, v, q_weight, k_weight, eps, inv_freq, k_cache, v_cache, k_scale, v_scale,
+                                      block_table, kv_seq_len, num_drafts, row_offsets, k_max, out_q, workspace,
+                                      interleaved, rope_scale, stream)
+    if st != SV_OK:
+        raise SvError(st, "spec_append8")
+
+
+def spec_attention8(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_seq_len, num_drafts, row_offsets, k_max: int,
+                    scale: float, window: int, sinks: int, out, out_lse, workspace, stream=None) -> None:
+    """spec_attention over a cache in 8 bits, as spec_append8 fills it (see include/spec_cache.h)."""
+    st = (_native or _load()).attention8(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_seq_len, num_drafts,
+                                         row_offsets, k_max, scale, window, sinks, out, out_lse, workspace, stream)
+    if st != SV_OK:
+        raise SvError(st, "spec_attention8")
+
+
+def spec_logits(logits, draft_tokens, num_drafts, row_offsets, k_max: int, repetition, presence, frequency, prior, bias,
+                mask, mask_rows, out, workspace, stream=None) -> None:
+    """Penalties for repeated tokens, biases and grammar masks on a verify step's logits (see
+    include/spec_logits.h).
+
+    logits, out [R, V] bf16 or fp32 (out may be logits); draft_tokens [R-B], num_drafts [B], row_offsets
+    [B+1] or None: int32, as in spec_verify; repetition, presence, frequency fp32 [B] or None; prior None or
+    (offsets [B+1], tokens [H], counts [H]) int32; bias None or (offsets [B+1], tokens [N] int32, values
+    [N] fp32); mask int32 [masks, words], a bit per token, and mask_rows int32 [R] (-1: none), or None
+    both; workspace: 256 bytes at least, zeroed once.
+    """
+    st = (_native or _load()).logits(logits, draft_tokens, num_drafts, row_offsets, k_max, repetition, presence,
+                                     frequency, *(prior or (None,) * 3), *(bias or (None,) * 3), mask, mask_rows, out,
+                                     workspace, stream)
+    if st != SV_OK:
+        raise SvError(st, "spec_logits")
 
 
 def spec_page_reserve(num_drafts, kv_seq_len, block_table, ref_count, page_size: int, workspace,
@@ -176,15 +239,37 @@ class PagedCache:
     k, v [layers, pages, page_size, heads, head_dim]; kv_seq_len [slots], block_table [slots,
     max_pages], ref_count [pages]: the state that spec_page_* work on.  All requests start empty.
 
+    With dtype float8_e4m3fn the cache is in 8 bits: k_scale, v_scale [layers, pages, page_size /
+    scale_tokens, heads] fp32 hold a scale for each scale_tokens tokens and head, each page's scales behind its numbers
+    in the same allocation, so that a page and its scales are shared, moved and copied as one.
+    append and attend then take queries of either 16-bit type.
+
     The cache is ready when the constructor returns (it waits for its fills), so that every method may
     be given any stream.  One cache's calls share its state and workspace: order those of different
     streams as for any tensors, by events or synchronisation.
     """
 
     def __init__(self, layers: int, slots: int, pages: int, page_size: int, max_pages: int, heads: int, head_dim: int,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", scale_tokens: int = 16):
         shape = (layers, pages, page_size, heads, head_dim)
-        self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        self.k_scale = self.v_scale = None
+        if dtype == torch.float8_e4m3fn:
+            scale_tokens = min(scale_tokens, page_size)
+            if scale_tokens < 1 or page_size % scale_tokens:
+                raise ValueError("scale_tokens must divide page_size")
+            blocks, size = page_size // scale_tokens, page_size * heads * head_dim
+            if size % 16:
+                raise ValueError("a page's keys must be a multiple of 16 bytes")
+            # pages as bytes: their numbers, then their scales, in multiples of 16
+            held = (layers, pages, size + (4 * blocks * heads + 15) // 16 * 16, 1, 1)
+            self._pages = tuple(torch.zeros(held, dtype=torch.uint8, device=device) for _ in range(2))
+            self.k, self.v = (x[:, :, :size, 0, 0].view(dtype).unflatten(2, shape[2:]) for x in self._pages)
+            self.k_scale, self.v_scale = (
+                x[:, :, :, 0, 0].view(torch.float32)[:, :, size // 4:size // 4 + blocks * heads].unflatten(2, (blocks, heads))
+                for x in self._pages)
+        else:
+            self._pages = None
+            self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
         ints = dict(dtype=torch.int32, device=device)
         self.kv_seq_len = torch.zeros(slots, **ints)
         self.block_table = torch.full((slots, max_pages), -1, **ints)
@@ -205,12 +290,22 @@ class PagedCache:
 
     def append(self, layer: int, q, k, v, q_weight, k_weight, eps, inv_freq, num_drafts, row_offsets, k_max, out_q,
                interleaved=False, rope_scale=1.0, stream=None) -> None:
+        if self.k_scale is not None:
+            spec_append8(q, k, v, q_weight, k_weight, eps, inv_freq, self.k[layer], self.v[layer], self.k_scale[layer],
+                         self.v_scale[layer], self.block_table, self.kv_seq_len, num_drafts, row_offsets, k_max, out_q,
+                         self.workspace, interleaved, rope_scale, stream)
+            return
         spec_append(q, k, v, q_weight, k_weight, eps, inv_freq, self.k[layer], self.v[layer], self.block_table,
                     self.kv_seq_len, num_drafts, row_offsets, k_max, out_q, self.workspace, interleaved, rope_scale,
                     stream)
 
     def attend(self, layer: int, q, num_drafts, row_offsets, k_max, scale, out, window=0, sinks=0, out_lse=None,
                stream=None) -> None:
+        if self.k_scale is not None:
+            spec_attention8(q, self.k[layer], self.v[layer], self.k_scale[layer], self.v_scale[layer], self.block_table,
+                            self.kv_seq_len, num_drafts, row_offsets, k_max, scale, window, sinks, out, out_lse,
+                            self.workspace, stream)
+            return
         spec_attention(q, self.k[layer], self.v[layer], self.block_table, self.kv_seq_len, num_drafts, row_offsets,
                        k_max, scale, window, sinks, out, out_lse, self.workspace, stream)
 
@@ -229,10 +324,10 @@ class PagedCache:
         src, dst = self._pairs[:, :parents.numel()]
         spec_page_fork(parents, children, fork_len, self.kv_seq_len, self.block_table, self.ref_count, self.page_size,
                        src, dst, self.workspace, stream)
-        spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)
+        spec_page_copy(*(self._pages or (self.k, self.v)), src, dst, self.workspace, stream)
 
     def compact(self, capacity: int, stream=None) -> None:
         """Moves up to `capacity` used pages down into the free ones below them."""
         src, dst = self._pairs[:, :capacity]
         spec_page_compact(self.block_table, self.ref_count, src, dst, self.workspace, stream)
-        spec_page_copy(self.k, self.v, src, dst, self.workspace, stream)
+        spec_page_copy(*(self._pages or (self.k, self.v)), src, dst, self.workspace, stream)

@@ -1,5 +1,5 @@
-// binding.cpp -- the cache-side calls and spec_rollback as Python functions: checks of the torch tensors, then one call
-// into libspecverify.so.  The same checks written in Python cost 12 to 15 us a call on the host that
+// binding.cpp -- the cache-side calls, spec_logits and spec_rollback as Python functions: checks of the torch
+// tensors, then one call into libspecverify.so.  The same checks written in Python cost 12 to 15 us a call on the host that
 // drives a GB300, more than several of the kernels run.
 //
 // Every function returns the library's status; a wrong tensor raises ValueError.  The library's entry
@@ -12,6 +12,7 @@
 #include <cstdarg>
 
 #include "../../include/spec_cache.h"
+#include "../../include/spec_logits.h"
 
 namespace {
 
@@ -25,6 +26,9 @@ struct Entry {
     decltype(&spec_page_copy) copy;
     decltype(&spec_rollback) rollback;
     decltype(&spec_cache_rollback) commit;
+    decltype(&spec_append8) append8;
+    decltype(&spec_attention8) attention8;
+    decltype(&spec_logits) logits;
     PyObject *raw_stream;   // torch._C._cuda_getCurrentRawStream
 } lib;
 
@@ -162,6 +166,52 @@ struct Args {
         c.block_table = static_cast<const int32_t *>(t.data_ptr());
         return c;
     }
+    // k_cache, v_cache, k_scale, v_scale and block_table of a cache in 8 bits at i .. i + 4.
+    sv_kv_cache8 cache8(int i, int64_t B) {
+        const at::Tensor &k = tensor(i, "k_cache"), &v = tensor(i + 1, "v_cache");
+        if (k.scalar_type() != c10::ScalarType::Float8_e4m3fn || v.scalar_type() != k.scalar_type())
+            fail("k_cache and v_cache", "both float8_e4m3fn");
+        if (k.dim() != 4 || k.sizes() != v.sizes() || k.strides() != v.strides())
+            fail("k_cache and v_cache", "[pages, slots, heads, head_dim], of one shape and strides");
+        if (k.stride(3) != 1) fail("k_cache and v_cache", "contiguous in head_dim");
+        const at::Tensor &ks = tensor(i + 2, "k_scale"), &vs = tensor(i + 3, "v_scale");
+        if (ks.scalar_type() != F32 || vs.scalar_type() != F32) fail("k_scale and v_scale", "both float32");
+        if (ks.dim() != 3 || ks.sizes() != vs.sizes() || ks.strides() != vs.strides() || ks.size(0) != k.size(0) ||
+            ks.size(2) != k.size(2) || ks.size(1) < 1 || k.size(1) % ks.size(1))
+            fail("k_scale and v_scale", "[pages, blocks of slots, heads], of one shape and strides");
+        for (int d = 0; d < 4; d++)
+            if (k.size(d) > INT32_MAX) fail("k_cache and v_cache", "smaller");
+        const at::Tensor &t = tensor(i + 4, "block_table");
+        if (t.scalar_type() != I32 || t.dim() != 2 || t.size(0) != B || !t.is_contiguous() || t.size(1) > INT32_MAX)
+            fail("block_table", "contiguous int32 [%lld, max_pages]", (long long)B);
+        // (a dimension of one element has any stride)
+        auto stride = [](const at::Tensor &x, int d, int64_t one) { return x.size(d) == 1 ? one : x.stride(d); };
+        sv_kv_cache8 c;
+        c.k = k.data_ptr();
+        c.v = v.data_ptr();
+        c.k_scale = static_cast<float *>(ks.data_ptr());
+        c.v_scale = static_cast<float *>(vs.data_ptr());
+        c.page_stride = stride(k, 0, 16);
+        c.token_stride = stride(k, 1, 16);
+        c.head_stride = stride(k, 2, 16);
+        c.scale_page_stride = stride(ks, 0, 1);
+        c.scale_block_stride = stride(ks, 1, 1);
+        c.scale_head_stride = stride(ks, 2, 1);
+        c.num_pages = (int32_t)k.size(0);
+        c.page_size = (int32_t)k.size(1);
+        c.scale_tokens = (int32_t)(k.size(1) / ks.size(1));
+        c.num_heads = (int32_t)k.size(2);
+        c.head_dim = (int32_t)k.size(3);
+        c.max_pages = (int32_t)t.size(1);
+        c.block_table = static_cast<const int32_t *>(t.data_ptr());
+        return c;
+    }
+    // The type of queries beside a cache in 8 bits.
+    static sv_dtype half_type(const at::Tensor &t, const char *name) {
+        if (t.scalar_type() == c10::ScalarType::BFloat16) return SV_BF16;
+        if (t.scalar_type() != c10::ScalarType::Half) fail(name, "bfloat16 or float16");
+        return SV_F16;
+    }
 };
 
 int32_t count32(int64_t n, const char *name) {
@@ -212,6 +262,94 @@ sv_status attention(Args a) {
     return unlocked(lib.attention, pq, sq, count32(Hq, "q"), nd, ro, ln, count32(n, "num_drafts"), a.i32(7, "k_max"),
                          count32(R, "q"), c, a.real(8), a.i32(9, "window"), a.i32(10, "sinks"), out,
                          static_cast<float *>(lse), ws, bytes, a.stream(14));
+}
+
+// q, k, v, q_weight, k_weight, eps, inv_freq, k_cache, v_cache, k_scale, v_scale, block_table, kv_seq_len, num_drafts,
+// row_offsets, k_max, out_q, workspace, interleaved, rope_scale, stream
+sv_status append8(Args a) {
+    int64_t n, half = 0, sq, sk, sv, so;
+    size_t bytes;
+    const int32_t *nd = ints(a.data(13, "num_drafts", I32, -1, &n));
+    const sv_kv_cache8 c = a.cache8(7, n);
+    const at::Tensor &q = a.tensor(0, "q");
+    if (q.dim() != 3) fail("q", "[rows, heads, head_dim]");
+    const sv_dtype dtype = Args::half_type(q, "q");
+    const c10::ScalarType type = q.scalar_type();
+    const int64_t R = q.size(0), Hq = q.size(1), D = c.head_dim;
+    void *pq = a.rows(0, "q", type, R, Hq, D, &sq), *pk = a.rows(1, "k", type, R, c.num_heads, D, &sk),
+         *pv = a.rows(2, "v", type, R, c.num_heads, D, &sv), *po = a.rows(16, "out_q", type, R, Hq, D, &so);
+    void *qw = a.optional(3, "q_weight", type, D), *kw = a.optional(4, "k_weight", type, D);
+    void *inv = a.optional(6, "inv_freq", F32, -1, &half);
+    const int32_t *ro = ints(a.optional(14, "row_offsets", I32, n + 1)), *ln = ints(a.data(12, "kv_seq_len", I32, n));
+    void *ws = a.workspace(17, &bytes);
+    const int il = PyObject_IsTrue(a.v[18]);
+    if (il < 0) throw Bad{};
+    return unlocked(lib.append8, pq, pk, pv, dtype, sq, sk, sv, count32(Hq, "q"), qw, kw, a.real(5),
+                    static_cast<const float *>(inv), count32(2 * half, "inv_freq"), il, a.real(19), nd, ro, ln,
+                    count32(n, "num_drafts"), a.i32(15, "k_max"), count32(R, "q"), c, po, so, ws, a.stream(20));
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, block_table, kv_seq_len, num_drafts, row_offsets, k_max, scale, window, sinks,
+// out, out_lse, workspace, stream
+sv_status attention8(Args a) {
+    int64_t n, sq;
+    size_t bytes;
+    const int32_t *nd = ints(a.data(7, "num_drafts", I32, -1, &n));
+    const sv_kv_cache8 c = a.cache8(1, n);
+    const at::Tensor &q = a.tensor(0, "q");
+    if (q.dim() != 3) fail("q", "[rows, heads, head_dim]");
+    const sv_dtype dtype = Args::half_type(q, "q");
+    const int64_t R = q.size(0), Hq = q.size(1);
+    void *pq = a.rows(0, "q", q.scalar_type(), R, Hq, c.head_dim, &sq);
+    const int32_t *ro = ints(a.optional(8, "row_offsets", I32, n + 1)), *ln = ints(a.data(6, "kv_seq_len", I32, n));
+    void *out = a.data(13, "out", q.scalar_type(), R * Hq * c.head_dim), *lse = a.optional(14, "out_lse", F32, R * Hq);
+    void *ws = a.workspace(15, &bytes);
+    return unlocked(lib.attention8, pq, dtype, sq, count32(Hq, "q"), nd, ro, ln, count32(n, "num_drafts"), a.i32(9, "k_max"),
+                    count32(R, "q"), c, a.real(10), a.i32(11, "window"), a.i32(12, "sinks"), out, static_cast<float *>(lse),
+                    ws, bytes, a.stream(16));
+}
+
+// logits, draft_tokens, num_drafts, row_offsets, k_max, repetition, presence, frequency, prior_offsets, prior_tokens,
+// prior_counts, bias_offsets, bias_tokens, bias_values, mask, mask_rows, out, workspace, stream
+sv_status logits(Args a) {
+    int64_t n, entries = 0;
+    size_t bytes;
+    const at::Tensor &t = a.tensor(0, "logits");
+    const c10::ScalarType type = t.scalar_type();
+    if (t.dim() != 2 || !t.is_contiguous() || (type != c10::ScalarType::BFloat16 && type != F32))
+        fail("logits", "contiguous bfloat16 or float32 [rows, V]");
+    const int64_t R = t.size(0), V = t.size(1);
+    const int32_t *nd = ints(a.data(2, "num_drafts", I32, -1, &n)), *ro = ints(a.optional(3, "row_offsets", I32, n + 1));
+    const int32_t *drafts = ints(a.optional(1, "draft_tokens", I32, R - n));
+    sv_logit_rules r = {};
+    auto floats = [](void *p) { return static_cast<const float *>(p); };
+    r.repetition = floats(a.optional(5, "repetition", F32, n));
+    r.presence = floats(a.optional(6, "presence", F32, n));
+    r.frequency = floats(a.optional(7, "frequency", F32, n));
+    if (!a.none(8)) {
+        r.prior_offsets = ints(a.data(8, "prior_offsets", I32, n + 1));
+        r.prior_tokens = ints(a.data(9, "prior_tokens", I32, -1, &entries));
+        r.prior_counts = ints(a.data(10, "prior_counts", I32, entries));
+        r.prior_len = count32(entries, "prior_tokens");
+    }
+    if (!a.none(11)) {
+        r.bias_offsets = ints(a.data(11, "bias_offsets", I32, n + 1));
+        r.bias_tokens = ints(a.data(12, "bias_tokens", I32, -1, &entries));
+        r.bias_values = floats(a.data(13, "bias_values", F32, entries));
+        r.bias_len = count32(entries, "bias_tokens");
+    }
+    if (a.none(14) != a.none(15)) fail("mask and mask_rows", "given together");
+    if (!a.none(14)) {
+        const at::Tensor &m = a.tensor(14, "mask");
+        if (m.scalar_type() != I32 || m.dim() != 2 || !m.is_contiguous()) fail("mask", "contiguous int32 [masks, words]");
+        r.masks = static_cast<const uint32_t *>(m.data_ptr());
+        r.num_masks = count32(m.size(0), "mask");
+        r.mask_words = count32(m.size(1), "mask");
+        r.mask_rows = ints(a.data(15, "mask_rows", I32, R));
+    }
+    void *out = a.data(16, "out", type, R * V), *ws = a.workspace(17, &bytes);
+    return unlocked(lib.logits, t.data_ptr(), type == F32 ? SV_F32 : SV_BF16, drafts, nd, ro, count32(n, "num_drafts"),
+                    a.i32(4, "k_max"), count32(V, "logits"), count32(R, "logits"), r, out, ws, a.stream(18));
 }
 
 struct State {
@@ -362,12 +500,13 @@ PyObject *call(PyObject *, PyObject *const *v, Py_ssize_t n) {
 
 // Addresses of the entry points in the order of Entry, then the raw-stream function.
 PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    if (n != 10) {
-        PyErr_SetString(PyExc_TypeError, "expected 10 arguments");
+    constexpr int ENTRIES = 12;
+    if (n != ENTRIES + 1) {
+        PyErr_Format(PyExc_TypeError, "expected %d arguments", ENTRIES + 1);
         return nullptr;
     }
-    void *p[9];
-    for (int i = 0; i < 9; i++) {
+    void *p[ENTRIES];
+    for (int i = 0; i < ENTRIES; i++) {
         p[i] = PyLong_AsVoidPtr(v[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -383,8 +522,11 @@ PyObject *init(PyObject *, PyObject *const *v, Py_ssize_t n) {
     lib.copy = reinterpret_cast<decltype(lib.copy)>(p[6]);
     lib.rollback = reinterpret_cast<decltype(lib.rollback)>(p[7]);
     lib.commit = reinterpret_cast<decltype(lib.commit)>(p[8]);
-    Py_INCREF(v[9]);
-    lib.raw_stream = v[9];
+    lib.append8 = reinterpret_cast<decltype(lib.append8)>(p[9]);
+    lib.attention8 = reinterpret_cast<decltype(lib.attention8)>(p[10]);
+    lib.logits = reinterpret_cast<decltype(lib.logits)>(p[11]);
+    Py_INCREF(v[ENTRIES]);
+    lib.raw_stream = v[ENTRIES];
     Py_RETURN_NONE;
 }
 
@@ -399,6 +541,9 @@ PyMethodDef methods[] = {FAST("init", init),
                          FAST("copy", (call<copy, 6>)),
                          FAST("rollback", (call<rollback, 5>)),
                          FAST("commit", (call<commit, 5>)),
+                         FAST("append8", (call<append8, 21>)),
+                         FAST("attention8", (call<attention8, 17>)),
+                         FAST("logits", (call<logits, 19>)),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Checks of tensors before the cache-side calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "sv_cache.cuh"
+#include "sv_rotate.cuh"
 #include "sv_tc.cuh"
 
 namespace svc {
@@ -25,45 +26,10 @@ struct AppendArgs {
     int Hq, half, interleaved;
 };
 
-// inv_freq / (2 pi) as a 64-bit binary fraction of a turn, modulo 1.
-__device__ __forceinline__ uint64_t turns_of(float f) {
-    const uint64_t inv2pi = 0x28BE60DB9391054Aull;   // round(2^64 / (2 pi))
-    const uint32_t u = __float_as_uint(f);
-    const int ex = (u >> 23) & 0xff;
-    const uint64_t m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
-    const int sh = 150 - (ex ? ex : 1);              // f = m 2^-sh
-    const uint64_t lo = m * inv2pi, hi = __umul64hi(m, inv2pi);
-    uint64_t t;
-    if (sh <= 0) t = sh > -64 ? lo << -sh : 0;
-    else if (sh < 64) t = (lo >> sh) | (hi << (64 - sh));
-    else t = sh < 128 ? hi >> (sh - 64) : 0;
-    return (u >> 31) ? 0 - t : t;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
-
 constexpr int AT = 256;   // threads per CTA
 constexpr int AU = 3;     // heads per thread and pass, all loaded before the first is used (4: 9.4 us, 2: 9.9)
 constexpr int OCC = 3;    // CTAs per SM (2: 10.4 us; 4 spill: 12.5)
 constexpr int ROWS = 16;  // rows per CTA at most: 16 KB of rotations
-
-// How the two elements of a pair come together: as neighbours; in one thread, which holds 4 elements
-// of each half (rotary_dim a multiple of 8); or through shared memory, at any distance.
-enum { PAIR_NEXT, PAIR_HALVES, PAIR_ANY };
 
 // Each CTA takes a few rows in a row.  LPH lanes hold one head, 8 elements each (a power of two >=
 // head_dim / 8), so a thread's elements are the same in every head it meets, and its weights and
