@@ -86,6 +86,13 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// 4 bytes in the background; the barrier counts this thread's share once they, and its earlier copies, are there.
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -130,6 +137,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// D[tmem] (+)= A[smem] B[smem] of 8-bit operands, each of either type; fp32 sums.
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor of a tile in 128-byte swizzled rows: 8-row groups are 1024
 // bytes apart (stride offset); `lead` is the distance between 64-element column blocks, which
 // only an operand whose rows run along K (the transposed one) uses.
@@ -144,7 +160,20 @@ __host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int M, int N, bool t
            (uint32_t)(M >> 4) << 24;
 }
 
-// 32 lanes x 32 (16) columns of 32 bits between tensor memory and registers.
+// Descriptor of an operand with N contiguous, without swizzle: blocks of 8 (along K) x 16 bytes (along N), 128
+// bytes each; `next_k` and `next_n` are the distances of neighbouring blocks.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t next_k, uint32_t next_n) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(next_k >> 4) << 16 | (uint64_t)(next_n >> 4) << 32 |
+           (uint64_t)1 << 46;
+}
+// Instruction descriptor for 8-bit operands: A e4m3, B e4m3 or e5m2, 128 x N; `transposed`: both are given with M and
+// N contiguous.
+__host__ __device__ constexpr uint32_t mma8_idesc(bool b_e5m2, int N, bool transposed) {
+    return 1u << 4 | (uint32_t)b_e5m2 << 10 | (uint32_t)transposed << 15 | (uint32_t)transposed << 16 |
+           (uint32_t)(N >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+// 32 lanes x 32 (16, 8) columns of 32 bits between tensor memory and registers.
 #define SVC_R32(r) \
     r(0), r(1), r(2), r(3), r(4), r(5), r(6), r(7), r(8), r(9), r(10), r(11), r(12), r(13), r(14), r(15), r(16), \
         r(17), r(18), r(19), r(20), r(21), r(22), r(23), r(24), r(25), r(26), r(27), r(28), r(29), r(30), r(31)
@@ -165,6 +194,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
         "%23, %24, %25, %26, %27, %28, %29, %30, %31};" ::SVC_R32(SVC_IN), "r"(addr) : "memory");
 #undef SVC_IN
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -179,6 +221,21 @@ __device__ __forceinline__ void after_wait32(uint32_t *v) {
 #define SVC_IO(i) "+r"(v[i])
     asm volatile("" : SVC_R32(SVC_IO));
 #undef SVC_IO
+}
+template <int N>
+__device__ __forceinline__ void after_wait(uint32_t *v) {
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+r"(v[i]));
+}
+
+// Whether `x` holds for any thread of `threads` (whole warps, all of which run this) that meet at barrier `id`.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any) : "r"(id), "r"(threads), "r"((uint32_t)x) : "memory");
+    return any != 0;
 }
 
 // Approximate power of two (within 2^-22 of its value), results below 2^-126 as zero.
@@ -205,6 +262,11 @@ __device__ __forceinline__ void split(uint64_t p, float &a, float &b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {

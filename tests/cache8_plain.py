@@ -38,6 +38,24 @@ def attention(q, k_cache, v_cache, k_scale, v_scale, *rest):
     return plain.attention(q, held(k_cache, k_scale), held(v_cache, v_scale), *rest)
 
 
+def smallest(q, k_cache, v_cache, k_scale, v_scale, table, lens, num_drafts, row_offsets, k_max, scale, window, sinks):
+    """For each output, the largest weight times its value's scale, times the sum of the magnitudes of the numbers that
+    the row sees: an error of e times the largest weight in each of them moves the output by up to e of this."""
+    R, Hq, D = q.shape
+    P, Hk = k_cache.shape[1], k_cache.shape[2]
+    k, one = held(k_cache, k_scale), held(v_cache, torch.ones_like(v_scale))
+    s = v_scale.double().nan_to_num(LEAST).clamp(LEAST, MOST).repeat_interleave(P // v_scale.shape[1], 1)
+    out = torch.zeros(R, Hq, D, dtype=torch.float64)
+    for b, row, n, L in plain.spans(num_drafts, row_offsets, lens, k_max):
+        for i in range(n):
+            j = torch.tensor(plain.visible(L - n + i, window, sinks))
+            page, slot = table[b][j // P].long(), j % P
+            z = scale * torch.einsum("hgd,jhd->hgj", q[row + i].double().view(Hk, Hq // Hk, D), k[page, slot])
+            w = (torch.softmax(z, -1) * s[page, slot].T[:, None]).amax(-1)
+            out[row + i] = (w[..., None] * one[page, slot].abs().sum(0)[:, None]).reshape(Hq, D)
+    return out
+
+
 def append(q, k, v, q_weight, k_weight, eps, inv_freq, k_cache, v_cache, k_scale, v_scale, table, lens, num_drafts,
            row_offsets, k_max, interleaved=False, rope_scale=1.0):
     """(q, its errors' magnitudes) in float64, and for keys and values a list of blocks:

@@ -4,6 +4,10 @@ Tolerances as for spec_attention (its test derives them): an output is off by ep
 weights' rounding (at most eps / 2 of S = sum_j p_j |v_j|; 2^-9 in bf16, whose eps / 2 is 2^-8), by twice what a score
 is off, and by (T + 16) 2^-23 of S for exponentials and sums.  A score is off by head_dim 2^-23 sum |q k| scale as there,
 and by the parts of the queries, 2^-21 of the row's largest element times sum |k| scale.
+A weight, times its value's scale, is held relative to the row's largest such product, which the kernel keeps at 2^12 or
+more, as a sum of e5m2 numbers: whatever its size it is off by at most half of their smallest step, 2^-17, and so
+by 2^-29 of the largest.  (Beside the relative rounding above this matters only where an output's large weights
+meet zeros.)
 """
 import math
 import random
@@ -98,19 +102,20 @@ class OnGpu:
 
 
 def reference(s):
-    """plain.attention, and what the queries' parts may move each row's scores by."""
+    """plain.attention, what the queries' parts may move each row's scores by, and the weights' smallest step each output."""
     rest = s["table"], s["lens"], s["nd"], s["ro"], s["k_max"], s["scale"], s["window"], s["sinks"]
     k, v = plain8.held(s["kc"], s["ks"]), plain8.held(s["vc"], s["vs"])
     ref = plain.attention(s["q"], k, v, *rest)
     top = s["q"].float().abs().amax(-1, keepdim=True).expand(s["q"].shape)
-    return *ref, 2.0 ** -21 * plain.attention(top, k, v, *rest)[3]
+    low = 2.0 ** -29 * plain8.smallest(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], *rest)
+    return *ref, 2.0 ** -21 * plain.attention(top, k, v, *rest)[3], low
 
 
 def check(s, out, lse, rows=None):
-    ro, rl, size, score, parts = reference(s)
+    ro, rl, size, score, parts, low = reference(s)
     D, T, eps = s["q"].shape[2], int(s["lens"].max()), torch.finfo(s["dt"]).eps
     off = D * 2.0 ** -23 * score.double() + parts
-    tol = eps / 2 * ro.abs() + size * (eps / 2 + 2 * off + (T + 16) * 2.0 ** -23)[..., None] + torch.finfo(s["dt"]).tiny
+    tol = eps / 2 * ro.abs() + size * (eps / 2 + 2 * off + (T + 16) * 2.0 ** -23)[..., None] + low + torch.finfo(s["dt"]).tiny
     rows = slice(None) if rows is None else rows
     d = (out.double() - ro).abs()[rows]
     assert bool((d <= tol[rows]).all()), (float((d / tol[rows]).max()), int((~(d <= tol[rows])).sum()))
