@@ -8,8 +8,8 @@
 // Products.  A key tile is the A operand, its 128 keys (for the scores) or 128 elements (for the output) the M of the
 // instruction, and the rows are its N:
 //     S^T[key, row] = K q^T,      O^T[element, row] += V^T P^T.
-// Few rows then cost few columns, and all four warps of a softmax group have work: a thread has one
-// key and all rows, so a key's scale is a register and the sum of a row is spread over the threads until the end.
+// Few rows then cost few columns, and all warps of a softmax group have work: a thread has one
+// key and half of the rows, so a key's scale is a register and the sum of a row is spread over the threads until the end.
 // The B operands are sums of 8-bit parts that lie side by side along N:
 //   - a query row, times the power of two that brings its largest element into (224, 448], is q0 + q1 / 16 (+ q2 / 256) with
 //     e4m3 q0 = RN(q), q1 = RN(16 (q - q0)): 4 bits each, so 2 parts hold a bf16 and 3 an fp16 without loss, for
@@ -22,8 +22,8 @@
 // The score of a key is c ks_j qs_r S (ks: the key's scale, qs: the row's power of two), and the weight that goes to the
 // product with v is p vs_j: log2 vs_j is added to the exponent, and m is the maximum of the sums.  l adds p alone.
 //
-// A CTA: a front warp (segments, queries in parts), one that loads keys, values (tensor copies of pages
-// into two rings) and scales (4-byte copies), one that issues S, one that issues P V, and two groups of 4 softmax warps,
+// A CTA: a front warp (segments, queries in parts), a K and a V warp (tensor copies of pages into two rings; with the
+// keys, 4-byte copies of both sides' scales), one that issues the matrix instructions, and two groups of 8 softmax warps,
 // which take alternate key tiles, each with its own S, P, m, l and O, joined at the end of a segment.  A group's warps
 // decide together, at a barrier per tile, whether a maximum lags too far; every decision that a barrier depends on is
 // taken that way, so a wait that runs out in one warp ends all of them.
@@ -35,11 +35,11 @@
 namespace svc {
 
 constexpr int STAGE8 = TILE * 128;       // bytes of a key tile: 128 bytes a key whatever head_dim
-constexpr int NTHREADS8 = 384;           // 2 x 4 softmax warps, then one warp for each of:
-constexpr int W_LOAD = 9, W_PV = 10, W_S = 11;   // 8 is the front warp
+constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then one warp for each of:
+constexpr int W_K = 17, W_V = 18, W_MMA = 19;   // 16 is the front warp
 constexpr int MAX_STAGES8 = 7, MAX_QBUFS8 = 4;
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
-constexpr int READERS8 = 11;             // warps that take each segment
+constexpr int READERS8 = 19;             // warps that take each segment
 
 template <typename E>
 struct Parts;
@@ -66,8 +66,7 @@ struct Attn8Args {
     int Hq, G, window, sinks;
     int k_stages, v_stages, q_bufs;
     int overhead;      // cost of a row tile beside its key tiles, in key tiles
-    int tile_rows;     // rows of a row tile at most: Parts<E>::ROWS
-    int rp;            // the same in this call, a multiple of 16
+    int tile_rows;     // rows of a row tile at most
     int pitch;         // of part_o: 64 or 128
 
     // Row tiles of M rows: as few as it takes, of one height, a multiple of 8.
@@ -84,10 +83,10 @@ struct Attn8Args {
 // Offsets in shared memory of what stands before the rings.
 struct Small8 {
     uint64_t k_full[MAX_STAGES8], k_empty[MAX_STAGES8], v_full[MAX_STAGES8], v_empty[MAX_STAGES8];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], both[2], drained[2], q_full[MAX_QBUFS8], q_empty[MAX_QBUFS8];
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], both[2], drained, q_full[MAX_QBUFS8], q_empty[MAX_QBUFS8];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
     int dead, tmem, patched[2][4], bad[16];
-    long long scan[16];
+    long long scan[24];
     Seg segs[SEGS];
     float scale[MAX_STAGES8][32];                 // a K stage's scales of keys (16) and of values
     __align__(16) float q_scale[MAX_QBUFS8][MAX_ROWS8];
@@ -141,19 +140,20 @@ __device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t *out) 
     out[P - 1] = __byte_perm(e5m2_of(a), e5m2_of(b), 0x5410);
 }
 
-template <typename E>
+// CHUNKS: of 8 rows that a softmax warp may have; a row tile has 16 CHUNKS rows at most.
+template <typename E, int CHUNKS>
 __global__ void __launch_bounds__(NTHREADS8, 1)
 attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-    constexpr int QP = Parts<E>::Q, PP = Parts<E>::P, ROUNDS = Parts<E>::ROWS / 16;
-    constexpr int S_COLS = QP * Parts<E>::ROWS, O_COLS = PP * Parts<E>::ROWS;
+    constexpr int QP = Parts<E>::Q, PP = Parts<E>::P;
+    constexpr int S_COLS = QP * 16 * CHUNKS, O_COLS = PP * 16 * CHUNKS;
     static_assert(2 * (S_COLS + O_COLS) <= 512, "tensor memory");
     constexpr int NW = NTHREADS8 / 32;
     extern __shared__ __align__(1024) char smem[];
     Small8 &sm = *reinterpret_cast<Small8 *>(smem);
     // [barriers and small state][ring of K tiles][ring of V tiles][query buffers][weights of each group]
     char *const k_p = smem + SMALL8, *const v_p = k_p + P.k_stages * STAGE8, *const q_p = v_p + P.v_stages * STAGE8;
-    const int q_buffer = QP * P.rp * 128, p_buffer = PP * P.rp * 128;
+    const int q_buffer = QP * P.tile_rows * 128, p_buffer = PP * P.tile_rows * 128;
     char *const p_p = q_p + P.q_bufs * q_buffer;
     volatile int *const dead = &sm.dead;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -163,22 +163,22 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     if (tid == 0) {
         for (int i = 0; i < MAX_STAGES8; i++) {
             mbar_init(bar(sm.k_full[i]), 33);    // the copies' bytes, and each lane's scale
-            mbar_init(bar(sm.k_empty[i]), 4);    // a group's warps
+            mbar_init(bar(sm.k_empty[i]), 8);    // a group's warps
             mbar_init(bar(sm.v_full[i]), 1);
             mbar_init(bar(sm.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(sm.s_full[i]), 1);
-            mbar_init(bar(sm.s_free[i]), 4);
-            mbar_init(bar(sm.p_full[i]), 4);
+            mbar_init(bar(sm.s_free[i]), 8);
+            mbar_init(bar(sm.p_full[i]), 8);
             mbar_init(bar(sm.o_done[i]), 1);
-            mbar_init(bar(sm.both[i]), 8);
-            mbar_init(bar(sm.drained[i]), 1);
+            mbar_init(bar(sm.both[i]), 16);
         }
         for (int i = 0; i < MAX_QBUFS8; i++) {
             mbar_init(bar(sm.q_full[i]), 1);
-            mbar_init(bar(sm.q_empty[i]), 9);    // the products, and the softmax warps (for scale and place)
+            mbar_init(bar(sm.q_empty[i]), 17);   // the products, and the softmax warps (for scale and place)
         }
+        mbar_init(bar(sm.drained), 1);
         sm.dead = 0;
     } else if (tid >= 64 && tid < 64 + 2 * SEGS) {
         const int i = tid - 64;
@@ -189,7 +189,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
         sm.bad[tid - 160] = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (warp == W_S) tmem_alloc(smem_addr(&sm.tmem), 512);
+    if (warp == W_MMA) tmem_alloc(smem_addr(&sm.tmem), 512);
     grid_wait();   // the work before this on the stream may still be writing what follows
 
     // The batch's units, and where this CTA's range begins, as in attention_kernel.
@@ -276,18 +276,21 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     };
     const int steps = (C.D + 31) / 32;                    // of 32 elements of a head
 
-    if (warp >= 8) {
-        regs_down<88>();   // to the softmax warps: 2 x 208 + 88 = 3 x 168
-        if (warp == W_LOAD) {
-            // Keys, values and scales of each segment's tiles.
-            const uint32_t k_ring = smem_addr(k_p), v_ring = smem_addr(v_p);
+    if (warp >= 16) {
+        regs_down<64>();   // to the softmax warps: 4 x 104 + 64 = 5 x 96
+        if (warp == W_K || warp == W_V) {
+            // Keys, or values, of each segment's tiles; with the keys, both sides' scales.
+            const bool is_v = warp == W_V;
+            const CUtensorMap *const map = is_v ? &map_v : &map_k;
+            uint64_t *const fulls = is_v ? sm.v_full : sm.k_full, *const empties = is_v ? sm.v_empty : sm.k_empty;
+            const uint32_t ring = smem_addr(is_v ? v_p : k_p), stages = is_v ? v_stages : k_stages;
             Seg s;
             const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
             const int sub = lane & (npg - 1), lane_tile = lane / npg;
             const int per = min(1 << C.block_shift, TILE), blocks = TILE / per;   // tokens per scale, scales per tile and side
             const int blk = lane & 15, blk_tok = blk * per, blk_page = blk_tok / box;
-            Place ka{0, 1}, va{0, 1};   // the first round finds every stage empty
-            uint32_t loads = 0, v_loads = 0;
+            Place at{0, 1};   // the first round finds every stage empty
+            uint32_t loads = 0;
             for (int seg = 0; ok && take(seg, s, true); seg++) {
                 // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
                 // serves several tiles, and is issued that many tiles ahead of its use
@@ -317,110 +320,118 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     }
                     const int base = s.base(t);
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128;
+                    const uint32_t full = bar(fulls[at.stage]);
                     __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
-                    ok = warp_wait(bar(sm.k_empty[ka.stage]), ka.parity, dead);
+                    ok = warp_wait(bar(empties[at.stage]), at.parity, dead);
                     if (!ok) break;
-                    if (P.withhold && loads == 0) {   // (its waits then run out, as they are meant to)
+                    if (P.withhold && !is_v && loads == 0) {   // (its waits then run out, as they are meant to)
                         ok = false;
                         break;
                     }
                     loads++;
-                    const uint32_t kf = bar(sm.k_full[ka.stage]);
-                    if (lane == 0) mbar_expect(kf, bytes);
+                    if (lane == 0) mbar_expect(full, bytes);
                     __syncwarp();
-                    const int y = base & (P_ - 1) & ~(box - 1);
-                    if (id >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * 128, &map_k, kf, 0, y, s.kvh, id);
-                    if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < s.len) {
-                        const int slot = (base + blk_tok) & (P_ - 1);
-                        const float *from = lane < 16 ? C.k_scale : C.v_scale;
-                        copy4(smem_addr(&sm.scale[ka.stage][lane]),
-                              from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + s.kvh * C.s_head);
+                    if (id >= 0)
+                        tma_load_4d(ring + at.stage * STAGE8 + sub * box * 128, map, full, 0, base & (P_ - 1) & ~(box - 1), s.kvh, id);
+                    if (!is_v) {
+                        if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < s.len) {
+                            const int slot = (base + blk_tok) & (P_ - 1);
+                            const float *from = lane < 16 ? C.k_scale : C.v_scale;
+                            copy4(smem_addr(&sm.scale[at.stage][lane]),
+                                  from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + s.kvh * C.s_head);
+                        }
+                        copies_arrive(full);
                     }
-                    copies_arrive(kf);
                     __syncwarp();
-                    ka.advance(k_stages);
-                    ok = warp_wait(bar(sm.v_empty[va.stage]), va.parity, dead);
-                    if (!ok) break;
-                    v_loads++;
-                    const uint32_t vf = bar(sm.v_full[va.stage]);
-                    if (lane == 0) mbar_expect(vf, bytes);
-                    __syncwarp();
-                    if (id >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * 128, &map_v, vf, 0, y, s.kvh, id);
-                    __syncwarp();
-                    va.advance(v_stages);
+                    at.advance(stages);
                 }
             }
             copies_commit();
             copies_wait<0>();
             if (!ok) {   // let the copies in flight land before the CTA may end
                 const uint32_t t0 = now_ns32();
-                for (uint32_t i = loads > k_stages ? loads - k_stages : 0; i < loads; i++)
-                    while (!mbar_try(bar(sm.k_full[i % k_stages]), i / k_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
-                for (uint32_t i = v_loads > v_stages ? v_loads - v_stages : 0; i < v_loads; i++)
-                    while (!mbar_try(bar(sm.v_full[i % v_stages]), i / v_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+                for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
+                    while (!mbar_try(bar(fulls[i % stages]), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
             }
-        } else if (warp == W_S) {
-            // Scores of each tile, as soon as its group has the last ones in registers.
+        } else if (warp == W_MMA) {
+            // Matrix instructions: each tile's scores as soon as its group has the last ones in registers, and its P V as
+            // soon as the weights are there, whichever comes first.  The whole warp runs this; one lane issues.
             const bool leader = elect();
-            Place ks{0, 0}, qs{0, 0};
-            uint32_t g = 0, nf = 3;   // the group whose turn it is; parities of each one's free S
-            Seg s;
-            for (int seg = 0; ok && take(seg, s, true); seg++) {
-                const int nt = s.t1 - s.t0, rp = (P.rows_of(s.M, s.m) + 15) & ~15;
-                const uint32_t idesc = mma8_idesc(false, QP * rp, false);
-                ok = warp_wait(bar(sm.q_full[qs.stage]), qs.parity, dead);
-                const uint64_t qd = smem_desc(smem_addr(q_p) + qs.stage * q_buffer, 16);
+            int sseg = 0, oseg = 0;                    // segments opened
+            int st = 0, snt = 0, srp = 0, ot = 0, ont = 0, orp = 0;   // tile, tiles and columns of a part of the current ones
+            auto open = [&](int &k, int &t, int &nt, int &rp, bool release) {
+                Seg s;
+                t = nt = 0;
+                if (!take(k++, s, release)) return;
+                nt = s.t1 - s.t0;
+                rp = (P.rows_of(s.M, s.m) + 15) & ~15;
+            };
+            open(sseg, st, snt, srp, false);
+            if (ok) open(oseg, ot, ont, orp, true);
+            Place ks{0, 0}, vs{0, 0}, qs{0, 0};
+            uint32_t gs = 0, go = 0, nf = 3, np = 0;   // groups whose turn it is; parities of each one's free S and next P
+            uint32_t polls = 0, idle_since = 0;
 #pragma unroll 1
-                for (int t = 0; ok && t < nt; t++) {
-                    ok = warp_wait(bar(sm.s_free[g]), nf >> g & 1, dead) && warp_wait(bar(sm.k_full[ks.stage]), ks.parity, dead);
-                    if (!ok) break;
-                    tc_fence_after();
+            while (ok && ont) {
+                // all that may be waited for is asked at once; every lane has to have seen it
+                uint32_t there = 0;
+                if (snt) {
+                    there = mbar_test(bar(sm.s_free[gs]), nf >> gs & 1) && mbar_test(bar(sm.k_full[ks.stage]), ks.parity) &&
+                            (st || mbar_test(bar(sm.q_full[qs.stage]), qs.parity));
+                }
+                there |= (uint32_t)(mbar_test(bar(sm.p_full[go]), np >> go & 1) && mbar_test(bar(sm.v_full[vs.stage]), vs.parity)) << 1;
+                there = __reduce_and_sync(0xffffffffu, there);
+                if (!there) {
+                    if (++polls & 255) continue;
+                    const uint32_t now = now_ns32() | 1;
+                    if (!idle_since) idle_since = now;
+                    const bool late = *dead || now - idle_since > WAIT_NS;
+                    if (__any_sync(0xffffffffu, late)) {
+                        *dead = 1;
+                        ok = false;
+                    }
+                    continue;
+                }
+                idle_since = 0;
+                tc_fence_after();
+                if (there & 1) {
                     if (leader) {
-                        const uint64_t kd = smem_desc(smem_addr(k_p) + ks.stage * STAGE8, 16);
+                        const uint32_t idesc = mma8_idesc(false, QP * srp, false);
+                        const uint64_t qd = smem_desc(smem_addr(q_p) + qs.stage * q_buffer, 16),
+                                       kd = smem_desc(smem_addr(k_p) + ks.stage * STAGE8, 16);
                         for (int k = 0; k < steps; k++)
-                            mma8_ss(tmem + g * S_COLS, kd + (uint64_t)(k * 2), qd + (uint64_t)(k * 2), idesc, k > 0);
-                        mma_commit(bar(sm.s_full[g]));
-                        if (t == nt - 1) mma_commit(bar(sm.q_empty[qs.stage]));
+                            mma8_ss(tmem + gs * S_COLS, kd + (uint64_t)(k * 2), qd + (uint64_t)(k * 2), idesc, k > 0);
+                        mma_commit(bar(sm.s_full[gs]));
+                        if (st == snt - 1) mma_commit(bar(sm.q_empty[qs.stage]));
                     }
                     __syncwarp();
-                    nf ^= 1u << g;
-                    g ^= 1;
+                    nf ^= 1u << gs;
+                    gs ^= 1;
                     ks.advance(k_stages);
+                    if (++st == snt) {
+                        qs.advance(q_bufs);
+                        open(sseg, st, snt, srp, false);
+                    }
                 }
-                qs.advance(q_bufs);
-            }
-            if (!ok) drain(sm.drained[0], leader);
-            __syncwarp();
-        } else if (warp == W_PV) {
-            // P V of each tile.
-            const bool leader = elect();
-            Place vs{0, 0};
-            uint32_t g = 0, np = 0;   // parities of each group's next P
-            Seg s;
-            for (int seg = 0; ok && take(seg, s, true); seg++) {
-                const int nt = s.t1 - s.t0, rp = (P.rows_of(s.M, s.m) + 15) & ~15;
-                const uint32_t idesc = mma8_idesc(true, PP * rp, true);
-#pragma unroll 1
-                for (int t = 0; ok && t < nt; t++) {
-                    ok = warp_wait(bar(sm.v_full[vs.stage]), vs.parity, dead) && warp_wait(bar(sm.p_full[g]), np >> g & 1, dead);
-                    if (!ok) break;
-                    tc_fence_after();
+                if ((there & 2) && ok) {
                     if (leader) {
+                        const uint32_t idesc = mma8_idesc(true, PP * orp, true);
                         const uint64_t vd = smem_desc(smem_addr(v_p) + vs.stage * STAGE8, STAGE8),
-                                       pd = smem_desc_plain(smem_addr(p_p) + g * p_buffer, 128, 2048);
+                                       pd = smem_desc_plain(smem_addr(p_p) + go * p_buffer, 128, 2048);
 #pragma unroll
                         for (int k = 0; k < 4; k++)
-                            mma8_ss(tmem + 2 * S_COLS + g * O_COLS, vd + (uint64_t)(k * (4096 >> 4)), pd + (uint64_t)(k * (512 >> 4)), idesc,
-                                    t >= 2 || k > 0);
-                        mma_commit(bar(sm.o_done[g]));
+                            mma8_ss(tmem + 2 * S_COLS + go * O_COLS, vd + (uint64_t)(k * (4096 >> 4)), pd + (uint64_t)(k * (512 >> 4)), idesc,
+                                    ot >= 2 || k > 0);
+                        mma_commit(bar(sm.o_done[go]));
                     }
                     __syncwarp();
-                    np ^= 1u << g;
-                    g ^= 1;
+                    np ^= 1u << go;
+                    go ^= 1;
                     vs.advance(v_stages);
+                    if (++ot == ont) open(oseg, ot, ont, orp, true);
                 }
             }
-            if (!ok) drain(sm.drained[1], leader);
+            if (!ok) drain(sm.drained, leader);
             __syncwarp();
         } else {
             // Front: the segments of this CTA's range, in order, and their queries in parts.  A lane looks at one of 16
@@ -520,7 +531,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 const int ch = lane & (lpr - 1), team = lane / lpr;
                 const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + ch * 8;
                 char *const to = q_p + at.stage * q_buffer;
-                constexpr int U = 4;
+                constexpr int U = 2;
 #pragma unroll 1
                 for (int r0 = 0; r0 < rp; r0 += U * rpw) {
                     uint4 raw[U];
@@ -580,22 +591,23 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             }
         }
     } else {
-        regs_up<208>();
-        // Softmax and epilogue: group g, a thread per key of a tile.
-        Seg s;
-        const int g = warp >> 2, key = (warp & 3) * 32 + lane;
+        regs_up<104>();
+        // Softmax and epilogue: group g, two threads per key of a tile, which have its rows by turns of 8.
+        const int g = warp >> 3, half = warp >> 2 & 1, key = (warp & 3) * 32 + lane, place = tid & 255;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
         const uint32_t t_s = tmem + g * S_COLS + lanes, t_o = tmem + 2 * S_COLS + lanes;
         const int block = key >> min(C.block_shift, 7);               // of this thread's key in a tile
-        char *const p_at = p_p + g * p_buffer + (key >> 3) * 128 + (key & 7) * 16;
-        auto any_of = [&](bool x) { return barrier_any(1 + g, 128, x); };
+        char *const p_at = p_p + g * p_buffer + (key >> 3) * 128 + (key & 7) * 16 + half * 8;
+        auto any_of = [&](bool x) { return barrier_any(1 + g, 256, x); };
         float *const neg_m = sm.neg_m[g], *const lift = sm.lift[g];
         uint32_t mine_done = 0, turn = 0, tiles = 0, joint = 0;   // own tiles; all tiles; barriers of both groups
         Place qs{0, 0};
 #pragma unroll 1
         for (int seg = 0;; seg++) {
-            const bool some = take(seg, s, false);
-            if (any_of(!ok) || !some) break;   // (the list is the same for all four warps)
+            ok = warp_wait(bar(sm.seg_full[seg & (SEGS - 1)]), seg / SEGS & 1, dead);
+            if (any_of(!ok)) break;
+            const Seg &s = sm.segs[seg & (SEGS - 1)];   // (its fields are read where they are needed)
+            if (s.nt == 0) break;
             const int nt = s.t1 - s.t0, mine = (g ^ turn) & 1;        // this group's first key tile
             const uint32_t tile0 = tiles;
             turn += nt;
@@ -616,11 +628,13 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 continue;
             }
             const bool pair = nt > 1;   // both groups hold a part of every row
-            float l[16 * ROUNDS];
+            float l[CHUNKS][8];
 #pragma unroll
-            for (int i = 0; i < 16 * ROUNDS; i++) l[i] = 0.f;
+            for (int c = 0; c < CHUNKS; c++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) l[c][i] = 0.f;
             bool any_tile = false;
-            if (key < MAX_ROWS8) neg_m[key] = UNSET8;
+            if (place < MAX_ROWS8) neg_m[place] = UNSET8;
             ok = warp_wait(bar(sm.q_full[qs.stage]), qs.parity, dead);   // (for the queries' scales and places)
             any_of(false);
 #pragma unroll 1
@@ -632,13 +646,14 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 if (!whole && !seen_by_all(P, s, j)) {   // a value that must not reach the product as it is
                     ok = ok && mbar_wait(bar(sm.v_full[v_stage]), v_round & 1, dead);
                     uint4 *const row = reinterpret_cast<uint4 *>(v_p + v_stage * STAGE8 + key * 128);
+                    // (each half 64 of its bytes, a different bank per lane)
                     if (!seen_by_any(P, s, j)) {         // (a slot never written may hold NaN, and 0 * NaN is NaN)
 #pragma unroll
-                        for (int i = 0; i < 8; i++) row[i ^ (key & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int i = 0; i < 4; i++) row[(4 * half + i) ^ (key & 7)] = make_uint4(0u, 0u, 0u, 0u);
                     } else {                             // (the epilogue gives its NaN to the rows that see it)
                         bool took = false;
 #pragma unroll 1
-                        for (int i = 0; i < 8; i++) {
+                        for (int i = 4 * half; i < 4 * half + 4; i++) {
                             uint4 w = row[i ^ (key & 7)];
                             uint32_t *p = &w.x;
                             bool hit = false;
@@ -659,22 +674,29 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 tc_fence_after();
                 const float ck = P.c * clean_scale(sm.scale[k_stage][block]);
                 const float lvs = lg2(clean_scale(sm.scale[k_stage][16 + block])), rvs = ex2(-lvs);
-                // the scores in powers of two, with the value's scale
-                float u[16 * ROUNDS];
+                // the scores in powers of two, with the value's scale.  Rows lie in order of their tokens, so those that see
+                // this key are neighbours: tokens from the key's own on, up to the last whose window has it.
+                int from = 0, to = 0x7fffffff;
+                if (!whole) {
+                    const int first = j - (s.len - s.n), row0 = P.first_row(s.M, s.m);
+                    from = min(max(first, 0), s.n) * P.G - row0;
+                    if (P.window && j >= P.sinks) to = min(max(first + P.window, 0), s.n) * P.G - row0;
+                }
+                float u[CHUNKS][8];
                 float most = -INFINITY;
 #pragma unroll
-                for (int rd = 0; rd < ROUNDS; rd++) {
-                    if (rd * 16 >= rp) break;
-                    uint32_t x[QP][16];
+                for (int c = 0; c < CHUNKS; c++) {
+                    const int r0 = 16 * c + 8 * half;
+                    if (r0 >= rows) break;
+                    uint32_t x[QP][8];
 #pragma unroll
-                    for (int part = 0; part < QP; part++) tmem_ld16(t_s + part * rp + rd * 16, x[part]);
+                    for (int part = 0; part < QP; part++) tmem_ld8(t_s + part * rp + r0, x[part]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int part = 0; part < QP; part++) after_wait<16>(x[part]);
+                    for (int part = 0; part < QP; part++) after_wait<8>(x[part]);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 qsc = *reinterpret_cast<const float4 *>(q_scale + rd * 16 + i);
-                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + rd * 16 + i);
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 qsc = *reinterpret_cast<const float4 *>(q_scale + r0 + i);
 #pragma unroll
                         for (int h = 0; h < 4; h += 2) {
                             auto pair_at = [&](int part) {
@@ -684,18 +706,21 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
 #pragma unroll
                             for (int part = QP - 2; part >= 0; part--) v = fma2(v, pair_of(0.0625f, 0.0625f), pair_at(part));
                             const uint64_t f = mul2(pair_of(ck, ck), h ? pair_of(qsc.z, qsc.w) : pair_of(qsc.x, qsc.y));
-                            v = fma2(v, f, pair_of(lvs, lvs));
-                            float &a = u[rd * 16 + i + h], &b = u[rd * 16 + i + h + 1];
-                            split(v, a, b);
-                            if (!whole) {
-                                const int p0 = s.len - s.n + (q_place[rd * 16 + i + h] >> 16), p1 = s.len - s.n + (q_place[rd * 16 + i + h + 1] >> 16);
-                                if (!sees(P, p0, j)) a = -INFINITY;
-                                if (!sees(P, p1, j)) b = -INFINITY;
-                            }
-                            float da, db;
-                            split(add2(pair_of(a, b), h ? pair_of(nm.z, nm.w) : pair_of(nm.x, nm.y)), da, db);
-                            most = max3(most, da, db);
+                            split(fma2(v, f, pair_of(lvs, lvs)), u[c][i + h], u[c][i + h + 1]);
                         }
+                    }
+                    if (!whole) {   // (rows from `from` up to `to` see this key)
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            if (r0 + i < from || r0 + i >= to) u[c][i] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
+                        float d[4];
+                        split(add2(pair_of(u[c][i], u[c][i + 1]), pair_of(nm.x, nm.y)), d[0], d[1]);
+                        split(add2(pair_of(u[c][i + 2], u[c][i + 3]), pair_of(nm.z, nm.w)), d[2], d[3]);
+                        most = max3(most, max3(d[0], d[1], d[2]), d[3]);
                     }
                 }
                 tc_fence_before();
@@ -709,7 +734,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     if (waited) return;
                     ok = warp_wait(bar(sm.o_done[g]), (mine_done - 1) & 1, dead) && ok;
                     tc_fence_after();
-                    if ((warp & 3) == 0 && lane == 0) mbar_arrive(bar(sm.v_empty[(tile - 2) % v_stages]));
+                    if ((warp & 7) == 0 && lane == 0) mbar_arrive(bar(sm.v_empty[(tile - 2) % v_stages]));
                     waited = true;
                 };
                 if (any_of(most > MOST8 || !ok)) {
@@ -719,49 +744,50 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     }
                     // lift the maxima: of the tile's keys over the warps, then of each row by a thread
 #pragma unroll
-                    for (int rd = 0; rd < ROUNDS; rd++) {
-                        if (rd * 16 >= rp) break;
+                    for (int c = 0; c < CHUNKS; c++) {
+                        if (16 * c + 8 * half >= rows) break;
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const int top = __reduce_max_sync(0xffffffffu, ordered(u[rd * 16 + i]));
-                            if (lane == 0) sm.top[g][warp & 3][rd * 16 + i] = top;
+                        for (int i = 0; i < 8; i++) {
+                            const int top = __reduce_max_sync(0xffffffffu, ordered(u[c][i]));
+                            if (lane == 0) sm.top[g][warp & 3][16 * c + 8 * half + i] = top;
                         }
                     }
                     any_of(false);
-                    if (key < rp) {
-                        int top = sm.top[g][0][key];
+                    if (place < (rows + 7) / 8 * 8) {
+                        int top = sm.top[g][0][place];
 #pragma unroll
-                        for (int w = 1; w < 4; w++) top = max(top, sm.top[g][w][key]);
-                        const float m = unordered(top), was = neg_m[key];
+                        for (int w = 1; w < 4; w++) top = max(top, sm.top[g][w][place]);
+                        const float m = unordered(top), was = neg_m[place];
                         float f = 1.f;
                         if (!(m <= INFINITY)) {   // a NaN that the row sees: it has no maximum any more
-                            neg_m[key] = NAN;
+                            neg_m[place] = NAN;
                         } else if (m + was > BIAS8) {
-                            neg_m[key] = BIAS8 - m;
+                            neg_m[place] = BIAS8 - m;
                             if (was != UNSET8) f = ex2((BIAS8 - was) - m);
                         }
-                        lift[key] = f;
+                        lift[place] = f;
                     }
                     any_of(false);
                     last_product();
 #pragma unroll
-                    for (int rd = 0; rd < ROUNDS; rd++) {
-                        if (rd * 16 >= rp) break;
-                        float f[16];
+                    for (int c = 0; c < CHUNKS; c++) {
+                        const int r0 = 16 * c + 8 * half;
+                        if (r0 >= rows) break;
+                        float f[8];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(lift + rd * 16 + i);
+                        for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(lift + r0 + i);
 #pragma unroll
-                        for (int i = 0; i < 16; i++) l[rd * 16 + i] *= f[i];
+                        for (int i = 0; i < 8; i++) l[c][i] *= f[i];
                         if (!any_tile) continue;
 #pragma unroll
                         for (int part = 0; part < PP; part++) {
-                            uint32_t o[16];
-                            tmem_ld16(t_o + g * O_COLS + part * rp + rd * 16, o);
+                            uint32_t o[8];
+                            tmem_ld8(t_o + g * O_COLS + part * rp + r0, o);
                             tmem_wait_ld();
-                            after_wait<16>(o);
+                            after_wait<8>(o);
 #pragma unroll
-                            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-                            tmem_st16(t_o + g * O_COLS + part * rp + rd * 16, o);
+                            for (int i = 0; i < 8; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+                            tmem_st8(t_o + g * O_COLS + part * rp + r0, o);
                         }
                     }
                     tmem_wait_st();
@@ -769,21 +795,22 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 last_product();
                 // the weights: their sum, and their parts
 #pragma unroll
-                for (int rd = 0; rd < ROUNDS; rd++) {
-                    if (rd * 16 >= rp) break;
-                    uint32_t w[PP][4];
+                for (int c = 0; c < CHUNKS; c++) {
+                    const int r0 = 16 * c + 8 * half;
+                    if (r0 >= rows) break;
+                    uint32_t w[PP][2];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + rd * 16 + i);
-                        const int at = rd * 16 + i;
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
                         float d[4];
-                        split(add2(pair_of(u[at], u[at + 1]), pair_of(nm.x, nm.y)), d[0], d[1]);
-                        split(add2(pair_of(u[at + 2], u[at + 3]), pair_of(nm.z, nm.w)), d[2], d[3]);
+                        split(add2(pair_of(u[c][i], u[c][i + 1]), pair_of(nm.x, nm.y)), d[0], d[1]);
+                        split(add2(pair_of(u[c][i + 2], u[c][i + 3]), pair_of(nm.z, nm.w)), d[2], d[3]);
 #pragma unroll
                         for (int e = 0; e < 4; e++) d[e] = ex2(d[e]);
 #pragma unroll
                         for (int e = 0; e < 4; e += 2)
-                            split(fma2(pair_of(d[e], d[e + 1]), pair_of(rvs, rvs), pair_of(l[at + e], l[at + e + 1])), l[at + e], l[at + e + 1]);
+                            split(fma2(pair_of(d[e], d[e + 1]), pair_of(rvs, rvs), pair_of(l[c][i + e], l[c][i + e + 1])), l[c][i + e],
+                                  l[c][i + e + 1]);
                         uint32_t parts[PP];
                         parts_of<PP>(half2_of(d[0], d[1]), half2_of(d[2], d[3]), parts);
 #pragma unroll
@@ -791,8 +818,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     }
 #pragma unroll
                     for (int part = 0; part < PP; part++)
-                        *reinterpret_cast<uint4 *>(p_at + ((part * rp >> 4) + rd) * 2048) =
-                            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
+                        *reinterpret_cast<uint2 *>(p_at + ((part * rp >> 4) + c) * 2048) = make_uint2(w[part][0], w[part][1]);
                 }
                 fence_proxy_async();
                 tc_fence_before();
@@ -803,29 +829,31 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             }
             // each row's sum over this warp's keys, while the last product runs
 #pragma unroll
-            for (int rd = 0; rd < ROUNDS; rd++) {
-                if (rd * 16 >= rp) break;
-                float *x = l + rd * 16;
+            for (int c = 0; c < CHUNKS; c++) {
+                if (16 * c + 8 * half >= rows) break;
+                float *x = l[c];
 #pragma unroll
-                for (int o = 16, n = 8; n; o >>= 1, n >>= 1)
+                for (int o = 16, n = 4; n; o >>= 1, n >>= 1)
 #pragma unroll
                     for (int i = 0; i < n; i++) {
                         const bool up = lane & o;
                         const float give = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
                         x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                     }
+                x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
                 x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-                if (!(lane & 1)) sm.sum[g][warp & 3][rd * 16 + (lane >> 1)] = x[0];
+                if (!(lane & 3)) sm.sum[g][warp & 3][16 * c + 8 * half + (lane >> 2)] = x[0];
             }
             if (ok) ok = warp_wait(bar(sm.o_done[g]), (mine_done - 1) & 1, dead);
-            if (ok && (warp & 3) == 0 && lane == 0)
+            if (ok && (warp & 7) == 0 && lane == 0)
                 mbar_arrive(bar(sm.v_empty[(tile0 + nt - 1 - ((nt - 1 - mine) & 1)) % v_stages]));
             if (any_of(!ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (key < rp) sm.total[g][key] = sm.sum[g][0][key] + sm.sum[g][1][key] + sm.sum[g][2][key] + sm.sum[g][3][key];
+            if (place < rows)
+                sm.total[g][place] = sm.sum[g][0][place] + sm.sum[g][1][place] + sm.sum[g][2][place] + sm.sum[g][3][place];
             if (pair) {   // the other group's maxima, sums and O
                 tc_fence_before();
                 __syncwarp();
@@ -843,24 +871,24 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             const bool broken = *reinterpret_cast<volatile int *>(&sm.bad[seg & 15]) == seg + 1;
             auto patched_by = [&](int i) { return *reinterpret_cast<volatile int *>(&sm.patched[i][seg & 3]) == seg; };
             const bool patch = patched_by(g) || (pair && patched_by(g ^ 1));
-            if (key < rows) {   // the row's maximum and sum, and the factors of the (up to) two sums O
-                const float m0 = BIAS8 - neg_m[key], m1 = pair ? BIAS8 - sm.neg_m[g ^ 1][key] : -UNSET8;
+            if (place < rows) {   // the row's maximum and sum, and the factors of the (up to) two sums O
+                const float m0 = BIAS8 - neg_m[place], m1 = pair ? BIAS8 - sm.neg_m[g ^ 1][place] : -UNSET8;
                 const float top = fmaxf(m0, m1), f0 = ex2(m0 - top), f1 = pair ? ex2(m1 - top) : 0.f;
-                float sum = sm.total[g][key] * f0 + (pair ? sm.total[g ^ 1][key] * f1 : 0.f);
+                float sum = sm.total[g][place] * f0 + (pair ? sm.total[g ^ 1][place] * f1 : 0.f);
                 if (broken) sum = NAN;
                 const float inv = sum == 0.f ? 0.f : rcp(sum);
-                sm.factor[g][g][key] = f0 * inv;
-                sm.factor[g][g ^ 1][key] = f1 * inv;
+                sm.factor[g][g][place] = f0 * inv;
+                sm.factor[g][g ^ 1][place] = f1 * inv;
                 if (!pair || g == 0) {
                     const float lse2 = sum == 0.f ? -INFINITY : top + lg2(sum) - BIAS8;
-                    const int place = q_place[key];
-                    if (!direct) P.part_lse[slot * MAX_ROWS8 + key] = lse2;
-                    else if (P.lse) P.lse[orow0 + (int64_t)(place >> 16) * P.Hq + (place & 0xffff)] = lse2 * 0.6931471805599453f;
+                    const int at = q_place[place];
+                    if (!direct) P.part_lse[slot * MAX_ROWS8 + place] = lse2;
+                    else if (P.lse) P.lse[orow0 + (int64_t)(at >> 16) * P.Hq + (at & 0xffff)] = lse2 * 0.6931471805599453f;
                 }
             }
             any_of(false);
 #pragma unroll 1
-            for (int c = pair ? 8 * g : 0; c < rows; c += pair ? 16 : 8) {
+            for (int c = pair ? 16 * g + 8 * half : 8 * half; c < rows; c += pair ? 32 : 16) {
                 uint32_t x[PP][8], y[PP][8];
 #pragma unroll
                 for (int part = 0; part < PP; part++) {
@@ -908,8 +936,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     for (int i = 0; i < 8; i++) {
                         if (c + i >= rows) break;
                         if (direct) {
-                            const int place = q_place[c + i];
-                            static_cast<E *>(P.out)[(orow0 + (int64_t)(place >> 16) * P.Hq + (place & 0xffff)) * C.D + key] = (E)o[i];
+                            const int at = q_place[c + i];
+                            static_cast<E *>(P.out)[(orow0 + (int64_t)(at >> 16) * P.Hq + (at & 0xffff)) * C.D + key] = (E)o[i];
                         } else {
                             P.part_o[((int64_t)slot * MAX_ROWS8 + c + i) * P.pitch + key] = o[i];
                         }
@@ -929,7 +957,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *dead) record_error(P.hdr, SV_DEV_TIMEOUT, 0);
-    if (warp == W_S) {
+    if (warp == W_MMA) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }
@@ -964,17 +992,16 @@ static Attn8Ws attn8_ws(int D) {
 
 constexpr int SMEM_MAX8 = 232448;
 
-template <typename E>
-static sv_status launch_attention8(const Batch &A, const Cache8 &C, Attn8Args P, const sv_kv_cache8 &cache, cudaStream_t st) {
+template <typename E, int CHUNKS>
+static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, const sv_kv_cache8 &cache, cudaStream_t st) {
     int dev = 0, nsm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
-    P.tile_rows = Parts<E>::ROWS;
-    P.rp = most_rows < P.tile_rows ? (most_rows + 15) / 16 * 16 : P.tile_rows;
-    P.q_bufs = P.rp <= 16 ? MAX_QBUFS8 : 2;
-    const int other = P.q_bufs * Parts<E>::Q * P.rp * 128 + 2 * Parts<E>::P * P.rp * 128;
+    P.tile_rows = 16 * CHUNKS;
+    P.q_bufs = P.tile_rows <= 16 ? MAX_QBUFS8 : 2;
+    const int other = P.q_bufs * Parts<E>::Q * P.tile_rows * 128 + 2 * Parts<E>::P * P.tile_rows * 128;
     const int stages = (SMEM_MAX8 - SMALL8 - other) / STAGE8;
     P.overhead = 2;
     P.k_stages = stages / 2 < MAX_STAGES8 ? stages / 2 : MAX_STAGES8;
@@ -988,7 +1015,7 @@ static sv_status launch_attention8(const Batch &A, const Cache8 &C, Attn8Args P,
     if (C.D % 128 && cache.head_stride % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas) ctas -= ctas % C.heads;
     if (most < ctas) ctas = (int)most;
     // (one limit for every call: another thread's call may come between this and the launch)
-    if (cudaFuncSetAttribute(attention8_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX8) != cudaSuccess)
+    if (cudaFuncSetAttribute(attention8_kernel<E, CHUNKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX8) != cudaSuccess)
         return SV_ERR_CUDA;
     // (after a runtime call that brings this host thread to the device)
     CUtensorMap mk, mv;
@@ -1003,7 +1030,7 @@ static sv_status launch_attention8(const Batch &A, const Cache8 &C, Attn8Args P,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attention8_kernel<E>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attention8_kernel<E, CHUNKS>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
     cfg.gridDim = dim3(ctas, (most_rows < 8 ? most_rows : 8) + 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -1011,6 +1038,14 @@ static sv_status launch_attention8(const Batch &A, const Cache8 &C, Attn8Args P,
                            : cudaLaunchKernelEx(&cfg, join_kernel<E, 64, Cache8, Attn8Args>, A, C, P)) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
+}
+
+template <typename E>
+static sv_status launch_attention8(const Batch &A, const Cache8 &C, const Attn8Args &P, const sv_kv_cache8 &cache, cudaStream_t st) {
+    const int rows = (A.k_max + 1) * P.G;
+    if (rows <= 16) return launch_rows8<E, 1>(A, C, P, cache, st);
+    if (rows <= 32 || Parts<E>::ROWS == 32) return launch_rows8<E, 2>(A, C, P, cache, st);
+    return launch_rows8<E, Parts<E>::ROWS / 16>(A, C, P, cache, st);
 }
 
 }  // namespace svc
