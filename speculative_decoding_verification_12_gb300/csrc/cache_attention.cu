@@ -76,7 +76,7 @@ struct AttnArgs {
     int q_rows, q_bufs;   // rows of a query buffer (a multiple of 8), and how many there are
 
     // Row tiles of M rows: one of up to 128, or as many of up to 256 as it takes.
-    static constexpr int PART = PART_ROWS;
+    static constexpr int PART = PART_ROWS, MAX_RANGES = MAX_CTAS, RANGE_BITS = 8;
     static __device__ __forceinline__ int tiles_of(int M) { return M <= TILE ? 1 : (M + 2 * TILE - 1) / (2 * TILE); }
     static __device__ __forceinline__ int first_row(int M, int m) { return m * 2 * TILE; }
     static __device__ __forceinline__ int rows_of(int M, int m) { return min(M - m * 2 * TILE, 2 * TILE); }

@@ -10,23 +10,26 @@
 //     S^T[key, row] = K q^T,      O^T[element, row] += V^T P^T.
 // Few rows then cost few columns, and all warps of a softmax group have work: a thread has one
 // key and half of the rows, so a key's scale is a register and the sum of a row is spread over the threads until the end.
-// The B operands are sums of 8-bit parts that lie side by side along N:
-//   - a query row, times the power of two that brings its largest element into (224, 448], is q0 + q1 / 16 (+ q2 / 256) with
-//     e4m3 q0 = RN(q), q1 = RN(16 (q - q0)): 4 bits each, so 2 parts hold a bf16 and 3 an fp16 without loss, for
-//     elements down to 2^-14 of the largest;
+// The B operands are sums of 8-bit parts:
+//   - a query row, times the power of two that brings its largest element into (224, 448], is q0 + q1 + q2 with
+//     q0 = RN(q) in e4m3, 4 bits, q1 = RN(q - q0) and q2 = RN(q - q0 - q1) in e5m2, 3 bits and a sign each: 10 bits and two
+//     signs hold a bf16 and an fp16 without loss, for elements down to 2^-14 of the largest, and the smallest step of
+//     e5m2 leaves 2^-24 of it below.  They are added up along K, in one accumulator: the keys are read three times,
+//     which costs less than the columns that parts side by side would take and a thread would have to add;
 //   - a weight in fp16 is a sum of its top byte, the top byte of the rest, and so on: an fp16's top byte is an e5m2
-//     number.  2 (3) of them and the rest rounded to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans
+//     number.  The parts lie side by side along N, so that the values are read once.  2 (3) of them and the rest rounded to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans
 //     2^-17 to 2^15.8, and the running maximum is kept between 2^12 and 2^15.5, so what is rounded away is below 2^-29 of
 //     a row's largest weight, and unbiased.  (e4m3 parts would end 2^-18 below it: 131 072 small weights
 //     would lose a percent of the sum.)
 // The score of a key is c ks_j qs_r S (ks: the key's scale, qs: the row's power of two), and the weight that goes to the
 // product with v is p vs_j: log2 vs_j is added to the exponent, and m is the maximum of the sums.  l adds p alone.
 //
-// A CTA: a front warp (segments, queries in parts), a K and a V warp (tensor copies of pages into two rings; with the
-// keys, 4-byte copies of both sides' scales), one that issues the matrix instructions, and two groups of 8 softmax warps,
-// which take alternate key tiles, each with its own S, P, m, l and O, joined at the end of a segment.  A group's warps
-// decide together, at a barrier per tile, whether a maximum lags too far; every decision that a barrier depends on is
-// taken that way, so a wait that runs out in one warp ends all of them.
+// A CTA works at two ranges at once.  It has a front warp (the segments of both ranges, half a warp each), a warp for each
+// range that loads keys and values (tensor copies of pages into two rings) and scales (4-byte copies), one that issues all
+// matrix instructions, and a group of 8 softmax warps for each range, which also brings its queries into parts.  While one
+// range changes from a segment to the next, the other keeps the memory busy.  A group's warps decide
+// together, at a barrier per tile, whether a maximum lags too far; every decision that a barrier depends on is taken
+// that way, so a wait that runs out in one warp ends all of them.
 #include "sv_cache8.cuh"
 #include "sv_launch.h"
 #include "sv_segments.cuh"
@@ -35,21 +38,23 @@
 namespace svc {
 
 constexpr int STAGE8 = TILE * 128;       // bytes of a key tile: 128 bytes a key whatever head_dim
-constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then one warp for each of:
-constexpr int W_K = 17, W_V = 18, W_MMA = 19;   // 16 is the front warp
-constexpr int MAX_STAGES8 = 7, MAX_QBUFS8 = 4;
+constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then
+constexpr int W_LOAD = 17, W_MMA = 19;   // 16: front; 17, 18: loads of each range; 19: matrix instructions
+constexpr int MAX_STAGES8 = 4;           // of a ring: keys and values of each range
+constexpr int SCALES8 = 8;               // tiles whose scales are kept (more than a ring's stages and one)
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
-constexpr int READERS8 = 19;             // warps that take each segment
+constexpr int READERS8 = 9;              // warps that take each segment
+constexpr int QP = 3;                    // parts of a query
 
 template <typename E>
 struct Parts;
 template <>
 struct Parts<__nv_bfloat16> {
-    static constexpr int Q = 2, P = 3, ROWS = 48;   // 2 (Q + P) ROWS columns of tensor memory
+    static constexpr int P = 3, ROWS = 48;   // (4 + 2 P) ROWS columns of tensor memory
 };
 template <>
 struct Parts<__half> {
-    static constexpr int Q = 3, P = 4, ROWS = 32;
+    static constexpr int P = 4, ROWS = 32;
 };
 
 struct Attn8Args {
@@ -58,19 +63,19 @@ struct Attn8Args {
     void *out;
     float *lse;
     int32_t *hdr;
-    int4 *desc;        // as in AttnArgs
-    float *part_lse;   // [2 * MAX_CTAS][PART]
-    float *part_o;     // [2 * MAX_CTAS][PART][pitch]
+    int4 *desc;        // as in AttnArgs, per range
+    float *part_lse;   // [2 * MAX_RANGES][PART]
+    float *part_o;     // [2 * MAX_RANGES][PART][pitch]
     float c;           // scale log2(e)
     int withhold;
     int Hq, G, window, sinks;
-    int k_stages, v_stages, q_bufs;
+    int k_stages, v_stages;   // of each range
     int overhead;      // cost of a row tile beside its key tiles, in key tiles
     int tile_rows;     // rows of a row tile at most
     int pitch;         // of part_o: 64 or 128
 
     // Row tiles of M rows: as few as it takes, of one height, a multiple of 8.
-    static constexpr int PART = MAX_ROWS8;
+    static constexpr int PART = MAX_ROWS8, MAX_RANGES = 2 * MAX_CTAS, RANGE_BITS = 10;
     __device__ __forceinline__ int tiles_of(int M) const { return (M + tile_rows - 1) / tile_rows; }
     __device__ __forceinline__ int height(int M) const {
         const int mt = tiles_of(M);
@@ -80,29 +85,30 @@ struct Attn8Args {
     __device__ __forceinline__ int rows_of(int M, int m) const { return min(M - m * height(M), height(M)); }
 };
 
-// Offsets in shared memory of what stands before the rings.
+// What stands in shared memory before the rings; [2]: of each range.
 struct Small8 {
-    uint64_t k_full[MAX_STAGES8], k_empty[MAX_STAGES8], v_full[MAX_STAGES8], v_empty[MAX_STAGES8];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], both[2], drained, q_full[MAX_QBUFS8], q_empty[MAX_QBUFS8];
-    uint64_t seg_full[SEGS], seg_empty[SEGS];
-    int dead, tmem, patched[2][4], bad[16];
+    uint64_t k_full[2][MAX_STAGES8], k_empty[2][MAX_STAGES8], v_full[2][MAX_STAGES8], v_empty[2][MAX_STAGES8];
+    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_full[2], drained;
+    uint64_t seg_full[2][SEGS], seg_empty[2][SEGS];
+    int dead, tmem, patched[2], bad[2][16];
+    int k_info[2][MAX_STAGES8], v_info[2][MAX_STAGES8];   // of a stage's tile, as the loading warp notes it: see INFO_*
     long long scan[24];
-    Seg segs[SEGS];
-    float scale[MAX_STAGES8][32];                 // a K stage's scales of keys (16) and of values
-    __align__(16) float q_scale[MAX_QBUFS8][MAX_ROWS8];
-    int q_place[MAX_QBUFS8][MAX_ROWS8];           // a row's token of the request << 16 | head of the group
-    __align__(16) float neg_m[2][MAX_ROWS8];      // BIAS - m, or UNSET
+    Seg segs[2][SEGS];
+    float scale[2][SCALES8][32];                  // a tile's scales of keys (16) and of values
+    __align__(16) float q_scale[2][MAX_ROWS8];
+    int q_place[2][MAX_ROWS8];                    // a row's token of the request << 16 | head of the group
+    __align__(16) float neg_m[2][MAX_ROWS8];      // BIAS - m; 0 before a row has a maximum
     __align__(16) float lift[2][MAX_ROWS8];
+    int set[2][MAX_ROWS8];                        // whether a row has a maximum
     int top[2][4][MAX_ROWS8];
     float sum[2][4][MAX_ROWS8];
-    float total[2][MAX_ROWS8];
-    float factor[2][2][MAX_ROWS8];                // [group that reads][group whose O]
+    float factor[2][MAX_ROWS8];
 };
 constexpr int SMALL8 = (sizeof(Small8) + 1023) / 1024 * 1024;
+constexpr int INFO_FIRST = 0x100;   // a segment's first tile; the low byte: columns of a part, or 0 at the end of the range
 
 constexpr float BIAS8 = 12.f;      // log2 of the largest weight, for a maximum that does not lag
 constexpr float MOST8 = 15.5f;     // and the largest that may be: 57344 is e5m2's last number
-constexpr float UNSET8 = 1e30f;    // neg_m of a row that has seen nothing yet
 
 // fp32 numbers as integers of the same order.
 __device__ __forceinline__ int ordered(float x) {
@@ -145,82 +151,86 @@ template <typename E, int CHUNKS>
 __global__ void __launch_bounds__(NTHREADS8, 1)
 attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-    constexpr int QP = Parts<E>::Q, PP = Parts<E>::P;
-    constexpr int S_COLS = QP * 16 * CHUNKS, O_COLS = PP * 16 * CHUNKS;
-    static_assert(2 * (S_COLS + O_COLS) <= 512, "tensor memory");
+    constexpr int PP = Parts<E>::P, ROWS = 16 * CHUNKS;
+    constexpr int S_COLS = ROWS, O_COLS = PP * ROWS;   // two S and one O of each range
+    static_assert(4 * S_COLS + 2 * O_COLS <= 512, "tensor memory");
     constexpr int NW = NTHREADS8 / 32;
+    constexpr int Q_BUFFER = QP * ROWS * 128, P_BUFFER = PP * ROWS * 128;
     extern __shared__ __align__(1024) char smem[];
     Small8 &sm = *reinterpret_cast<Small8 *>(smem);
-    // [barriers and small state][ring of K tiles][ring of V tiles][query buffers][weights of each group]
-    char *const k_p = smem + SMALL8, *const v_p = k_p + P.k_stages * STAGE8, *const q_p = v_p + P.v_stages * STAGE8;
-    const int q_buffer = QP * P.tile_rows * 128, p_buffer = PP * P.tile_rows * 128;
-    char *const p_p = q_p + P.q_bufs * q_buffer;
+    // [barriers and small state][rings of K tiles][rings of V tiles][queries of each range][weights of each range]
+    char *const k_p = smem + SMALL8, *const v_p = k_p + 2 * P.k_stages * STAGE8, *const q_p = v_p + 2 * P.v_stages * STAGE8;
+    char *const p_p = q_p + 2 * Q_BUFFER;
     volatile int *const dead = &sm.dead;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t k_stages = P.k_stages, v_stages = P.v_stages, q_bufs = P.q_bufs;
+    const uint32_t k_stages = P.k_stages, v_stages = P.v_stages;
     auto bar = [&](const uint64_t &b) { return smem_addr(&b); };
 
-    if (tid == 0) {
+    if (tid < 2) {
+        const int w = tid;
         for (int i = 0; i < MAX_STAGES8; i++) {
-            mbar_init(bar(sm.k_full[i]), 33);    // the copies' bytes, and each lane's scale
-            mbar_init(bar(sm.k_empty[i]), 8);    // a group's warps
-            mbar_init(bar(sm.v_full[i]), 1);
-            mbar_init(bar(sm.v_empty[i]), 1);
+            mbar_init(bar(sm.k_full[w][i]), 33);    // the copies' bytes, and each lane's scale
+            mbar_init(bar(sm.k_empty[w][i]), 1);
+            mbar_init(bar(sm.v_full[w][i]), 1);
+            mbar_init(bar(sm.v_empty[w][i]), 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(bar(sm.s_full[i]), 1);
-            mbar_init(bar(sm.s_free[i]), 8);
-            mbar_init(bar(sm.p_full[i]), 8);
-            mbar_init(bar(sm.o_done[i]), 1);
-            mbar_init(bar(sm.both[i]), 16);
+            mbar_init(bar(sm.s_full[w][i]), 1);
+            mbar_init(bar(sm.s_free[w][i]), 8);     // the group's warps
         }
-        for (int i = 0; i < MAX_QBUFS8; i++) {
-            mbar_init(bar(sm.q_full[i]), 1);
-            mbar_init(bar(sm.q_empty[i]), 17);   // the products, and the softmax warps (for scale and place)
+        mbar_init(bar(sm.p_full[w]), 8);
+        mbar_init(bar(sm.o_done[w]), 1);
+        mbar_init(bar(sm.q_full[w]), 8);
+        if (w == 0) {
+            mbar_init(bar(sm.drained), 1);
+            sm.dead = 0;
         }
-        mbar_init(bar(sm.drained), 1);
-        sm.dead = 0;
-    } else if (tid >= 64 && tid < 64 + 2 * SEGS) {
-        const int i = tid - 64;
-        mbar_init(i < SEGS ? bar(sm.seg_full[i]) : bar(sm.seg_empty[i - SEGS]), i < SEGS ? 1 : READERS8);
-    } else if (tid >= 128 && tid < 136) {
-        sm.patched[(tid - 128) >> 2][tid & 3] = -1;
-    } else if (tid >= 160 && tid < 176) {
-        sm.bad[tid - 160] = 0;
+    } else if (tid >= 64 && tid < 64 + 4 * SEGS) {
+        const int i = tid - 64, w = i / (2 * SEGS), k = i % (2 * SEGS);
+        mbar_init(k < SEGS ? bar(sm.seg_full[w][k]) : bar(sm.seg_empty[w][k - SEGS]), k < SEGS ? 1 : READERS8);
+    } else if (tid >= 256 && tid < 256 + 32) {
+        sm.bad[(tid >> 4) & 1][tid & 15] = 0;
+    } else if (tid >= 320 && tid < 322) {
+        sm.patched[tid - 320] = -1;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (warp == W_MMA) tmem_alloc(smem_addr(&sm.tmem), 512);
     grid_wait();   // the work before this on the stream may still be writing what follows
 
-    // The batch's units, and where this CTA's range begins, as in attention_kernel.
-    long long &start_pre = sm.scan[NW], &start_b = sm.scan[NW + 1];
-    long long W = 0, T = 0, lo = 0, hi = 0, before = 0;   // units of one key head, of all, and this CTA's range
-    int nc = 0, kvh0 = 0;
-    const int cta = blockIdx.x;
+    // The batch's units, and where this CTA's ranges begin, as in attention_kernel; range r of `nr` is the first of CTA r,
+    // or the second of CTA r - gridDim.x, so that a few ranges lie on as many multiprocessors.
     auto units_of = [&](const Req &r) { return r.nt ? (long long)(r.nt + P.overhead) * r.mt : 0ll; };
-    auto range = [&]() {   // [T cta / nc, T (cta + 1) / nc), and the head that it begins in
-        T = W * C.heads;
-        nc = (int)min((long long)gridDim.x, T);
-        if (cta < nc) {
-            const long long q = quotient(T, nc);
-            const int rest = (int)(T - q * nc);
-            lo = q * cta + rest * cta / nc;
-            hi = q * (cta + 1) + rest * (cta + 1) / nc;
-            if (lo < hi) kvh0 = (int)quotient64(lo, W);
-        }
+    long long W = 0;          // units of one key head
+    struct Range {
+        long long lo, hi;
+        int kvh, nr;          // the key head that it begins in, ranges in all
     };
+    auto range = [&](int w) {
+        const long long T = W * C.heads;
+        Range R = {0, 0, 0, (int)min(2ll * gridDim.x, T)};
+        const int id = w * gridDim.x + blockIdx.x;
+        if (id < R.nr) {
+            const long long q = quotient(T, R.nr);
+            const int rest = (int)(T - q * R.nr);
+            R.lo = q * id + (long long)rest * id / R.nr;
+            R.hi = q * (id + 1) + (long long)rest * (id + 1) / R.nr;
+            if (R.lo < R.hi) R.kvh = (int)quotient64(R.lo, W);
+        }
+        return R;
+    };
+    long long *const start_pre = sm.scan + NW, *const start_b = sm.scan + NW + 2;
     if (A.B > SMALL_BATCH) {
         __syncthreads();   // (barriers and flags are set)
 #pragma unroll 1
         for (int pass = A.B <= NTHREADS8; pass < 2; pass++) {   // pass 0 sums, pass 1 finds
-            before = 0;
+            long long before = 0, at[2] = {-1, -1};
 #pragma unroll 1
             for (int b0 = 0; b0 < A.B; b0 += NTHREADS8) {
                 const int b = b0 + tid;
                 Req r = {};
                 if (b < A.B) r = req_of(A, C, P, b);
-                const long long w = units_of(r);
-                long long inc = w;
+                const long long u = units_of(r);
+                long long inc = u;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -229,8 +239,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 if (b0) __syncthreads();
                 if (lane == 31) sm.scan[warp] = inc;
                 __syncthreads();
-                long long pre = before + inc - w, all = 0;
-#pragma unroll
+                long long pre = before + inc - u, all = 0;
+#pragma unroll 4
                 for (int i = 0; i < NW; i++) {
                     const long long x = sm.scan[i];
                     if (i < warp) pre += x;
@@ -240,10 +250,15 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 if (pass == 0) continue;
                 if (b0 == 0) {
                     if (A.B <= NTHREADS8) W = all;
-                    range();
+#pragma unroll
+                    for (int w = 0; w < 2; w++) {
+                        const Range R = range(w);
+                        if (R.lo < R.hi) at[w] = R.lo - R.kvh * W;
+                    }
                 }
-                const long long at = lo - kvh0 * W;
-                if (lo < hi && pre <= at && at < pre + w) start_b = b, start_pre = pre;
+#pragma unroll
+                for (int w = 0; w < 2; w++)
+                    if (at[w] >= 0 && pre <= at[w] && at[w] < pre + u) start_b[w] = b, start_pre[w] = pre;
             }
             if (pass == 0) W = before;
             __syncthreads();
@@ -254,44 +269,115 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile int *>(&sm.tmem);
     grid_launch_dependents();
-
-    // Takes segment k into registers; false at the end of the list, or when a wait ran out (ok).
     bool ok = true;
-    auto take = [&](int k, Seg &s, bool release_now) {
-        const int slot = k & (SEGS - 1);
-        ok = warp_wait(bar(sm.seg_full[slot]), k / SEGS & 1, dead);
-        if (!ok) return false;
-        int4 *to = reinterpret_cast<int4 *>(&s);
-        const int4 *from = reinterpret_cast<const int4 *>(sm.segs + slot);
-#pragma unroll
-        for (int i = 0; i < 4; i++) to[i] = from[i];
-        __syncwarp();
-        if (release_now && lane == 0) mbar_arrive(bar(sm.seg_empty[slot]));
-        return s.nt > 0;
-    };
-    auto drain = [&](uint64_t &barrier, bool leader) {   // the matrix instructions in flight, before tensor memory is given back
-        if (leader) mma_commit(bar(barrier));
-        const uint32_t t0 = now_ns32();
-        while (!mbar_try(bar(barrier), 0) && now_ns32() - t0 < WAIT_NS) {}
-    };
-    const int steps = (C.D + 31) / 32;                    // of 32 elements of a head
 
     if (warp >= 16) {
         regs_down<64>();   // to the softmax warps: 4 x 104 + 64 = 5 x 96
-        if (warp == W_K || warp == W_V) {
-            // Keys, or values, of each segment's tiles; with the keys, both sides' scales.
-            const bool is_v = warp == W_V;
-            const CUtensorMap *const map = is_v ? &map_v : &map_k;
-            uint64_t *const fulls = is_v ? sm.v_full : sm.k_full, *const empties = is_v ? sm.v_empty : sm.k_empty;
-            const uint32_t ring = smem_addr(is_v ? v_p : k_p), stages = is_v ? v_stages : k_stages;
-            Seg s;
+        if (warp == 16) {
+            // Front: the segments of the CTA's ranges, in order.  Each half of the warp works at one, a lane at one of 16
+            // requests at a time.
+            const int w = lane >> 4, at = lane & 15;
+            const uint32_t half_mask = 0xffffu << (lane & 16);
+            uint32_t pushed = 0;             // segments handed out
+            Req r = {};
+            long long first = 0, sum = 0;    // this lane's request's first unit, all 16's units
+            auto look = [&](int b) {         // at requests b .. b + 15: first and sum from this head's start
+                r.nt = r.mt = 0;
+                if (b + at < A.B) r = req_of(A, C, P, b + at);
+                const long long u = units_of(r);
+                sum = u;
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    const long long y = __shfl_up_sync(half_mask, sum, o, 16);
+                    if (at >= o) sum += y;
+                }
+                first = sum - u;
+                sum = __shfl_sync(half_mask, sum, 15, 16);
+            };
+            if (A.B <= SMALL_BATCH) {
+                look(0);
+                W = sum;
+            }
+            const Range R = range(w);
+            const int id = w * gridDim.x + blockIdx.x;
+            if (at == 0) P.desc[id] = make_int4(-1, 0, 0, 0);
+            __syncwarp(half_mask);
+            const bool scanned = A.B > SMALL_BATCH && R.lo < R.hi;
+            int kvh = R.kvh, b_base = scanned ? (int)start_b[w] : 0, m = 0;
+            long long pre = scanned ? start_pre[w] : 0;   // units of this head before request b_base
+            auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
+                const uint32_t slot = k & (SEGS - 1);
+                const bool free = mbar_wait(bar(sm.seg_empty[w][slot]), (k / SEGS & 1) ^ 1, dead);
+                if (free) {
+                    sm.segs[w][slot] = s;
+                    mbar_arrive(bar(sm.seg_full[w][slot]));
+                }
+                return free;
+            };
+            bool fresh = true;
+#pragma unroll 1
+            for (bool more = R.lo < R.hi; ok && more;) {
+                if (fresh) {
+                    if (A.B > SMALL_BATCH) look(b_base);
+                    m = 0;
+                    fresh = false;
+                }
+                // row tile m of each of them, as far as it lies in [lo, hi)
+                const int per = r.nt + P.overhead;
+                const long long mine = kvh * W + pre + first + (long long)m * per;
+                Seg s;
+                s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
+                s.b = b_base + at;
+                s.kvh = kvh;
+                s.m = m;
+                s.solo = 0;
+                // (the range of the row tile's last unit has its last key tile)
+                s.t0 = max((int)min(max(R.lo - mine, 0ll), (long long)per) - P.overhead, 0);
+                s.t1 = (int)min(max(R.hi - mine, 0ll), (long long)per) - P.overhead;
+                const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
+                const uint32_t mask = __ballot_sync(half_mask, any);
+                if (any) {
+                    ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
+                    if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the range of its last unit
+                        const long long last = mine + per, T = W * C.heads;
+                        P.desc[id] = make_int4(s.row0, s.kvh, s.m, s.M << Attn8Args::RANGE_BITS | ((int)((last * R.nr + T - 1) / T) - 1));
+                    }
+                }
+                ok = __all_sync(half_mask, ok);
+                pushed += __popc(mask);
+                if (__any_sync(half_mask, ++m < r.mt)) continue;
+                fresh = true;
+                pre += sum;
+                b_base += SMALL_BATCH;
+                more = kvh * W + pre < R.hi;
+                if (b_base >= A.B) {
+                    kvh++;
+                    b_base = 0;
+                    pre = 0;
+                    more = kvh * W < R.hi;
+                }
+            }
+            Seg end = {};
+            if (ok && at == 0) push(pushed, end);
+            __syncwarp();
+        } else if (warp < W_MMA) {
+            // Keys, values and scales of a range's tiles.
+            const int w = warp - W_LOAD;
+            const uint32_t k_ring = smem_addr(k_p) + w * k_stages * STAGE8, v_ring = smem_addr(v_p) + w * v_stages * STAGE8;
             const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
             const int sub = lane & (npg - 1), lane_tile = lane / npg;
             const int per = min(1 << C.block_shift, TILE), blocks = TILE / per;   // tokens per scale, scales per tile and side
-            const int blk = lane & 15, blk_tok = blk * per, blk_page = blk_tok / box;
-            Place at{0, 1};   // the first round finds every stage empty
-            uint32_t loads = 0;
-            for (int seg = 0; ok && take(seg, s, true); seg++) {
+            const int blk = lane & 15, blk_tok = blk * per, blk_page = (blk_tok / box) & (npg - 1);
+            Place ka{0, 1}, va{0, 1};   // the first round finds every stage empty
+            uint32_t k_loads = 0, v_loads = 0;
+            for (int seg = 0;; seg++) {
+                ok = warp_wait(bar(sm.seg_full[w][seg & (SEGS - 1)]), seg / SEGS & 1, dead);
+                if (!ok) break;
+                const Seg s = sm.segs[w][seg & (SEGS - 1)];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sm.seg_empty[w][seg & (SEGS - 1)]));
+                if (s.nt == 0) break;
+                const int columns = (P.rows_of(s.M, s.m) + 15) & ~15;
                 // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
                 // serves several tiles, and is issued that many tiles ahead of its use
                 const int32_t *table = C.table + (int64_t)s.b * C.max_pages;
@@ -311,78 +397,146 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     }
                     // this lane's page of tile t (lanes below npg), or -1, and its block's
                     int id = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
-                    const int of_block = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + (blk_page & (npg - 1)));
+                    const int of_block = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + blk_page);
                     if (lane >= npg) id = -1;
                     if (id == C.num_pages) {
-                        *reinterpret_cast<volatile int *>(&sm.bad[seg & 15]) = seg + 1;
+                        *reinterpret_cast<volatile int *>(&sm.bad[w][seg & 15]) = seg + 1;
                         record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
                         id = -1;
                     }
-                    const int base = s.base(t);
+                    const int base = s.base(t), y = base & (P_ - 1) & ~(box - 1), info = columns | (t == s.t0 ? INFO_FIRST : 0);
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128;
-                    const uint32_t full = bar(fulls[at.stage]);
+                    const uint32_t kf = bar(sm.k_full[w][ka.stage]), vf = bar(sm.v_full[w][va.stage]);
                     __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
-                    ok = warp_wait(bar(empties[at.stage]), at.parity, dead);
+                    ok = warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
                     if (!ok) break;
-                    if (P.withhold && !is_v && loads == 0) {   // (its waits then run out, as they are meant to)
+                    if (P.withhold && k_loads == 0) {   // (its waits then run out, as they are meant to)
                         ok = false;
                         break;
                     }
-                    loads++;
-                    if (lane == 0) mbar_expect(full, bytes);
-                    __syncwarp();
-                    if (id >= 0)
-                        tma_load_4d(ring + at.stage * STAGE8 + sub * box * 128, map, full, 0, base & (P_ - 1) & ~(box - 1), s.kvh, id);
-                    if (!is_v) {
-                        if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < s.len) {
-                            const int slot = (base + blk_tok) & (P_ - 1);
-                            const float *from = lane < 16 ? C.k_scale : C.v_scale;
-                            copy4(smem_addr(&sm.scale[at.stage][lane]),
-                                  from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + s.kvh * C.s_head);
-                        }
-                        copies_arrive(full);
+                    if (lane == 0) {
+                        sm.k_info[w][ka.stage] = info;
+                        mbar_expect(kf, bytes);
                     }
                     __syncwarp();
-                    at.advance(stages);
+                    if (id >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * 128, &map_k, kf, 0, y, s.kvh, id);
+                    if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < s.len) {
+                        const int slot = (base + blk_tok) & (P_ - 1);
+                        const float *from = lane < 16 ? C.k_scale : C.v_scale;
+                        copy4(smem_addr(&sm.scale[w][k_loads & (SCALES8 - 1)][lane]),
+                              from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + s.kvh * C.s_head);
+                    }
+                    copies_arrive(kf);
+                    __syncwarp();
+                    k_loads++;
+                    ka.advance(k_stages);
+                    ok = warp_wait(bar(sm.v_empty[w][va.stage]), va.parity, dead);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        sm.v_info[w][va.stage] = info;
+                        mbar_expect(vf, bytes);
+                    }
+                    __syncwarp();
+                    if (id >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * 128, &map_v, vf, 0, y, s.kvh, id);
+                    __syncwarp();
+                    v_loads++;
+                    va.advance(v_stages);
                 }
+                if (!ok) break;
+            }
+            if (ok) ok = warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
+            if (ok) {   // the end of the range, for the matrix warp
+                if (lane == 0) {
+                    sm.k_info[w][ka.stage] = 0;
+                    mbar_expect(bar(sm.k_full[w][ka.stage]), 0);
+                }
+                __syncwarp();
+                copies_arrive(bar(sm.k_full[w][ka.stage]));
             }
             copies_commit();
             copies_wait<0>();
             if (!ok) {   // let the copies in flight land before the CTA may end
                 const uint32_t t0 = now_ns32();
-                for (uint32_t i = loads > stages ? loads - stages : 0; i < loads; i++)
-                    while (!mbar_try(bar(fulls[i % stages]), i / stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+                for (uint32_t i = k_loads > k_stages ? k_loads - k_stages : 0; i < k_loads; i++)
+                    while (!mbar_try(bar(sm.k_full[w][i % k_stages]), i / k_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+                for (uint32_t i = v_loads > v_stages ? v_loads - v_stages : 0; i < v_loads; i++)
+                    while (!mbar_try(bar(sm.v_full[w][i % v_stages]), i / v_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
             }
-        } else if (warp == W_MMA) {
-            // Matrix instructions: each tile's scores as soon as its group has the last ones in registers, and its P V as
-            // soon as the weights are there, whichever comes first.  The whole warp runs this; one lane issues.
+        } else {
+            // Matrix instructions of both ranges: a tile's scores as soon as there is an S to put them in, its P V as soon as
+            // the weights are there.  The whole warp runs this; one lane issues.
             const bool leader = elect();
-            int sseg = 0, oseg = 0;                    // segments opened
-            int st = 0, snt = 0, srp = 0, ot = 0, ont = 0, orp = 0;   // tile, tiles and columns of a part of the current ones
-            auto open = [&](int &k, int &t, int &nt, int &rp, bool release) {
-                Seg s;
-                t = nt = 0;
-                if (!take(k++, s, release)) return;
-                nt = s.t1 - s.t0;
-                rp = (P.rows_of(s.M, s.m) + 15) & ~15;
-            };
-            open(sseg, st, snt, srp, false);
-            if (ok) open(oseg, ot, ont, orp, true);
-            Place ks{0, 0}, vs{0, 0}, qs{0, 0};
-            uint32_t gs = 0, go = 0, nf = 3, np = 0;   // groups whose turn it is; parities of each one's free S and next P
+            const int steps = (C.D + 31) / 32;         // of 32 elements of a head
+            Place ks[2] = {{0, 0}, {0, 0}}, vs[2] = {{0, 0}, {0, 0}};
+            uint32_t n_s[2] = {0, 0}, n_o[2] = {0, 0}, n_q[2] = {0, 0};   // scores and products issued, queries taken
+            uint32_t running = 3;                      // ranges that have not ended
             uint32_t polls = 0, idle_since = 0;
 #pragma unroll 1
-            while (ok && ont) {
+            while (ok && running | (n_s[0] - n_o[0]) | (n_s[1] - n_o[1])) {
                 // all that may be waited for is asked at once; every lane has to have seen it
                 uint32_t there = 0;
-                if (snt) {
-                    there = mbar_test(bar(sm.s_free[gs]), nf >> gs & 1) && mbar_test(bar(sm.k_full[ks.stage]), ks.parity) &&
-                            (st || mbar_test(bar(sm.q_full[qs.stage]), qs.parity));
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    const uint32_t free = mbar_test(bar(sm.s_free[w][n_s[w] & 1]), (n_s[w] >> 1 & 1) ^ 1),
+                                   keys = mbar_test(bar(sm.k_full[w][ks[w].stage]), ks[w].parity),
+                                   weights = mbar_test(bar(sm.p_full[w]), n_o[w] & 1),
+                                   values = mbar_test(bar(sm.v_full[w][vs[w].stage]), vs[w].parity);
+                    there |= (free & keys & (running >> w)) << w | (weights & values & (uint32_t)(n_s[w] != n_o[w])) << (2 + w);
                 }
-                there |= (uint32_t)(mbar_test(bar(sm.p_full[go]), np >> go & 1) && mbar_test(bar(sm.v_full[vs.stage]), vs.parity)) << 1;
                 there = __reduce_and_sync(0xffffffffu, there);
-                if (!there) {
-                    if (++polls & 255) continue;
+                bool any = false;
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    if (there >> (2 + w) & 1) {
+                        tc_fence_after();
+                        const int info = *reinterpret_cast<volatile int *>(&sm.v_info[w][vs[w].stage]);
+                        if (leader) {
+                            const uint32_t idesc = mma8_idesc(true, PP * (info & 0xff), true);
+                            const uint64_t vd = smem_desc(smem_addr(v_p) + (w * v_stages + vs[w].stage) * STAGE8, STAGE8),
+                                           pd = smem_desc_plain(smem_addr(p_p) + w * P_BUFFER, 128, 2048);
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                mma8_ss(tmem + 4 * S_COLS + w * O_COLS, vd + (uint64_t)(k * (4096 >> 4)), pd + (uint64_t)(k * (512 >> 4)),
+                                        idesc, !(info & INFO_FIRST) || k > 0);
+                            mma_commit(bar(sm.o_done[w]));
+                        }
+                        __syncwarp();
+                        n_o[w]++;
+                        vs[w].advance(v_stages);
+                        any = true;
+                    }
+                    if (there >> w & 1) {
+                        const int info = *reinterpret_cast<volatile int *>(&sm.k_info[w][ks[w].stage]);
+                        if (info == 0) {
+                            running &= ~(1u << w);
+                            any = true;
+                        } else if (!(info & INFO_FIRST) || warp_try(bar(sm.q_full[w]), n_q[w] & 1)) {
+                            tc_fence_after();
+                            if (leader) {
+                                const int columns = info & 0xff;
+                                const uint64_t kd = smem_desc(smem_addr(k_p) + (w * k_stages + ks[w].stage) * STAGE8, 16),
+                                               qd = smem_desc(smem_addr(q_p) + w * Q_BUFFER, 16);
+                                const uint32_t d = tmem + (2 * w + (n_s[w] & 1)) * S_COLS;
+#pragma unroll
+                                for (int part = 0; part < QP; part++) {
+                                    const uint32_t idesc = mma8_idesc(part > 0, columns, false);
+                                    for (int k = 0; k < steps; k++)
+                                        mma8_ss(d, kd + (uint64_t)(k * 2), qd + (uint64_t)(part * columns * (128 >> 4) + k * 2), idesc,
+                                                part > 0 || k > 0);
+                                }
+                                mma_commit(bar(sm.s_full[w][n_s[w] & 1]));
+                            }
+                            __syncwarp();
+                            n_q[w] += info & INFO_FIRST ? 1 : 0;
+                            n_s[w]++;
+                            ks[w].advance(k_stages);
+                            any = true;
+                        }
+                    }
+                }
+                if (any) {
+                    idle_since = 0;
+                } else if (!(++polls & 255)) {
                     const uint32_t now = now_ns32() | 1;
                     if (!idle_since) idle_since = now;
                     const bool late = *dead || now - idle_since > WAIT_NS;
@@ -390,262 +544,106 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         *dead = 1;
                         ok = false;
                     }
-                    continue;
-                }
-                idle_since = 0;
-                tc_fence_after();
-                if (there & 1) {
-                    if (leader) {
-                        const uint32_t idesc = mma8_idesc(false, QP * srp, false);
-                        const uint64_t qd = smem_desc(smem_addr(q_p) + qs.stage * q_buffer, 16),
-                                       kd = smem_desc(smem_addr(k_p) + ks.stage * STAGE8, 16);
-                        for (int k = 0; k < steps; k++)
-                            mma8_ss(tmem + gs * S_COLS, kd + (uint64_t)(k * 2), qd + (uint64_t)(k * 2), idesc, k > 0);
-                        mma_commit(bar(sm.s_full[gs]));
-                        if (st == snt - 1) mma_commit(bar(sm.q_empty[qs.stage]));
-                    }
-                    __syncwarp();
-                    nf ^= 1u << gs;
-                    gs ^= 1;
-                    ks.advance(k_stages);
-                    if (++st == snt) {
-                        qs.advance(q_bufs);
-                        open(sseg, st, snt, srp, false);
-                    }
-                }
-                if ((there & 2) && ok) {
-                    if (leader) {
-                        const uint32_t idesc = mma8_idesc(true, PP * orp, true);
-                        const uint64_t vd = smem_desc(smem_addr(v_p) + vs.stage * STAGE8, STAGE8),
-                                       pd = smem_desc_plain(smem_addr(p_p) + go * p_buffer, 128, 2048);
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            mma8_ss(tmem + 2 * S_COLS + go * O_COLS, vd + (uint64_t)(k * (4096 >> 4)), pd + (uint64_t)(k * (512 >> 4)), idesc,
-                                    ot >= 2 || k > 0);
-                        mma_commit(bar(sm.o_done[go]));
-                    }
-                    __syncwarp();
-                    np ^= 1u << go;
-                    go ^= 1;
-                    vs.advance(v_stages);
-                    if (++ot == ont) open(oseg, ot, ont, orp, true);
                 }
             }
-            if (!ok) drain(sm.drained, leader);
-            __syncwarp();
-        } else {
-            // Front: the segments of this CTA's range, in order, and their queries in parts.  A lane looks at one of 16
-            // requests at a time.
-            uint32_t pushed = 0, done = 0;   // segments handed out, and with their queries there
-            Req r = {};
-            long long first = 0, sum = 0;    // this lane's request's first unit, all 16's units
-            bool fresh = true;
-            auto look = [&](int b) {         // at requests b .. b + 15: first and sum from this head's start
-                r.nt = r.mt = 0;
-                if (lane < SMALL_BATCH && b + lane < A.B) r = req_of(A, C, P, b + lane);
-                const long long w = units_of(r);
-                sum = w;
-#pragma unroll
-                for (int o = 1; o < SMALL_BATCH; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += y;
-                }
-                first = sum - w;
-                sum = __shfl_sync(0xffffffffu, sum, SMALL_BATCH - 1);
-            };
-            if (A.B <= SMALL_BATCH) {
-                look(0);
-                W = sum;
-                range();
+            if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
+                if (leader) mma_commit(bar(sm.drained));
+                const uint32_t t0 = now_ns32();
+                while (!mbar_try(bar(sm.drained), 0) && now_ns32() - t0 < WAIT_NS) {}
             }
-            int kvh = kvh0, b_base = A.B > SMALL_BATCH && lo < hi ? (int)start_b : 0, m = 0;
-            long long pre = A.B > SMALL_BATCH && lo < hi ? start_pre : 0;   // units of this head before request b_base
-            Place at{0, 1};                  // query buffer to fill
-            if (lane == 0) P.desc[cta] = make_int4(-1, 0, 0, 0);
             __syncwarp();
-            auto push = [&](uint32_t k, const Seg &s) {   // (any subset of lanes, each its own k)
-                const uint32_t slot = k & (SEGS - 1);
-                const bool free = mbar_wait(bar(sm.seg_empty[slot]), (k / SEGS & 1) ^ 1, dead);
-                if (free) {
-                    sm.segs[slot] = s;
-                    mbar_arrive(bar(sm.seg_full[slot]));
-                }
-                return free;
-            };
+        }
+    } else {
+        regs_up<104>();
+        // Softmax and epilogue of range g: two threads per key of a tile, which have its rows by turns of 8.
+        const int g = warp >> 3, half = warp >> 2 & 1, key = (warp & 3) * 32 + lane, place = tid & 255;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
+        const uint32_t t_s = tmem + 2 * g * S_COLS + lanes, t_o = tmem + 4 * S_COLS + g * O_COLS + lanes;
+        const int block = key >> min(C.block_shift, 7);               // of this thread's key in a tile
+        char *const q_at = q_p + g * Q_BUFFER;
+        char *const p_at = p_p + g * P_BUFFER + (key >> 3) * 128 + (key & 7) * 16 + half * 8;
+        const bool speaker = (warp & 7) == 0 && lane == 0;            // arrives for the group
+        auto any_of = [&](bool x) { return barrier_any(1 + g, 256, x); };
+        const float *const q_scale = sm.q_scale[g];
+        const int *const q_place = sm.q_place[g];
+        float *const neg_m = sm.neg_m[g], *const lift = sm.lift[g];
+        uint32_t done = 0;                                            // tiles
+        Place kp{0, 0}, vp{0, 0};
 #pragma unroll 1
-            for (bool more = lo < hi, ended = false; ok;) {
-#pragma unroll 1
-                while (ok && more && pushed - done < 12) {
-                    if (fresh) {
-                        if (A.B > SMALL_BATCH) look(b_base);
-                        m = 0;
-                        fresh = false;
-                    }
-                    // row tile m of each of them, as far as it lies in [lo, hi)
-                    const int per = r.nt + P.overhead;
-                    const long long mine = kvh * W + pre + first + (long long)m * per;
-                    Seg s;
-                    s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
-                    s.b = b_base + lane;
-                    s.kvh = kvh;
-                    s.m = m;
-                    s.solo = 0;
-                    // (the CTA of the row tile's last unit has its last key tile)
-                    s.t0 = max((int)min(max(lo - mine, 0ll), (long long)per) - P.overhead, 0);
-                    s.t1 = (int)min(max(hi - mine, 0ll), (long long)per) - P.overhead;
-                    const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
-                    const uint32_t mask = __ballot_sync(0xffffffffu, any);
-                    if (any) {
-                        ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
-                        if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the CTA of its last unit
-                            const long long last = mine + per;
-                            P.desc[cta] = make_int4(s.row0, s.kvh, s.m, s.M << 8 | ((int)((last * nc + T - 1) / T) - 1));
-                        }
-                    }
-                    ok = __all_sync(0xffffffffu, ok);
-                    pushed += __popc(mask);
-                    if (__any_sync(0xffffffffu, ++m < r.mt)) continue;
-                    fresh = true;
-                    pre += sum;
-                    b_base += SMALL_BATCH;
-                    more = kvh * W + pre < hi;
-                    if (b_base >= A.B) {
-                        kvh++;
-                        b_base = 0;
-                        pre = 0;
-                        more = kvh * W < hi;
-                    }
-                }
-                if (!more && !ended && ok) {
-                    Seg s = {};
-                    if (lane == 0) ok = push(pushed, s);
-                    ok = __all_sync(0xffffffffu, ok);
-                    ended = true;
-                }
-                if (!ok || done == pushed) break;   // (nothing is left)
-                ok = warp_wait(bar(sm.q_empty[at.stage]), at.parity, dead);
-                if (!ok) break;
-                const Seg &s = sm.segs[done & (SEGS - 1)];   // (not written again before its queries are there)
-                const int row0 = P.first_row(s.M, s.m), rows = P.rows_of(s.M, s.m), rp = (rows + 15) & ~15;
-                const int lpr = C.D > 64 ? 16 : 8, rpw = 32 / lpr;   // lanes of a row, rows per warp step
-                const int ch = lane & (lpr - 1), team = lane / lpr;
+        for (int seg = 0;; seg++) {
+            ok = warp_wait(bar(sm.seg_full[g][seg & (SEGS - 1)]), seg / SEGS & 1, dead);
+            if (any_of(!ok)) break;
+            const Seg &s = sm.segs[g][seg & (SEGS - 1)];   // (its fields are read where they are needed)
+            if (s.nt == 0) break;
+            const int rows = P.rows_of(s.M, s.m), rp = (rows + 15) & ~15;
+            {   // queries in parts, swizzled as the matrix instruction reads them (no product reads the last ones any more)
+                const int lpr = C.D > 64 ? 16 : 8, rpp = 256 / lpr;   // lanes of a row, rows per pass of the group
+                const int ch = place & (lpr - 1), row0 = P.first_row(s.M, s.m);
                 const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + ch * 8;
-                char *const to = q_p + at.stage * q_buffer;
-                constexpr int U = 2;
 #pragma unroll 1
-                for (int r0 = 0; r0 < rp; r0 += U * rpw) {
-                    uint4 raw[U];
-                    int place[U];
+                for (int row = place / lpr; row < (rp + rpp - 1) / rpp * rpp; row += rpp) {   // (the whole warp)
+                    const int rr = row0 + row, tok = rr / P.G, head = rr - tok * P.G;
+                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < rows && ch * 8 < C.D) raw = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)head * C.D);
+                    float x[8], top = 0.f;
+                    unpack8<E>(raw, x);
+                    bool finite = true;
 #pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        const int row = r0 + u * rpw + team, rr = row0 + row, tok = rr / P.G, head = rr - tok * P.G;
-                        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                        place[u] = tok << 16 | head;
-                        if (row < rows && ch * 8 < C.D)
-                            raw[u] = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)head * C.D);
+                    for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[e])), finite = finite && fabsf(x[e]) < INFINITY;
+                    if (!finite) top = INFINITY;
+                    for (int o = lpr / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // the power of two s with top in (224 s, 448 s]
+                    const uint32_t b = __float_as_uint(top);
+                    const int k = (int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7);
+                    const float size = __uint_as_float((uint32_t)(min(max(k, -118), 118) + 127) << 23), inv = 1.f / size;
+                    if (row >= rp) continue;
+                    if (ch == 0) {
+                        sm.q_scale[g][row] = top < INFINITY ? size : NAN;
+                        sm.q_place[g][row] = tok << 16 | head;
                     }
 #pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        const int row = r0 + u * rpw + team;
-                        float x[8], top = 0.f;
-                        unpack8<E>(raw[u], x);
+                    for (int e = 0; e < 8; e++) x[e] *= inv;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) top = fabsf(x[e]) < INFINITY ? fmaxf(top, fabsf(x[e])) : INFINITY;
-                        // (an infinity stays: fmaxf(inf, x), and what is not finite sets it again)
+                    for (int part = 0; part < QP; part++) {
+                        uint32_t two[4];
 #pragma unroll
-                        for (int e = 0; e < 8; e++) top = fabsf(x[e]) < INFINITY ? top : INFINITY;
-                        for (int o = lpr / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        // the power of two s with top in (224 s, 448 s]
-                        const uint32_t b = __float_as_uint(top);
-                        const int k = (int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7);
-                        const float s_ = __uint_as_float((uint32_t)(min(max(k, -118), 118) + 127) << 23), inv = 1.f / s_;
-                        if (row < rp) {
-                            if (ch == 0) {
-                                sm.q_scale[at.stage][row] = top < INFINITY ? s_ : NAN;
-                                sm.q_place[at.stage][row] = place[u];
+                        for (int e = 0; e < 4; e++) {
+                            float2 y;
+                            if (part == 0) {
+                                two[e] = pack_e4m3(x[2 * e], x[2 * e + 1]);
+                                y = unpack_e4m3(two[e]);
+                            } else {
+                                two[e] = e5m2_of(half2_of(x[2 * e], x[2 * e + 1]));   // (the rest has at most 7 bits)
+                                y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two[e], __NV_E5M2)));
                             }
-#pragma unroll
-                            for (int e = 0; e < 8; e++) x[e] *= inv;
-#pragma unroll
-                            for (int part = 0; part < QP; part++) {
-                                uint32_t two[4];
-#pragma unroll
-                                for (int e = 0; e < 4; e++) {
-                                    two[e] = pack_e4m3(x[2 * e], x[2 * e + 1]);
-                                    const float2 y = unpack_e4m3(two[e]);
-                                    x[2 * e] = (x[2 * e] - y.x) * 16.f;
-                                    x[2 * e + 1] = (x[2 * e + 1] - y.y) * 16.f;
-                                }
-                                const int n = part * rp + row;
-                                *reinterpret_cast<uint2 *>(to + n * 128 + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8) =
-                                    make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
-                            }
+                            x[2 * e] -= y.x;
+                            x[2 * e + 1] -= y.y;
                         }
+                        const int n = part * rp + row;
+                        *reinterpret_cast<uint2 *>(q_at + n * 128 + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8) =
+                            make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
                     }
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sm.q_full[at.stage]));
-                done++;
-                at.advance(q_bufs);
+                if (lane == 0) mbar_arrive(bar(sm.q_full[g]));
             }
-        }
-    } else {
-        regs_up<104>();
-        // Softmax and epilogue: group g, two threads per key of a tile, which have its rows by turns of 8.
-        const int g = warp >> 3, half = warp >> 2 & 1, key = (warp & 3) * 32 + lane, place = tid & 255;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
-        const uint32_t t_s = tmem + g * S_COLS + lanes, t_o = tmem + 2 * S_COLS + lanes;
-        const int block = key >> min(C.block_shift, 7);               // of this thread's key in a tile
-        char *const p_at = p_p + g * p_buffer + (key >> 3) * 128 + (key & 7) * 16 + half * 8;
-        auto any_of = [&](bool x) { return barrier_any(1 + g, 256, x); };
-        float *const neg_m = sm.neg_m[g], *const lift = sm.lift[g];
-        uint32_t mine_done = 0, turn = 0, tiles = 0, joint = 0;   // own tiles; all tiles; barriers of both groups
-        Place qs{0, 0};
-#pragma unroll 1
-        for (int seg = 0;; seg++) {
-            ok = warp_wait(bar(sm.seg_full[seg & (SEGS - 1)]), seg / SEGS & 1, dead);
-            if (any_of(!ok)) break;
-            const Seg &s = sm.segs[seg & (SEGS - 1)];   // (its fields are read where they are needed)
-            if (s.nt == 0) break;
-            const int nt = s.t1 - s.t0, mine = (g ^ turn) & 1;        // this group's first key tile
-            const uint32_t tile0 = tiles;
-            turn += nt;
-            tiles += nt;
-            const int rows = P.rows_of(s.M, s.m), rp = (rows + 15) & ~15;
-            const float *const q_scale = sm.q_scale[qs.stage];
-            const int *const q_place = sm.q_place[qs.stage];
-            auto release = [&]() {   // the segment's and its queries' buffers
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(sm.q_empty[qs.stage]));
-                    mbar_arrive(bar(sm.seg_empty[seg & (SEGS - 1)]));
-                }
-                qs.advance(q_bufs);
-            };
-            if (mine >= nt) {   // the other group's alone
-                release();
-                continue;
-            }
-            const bool pair = nt > 1;   // both groups hold a part of every row
             float l[CHUNKS][8];
 #pragma unroll
             for (int c = 0; c < CHUNKS; c++)
 #pragma unroll
                 for (int i = 0; i < 8; i++) l[c][i] = 0.f;
-            bool any_tile = false;
-            if (place < MAX_ROWS8) neg_m[place] = UNSET8;
-            ok = warp_wait(bar(sm.q_full[qs.stage]), qs.parity, dead);   // (for the queries' scales and places)
+            if (place < MAX_ROWS8) neg_m[place] = 0.f, sm.set[g][place] = 0;
             any_of(false);
+            bool any_tile = false, pending = true;   // whether O holds something, and a row may be without a maximum
+            bool failed = false;                     // (the group's decision; `ok` is this warp's alone)
 #pragma unroll 1
-            for (int t = mine; t < nt; t += 2) {
-                const int base = s.base(s.t0 + t), j = base + key;
+            for (int t = s.t0; t < s.t1; t++) {
+                const int base = s.base(t), j = base + key;
                 const bool whole = whole_tile(P, s, base);
-                const uint32_t tile = tile0 + t, k_round = tile / k_stages, k_stage = tile - k_round * k_stages,
-                               v_round = tile / v_stages, v_stage = tile - v_round * v_stages;
                 if (!whole && !seen_by_all(P, s, j)) {   // a value that must not reach the product as it is
-                    ok = ok && mbar_wait(bar(sm.v_full[v_stage]), v_round & 1, dead);
-                    uint4 *const row = reinterpret_cast<uint4 *>(v_p + v_stage * STAGE8 + key * 128);
+                    ok = ok && mbar_wait(bar(sm.v_full[g][vp.stage]), vp.parity, dead);
+                    uint4 *const row = reinterpret_cast<uint4 *>(v_p + (g * v_stages + vp.stage) * STAGE8 + key * 128);
                     // (each half 64 of its bytes, a different bank per lane)
                     if (!seen_by_any(P, s, j)) {         // (a slot never written may hold NaN, and 0 * NaN is NaN)
 #pragma unroll
@@ -654,8 +652,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         bool took = false;
 #pragma unroll 1
                         for (int i = 4 * half; i < 4 * half + 4; i++) {
-                            uint4 w = row[i ^ (key & 7)];
-                            uint32_t *p = &w.x;
+                            uint4 v = row[i ^ (key & 7)];
+                            uint32_t *p = &v.x;
                             bool hit = false;
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
@@ -663,83 +661,71 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                                 p[e] &= ~nan;
                                 hit |= nan != 0;
                             }
-                            if (hit) row[i ^ (key & 7)] = w, took = true;
+                            if (hit) row[i ^ (key & 7)] = v, took = true;
                         }
-                        if (took) *reinterpret_cast<volatile int *>(&sm.patched[g][seg & 3]) = seg;
+                        if (took) *reinterpret_cast<volatile int *>(&sm.patched[g]) = seg;
                     }
                 }
                 __syncwarp();
-                ok = warp_wait(bar(sm.s_full[g]), mine_done & 1, dead) && ok;
-                ok = warp_wait(bar(sm.k_full[k_stage]), k_round & 1, dead) && ok;   // (complete: for the scales)
-                tc_fence_after();
-                const float ck = P.c * clean_scale(sm.scale[k_stage][block]);
-                const float lvs = lg2(clean_scale(sm.scale[k_stage][16 + block])), rvs = ex2(-lvs);
-                // the scores in powers of two, with the value's scale.  Rows lie in order of their tokens, so those that see
-                // this key are neighbours: tokens from the key's own on, up to the last whose window has it.
+                // Rows lie in order of their tokens, so those that see this key are neighbours: tokens from the key's own on,
+                // up to the last whose window has it.
                 int from = 0, to = 0x7fffffff;
                 if (!whole) {
                     const int first = j - (s.len - s.n), row0 = P.first_row(s.M, s.m);
                     from = min(max(first, 0), s.n) * P.G - row0;
                     if (P.window && j >= P.sinks) to = min(max(first + P.window, 0), s.n) * P.G - row0;
                 }
-                float u[CHUNKS][8];
-                float most = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < CHUNKS; c++) {
-                    const int r0 = 16 * c + 8 * half;
-                    if (r0 >= rows) break;
-                    uint32_t x[QP][8];
-#pragma unroll
-                    for (int part = 0; part < QP; part++) tmem_ld8(t_s + part * rp + r0, x[part]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int part = 0; part < QP; part++) after_wait<8>(x[part]);
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 qsc = *reinterpret_cast<const float4 *>(q_scale + r0 + i);
-#pragma unroll
-                        for (int h = 0; h < 4; h += 2) {
-                            auto pair_at = [&](int part) {
-                                return pair_of(__uint_as_float(x[part][i + h]), __uint_as_float(x[part][i + h + 1]));
-                            };
-                            uint64_t v = pair_at(QP - 1);
-#pragma unroll
-                            for (int part = QP - 2; part >= 0; part--) v = fma2(v, pair_of(0.0625f, 0.0625f), pair_at(part));
-                            const uint64_t f = mul2(pair_of(ck, ck), h ? pair_of(qsc.z, qsc.w) : pair_of(qsc.x, qsc.y));
-                            split(fma2(v, f, pair_of(lvs, lvs)), u[c][i + h], u[c][i + h + 1]);
-                        }
-                    }
-                    if (!whole) {   // (rows from `from` up to `to` see this key)
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            if (r0 + i < from || r0 + i >= to) u[c][i] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
-                        float d[4];
-                        split(add2(pair_of(u[c][i], u[c][i + 1]), pair_of(nm.x, nm.y)), d[0], d[1]);
-                        split(add2(pair_of(u[c][i + 2], u[c][i + 3]), pair_of(nm.z, nm.w)), d[2], d[3]);
-                        most = max3(most, max3(d[0], d[1], d[2]), d[3]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(sm.s_free[g]));
-                    mbar_arrive(bar(sm.k_empty[k_stage]));
-                }
+                const uint32_t buffer = done & 1;
+                ok = warp_wait(bar(sm.s_full[g][buffer]), done >> 1 & 1, dead) && ok;
+                ok = warp_wait(bar(sm.k_full[g][kp.stage]), kp.parity, dead) && ok;   // (complete: for the scales)
+                tc_fence_after();
+                const float *const scales = sm.scale[g][done & (SCALES8 - 1)];
+                const float ck = P.c * clean_scale(scales[block]);
+                const float lvs = lg2(clean_scale(scales[16 + block])), rvs = ex2(-lvs);
                 bool waited = !any_tile;
                 auto last_product = [&]() {   // the group's last product is through with its weights, its V tile and O
                     if (waited) return;
-                    ok = warp_wait(bar(sm.o_done[g]), (mine_done - 1) & 1, dead) && ok;
+                    ok = warp_wait(bar(sm.o_done[g]), (done - 1) & 1, dead) && ok;
                     tc_fence_after();
-                    if ((warp & 7) == 0 && lane == 0) mbar_arrive(bar(sm.v_empty[(tile - 2) % v_stages]));
+                    if (speaker) mbar_arrive(bar(sm.v_empty[g][(vp.stage ? vp.stage : v_stages) - 1]));
                     waited = true;
                 };
-                if (any_of(most > MOST8 || !ok)) {
+                // exponents of the weights: scores in powers of two, with the value's scale, from the row's maximum on.  A second
+                // time where a maximum had to be lifted.
+                float u[CHUNKS][8];
+#pragma unroll 1
+                for (int pass = 0;; pass++) {
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < CHUNKS; c++) {
+                        const int r0 = 16 * c + 8 * half;
+                        if (r0 >= rows) break;
+                        uint32_t x[8];
+                        tmem_ld8(t_s + buffer * S_COLS + r0, x);
+                        tmem_wait_ld();
+                        after_wait<8>(x);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 4) {
+                            const float4 qs = *reinterpret_cast<const float4 *>(q_scale + r0 + i), nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
+                            const uint64_t cc = pair_of(ck, ck), ll = pair_of(lvs, lvs);
+                            auto step = [&](uint32_t a, uint32_t b, float qa, float qb, float ma, float mb, float &ua, float &ub) {
+                                const uint64_t v = fma2(pair_of(__uint_as_float(a), __uint_as_float(b)), mul2(cc, pair_of(qa, qb)), ll);
+                                split(add2(v, pair_of(ma, mb)), ua, ub);
+                            };
+                            step(x[i], x[i + 1], qs.x, qs.y, nm.x, nm.y, u[c][i], u[c][i + 1]);
+                            step(x[i + 2], x[i + 3], qs.z, qs.w, nm.z, nm.w, u[c][i + 2], u[c][i + 3]);
+                        }
+                        if (!whole) {   // (rows from `from` up to `to` see this key)
+#pragma unroll
+                            for (int i = 0; i < 8; i++)
+                                if (r0 + i < from || r0 + i >= to) u[c][i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) most = max3(most, u[c][i], u[c][i + 1]);
+                    }
+                    if (pass || !any_of(pending || most > MOST8 || !ok)) break;
                     if (any_of(!ok)) {
-                        ok = false;
+                        failed = true;
                         break;
                     }
                     // lift the maxima: of the tile's keys over the warps, then of each row by a thread
@@ -753,21 +739,28 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         }
                     }
                     any_of(false);
+                    bool without = false;
                     if (place < (rows + 7) / 8 * 8) {
                         int top = sm.top[g][0][place];
 #pragma unroll
-                        for (int w = 1; w < 4; w++) top = max(top, sm.top[g][w][place]);
-                        const float m = unordered(top), was = neg_m[place];
+                        for (int q = 1; q < 4; q++) top = max(top, sm.top[g][q][place]);
+                        const float m = unordered(top), was = neg_m[place];   // (m: from the last maximum on)
+                        const bool set = sm.set[g][place];
                         float f = 1.f;
                         if (!(m <= INFINITY)) {   // a NaN that the row sees: it has no maximum any more
                             neg_m[place] = NAN;
-                        } else if (m + was > BIAS8) {
-                            neg_m[place] = BIAS8 - m;
-                            if (was != UNSET8) f = ex2((BIAS8 - was) - m);
+                            sm.set[g][place] = 1;
+                        } else if (m > (set ? BIAS8 : -INFINITY)) {
+                            const float now = was + (BIAS8 - m);
+                            if (set) f = ex2(now - was);
+                            neg_m[place] = now;
+                            sm.set[g][place] = 1;
+                        } else if (!set && place < rows) {
+                            without = true;
                         }
                         lift[place] = f;
                     }
-                    any_of(false);
+                    pending = any_of(without);
                     last_product();
 #pragma unroll
                     for (int c = 0; c < CHUNKS; c++) {
@@ -779,19 +772,26 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
 #pragma unroll
                         for (int i = 0; i < 8; i++) l[c][i] *= f[i];
                         if (!any_tile) continue;
-#pragma unroll
+#pragma unroll 1
                         for (int part = 0; part < PP; part++) {
                             uint32_t o[8];
-                            tmem_ld8(t_o + g * O_COLS + part * rp + r0, o);
+                            tmem_ld8(t_o + part * rp + r0, o);
                             tmem_wait_ld();
                             after_wait<8>(o);
 #pragma unroll
                             for (int i = 0; i < 8; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-                            tmem_st8(t_o + g * O_COLS + part * rp + r0, o);
+                            tmem_st8(t_o + part * rp + r0, o);
                         }
                     }
                     tmem_wait_st();
                 }
+                if (failed) break;
+                // (all warps are through with the waits for this tile's scores and scales: its stage may be filled again)
+                if (speaker) mbar_arrive(bar(sm.k_empty[g][kp.stage]));
+                kp.advance(k_stages);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sm.s_free[g][buffer]));
                 last_product();
                 // the weights: their sum, and their parts
 #pragma unroll
@@ -801,12 +801,9 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     uint32_t w[PP][2];
 #pragma unroll
                     for (int i = 0; i < 8; i += 4) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
                         float d[4];
-                        split(add2(pair_of(u[c][i], u[c][i + 1]), pair_of(nm.x, nm.y)), d[0], d[1]);
-                        split(add2(pair_of(u[c][i + 2], u[c][i + 3]), pair_of(nm.z, nm.w)), d[2], d[3]);
 #pragma unroll
-                        for (int e = 0; e < 4; e++) d[e] = ex2(d[e]);
+                        for (int e = 0; e < 4; e++) d[e] = ex2(u[c][i + e]);
 #pragma unroll
                         for (int e = 0; e < 4; e += 2)
                             split(fma2(pair_of(d[e], d[e + 1]), pair_of(rvs, rvs), pair_of(l[c][i + e], l[c][i + e + 1])), l[c][i + e],
@@ -824,7 +821,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sm.p_full[g]));
-                mine_done++;
+                done++;
+                vp.advance(v_stages);
                 any_tile = true;
             }
             // each row's sum over this warp's keys, while the last product runs
@@ -844,72 +842,46 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
                 if (!(lane & 3)) sm.sum[g][warp & 3][16 * c + 8 * half + (lane >> 2)] = x[0];
             }
-            if (ok) ok = warp_wait(bar(sm.o_done[g]), (mine_done - 1) & 1, dead);
-            if (ok && (warp & 7) == 0 && lane == 0)
-                mbar_arrive(bar(sm.v_empty[(tile0 + nt - 1 - ((nt - 1 - mine) & 1)) % v_stages]));
+            if (failed) ok = false;
+            if (ok) {
+                ok = warp_wait(bar(sm.o_done[g]), (done - 1) & 1, dead);
+                if (speaker) mbar_arrive(bar(sm.v_empty[g][(vp.stage ? vp.stage : v_stages) - 1]));
+            }
             if (any_of(!ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (place < rows)
-                sm.total[g][place] = sm.sum[g][0][place] + sm.sum[g][1][place] + sm.sum[g][2][place] + sm.sum[g][3][place];
-            if (pair) {   // the other group's maxima, sums and O
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sm.both[0]));
-                ok = warp_wait(bar(sm.both[0]), joint & 1, dead);
-                tc_fence_after();
-            }
-            if (any_of(!ok)) {
-                ok = false;
-                break;
-            }
             const bool direct = s.t0 == 0 && s.t1 == s.nt;
-            const int slot = 2 * cta + (s.t0 > 0 ? 0 : 1);
+            const int slot = 2 * (g * gridDim.x + blockIdx.x) + (s.t0 > 0 ? 0 : 1);
             const int64_t orow0 = (int64_t)s.row0 * P.Hq + s.kvh * P.G;
-            const bool broken = *reinterpret_cast<volatile int *>(&sm.bad[seg & 15]) == seg + 1;
-            auto patched_by = [&](int i) { return *reinterpret_cast<volatile int *>(&sm.patched[i][seg & 3]) == seg; };
-            const bool patch = patched_by(g) || (pair && patched_by(g ^ 1));
-            if (place < rows) {   // the row's maximum and sum, and the factors of the (up to) two sums O
-                const float m0 = BIAS8 - neg_m[place], m1 = pair ? BIAS8 - sm.neg_m[g ^ 1][place] : -UNSET8;
-                const float top = fmaxf(m0, m1), f0 = ex2(m0 - top), f1 = pair ? ex2(m1 - top) : 0.f;
-                float sum = sm.total[g][place] * f0 + (pair ? sm.total[g ^ 1][place] * f1 : 0.f);
+            const bool broken = *reinterpret_cast<volatile int *>(&sm.bad[g][seg & 15]) == seg + 1;
+            const bool patch = *reinterpret_cast<volatile int *>(&sm.patched[g]) == seg;
+            if (place < rows) {   // the row's sum, and what its O is multiplied by
+                float sum = sm.sum[g][0][place] + sm.sum[g][1][place] + sm.sum[g][2][place] + sm.sum[g][3][place];
                 if (broken) sum = NAN;
-                const float inv = sum == 0.f ? 0.f : rcp(sum);
-                sm.factor[g][g][place] = f0 * inv;
-                sm.factor[g][g ^ 1][place] = f1 * inv;
-                if (!pair || g == 0) {
-                    const float lse2 = sum == 0.f ? -INFINITY : top + lg2(sum) - BIAS8;
-                    const int at = q_place[place];
-                    if (!direct) P.part_lse[slot * MAX_ROWS8 + place] = lse2;
-                    else if (P.lse) P.lse[orow0 + (int64_t)(at >> 16) * P.Hq + (at & 0xffff)] = lse2 * 0.6931471805599453f;
-                }
+                sm.factor[g][place] = sum == 0.f ? 0.f : rcp(sum);
+                const float lse2 = sum == 0.f ? -INFINITY : lg2(sum) - neg_m[place];
+                const int at = q_place[place];
+                if (!direct) P.part_lse[slot * MAX_ROWS8 + place] = lse2;
+                else if (P.lse) P.lse[orow0 + (int64_t)(at >> 16) * P.Hq + (at & 0xffff)] = lse2 * 0.6931471805599453f;
             }
             any_of(false);
 #pragma unroll 1
-            for (int c = pair ? 16 * g + 8 * half : 8 * half; c < rows; c += pair ? 32 : 16) {
-                uint32_t x[PP][8], y[PP][8];
+            for (int c = 8 * half; c < rows; c += 16) {
+                uint32_t x[PP][8];
 #pragma unroll
-                for (int part = 0; part < PP; part++) {
-                    tmem_ld8(t_o + g * O_COLS + part * rp + c, x[part]);
-                    if (pair) tmem_ld8(t_o + (g ^ 1) * O_COLS + part * rp + c, y[part]);
-                }
+                for (int part = 0; part < PP; part++) tmem_ld8(t_o + part * rp + c, x[part]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int part = 0; part < PP; part++) after_wait<8>(x[part]), after_wait<8>(y[part]);
+                for (int part = 0; part < PP; part++) after_wait<8>(x[part]);
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    float a = 0.f, b = 0.f;
+                    float a = 0.f;
 #pragma unroll
                     for (int part = PP - 1; part >= 0; part--) a += __uint_as_float(x[part][i]);
-                    o[i] = a * sm.factor[g][g][c + i];
-                    if (pair) {
-#pragma unroll
-                        for (int part = PP - 1; part >= 0; part--) b += __uint_as_float(y[part][i]);
-                        o[i] = fmaf(b, sm.factor[g][g ^ 1][c + i], o[i]);
-                    }
+                    o[i] = a * sm.factor[g][c + i];
                 }
                 if (patch && key < C.D) {   // NaN elements of values that some rows do not see, for those that do
 #pragma unroll 1
@@ -946,12 +918,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 __syncwarp();
             }
             tc_fence_before();
-            if (pair) {   // neither group's next product may overwrite an O that the other still reads
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sm.both[1]));
-                ok = warp_wait(bar(sm.both[1]), joint++ & 1, dead);
-            }
-            release();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm.seg_empty[g][seg & (SEGS - 1)]));
         }
     }
     tc_fence_before();
@@ -984,9 +952,10 @@ struct Attn8Ws {
 static Attn8Ws attn8_ws(int D) {
     Attn8Ws L;
     L.desc = HEADER;
-    L.lse = L.desc + MAX_CTAS * sizeof(int4);
-    L.o = L.lse + (size_t)2 * MAX_CTAS * MAX_ROWS8 * 4;
-    L.total = L.o + (size_t)2 * MAX_CTAS * MAX_ROWS8 * (D <= 64 ? 64 : 128) * 4;
+    constexpr size_t RANGES = Attn8Args::MAX_RANGES;
+    L.lse = L.desc + RANGES * sizeof(int4);
+    L.o = L.lse + 2 * RANGES * MAX_ROWS8 * 4;
+    L.total = L.o + 2 * RANGES * MAX_ROWS8 * (D <= 64 ? 64 : 128) * 4;
     return L;
 }
 
@@ -1000,13 +969,12 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
         return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
     P.tile_rows = 16 * CHUNKS;
-    P.q_bufs = P.tile_rows <= 16 ? MAX_QBUFS8 : 2;
-    const int other = P.q_bufs * Parts<E>::Q * P.tile_rows * 128 + 2 * Parts<E>::P * P.tile_rows * 128;
-    const int stages = (SMEM_MAX8 - SMALL8 - other) / STAGE8;
+    const int other = 2 * (QP + Parts<E>::P) * P.tile_rows * 128, stages = (SMEM_MAX8 - SMALL8 - other) / (2 * STAGE8);
     P.overhead = 2;
+    // (values wait longer than keys for their use: the odd stage is theirs)
     P.k_stages = stages / 2 < MAX_STAGES8 ? stages / 2 : MAX_STAGES8;
     P.v_stages = stages - P.k_stages < MAX_STAGES8 ? stages - P.k_stages : MAX_STAGES8;
-    const int smem = SMALL8 + other + (P.k_stages + P.v_stages) * STAGE8;
+    const int smem = SMALL8 + other + 2 * (P.k_stages + P.v_stages) * STAGE8;
     // no more CTAs than the batch can have units
     const long long most = (long long)A.B * C.heads * (((long long)most_rows + P.tile_rows - 1) / P.tile_rows) *
                            ((((long long)C.max_pages << C.page_shift) + TILE - 1) / TILE + P.overhead);
@@ -1031,7 +999,7 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attention8_kernel<E, CHUNKS>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
-    cfg.gridDim = dim3(ctas, (most_rows < 8 ? most_rows : 8) + 1);
+    cfg.gridDim = dim3(2 * ctas, (most_rows < 8 ? most_rows : 8) + 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return (P.pitch == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<E, 128, Cache8, Attn8Args>, A, C, P)

@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_joined(const ArgsT &P, const CacheT &C, in
                                              float top) {
     if (sub * 4 >= C.D) return;
     const float inv = 1.f / sum;
-    const int rr = P.first_row(d.w >> 8, d.z) + rt, tok = rr / P.G;
+    const int rr = P.first_row(d.w >> ArgsT::RANGE_BITS, d.z) + rt, tok = rr / P.G;
     const int64_t orow = (int64_t)(d.x + tok) * P.Hq + d.y * P.G + rr - tok * P.G;
     *reinterpret_cast<uint2 *>(static_cast<E *>(P.out) + orow * C.D + sub * 4) =
         make_uint2(Num<E>::down(o.x * inv, o.y * inv), Num<E>::down(o.z * inv, o.w * inv));
@@ -112,16 +112,16 @@ __device__ __forceinline__ void store_joined(const ArgsT &P, const CacheT &C, in
 }
 
 // Joins the parts of the row tiles that several CTAs hold, in order of the CTAs, and sets the rows
-// that no request uses.  Blocks (c, y): rows y, y + ny, ... of the row tile that begins in CTA c; the last y
+// that no request uses.  Blocks (c, y): rows y, y + ny, ... of the row tile that begins in range c; the last y
 // has the rows that no request uses.
 // Many rows of few parts (long draft chains): a row per DP / 4 lanes.  Else a row's parts are spread over
 // the block, 16 bytes of a part per thread, and the thread groups' sums are added in shared memory: one
 // long request's parts (19 for 131 072 keys) then come in one round trip.
 template <typename E, int DP, typename CacheT, typename ArgsT>
 __global__ void __launch_bounds__(256) join_kernel(const Batch A, const CacheT C, const ArgsT P) {
-    constexpr int PART_ROWS = ArgsT::PART;
+    constexpr int PART_ROWS = ArgsT::PART, MAX_PARTS = ArgsT::MAX_RANGES, OWN = (MAX_PARTS + 255) / 256;   // parts of a thread
     constexpr int TPP = DP / 4, LANES = 256 / TPP;   // threads per part, parts at a time
-    __shared__ float weight[MAX_CTAS];
+    __shared__ float weight[MAX_PARTS];
     __shared__ float4 sums[LANES][TPP];
     __shared__ float red[2][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const CacheT C
     if ((int)blockIdx.y < ny) {
         const int4 d = P.desc[blockIdx.x];
         if (d.x < 0) return;
-        const int rows = P.rows_of(d.w >> 8, d.z), first = blockIdx.x, parts = (d.w & 255) - first + 1;
+        const int rows = P.rows_of(d.w >> ArgsT::RANGE_BITS, d.z), first = blockIdx.x,
+                  parts = (d.w & ((1 << ArgsT::RANGE_BITS) - 1)) - first + 1;
         auto slot = [&](int p) { return 2 * (first + p) + (p == 0); };
         if (parts <= TPP && rows > 2 * ny) {
             const int sub = lane % TPP;
@@ -163,7 +164,12 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const CacheT C
             }
         } else for (int rt = blockIdx.y; rt < rows; rt += ny) {
             const float *lse = P.part_lse + rt;
-            const float v = tid < parts ? lse[slot(tid) * PART_ROWS] : -INFINITY;   // (parts <= MAX_CTAS < 256)
+            float v[OWN], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < OWN; i++) {
+                v[i] = tid + 256 * i < parts ? lse[slot(tid + 256 * i) * PART_ROWS] : -INFINITY;
+                top = i ? fmaxf(top, v[i]) : v[i];
+            }
             const float *from = P.part_o + (int64_t)rt * DP + (tid % TPP) * 4;
             float4 x[4];
 #pragma unroll
@@ -172,14 +178,18 @@ __global__ void __launch_bounds__(256) join_kernel(const Batch A, const CacheT C
                 x[i] = p < parts ? *reinterpret_cast<const float4 *>(from + (int64_t)slot(p) * PART_ROWS * DP)
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            float top = v;
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (lane == 0) red[0][warp] = top;
             __syncthreads();
             top = red[0][0];
             for (int i = 1; i < 8; i++) top = fmaxf(top, red[0][i]);
-            float f = v == -INFINITY ? 0.f : ex2(v - top);   // (NaN where a part is)
-            if (tid < parts) weight[tid] = f;
+            float f = 0.f;
+#pragma unroll
+            for (int i = 0; i < OWN; i++) {
+                const float w = v[i] == -INFINITY ? 0.f : ex2(v[i] - top);   // (NaN where a part is)
+                if (tid + 256 * i < parts) weight[tid + 256 * i] = w;
+                f = i ? f + w : w;
+            }
             for (int o = 16; o; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
             if (lane == 0) red[1][warp] = f;
             __syncthreads();
