@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
     };
 
     const int warps = P.split * (AT8 / 32), w = part * (AT8 / 32) + (tid >> 5);
-    const int T = 1 << C.block_shift, block0 = pos0 >> C.block_shift;
+    const int block0 = pos0 >> C.block_shift;
     const int blocks = ((s.len - 1) >> C.block_shift) - block0 + 1, stores = 2 * Hk * blocks;
     for (int u = w; u < stores; u += warps) {
         const int side = u / blocks, block = block0 + u - side * blocks;

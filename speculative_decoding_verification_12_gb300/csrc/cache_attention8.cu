@@ -44,17 +44,16 @@ constexpr int MAX_STAGES8 = 4;           // of a ring: keys and values of each r
 constexpr int SCALES8 = 8;               // tiles whose scales are kept (more than a ring's stages and one)
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
 constexpr int READERS8 = 9;              // warps that take each segment
-constexpr int QP = 3;                    // parts of a query
 
 template <typename E>
 struct Parts;
 template <>
 struct Parts<__nv_bfloat16> {
-    static constexpr int P = 3, ROWS = 48;   // (4 + 2 P) ROWS columns of tensor memory
+    static constexpr int Q = 2, P = 3, ROWS = 48;   // (4 + 2 P) ROWS columns of tensor memory
 };
 template <>
 struct Parts<__half> {
-    static constexpr int P = 4, ROWS = 32;
+    static constexpr int Q = 3, P = 4, ROWS = 32;
 };
 
 struct Attn8Args {
@@ -134,16 +133,18 @@ __device__ __forceinline__ uint32_t e5m2_of(uint32_t half2) {
     return __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E5M2);
 }
 
-// Four fp16 weights (two pairs of rows) as P parts: part i of them in out[i].
+// Four fp16 weights (two pairs of rows) as P parts: part i of them in out[i].  `up` is 1 or 2 in each half: with
+// 3 parts the last 2 of 11 bits go, and a tie between two numbers of 9 bits goes up or down by the key's parity.
 template <int P>
-__device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t *out) {
+__device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t up, uint32_t *out) {
+    if (P == 3) a += up, b += up;
 #pragma unroll
-    for (int i = 0; i < P - 1; i++) {
+    for (int i = 0; i < P; i++) {
         out[i] = __byte_perm(a, b, 0x7531);
+        if (i == P - 1) break;
         a = sub_half2(a, a & 0xff00ff00u);
         b = sub_half2(b, b & 0xff00ff00u);
     }
-    out[P - 1] = __byte_perm(e5m2_of(a), e5m2_of(b), 0x5410);
 }
 
 // CHUNKS: of 8 rows that a softmax warp may have; a row tile has 16 CHUNKS rows at most.
@@ -151,7 +152,7 @@ template <typename E, int CHUNKS>
 __global__ void __launch_bounds__(NTHREADS8, 1)
 attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-    constexpr int PP = Parts<E>::P, ROWS = 16 * CHUNKS;
+    constexpr int QP = Parts<E>::Q, PP = Parts<E>::P, ROWS = 16 * CHUNKS;
     constexpr int S_COLS = ROWS, O_COLS = PP * ROWS;   // two S and one O of each range
     static_assert(4 * S_COLS + 2 * O_COLS <= 512, "tensor memory");
     constexpr int NW = NTHREADS8 / 32;
@@ -562,6 +563,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
         const int block = key >> min(C.block_shift, 7);               // of this thread's key in a tile
         char *const q_at = q_p + g * Q_BUFFER;
         char *const p_at = p_p + g * P_BUFFER + (key >> 3) * 128 + (key & 7) * 16 + half * 8;
+        const uint32_t tie = key & 1 ? 0x00020002u : 0x00010001u;      // see parts_of
         const bool speaker = (warp & 7) == 0 && lane == 0;            // arrives for the group
         auto any_of = [&](bool x) { return barrier_any(1 + g, 256, x); };
         const float *const q_scale = sm.q_scale[g];
@@ -576,30 +578,39 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             const Seg &s = sm.segs[g][seg & (SEGS - 1)];   // (its fields are read where they are needed)
             if (s.nt == 0) break;
             const int rows = P.rows_of(s.M, s.m), rp = (rows + 15) & ~15;
+            const int t1 = s.t1, ns = s.ns, w0 = s.w0, shared = s.len - s.n;   // (tokens that every row sees, but for the window)
             {   // queries in parts, swizzled as the matrix instruction reads them (no product reads the last ones any more)
                 const int lpr = C.D > 64 ? 16 : 8, rpp = 256 / lpr;   // lanes of a row, rows per pass of the group
                 const int ch = place & (lpr - 1), row0 = P.first_row(s.M, s.m);
                 const E *q = static_cast<const E *>(P.q) + s.row0 * P.q_stride + (int64_t)s.kvh * P.G * C.D + ch * 8;
-#pragma unroll 1
-                for (int row = place / lpr; row < (rp + rpp - 1) / rpp * rpp; row += rpp) {   // (the whole warp)
-                    const int rr = row0 + row, tok = rr / P.G, head = rr - tok * P.G;
-                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < rows && ch * 8 < C.D) raw = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)head * C.D);
+                uint4 raw[CHUNKS];
+                int at[CHUNKS];
+#pragma unroll
+                for (int i = 0; i < CHUNKS; i++) {   // (256 / 16 rows at least a pass)
+                    const int row = place / lpr + i * rpp, rr = row0 + row, tok = rr / P.G, head = rr - tok * P.G;
+                    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                    at[i] = tok << 16 | head;
+                    if (row < rows && ch * 8 < C.D) raw[i] = *reinterpret_cast<const uint4 *>(q + tok * P.q_stride + (int64_t)head * C.D);
+                }
+#pragma unroll
+                for (int i = 0; i < CHUNKS; i++) {
+                    const int row = place / lpr + i * rpp;
+                    if (i * rpp >= rp) break;   // (the whole group)
                     float x[8], top = 0.f;
-                    unpack8<E>(raw, x);
+                    unpack8<E>(raw[i], x);
                     bool finite = true;
 #pragma unroll
                     for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[e])), finite = finite && fabsf(x[e]) < INFINITY;
                     if (!finite) top = INFINITY;
                     for (int o = lpr / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the power of two s with top in (224 s, 448 s]
+                    // the power of two 2^k with top in (224, 448] 2^k
                     const uint32_t b = __float_as_uint(top);
-                    const int k = (int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7);
-                    const float size = __uint_as_float((uint32_t)(min(max(k, -118), 118) + 127) << 23), inv = 1.f / size;
+                    const int k = min(max((int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7), -118), 118);
+                    const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
                     if (row >= rp) continue;
                     if (ch == 0) {
-                        sm.q_scale[g][row] = top < INFINITY ? size : NAN;
-                        sm.q_place[g][row] = tok << 16 | head;
+                        sm.q_scale[g][row] = top < INFINITY ? __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
+                        sm.q_place[g][row] = at[i];
                     }
 #pragma unroll
                     for (int e = 0; e < 8; e++) x[e] *= inv;
@@ -628,19 +639,19 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sm.q_full[g]));
             }
-            float l[CHUNKS][8];
+            uint64_t l[CHUNKS][4];   // pairs of rows
 #pragma unroll
             for (int c = 0; c < CHUNKS; c++)
 #pragma unroll
-                for (int i = 0; i < 8; i++) l[c][i] = 0.f;
+                for (int i = 0; i < 4; i++) l[c][i] = 0;
             if (place < MAX_ROWS8) neg_m[place] = 0.f, sm.set[g][place] = 0;
             any_of(false);
             bool any_tile = false, pending = true;   // whether O holds something, and a row may be without a maximum
             bool failed = false;                     // (the group's decision; `ok` is this warp's alone)
 #pragma unroll 1
-            for (int t = s.t0; t < s.t1; t++) {
-                const int base = s.base(t), j = base + key;
-                const bool whole = whole_tile(P, s, base);
+            for (int t = s.t0; t < t1; t++) {
+                const int base = (t < ns ? t : w0 + t - ns) * TILE, j = base + key;
+                const bool whole = base + TILE - 1 <= shared && (!P.window || whole_tile(P, s, base));
                 if (!whole && !seen_by_all(P, s, j)) {   // a value that must not reach the product as it is
                     ok = ok && mbar_wait(bar(sm.v_full[g][vp.stage]), vp.parity, dead);
                     uint4 *const row = reinterpret_cast<uint4 *>(v_p + (g * v_stages + vp.stage) * STAGE8 + key * 128);
@@ -671,9 +682,10 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 // up to the last whose window has it.
                 int from = 0, to = 0x7fffffff;
                 if (!whole) {
-                    const int first = j - (s.len - s.n), row0 = P.first_row(s.M, s.m);
+                    const int first = j - shared, row0 = P.first_row(s.M, s.m);
                     from = min(max(first, 0), s.n) * P.G - row0;
-                    if (P.window && j >= P.sinks) to = min(max(first + P.window, 0), s.n) * P.G - row0;
+                    // (and never the rows that fill the tile up: a slot that was not loaded must not lift anything)
+                    to = P.window && j >= P.sinks ? min(min(max(first + P.window, 0), s.n) * P.G - row0, rows) : rows;
                 }
                 const uint32_t buffer = done & 1;
                 ok = warp_wait(bar(sm.s_full[g][buffer]), done >> 1 & 1, dead) && ok;
@@ -692,7 +704,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 };
                 // exponents of the weights: scores in powers of two, with the value's scale, from the row's maximum on.  A second
                 // time where a maximum had to be lifted.
-                float u[CHUNKS][8];
+                const uint64_t cc = pair_of(ck, ck), ll = pair_of(lvs, lvs), rr = pair_of(rvs, rvs);
+                uint64_t u[CHUNKS][4];   // pairs of rows
 #pragma unroll 1
                 for (int pass = 0;; pass++) {
                     float most = -INFINITY;
@@ -705,23 +718,31 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         tmem_wait_ld();
                         after_wait<8>(x);
 #pragma unroll
-                        for (int i = 0; i < 8; i += 4) {
-                            const float4 qs = *reinterpret_cast<const float4 *>(q_scale + r0 + i), nm = *reinterpret_cast<const float4 *>(neg_m + r0 + i);
-                            const uint64_t cc = pair_of(ck, ck), ll = pair_of(lvs, lvs);
-                            auto step = [&](uint32_t a, uint32_t b, float qa, float qb, float ma, float mb, float &ua, float &ub) {
-                                const uint64_t v = fma2(pair_of(__uint_as_float(a), __uint_as_float(b)), mul2(cc, pair_of(qa, qb)), ll);
-                                split(add2(v, pair_of(ma, mb)), ua, ub);
-                            };
-                            step(x[i], x[i + 1], qs.x, qs.y, nm.x, nm.y, u[c][i], u[c][i + 1]);
-                            step(x[i + 2], x[i + 3], qs.z, qs.w, nm.z, nm.w, u[c][i + 2], u[c][i + 3]);
+                        for (int i = 0; i < 4; i += 2) {
+                            const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(q_scale + r0 + 2 * i),
+                                             nm = *reinterpret_cast<const ulonglong2 *>(neg_m + r0 + 2 * i);
+                            auto score = [&](int k) { return pair_of(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])); };
+                            u[c][i] = add2(fma2(score(i), mul2(cc, qs.x), ll), nm.x);
+                            u[c][i + 1] = add2(fma2(score(i + 1), mul2(cc, qs.y), ll), nm.y);
                         }
-                        if (!whole) {   // (rows from `from` up to `to` see this key)
+                        if (!whole) {   // rows from `from` up to `to` see this key
+                            // (their comparisons stay in here: taken out of the loop they were a fifth of its instructions)
+                            int f = from, e = to;
+                            asm volatile("" : "+r"(f), "+r"(e));
 #pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                if (r0 + i < from || r0 + i >= to) u[c][i] = -INFINITY;
+                            for (int i = 0; i < 4; i++) {
+                                float y, z;
+                                split(u[c][i], y, z);
+                                const int r = r0 + 2 * i;
+                                u[c][i] = pair_of(r >= f && r < e ? y : -INFINITY, r + 1 >= f && r + 1 < e ? z : -INFINITY);
+                            }
                         }
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) most = max3(most, u[c][i], u[c][i + 1]);
+                        for (int i = 0; i < 4; i++) {
+                            float y, z;
+                            split(u[c][i], y, z);
+                            most = max3(most, y, z);
+                        }
                     }
                     if (pass || !any_of(pending || most > MOST8 || !ok)) break;
                     if (any_of(!ok)) {
@@ -734,7 +755,9 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         if (16 * c + 8 * half >= rows) break;
 #pragma unroll
                         for (int i = 0; i < 8; i++) {
-                            const int top = __reduce_max_sync(0xffffffffu, ordered(u[c][i]));
+                            float y, z;
+                            split(u[c][i / 2], y, z);
+                            const int top = __reduce_max_sync(0xffffffffu, ordered(i & 1 ? z : y));
                             if (lane == 0) sm.top[g][warp & 3][16 * c + 8 * half + i] = top;
                         }
                     }
@@ -770,7 +793,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
 #pragma unroll
                         for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(lift + r0 + i);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) l[c][i] *= f[i];
+                        for (int i = 0; i < 4; i++) l[c][i] = mul2(l[c][i], pair_of(f[2 * i], f[2 * i + 1]));
                         if (!any_tile) continue;
 #pragma unroll 1
                         for (int part = 0; part < PP; part++) {
@@ -802,14 +825,14 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
 #pragma unroll
                     for (int i = 0; i < 8; i += 4) {
                         float d[4];
+                        split(u[c][i / 2], d[0], d[1]);
+                        split(u[c][i / 2 + 1], d[2], d[3]);
 #pragma unroll
-                        for (int e = 0; e < 4; e++) d[e] = ex2(u[c][i + e]);
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2)
-                            split(fma2(pair_of(d[e], d[e + 1]), pair_of(rvs, rvs), pair_of(l[c][i + e], l[c][i + e + 1])), l[c][i + e],
-                                  l[c][i + e + 1]);
+                        for (int e = 0; e < 4; e++) d[e] = ex2(d[e]);
+                        l[c][i / 2] = fma2(pair_of(d[0], d[1]), rr, l[c][i / 2]);
+                        l[c][i / 2 + 1] = fma2(pair_of(d[2], d[3]), rr, l[c][i / 2 + 1]);
                         uint32_t parts[PP];
-                        parts_of<PP>(half2_of(d[0], d[1]), half2_of(d[2], d[3]), parts);
+                        parts_of<PP>(half2_of(d[0], d[1]), half2_of(d[2], d[3]), tie, parts);
 #pragma unroll
                         for (int part = 0; part < PP; part++) w[part][i / 4] = parts[part];
                     }
@@ -829,7 +852,9 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
 #pragma unroll
             for (int c = 0; c < CHUNKS; c++) {
                 if (16 * c + 8 * half >= rows) break;
-                float *x = l[c];
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; i++) split(l[c][i], x[2 * i], x[2 * i + 1]);
 #pragma unroll
                 for (int o = 16, n = 4; n; o >>= 1, n >>= 1)
 #pragma unroll
@@ -969,7 +994,7 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
         return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
     P.tile_rows = 16 * CHUNKS;
-    const int other = 2 * (QP + Parts<E>::P) * P.tile_rows * 128, stages = (SMEM_MAX8 - SMALL8 - other) / (2 * STAGE8);
+    const int other = 2 * (Parts<E>::Q + Parts<E>::P) * P.tile_rows * 128, stages = (SMEM_MAX8 - SMALL8 - other) / (2 * STAGE8);
     P.overhead = 2;
     // (values wait longer than keys for their use: the odd stage is theirs)
     P.k_stages = stages / 2 < MAX_STAGES8 ? stages / 2 : MAX_STAGES8;

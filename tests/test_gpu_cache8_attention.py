@@ -5,8 +5,8 @@ weights' rounding (at most eps / 2 of S = sum_j p_j |v_j|; 2^-9 in bf16, whose e
 is off, and by (T + 16) 2^-23 of S for exponentials and sums.  A score is off by head_dim 2^-23 sum |q k| scale as there,
 and by the parts of the queries, 2^-21 of the row's largest element times sum |k| scale.
 A weight, times its value's scale, is held relative to the row's largest such product, which the kernel keeps at 2^12 or
-more, as a sum of e5m2 numbers: whatever its size it is off by at most half of their smallest step, 2^-17, and so
-by 2^-29 of the largest.  (Beside the relative rounding above this matters only where an output's large weights
+more, as a sum of e5m2 numbers: whatever its size it is off by at most their smallest step, 2^-16, where it is cut off,
+and so by 2^-28 of the largest.  (Beside the relative rounding above this matters only where an output's large weights
 meet zeros.)
 """
 import math
@@ -107,7 +107,7 @@ def reference(s):
     k, v = plain8.held(s["kc"], s["ks"]), plain8.held(s["vc"], s["vs"])
     ref = plain.attention(s["q"], k, v, *rest)
     top = s["q"].float().abs().amax(-1, keepdim=True).expand(s["q"].shape)
-    low = 2.0 ** -29 * plain8.smallest(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], *rest)
+    low = 2.0 ** -28 * plain8.smallest(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], *rest)
     return *ref, 2.0 ** -21 * plain.attention(top, k, v, *rest)[3], low
 
 
