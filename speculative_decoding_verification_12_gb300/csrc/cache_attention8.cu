@@ -39,7 +39,7 @@ namespace svc {
 
 constexpr int STAGE8 = TILE * 128;       // bytes of a key tile: 128 bytes a key whatever head_dim
 constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then
-constexpr int W_LOAD = 17, W_MMA = 19;   // 16: front; 17, 18: loads of each range; 19: matrix instructions
+constexpr int W_MMA = 18;                // 16, 17: loads of each range; 18, 19: its matrix instructions
 constexpr int MAX_STAGES8 = 4;           // of a ring: keys and values of each range
 constexpr int SCALES8 = 8;               // tiles whose scales are kept (more than a ring's stages and one)
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
@@ -87,7 +87,7 @@ struct Attn8Args {
 // What stands in shared memory before the rings; [2]: of each range.
 struct Small8 {
     uint64_t k_full[2][MAX_STAGES8], k_empty[2][MAX_STAGES8], v_full[2][MAX_STAGES8], v_empty[2][MAX_STAGES8];
-    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_full[2], drained;
+    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_full[2], drained[2];
     uint64_t seg_full[2][SEGS], seg_empty[2][SEGS];
     int dead, tmem, patched[2], bad[2][16];
     int k_info[2][MAX_STAGES8], v_info[2][MAX_STAGES8];   // of a stage's tile, as the loading warp notes it: see INFO_*
@@ -115,6 +115,15 @@ __device__ __forceinline__ int ordered(float x) {
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// A matrix descriptor `by` bytes further on (within shared memory's 18 bits, so that nothing is carried).
+__device__ __forceinline__ uint64_t further(uint64_t desc, uint32_t by) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(desc));
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (by >> 4)), "r"(hi));
+    return d;
+}
 
 __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -176,16 +185,14 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             mbar_init(bar(sm.v_empty[w][i]), 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(bar(sm.s_full[w][i]), 1);
+            mbar_init(bar(sm.s_full[w][i]), 2);     // the products, and the matrix warp (for the scales)
             mbar_init(bar(sm.s_free[w][i]), 8);     // the group's warps
         }
         mbar_init(bar(sm.p_full[w]), 8);
         mbar_init(bar(sm.o_done[w]), 1);
         mbar_init(bar(sm.q_full[w]), 8);
-        if (w == 0) {
-            mbar_init(bar(sm.drained), 1);
-            sm.dead = 0;
-        }
+        mbar_init(bar(sm.drained[w]), 1);
+        if (w == 0) sm.dead = 0;
     } else if (tid >= 64 && tid < 64 + 4 * SEGS) {
         const int i = tid - 64, w = i / (2 * SEGS), k = i % (2 * SEGS);
         mbar_init(k < SEGS ? bar(sm.seg_full[w][k]) : bar(sm.seg_empty[w][k - SEGS]), k < SEGS ? 1 : READERS8);
@@ -273,27 +280,27 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     bool ok = true;
 
     if (warp >= 16) {
-        regs_down<64>();   // to the softmax warps: 4 x 104 + 64 = 5 x 96
-        if (warp == 16) {
-            // Front: the segments of the CTA's ranges, in order.  Each half of the warp works at one, a lane at one of 16
-            // requests at a time.
-            const int w = lane >> 4, at = lane & 15;
-            const uint32_t half_mask = 0xffffu << (lane & 16);
+        if (CHUNKS == 3) regs_down<64>();   // to the softmax warps: 4 x 104 + 64 = 5 x 96
+        const int w = warp & 1;   // the range
+        const bool leader = elect();
+        if (warp < W_MMA) {
+            // A range's segments, in order, and the keys, values and scales of their tiles.  A lane looks at one of 16
+            // requests at a time and hands out its segments; then their tiles are loaded.
             uint32_t pushed = 0;             // segments handed out
             Req r = {};
             long long first = 0, sum = 0;    // this lane's request's first unit, all 16's units
             auto look = [&](int b) {         // at requests b .. b + 15: first and sum from this head's start
                 r.nt = r.mt = 0;
-                if (b + at < A.B) r = req_of(A, C, P, b + at);
+                if (lane < SMALL_BATCH && b + lane < A.B) r = req_of(A, C, P, b + lane);
                 const long long u = units_of(r);
                 sum = u;
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    const long long y = __shfl_up_sync(half_mask, sum, o, 16);
-                    if (at >= o) sum += y;
+                for (int o = 1; o < SMALL_BATCH; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
                 }
                 first = sum - u;
-                sum = __shfl_sync(half_mask, sum, 15, 16);
+                sum = __shfl_sync(0xffffffffu, sum, SMALL_BATCH - 1);
             };
             if (A.B <= SMALL_BATCH) {
                 look(0);
@@ -301,8 +308,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             }
             const Range R = range(w);
             const int id = w * gridDim.x + blockIdx.x;
-            if (at == 0) P.desc[id] = make_int4(-1, 0, 0, 0);
-            __syncwarp(half_mask);
+            if (lane == 0) P.desc[id] = make_int4(-1, 0, 0, 0);
+            __syncwarp();
             const bool scanned = A.B > SMALL_BATCH && R.lo < R.hi;
             int kvh = R.kvh, b_base = scanned ? (int)start_b[w] : 0, m = 0;
             long long pre = scanned ? start_pre[w] : 0;   // units of this head before request b_base
@@ -315,9 +322,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 }
                 return free;
             };
-            bool fresh = true;
-#pragma unroll 1
-            for (bool more = R.lo < R.hi; ok && more;) {
+            bool fresh = true, more = R.lo < R.hi;
+            auto hand_out = [&]() {   // the next segments: one more row tile of each of the 16 requests
                 if (fresh) {
                     if (A.B > SMALL_BATCH) look(b_base);
                     m = 0;
@@ -328,7 +334,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 const long long mine = kvh * W + pre + first + (long long)m * per;
                 Seg s;
                 s.row0 = r.row0, s.n = r.n, s.len = r.len, s.M = r.M, s.lo = r.lo, s.w0 = r.w0, s.ns = r.ns, s.nt = r.nt;
-                s.b = b_base + at;
+                s.b = b_base + lane;
                 s.kvh = kvh;
                 s.m = m;
                 s.solo = 0;
@@ -336,7 +342,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 s.t0 = max((int)min(max(R.lo - mine, 0ll), (long long)per) - P.overhead, 0);
                 s.t1 = (int)min(max(R.hi - mine, 0ll), (long long)per) - P.overhead;
                 const bool any = r.nt && m < r.mt && s.t1 > s.t0;   // (else nothing, or the overhead alone)
-                const uint32_t mask = __ballot_sync(half_mask, any);
+                const uint32_t mask = __ballot_sync(0xffffffffu, any);
                 if (any) {
                     ok = push(pushed + __popc(mask & ((1u << lane) - 1)), s);
                     if (s.t0 == 0 && s.t1 < s.nt) {   // begins here and ends elsewhere: in the range of its last unit
@@ -344,9 +350,9 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         P.desc[id] = make_int4(s.row0, s.kvh, s.m, s.M << Attn8Args::RANGE_BITS | ((int)((last * R.nr + T - 1) / T) - 1));
                     }
                 }
-                ok = __all_sync(half_mask, ok);
+                ok = __all_sync(0xffffffffu, ok);
                 pushed += __popc(mask);
-                if (__any_sync(half_mask, ++m < r.mt)) continue;
+                if (__any_sync(0xffffffffu, ++m < r.mt)) return;
                 fresh = true;
                 pre += sum;
                 b_base += SMALL_BATCH;
@@ -357,13 +363,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     pre = 0;
                     more = kvh * W < R.hi;
                 }
-            }
-            Seg end = {};
-            if (ok && at == 0) push(pushed, end);
-            __syncwarp();
-        } else if (warp < W_MMA) {
-            // Keys, values and scales of a range's tiles.
-            const int w = warp - W_LOAD;
+            };
             const uint32_t k_ring = smem_addr(k_p) + w * k_stages * STAGE8, v_ring = smem_addr(v_p) + w * v_stages * STAGE8;
             const int P_ = 1 << C.page_shift, box = min(P_, TILE), npg = TILE / box, tpl = 32 / npg;
             const int sub = lane & (npg - 1), lane_tile = lane / npg;
@@ -371,42 +371,45 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             const int blk = lane & 15, blk_tok = blk * per, blk_page = (blk_tok / box) & (npg - 1);
             Place ka{0, 1}, va{0, 1};   // the first round finds every stage empty
             uint32_t k_loads = 0, v_loads = 0;
-            for (int seg = 0;; seg++) {
-                ok = warp_wait(bar(sm.seg_full[w][seg & (SEGS - 1)]), seg / SEGS & 1, dead);
-                if (!ok) break;
-                const Seg s = sm.segs[w][seg & (SEGS - 1)];
+            for (uint32_t seg = 0; ok; seg++) {
+                while (ok && more && pushed == seg) hand_out();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sm.seg_empty[w][seg & (SEGS - 1)]));
-                if (s.nt == 0) break;
+                if (!ok || pushed == seg) break;
+                const Seg &s = sm.segs[w][seg & (SEGS - 1)];   // (as this warp wrote it; released below)
+                const int t1 = s.t1, ns = s.ns, w0 = s.w0, len = s.len, kv = s.kvh, s_lo = s.lo;
                 const int columns = (P.rows_of(s.M, s.m) + 15) & ~15;
                 // a lane's page of `tpl` tiles from t on (npg lanes a tile), or -1: one load of the table
                 // serves several tiles, and is issued that many tiles ahead of its use
                 const int32_t *table = C.table + (int64_t)s.b * C.max_pages;
+                auto base_of = [&](int t) { return (t < ns ? t : w0 + t - ns) * TILE; };
                 auto fetch = [&](int t) {
                     t += lane_tile;
-                    const int j = s.base(t) + sub * box;
-                    if (t >= s.t1 || j >= s.len || !(j + box > s.lo || j < P.sinks)) return -1;
+                    const int j = base_of(t) + sub * box;
+                    if (t >= t1 || j >= len || !(j + box > s_lo || j < P.sinks)) return -1;
                     return (int)min((uint32_t)table[j >> C.page_shift], (uint32_t)C.num_pages);   // (num_pages: not a page)
                 };
-                int ids = -1, ahead = fetch(s.t0), t_ids = s.t0 - tpl;
+                const int t0 = s.t0, b = s.b;
+                int ids = -1, ahead = fetch(t0), t_ids = t0 - tpl;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sm.seg_empty[w][seg & (SEGS - 1)]));
 #pragma unroll 1
-                for (int t = s.t0; t < s.t1; t++) {
+                for (int t = t0; t < t1; t++) {
                     if (t == t_ids + tpl) {
                         ids = ahead;
                         t_ids = t;
                         ahead = fetch(t + tpl);
                     }
                     // this lane's page of tile t (lanes below npg), or -1, and its block's
-                    int id = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
+                    int page = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + sub);
                     const int of_block = __shfl_sync(0xffffffffu, ids, (t - t_ids) * npg + blk_page);
-                    if (lane >= npg) id = -1;
-                    if (id == C.num_pages) {
+                    if (lane >= npg) page = -1;
+                    if (page == C.num_pages) {
                         *reinterpret_cast<volatile int *>(&sm.bad[w][seg & 15]) = seg + 1;
-                        record_error(P.hdr, SV_DEV_BAD_PAGE, s.b);
-                        id = -1;
+                        record_error(P.hdr, SV_DEV_BAD_PAGE, b);
+                        page = -1;
                     }
-                    const int base = s.base(t), y = base & (P_ - 1) & ~(box - 1), info = columns | (t == s.t0 ? INFO_FIRST : 0);
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * box * 128;
+                    const int base = base_of(t), y = base & (P_ - 1) & ~(box - 1), info = columns | (t == t0 ? INFO_FIRST : 0);
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
                     const uint32_t kf = bar(sm.k_full[w][ka.stage]), vf = bar(sm.v_full[w][va.stage]);
                     __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
                     ok = warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
@@ -420,12 +423,12 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         mbar_expect(kf, bytes);
                     }
                     __syncwarp();
-                    if (id >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * 128, &map_k, kf, 0, y, s.kvh, id);
-                    if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < s.len) {
+                    if (page >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * 128, &map_k, kf, 0, y, kv, page);
+                    if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < len) {
                         const int slot = (base + blk_tok) & (P_ - 1);
                         const float *from = lane < 16 ? C.k_scale : C.v_scale;
                         copy4(smem_addr(&sm.scale[w][k_loads & (SCALES8 - 1)][lane]),
-                              from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + s.kvh * C.s_head);
+                              from + of_block * C.s_page + (slot >> C.block_shift) * C.s_block + kv * C.s_head);
                     }
                     copies_arrive(kf);
                     __syncwarp();
@@ -438,15 +441,18 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         mbar_expect(vf, bytes);
                     }
                     __syncwarp();
-                    if (id >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * 128, &map_v, vf, 0, y, s.kvh, id);
+                    if (page >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * 128, &map_v, vf, 0, y, kv, page);
                     __syncwarp();
                     v_loads++;
                     va.advance(v_stages);
                 }
-                if (!ok) break;
             }
-            if (ok) ok = warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
-            if (ok) {   // the end of the range, for the matrix warp
+            if (ok) {   // the end of the range, for the softmax and the matrix warps
+                const Seg end = {};
+                if (lane == 0) ok = push(pushed, end);
+                ok = __all_sync(0xffffffffu, ok) && warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
+            }
+            if (ok) {
                 if (lane == 0) {
                     sm.k_info[w][ka.stage] = 0;
                     mbar_expect(bar(sm.k_full[w][ka.stage]), 0);
@@ -457,105 +463,103 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             copies_commit();
             copies_wait<0>();
             if (!ok) {   // let the copies in flight land before the CTA may end
-                const uint32_t t0 = now_ns32();
+                const uint32_t since = now_ns32();
                 for (uint32_t i = k_loads > k_stages ? k_loads - k_stages : 0; i < k_loads; i++)
-                    while (!mbar_try(bar(sm.k_full[w][i % k_stages]), i / k_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+                    while (!mbar_try(bar(sm.k_full[w][i % k_stages]), i / k_stages & 1) && now_ns32() - since < WAIT_NS) {}
                 for (uint32_t i = v_loads > v_stages ? v_loads - v_stages : 0; i < v_loads; i++)
-                    while (!mbar_try(bar(sm.v_full[w][i % v_stages]), i / v_stages & 1) && now_ns32() - t0 < WAIT_NS) {}
+                    while (!mbar_try(bar(sm.v_full[w][i % v_stages]), i / v_stages & 1) && now_ns32() - since < WAIT_NS) {}
             }
         } else {
-            // Matrix instructions of both ranges: a tile's scores as soon as there is an S to put them in, its P V as soon as
-            // the weights are there.  The whole warp runs this; one lane issues.
-            const bool leader = elect();
+            // A range's matrix instructions: a tile's scores as soon as there is an S to put them in, its P V as soon as the
+            // weights are there.
+            // The whole warp runs this; one lane issues.
             const int steps = (C.D + 31) / 32;         // of 32 elements of a head
-            Place ks[2] = {{0, 0}, {0, 0}}, vs[2] = {{0, 0}, {0, 0}};
-            uint32_t n_s[2] = {0, 0}, n_o[2] = {0, 0}, n_q[2] = {0, 0};   // scores and products issued, queries taken
-            uint32_t running = 3;                      // ranges that have not ended
-            uint32_t polls = 0, idle_since = 0;
+            Place ks{0, 0}, vs{0, 0};
+            uint32_t n_s = 0, n_o = 0, n_q = 0;        // scores and products issued, queries taken
+            bool more = true;                          // the range has not ended
+            const uint64_t qd = smem_desc(smem_addr(q_p) + w * Q_BUFFER, 16),
+                           pd = smem_desc_plain(smem_addr(p_p) + w * P_BUFFER, 128, 2048);
+            auto scores = [&]() {
+                const int info = *reinterpret_cast<volatile int *>(&sm.k_info[w][ks.stage]);
+                if (info == 0) {
+                    more = false;
+                    return;
+                }
+                if (info & INFO_FIRST) {
+                    // (the queries come when the segment before is done, so no product is waited for meanwhile)
+                    ok = warp_wait(bar(sm.q_full[w]), n_q++ & 1, dead);
+                    if (!ok) return;
+                }
+                tc_fence_after();
+                if (leader) {
+                    const int columns = info & 0xff;
+                    const uint64_t kd = smem_desc(smem_addr(k_p) + (w * k_stages + ks.stage) * STAGE8, 16);
+                    const uint32_t d = tmem + (2 * w + (n_s & 1)) * S_COLS;
+#pragma unroll
+                    for (int part = 0; part < QP; part++) {
+                        const uint32_t idesc = mma8_idesc(part > 0, columns, false);
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (k < steps)
+                                mma8_ss(d, further(kd, k * 32), further(qd, part * columns * 128 + k * 32), idesc, part > 0 || k > 0);
+                    }
+                    mbar_arrive(bar(sm.s_full[w][n_s & 1]));   // (it has waited for the keys, and so for the scales)
+                    mma_commit(bar(sm.s_full[w][n_s & 1]));
+                    mma_commit(bar(sm.k_empty[w][ks.stage]));
+                }
+                __syncwarp();
+                n_s++;
+                ks.advance(k_stages);
+            };
+            auto product = [&]() {
+                tc_fence_after();
+                const int info = *reinterpret_cast<volatile int *>(&sm.v_info[w][vs.stage]);
+                if (leader) {
+                    const uint32_t idesc = mma8_idesc(true, PP * (info & 0xff), true);
+                    const uint64_t vd = smem_desc(smem_addr(v_p) + (w * v_stages + vs.stage) * STAGE8, STAGE8);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma8_ss(tmem + 4 * S_COLS + w * O_COLS, further(vd, k * 4096), further(pd, k * 512), idesc,
+                                !(info & INFO_FIRST) || k > 0);
+                    mma_commit(bar(sm.o_done[w]));
+                    mma_commit(bar(sm.v_empty[w][vs.stage]));
+                }
+                __syncwarp();
+                n_o++;
+                vs.advance(v_stages);
+            };
+            uint32_t idle_since = 0, polls = 0;
 #pragma unroll 1
-            while (ok && running | (n_s[0] - n_o[0]) | (n_s[1] - n_o[1])) {
-                // all that may be waited for is asked at once; every lane has to have seen it
+            while (ok && (more || n_o < n_s)) {
+                // both are asked at once; every lane has to have seen it.  A segment's first S waits until the products of the
+                // one before are issued, since its queries come after them.
                 uint32_t there = 0;
-#pragma unroll
-                for (int w = 0; w < 2; w++) {
-                    const uint32_t free = mbar_test(bar(sm.s_free[w][n_s[w] & 1]), (n_s[w] >> 1 & 1) ^ 1),
-                                   keys = mbar_test(bar(sm.k_full[w][ks[w].stage]), ks[w].parity),
-                                   weights = mbar_test(bar(sm.p_full[w]), n_o[w] & 1),
-                                   values = mbar_test(bar(sm.v_full[w][vs[w].stage]), vs[w].parity);
-                    there |= (free & keys & (running >> w)) << w | (weights & values & (uint32_t)(n_s[w] != n_o[w])) << (2 + w);
-                }
+                if (more && mbar_test(bar(sm.k_full[w][ks.stage]), ks.parity) && mbar_test(bar(sm.s_free[w][n_s & 1]), (n_s >> 1 & 1) ^ 1)) there = 1;
+                if (n_o < n_s && mbar_test(bar(sm.p_full[w]), n_o & 1) && mbar_test(bar(sm.v_full[w][vs.stage]), vs.parity)) there |= 2;
                 there = __reduce_and_sync(0xffffffffu, there);
-                bool any = false;
-#pragma unroll
-                for (int w = 0; w < 2; w++) {
-                    if (there >> (2 + w) & 1) {
-                        tc_fence_after();
-                        const int info = *reinterpret_cast<volatile int *>(&sm.v_info[w][vs[w].stage]);
-                        if (leader) {
-                            const uint32_t idesc = mma8_idesc(true, PP * (info & 0xff), true);
-                            const uint64_t vd = smem_desc(smem_addr(v_p) + (w * v_stages + vs[w].stage) * STAGE8, STAGE8),
-                                           pd = smem_desc_plain(smem_addr(p_p) + w * P_BUFFER, 128, 2048);
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                mma8_ss(tmem + 4 * S_COLS + w * O_COLS, vd + (uint64_t)(k * (4096 >> 4)), pd + (uint64_t)(k * (512 >> 4)),
-                                        idesc, !(info & INFO_FIRST) || k > 0);
-                            mma_commit(bar(sm.o_done[w]));
-                        }
-                        __syncwarp();
-                        n_o[w]++;
-                        vs[w].advance(v_stages);
-                        any = true;
-                    }
-                    if (there >> w & 1) {
-                        const int info = *reinterpret_cast<volatile int *>(&sm.k_info[w][ks[w].stage]);
-                        if (info == 0) {
-                            running &= ~(1u << w);
-                            any = true;
-                        } else if (!(info & INFO_FIRST) || warp_try(bar(sm.q_full[w]), n_q[w] & 1)) {
-                            tc_fence_after();
-                            if (leader) {
-                                const int columns = info & 0xff;
-                                const uint64_t kd = smem_desc(smem_addr(k_p) + (w * k_stages + ks[w].stage) * STAGE8, 16),
-                                               qd = smem_desc(smem_addr(q_p) + w * Q_BUFFER, 16);
-                                const uint32_t d = tmem + (2 * w + (n_s[w] & 1)) * S_COLS;
-#pragma unroll
-                                for (int part = 0; part < QP; part++) {
-                                    const uint32_t idesc = mma8_idesc(part > 0, columns, false);
-                                    for (int k = 0; k < steps; k++)
-                                        mma8_ss(d, kd + (uint64_t)(k * 2), qd + (uint64_t)(part * columns * (128 >> 4) + k * 2), idesc,
-                                                part > 0 || k > 0);
-                                }
-                                mma_commit(bar(sm.s_full[w][n_s[w] & 1]));
-                            }
-                            __syncwarp();
-                            n_q[w] += info & INFO_FIRST ? 1 : 0;
-                            n_s[w]++;
-                            ks[w].advance(k_stages);
-                            any = true;
-                        }
-                    }
-                }
-                if (any) {
+                if (there & 2) product();
+                const bool next = (there & 1) && (n_s == n_o || !(*reinterpret_cast<volatile int *>(&sm.k_info[w][ks.stage]) & INFO_FIRST));
+                if (next) scores();
+                if (next || there & 2) {
                     idle_since = 0;
                 } else if (!(++polls & 255)) {
                     const uint32_t now = now_ns32() | 1;
                     if (!idle_since) idle_since = now;
-                    const bool late = *dead || now - idle_since > WAIT_NS;
-                    if (__any_sync(0xffffffffu, late)) {
+                    if (__any_sync(0xffffffffu, *dead || now - idle_since > WAIT_NS)) {
                         *dead = 1;
                         ok = false;
                     }
                 }
             }
             if (!ok) {   // wait for the matrix instructions in flight before tensor memory is given back
-                if (leader) mma_commit(bar(sm.drained));
-                const uint32_t t0 = now_ns32();
-                while (!mbar_try(bar(sm.drained), 0) && now_ns32() - t0 < WAIT_NS) {}
+                if (leader) mma_commit(bar(sm.drained[w]));
+                const uint32_t since = now_ns32();
+                while (!mbar_try(bar(sm.drained[w]), 0) && now_ns32() - since < WAIT_NS) {}
             }
             __syncwarp();
         }
     } else {
-        regs_up<104>();
+        if (CHUNKS == 3) regs_up<104>();
         // Softmax and epilogue of range g: two threads per key of a tile, which have its rows by turns of 8.
         const int g = warp >> 3, half = warp >> 2 & 1, key = (warp & 3) * 32 + lane, place = tid & 255;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // this warp's 32 lanes of tensor memory
@@ -564,13 +568,12 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
         char *const q_at = q_p + g * Q_BUFFER;
         char *const p_at = p_p + g * P_BUFFER + (key >> 3) * 128 + (key & 7) * 16 + half * 8;
         const uint32_t tie = key & 1 ? 0x00020002u : 0x00010001u;      // see parts_of
-        const bool speaker = (warp & 7) == 0 && lane == 0;            // arrives for the group
         auto any_of = [&](bool x) { return barrier_any(1 + g, 256, x); };
         const float *const q_scale = sm.q_scale[g];
         const int *const q_place = sm.q_place[g];
         float *const neg_m = sm.neg_m[g], *const lift = sm.lift[g];
         uint32_t done = 0;                                            // tiles
-        Place kp{0, 0}, vp{0, 0};
+        Place vp{0, 0};
 #pragma unroll 1
         for (int seg = 0;; seg++) {
             ok = warp_wait(bar(sm.seg_full[g][seg & (SEGS - 1)]), seg / SEGS & 1, dead);
@@ -677,7 +680,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         if (took) *reinterpret_cast<volatile int *>(&sm.patched[g]) = seg;
                     }
                 }
-                __syncwarp();
+                if (!whole) __syncwarp();
                 // Rows lie in order of their tokens, so those that see this key are neighbours: tokens from the key's own on,
                 // up to the last whose window has it.
                 int from = 0, to = 0x7fffffff;
@@ -687,9 +690,13 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     // (and never the rows that fill the tile up: a slot that was not loaded must not lift anything)
                     to = P.window && j >= P.sinks ? min(min(max(first + P.window, 0), s.n) * P.G - row0, rows) : rows;
                 }
+                // the scores (and the scales that came with the keys) and the last product: asked at once, and waited for where they
+                // are not there yet
                 const uint32_t buffer = done & 1;
-                ok = warp_wait(bar(sm.s_full[g][buffer]), done >> 1 & 1, dead) && ok;
-                ok = warp_wait(bar(sm.k_full[g][kp.stage]), kp.parity, dead) && ok;   // (complete: for the scales)
+                uint32_t there = mbar_test(bar(sm.s_full[g][buffer]), done >> 1 & 1) |
+                                 (uint32_t)mbar_test(bar(sm.o_done[g]), (done - 1) & 1) << 2;
+                there = __reduce_and_sync(0xffffffffu, there);
+                if (!(there & 1)) ok = warp_wait(bar(sm.s_full[g][buffer]), done >> 1 & 1, dead) && ok;
                 tc_fence_after();
                 const float *const scales = sm.scale[g][done & (SCALES8 - 1)];
                 const float ck = P.c * clean_scale(scales[block]);
@@ -697,9 +704,10 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 bool waited = !any_tile;
                 auto last_product = [&]() {   // the group's last product is through with its weights, its V tile and O
                     if (waited) return;
-                    ok = warp_wait(bar(sm.o_done[g]), (done - 1) & 1, dead) && ok;
-                    tc_fence_after();
-                    if (speaker) mbar_arrive(bar(sm.v_empty[g][(vp.stage ? vp.stage : v_stages) - 1]));
+                    if (!(there & 4)) {
+                        ok = warp_wait(bar(sm.o_done[g]), (done - 1) & 1, dead) && ok;
+                        tc_fence_after();
+                    }
                     waited = true;
                 };
                 // exponents of the weights: scores in powers of two, with the value's scale, from the row's maximum on.  A second
@@ -809,9 +817,6 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     tmem_wait_st();
                 }
                 if (failed) break;
-                // (all warps are through with the waits for this tile's scores and scales: its stage may be filled again)
-                if (speaker) mbar_arrive(bar(sm.k_empty[g][kp.stage]));
-                kp.advance(k_stages);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sm.s_free[g][buffer]));
@@ -870,7 +875,6 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
             if (failed) ok = false;
             if (ok) {
                 ok = warp_wait(bar(sm.o_done[g]), (done - 1) & 1, dead);
-                if (speaker) mbar_arrive(bar(sm.v_empty[g][(vp.stage ? vp.stage : v_stages) - 1]));
             }
             if (any_of(!ok)) {
                 ok = false;

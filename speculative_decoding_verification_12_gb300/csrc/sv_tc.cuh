@@ -71,37 +71,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
-// The same with few instructions a poll, for a CTA of many warps whose issue slots the polls would take: 64 of them
-// between two looks at the timer.
-__device__ __forceinline__ bool mbar_wait_tight(uint32_t bar, uint32_t parity, volatile int *dead) {
-    uint32_t t0 = 0;
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, 64;\n\t"
-            "again:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra done;\n\t"
-            "sub.u32 n, n, 1;\n\t"
-            "setp.ne.u32 q, n, 0;\n\t"
-            "@q bra again;\n\t"
-            "done:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (ok) return true;
-        const uint32_t now = now_ns32() | 1;
-        if (!t0) t0 = now;
-        if (*dead || now - t0 > WAIT_NS) {
-            *dead = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool warp_wait_tight(uint32_t bar, uint32_t parity, volatile int *dead) {
-    return __all_sync(0xffffffffu, mbar_wait_tight(bar, parity, dead));
-}
-
 // The same for a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead));
