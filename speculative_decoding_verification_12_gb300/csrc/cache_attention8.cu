@@ -37,10 +37,9 @@
 
 namespace svc {
 
-constexpr int STAGE8 = TILE * 128;       // bytes of a key tile: 128 bytes a key whatever head_dim
 constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then
 constexpr int W_MMA = 18;                // 16, 17: loads of each range; 18, 19: its matrix instructions
-constexpr int MAX_STAGES8 = 4;           // of a ring: keys and values of each range
+constexpr int MAX_STAGES8 = 7;           // of a ring: keys and values of each range
 constexpr int SCALES8 = 8;               // tiles whose scales are kept (more than a ring's stages and one)
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
 constexpr int READERS8 = 9;              // warps that take each segment
@@ -116,6 +115,15 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
+// Descriptor of a tile of WIDTH-byte rows, swizzled over as many bytes, for a product with the rows (K q^T) or the
+// columns (V^T P^T) as M.  With 64 columns the upper half of the second's M is no columns: it reads the 8 rows after, and
+// reaches only lanes of the output that nothing uses.
+template <int WIDTH>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+    if (WIDTH == 128) return smem_desc(addr, 16);
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(512 >> 4) << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)4 << 61;
+}
 // A matrix descriptor `by` bytes further on (within shared memory's 18 bits, so that nothing is carried).
 __device__ __forceinline__ uint64_t further(uint64_t desc, uint32_t by) {
     uint32_t lo, hi;
@@ -156,8 +164,10 @@ __device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t up, ui
     }
 }
 
-// CHUNKS: of 8 rows that a softmax warp may have; a row tile has 16 CHUNKS rows at most.
-template <typename E, int CHUNKS>
+// CHUNKS: of 8 rows that a softmax warp may have; a row tile has 16 CHUNKS rows at most.  WIDTH: bytes of a key in a
+// stage, 64 where head_dim allows: half the bytes leave room for twice the stages, and the memory's latency needs them
+// (256 x 5 rows of 64-wide heads over 4096 keys: 341 us with 128).
+template <typename E, int CHUNKS, int WIDTH>
 __global__ void __launch_bounds__(NTHREADS8, 1)
 attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
@@ -165,7 +175,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     constexpr int S_COLS = ROWS, O_COLS = PP * ROWS;   // two S and one O of each range
     static_assert(4 * S_COLS + 2 * O_COLS <= 512, "tensor memory");
     constexpr int NW = NTHREADS8 / 32;
-    constexpr int Q_BUFFER = QP * ROWS * 128, P_BUFFER = PP * ROWS * 128;
+    constexpr int STAGE8 = TILE * WIDTH, Q_BUFFER = QP * ROWS * 128, P_BUFFER = PP * ROWS * 128;
     extern __shared__ __align__(1024) char smem[];
     Small8 &sm = *reinterpret_cast<Small8 *>(smem);
     // [barriers and small state][rings of K tiles][rings of V tiles][queries of each range][weights of each range]
@@ -409,7 +419,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         page = -1;
                     }
                     const int base = base_of(t), y = base & (P_ - 1) & ~(box - 1), info = columns | (t == t0 ? INFO_FIRST : 0);
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * WIDTH;
                     const uint32_t kf = bar(sm.k_full[w][ka.stage]), vf = bar(sm.v_full[w][va.stage]);
                     __syncwarp();   // (a bad page noted by any lane, before the arrival that publishes it)
                     ok = warp_wait(bar(sm.k_empty[w][ka.stage]), ka.parity, dead);
@@ -423,7 +433,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         mbar_expect(kf, bytes);
                     }
                     __syncwarp();
-                    if (page >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * 128, &map_k, kf, 0, y, kv, page);
+                    if (page >= 0) tma_load_4d(k_ring + ka.stage * STAGE8 + sub * box * WIDTH, &map_k, kf, 0, y, kv, page);
                     if (blk < blocks && of_block >= 0 && of_block < C.num_pages && base + blk_tok < len) {
                         const int slot = (base + blk_tok) & (P_ - 1);
                         const float *from = lane < 16 ? C.k_scale : C.v_scale;
@@ -441,7 +451,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                         mbar_expect(vf, bytes);
                     }
                     __syncwarp();
-                    if (page >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * 128, &map_v, vf, 0, y, kv, page);
+                    if (page >= 0) tma_load_4d(v_ring + va.stage * STAGE8 + sub * box * WIDTH, &map_v, vf, 0, y, kv, page);
                     __syncwarp();
                     v_loads++;
                     va.advance(v_stages);
@@ -493,14 +503,14 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 tc_fence_after();
                 if (leader) {
                     const int columns = info & 0xff;
-                    const uint64_t kd = smem_desc(smem_addr(k_p) + (w * k_stages + ks.stage) * STAGE8, 16);
+                    const uint64_t kd = tile_desc<WIDTH>(smem_addr(k_p) + (w * k_stages + ks.stage) * STAGE8);
                     const uint32_t d = tmem + (2 * w + (n_s & 1)) * S_COLS;
 #pragma unroll
                     for (int part = 0; part < QP; part++) {
                         const uint32_t idesc = mma8_idesc(part > 0, columns, false);
 #pragma unroll
                         for (int k = 0; k < 4; k++)
-                            if (k < steps)
+                            if (k < WIDTH / 32 && k < steps)
                                 mma8_ss(d, further(kd, k * 32), further(qd, part * columns * 128 + k * 32), idesc, part > 0 || k > 0);
                     }
                     mbar_arrive(bar(sm.s_full[w][n_s & 1]));   // (it has waited for the keys, and so for the scales)
@@ -516,10 +526,10 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 const int info = *reinterpret_cast<volatile int *>(&sm.v_info[w][vs.stage]);
                 if (leader) {
                     const uint32_t idesc = mma8_idesc(true, PP * (info & 0xff), true);
-                    const uint64_t vd = smem_desc(smem_addr(v_p) + (w * v_stages + vs.stage) * STAGE8, STAGE8);
+                    const uint64_t vd = tile_desc<WIDTH>(smem_addr(v_p) + (w * v_stages + vs.stage) * STAGE8);
 #pragma unroll
                     for (int k = 0; k < 4; k++)
-                        mma8_ss(tmem + 4 * S_COLS + w * O_COLS, further(vd, k * 4096), further(pd, k * 512), idesc,
+                        mma8_ss(tmem + 4 * S_COLS + w * O_COLS, further(vd, k * 32 * WIDTH), further(pd, k * 512), idesc,
                                 !(info & INFO_FIRST) || k > 0);
                     mma_commit(bar(sm.o_done[w]));
                     mma_commit(bar(sm.v_empty[w][vs.stage]));
@@ -657,16 +667,17 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 const bool whole = base + TILE - 1 <= shared && (!P.window || whole_tile(P, s, base));
                 if (!whole && !seen_by_all(P, s, j)) {   // a value that must not reach the product as it is
                     ok = ok && mbar_wait(bar(sm.v_full[g][vp.stage]), vp.parity, dead);
-                    uint4 *const row = reinterpret_cast<uint4 *>(v_p + (g * v_stages + vp.stage) * STAGE8 + key * 128);
-                    // (each half 64 of its bytes, a different bank per lane)
+                    uint4 *const row = reinterpret_cast<uint4 *>(v_p + (g * v_stages + vp.stage) * STAGE8 + key * WIDTH);
+                    constexpr int HALF = WIDTH / 32;     // 16-byte pieces of a half of it
+                    // (each half of the threads has half of its bytes, a different bank per lane)
                     if (!seen_by_any(P, s, j)) {         // (a slot never written may hold NaN, and 0 * NaN is NaN)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) row[(4 * half + i) ^ (key & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int i = 0; i < HALF; i++) row[(HALF * half + i) ^ (key & (2 * HALF - 1))] = make_uint4(0u, 0u, 0u, 0u);
                     } else {                             // (the epilogue gives its NaN to the rows that see it)
                         bool took = false;
 #pragma unroll 1
-                        for (int i = 4 * half; i < 4 * half + 4; i++) {
-                            uint4 v = row[i ^ (key & 7)];
+                        for (int i = HALF * half; i < HALF * half + HALF; i++) {
+                            uint4 v = row[i ^ (key & (2 * HALF - 1))];
                             uint32_t *p = &v.x;
                             bool hit = false;
 #pragma unroll
@@ -675,7 +686,7 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                                 p[e] &= ~nan;
                                 hit |= nan != 0;
                             }
-                            if (hit) row[i ^ (key & 7)] = v, took = true;
+                            if (hit) row[i ^ (key & (2 * HALF - 1))] = v, took = true;
                         }
                         if (took) *reinterpret_cast<volatile int *>(&sm.patched[g]) = seg;
                     }
@@ -960,17 +971,17 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
     }
 }
 
-// Tensor map of a cache in 8 bits: (byte, slot, head, page), boxes of 128 bytes x the slots of one page that fit a
+// Tensor map of a cache in 8 bits: (byte, slot, head, page), boxes of `width` bytes x the slots of one page that fit a
 // key tile.  Bytes past head_dim read as zero.
-static bool encode8(CUtensorMap *map, const sv_kv_cache8 &c, void *ptr) {
+static bool encode8(CUtensorMap *map, const sv_kv_cache8 &c, void *ptr, int width) {
     EncodeFn f = encode_fn();
     if (!f) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
                                 (cuuint64_t)c.num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
-    const cuuint32_t box[4] = {128, (cuuint32_t)(c.page_size < TILE ? c.page_size : TILE), 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)(c.page_size < TILE ? c.page_size : TILE), 1, 1}, one[4] = {1, 1, 1, 1};
     return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, ptr, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B,
+             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              c.head_dim % 128 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -990,7 +1001,7 @@ static Attn8Ws attn8_ws(int D) {
 
 constexpr int SMEM_MAX8 = 232448;
 
-template <typename E, int CHUNKS>
+template <typename E, int CHUNKS, int WIDTH>
 static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, const sv_kv_cache8 &cache, cudaStream_t st) {
     int dev = 0, nsm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -998,6 +1009,7 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
         return SV_ERR_CUDA;
     const int most_rows = (A.k_max + 1) * P.G;
     P.tile_rows = 16 * CHUNKS;
+    constexpr int STAGE8 = TILE * WIDTH;
     const int other = 2 * (Parts<E>::Q + Parts<E>::P) * P.tile_rows * 128, stages = (SMEM_MAX8 - SMALL8 - other) / (2 * STAGE8);
     P.overhead = 2;
     // (values wait longer than keys for their use: the odd stage is theirs)
@@ -1012,11 +1024,11 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
     if (C.D % 128 && cache.head_stride % 128 && C.heads <= 16 && ctas % C.heads * 20 <= ctas) ctas -= ctas % C.heads;
     if (most < ctas) ctas = (int)most;
     // (one limit for every call: another thread's call may come between this and the launch)
-    if (cudaFuncSetAttribute(attention8_kernel<E, CHUNKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX8) != cudaSuccess)
+    if (cudaFuncSetAttribute(attention8_kernel<E, CHUNKS, WIDTH>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX8) != cudaSuccess)
         return SV_ERR_CUDA;
     // (after a runtime call that brings this host thread to the device)
     CUtensorMap mk, mv;
-    if (!encode8(&mk, cache, cache.k) || !encode8(&mv, cache, cache.v)) return SV_ERR_CUDA;
+    if (!encode8(&mk, cache, cache.k, WIDTH) || !encode8(&mv, cache, cache.v, WIDTH)) return SV_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(NTHREADS8);
@@ -1027,7 +1039,7 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attention8_kernel<E, CHUNKS>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attention8_kernel<E, CHUNKS, WIDTH>, A, C, P, mk, mv) != cudaSuccess) return SV_ERR_CUDA;
     cfg.gridDim = dim3(2 * ctas, (most_rows < 8 ? most_rows : 8) + 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -1037,12 +1049,12 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
                : SV_ERR_CUDA;
 }
 
-template <typename E>
+template <typename E, int WIDTH>
 static sv_status launch_attention8(const Batch &A, const Cache8 &C, const Attn8Args &P, const sv_kv_cache8 &cache, cudaStream_t st) {
     const int rows = (A.k_max + 1) * P.G;
-    if (rows <= 16) return launch_rows8<E, 1>(A, C, P, cache, st);
-    if (rows <= 32 || Parts<E>::ROWS == 32) return launch_rows8<E, 2>(A, C, P, cache, st);
-    return launch_rows8<E, Parts<E>::ROWS / 16>(A, C, P, cache, st);
+    if (rows <= 16) return launch_rows8<E, 1, WIDTH>(A, C, P, cache, st);
+    if (rows <= 32 || Parts<E>::ROWS == 32) return launch_rows8<E, 2, WIDTH>(A, C, P, cache, st);
+    return launch_rows8<E, Parts<E>::ROWS / 16, WIDTH>(A, C, P, cache, st);
 }
 
 }  // namespace svc
@@ -1085,6 +1097,8 @@ extern "C" sv_status spec_attention8(const void *q, sv_dtype dtype, int64_t q_st
     P.sinks = sinks;
     P.pitch = cache.head_dim <= 64 ? 64 : 128;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == SV_BF16 ? launch_attention8<__nv_bfloat16>(A, C, P, cache, st)
-                            : launch_attention8<__half>(A, C, P, cache, st);
+    const bool wide = cache.head_dim > 64;
+    if (dtype == SV_BF16)
+        return wide ? launch_attention8<__nv_bfloat16, 128>(A, C, P, cache, st) : launch_attention8<__nv_bfloat16, 64>(A, C, P, cache, st);
+    return wide ? launch_attention8<__half, 128>(A, C, P, cache, st) : launch_attention8<__half, 64>(A, C, P, cache, st);
 }
