@@ -11,6 +11,12 @@
 // Work.  One or more CTAs per request.  A warp takes a task at a time: the new tokens of one block of one key
 // or value head (LPH lanes a token, so 2 or 4 tokens side by side, up to 4 such steps kept in registers
 // between the maximum and the rounding, more are computed twice), or 2 or 4 query heads of a row.
+//
+// What bounds it: issue and one wave's latency.  256 x 5 rows of 32 + 2 x 8 heads of 128 take 15.6 us in a graph (18.8 with
+// inputs that are not in L2; 28 MB, 4.2 us at the memory's rate), where a request is 32 000 warp instructions and a CTA's
+// chain is offsets -> length -> page -> rotations -> tasks; one row takes 4.2 us, the launch.  Integer divisions between
+// tasks, and one per pair of the rotations, were a tenth of the instructions (17.7 us).  Asking for the next task's elements
+// before this one's are worked on: 19.7, the registers then leave fewer CTAs; 8 warps a CTA: 16.9.
 #include "sv_cache8.cuh"
 #include "sv_rotate.cuh"
 #include "sv_tc.cuh"
@@ -29,7 +35,7 @@ struct Append8Args {
     int split;   // CTAs per request
 };
 
-constexpr int AT8 = 256;         // threads per CTA
+constexpr int AT8 = 128;         // threads per CTA (256 x 5 rows of 48 heads: 15.6 us, 16.9 with 256)
 constexpr int STEPS = 4;         // steps of a task whose elements stay in registers
 
 template <typename E, int LPH, int PAIR>
@@ -89,13 +95,17 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
         }
         page_of[i] = page;
     }
-    for (int i = tid; i < n * P.half; i += AT8) {
-        const int row = i / P.half, j = i - row * P.half;
-        const float f = P.inv_freq[j];
-        float sn, cs;
-        sincospif((float)(int32_t)(uint32_t)(turns_of(f) * (uint64_t)(uint32_t)(pos0 + row) >> 32) * 0x1p-31f, &sn, &cs);
-        if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
-        turn[row][j] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
+    {
+        const int hp = P.half > 32 ? 64 : 32, pair = tid & (hp - 1);   // threads per row
+        const float f = pair < P.half ? P.inv_freq[pair] : 0.f;
+        const uint64_t turns = turns_of(f);
+        if (pair < P.half)
+            for (int row = tid / hp; row < n; row += AT8 / hp) {
+                float sn, cs;
+                sincospif((float)(int32_t)(uint32_t)(turns * (uint64_t)(uint32_t)(pos0 + row) >> 32) * 0x1p-31f, &sn, &cs);
+                if (!(fabsf(f) < INFINITY)) sn = cs = NAN;
+                turn[row][pair] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
+            }
     }
     constexpr uint32_t ONE2 = Num<E>::ONE2;
     uint4 qw = make_uint4(ONE2, ONE2, ONE2, ONE2), kw = qw;   // (no weight: ones)
@@ -154,8 +164,12 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
     const int warps = P.split * (AT8 / 32), w = part * (AT8 / 32) + (tid >> 5);
     const int block0 = pos0 >> C.block_shift;
     const int blocks = ((s.len - 1) >> C.block_shift) - block0 + 1, stores = 2 * Hk * blocks;
-    for (int u = w; u < stores; u += warps) {
-        const int side = u / blocks, block = block0 + u - side * blocks;
+    const int side_step = warps / blocks, block_step = warps - side_step * blocks;   // from a warp's task to its next
+    for (int side = w / blocks, block = block0 + w - side * blocks; side < 2 * Hk; side += side_step, block += block_step) {
+        if (block >= block0 + blocks) {
+            block -= blocks;
+            if (++side >= 2 * Hk) break;
+        }
         const bool is_v = side >= Hk;
         const int h = is_v ? side - Hk : side;
         const int lo = max(pos0, block << C.block_shift), hi = min(s.len, (block + 1) << C.block_shift), count = hi - lo;
@@ -232,20 +246,27 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
     }
 
     // queries: after the stores, so that every warp has as many tasks
-    const int steps = (Hq + HPW - 1) / HPW, tasks = n * steps;
-    for (int u0 = (w + warps - stores % warps) % warps; u0 < tasks; u0 += STEPS * warps) {
+    const int steps = (Hq + HPW - 1) / HPW, row_step = warps / steps, col_step = warps - row_step * steps;
+    const int first = (w + warps - stores % warps) % warps;
+    int row = first / steps, col = first - row * steps;   // of this warp's next task
+    while (row < n) {
         uint4 raw[STEPS];
+        int rows[STEPS], heads[STEPS];
 #pragma unroll
         for (int e = 0; e < STEPS; e++) {
-            const int u = u0 + e * warps, row = u / steps, h = (u - row * steps) * HPW + team;
+            rows[e] = row;
+            heads[e] = col * HPW + team;
             raw[e] = make_uint4(0u, 0u, 0u, 0u);
-            if (u < tasks && in && h < Hq)
-                raw[e] = take(static_cast<const E *>(P.q) + (int64_t)(s.row0 + row) * P.q_stride + (int64_t)h * D);
+            if (row < n && in && heads[e] < Hq)
+                raw[e] = take(static_cast<const E *>(P.q) + (int64_t)(s.row0 + row) * P.q_stride + (int64_t)heads[e] * D);
+            row += row_step;
+            col += col_step;
+            if (col >= steps) col -= steps, row++;
         }
 #pragma unroll
         for (int e = 0; e < STEPS; e++) {
-            const int u = u0 + e * warps, row = u / steps, h = (u - row * steps) * HPW + team;
-            if (u >= tasks) break;   // (the whole warp)
+            const int row = rows[e], h = heads[e];
+            if (row >= n) break;   // (the whole warp)
             float2 x[4];
             turned(raw[e], qw, P.qw != nullptr, row, x);
             uint4 y = pack8<E>(reinterpret_cast<const float *>(x));
@@ -268,10 +289,10 @@ static cudaError_t launch_append8(const Batch &A, const Cache8 &C, Append8Args P
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // up to 4 CTAs per SM, and no more warps than tasks
+    // one wave of up to 4 CTAs per SM, and no more warps than tasks
     const int tasks = ((A.k_max + 1) * P.Hq + 2 * C.heads) / 2;
     P.split = 4 * nsm / A.B;
-    P.split = P.split < (tasks + 7) / 8 ? P.split : (tasks + 7) / 8;
+    P.split = P.split < (tasks + 3) / 4 ? P.split : (tasks + 3) / 4;
     P.split = P.split > 1 ? P.split : 1;
     auto *const kernel = P.interleaved || P.half == 0 ? append8_kernel<E, LPH, PAIR_NEXT>
                          : P.half % 4 == 0            ? append8_kernel<E, LPH, PAIR_HALVES>

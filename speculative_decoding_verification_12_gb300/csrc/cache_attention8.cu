@@ -1011,7 +1011,9 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
     P.tile_rows = 16 * CHUNKS;
     constexpr int STAGE8 = TILE * WIDTH;
     const int other = 2 * (Parts<E>::Q + Parts<E>::P) * P.tile_rows * 128, stages = (SMEM_MAX8 - SMALL8 - other) / (2 * STAGE8);
-    P.overhead = 2;
+    // A row tile costs about 4 key tiles beside its own.  96 ragged requests of 64 columns: 114, 93, 83, 79, 80 us with 1, 2, 3, 4, 6;
+    // 64 of 128 columns 84, 73, 62, 57, 60; uniform batches within 1 %.
+    P.overhead = 4;
     // (values wait longer than keys for their use: the odd stage is theirs)
     P.k_stages = stages / 2 < MAX_STAGES8 ? stages / 2 : MAX_STAGES8;
     P.v_stages = stages - P.k_stages < MAX_STAGES8 ? stages - P.k_stages : MAX_STAGES8;

@@ -5,10 +5,10 @@
 // where the row's mask refuses the token; fp32, rounded once.  Masks touch every token, the other rules
 // a few hundred of a row.
 //
-// One pass.  A CTA takes one piece of one row: it copies the piece and puts the refused tokens to -inf, 16 bytes
+// One pass.  A CTA takes a piece of one row: it copies the piece and puts the refused tokens to -inf, 16 bytes
 // at a time, or, where the output is the input, writes the refused tokens alone.  After a barrier its threads take the
 // entries of the request's sorted lists that lie in the piece: a token in several of history, drafts and biases
-// is the first one's, which looks it up in the others, so every element has one writer and one
+// is the first one's, which looks it up in the others and marks it there, so every element has one writer and one
 // rounding.  What the entries read again of the piece is still in L2.
 #include <math.h>
 
@@ -26,9 +26,13 @@ struct LogitArgs {
     int32_t *hdr;
     int V;
     int penalties;   // whether any is given
+    int piece;       // tokens of a row per CTA, a multiple of a pass of its threads
 };
 
-constexpr int LT = 256;   // threads per CTA
+constexpr int LT = 256;       // threads per CTA
+constexpr int MOST_STEPS = 16;   // of a piece that has entries: what they read again is to be in L2 still (512 requests of 1500
+                                // tokens, 151 937 logits: 308, 279, 323, 354 us with 8, 16, 24, 40)
+constexpr int BIASES = 256;   // of a piece that are kept in shared memory
 
 template <typename E>
 struct Logit;
@@ -95,36 +99,38 @@ __device__ __forceinline__ bool unsound(const int32_t *ids, const int32_t *count
     return bad;
 }
 
-// NV: 16-byte vectors per thread.
-template <typename E, int NV>
-__global__ void __launch_bounds__(LT) logits_kernel(const Batch A, const LogitArgs P) {
-    constexpr int VEC = Logit<E>::VEC, PIECE = LT * NV * VEC;
+// SAME: the output is the input.
+template <typename E, bool SAME>
+__global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A, const LogitArgs P) {
+    constexpr int VEC = Logit<E>::VEC, STEP = LT * VEC, NV = 4;   // NV: 16-byte vectors of a thread on their way at a time
     __shared__ int drafts[MAXK];
     __shared__ int range[4];              // this piece's entries of the history and of the biases
     __shared__ int ends[4];               // the request's
     __shared__ int status, mask_at, row_i, request;
+    __shared__ int bias_ids[BIASES];      // this piece's biases, if they are no more
+    __shared__ uint8_t draft_done[MAXK], bias_done[BIASES];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x, V = P.V;
     const int64_t row_at = (int64_t)row * V;
-    const int lead = (int)(row_at % VEC);            // elements of the row's first 16 bytes that are not its own
-    const int c0 = max((int)blockIdx.y * PIECE - lead, 0), c1 = (int)min((int64_t)(blockIdx.y + 1) * PIECE - lead, (int64_t)V);
+    // elements of the row's first 128 bytes that are not its own: the warps' accesses are whole lines
+    const int lead = (int)((((uintptr_t)P.out & 127) / sizeof(E) + row_at) % (128 / sizeof(E)));
+    const int c0 = max((int)blockIdx.y * P.piece - lead, 0), c1 = (int)min((int64_t)(blockIdx.y + 1) * P.piece - lead, (int64_t)V);
     if (c0 >= c1) return;
     const E *in = static_cast<const E *>(P.in) + row_at;
     E *out = static_cast<E *>(P.out) + row_at;
-    const bool same = P.in == P.out;
 
     grid_wait();
     grid_launch_dependents();
-    // this thread's vectors, under way while the request is found
+    // this thread's first vectors, under way while the request is found
     uint4 x[NV];
-    const int base = (int)blockIdx.y * PIECE - lead + tid * VEC;   // token of the first element
-    if (!same) {
+    const int base = (int)blockIdx.y * P.piece - lead + tid * VEC;   // token of the first element
+    auto whole = [&](int v) { return v >= 0 && v < c1 && v + VEC <= V; };
+    auto fetch = [&](int v0) {
 #pragma unroll
-        for (int k = 0; k < NV; k++) {
-            const int v = base + k * LT * VEC;
-            if (v >= 0 && v + VEC <= V) x[k] = *reinterpret_cast<const uint4 *>(in + v);
-        }
-    }
+        for (int k = 0; k < NV; k++)
+            if (whole(v0 + k * STEP)) x[k] = *reinterpret_cast<const uint4 *>(in + v0 + k * STEP);
+    };
+    if (!SAME) fetch(base);
     if (warp == 0) {
         // the row's request, and whether it is sound: status 0 used, 1 unused, 2 in error
         const int b = __shfl_sync(0xffffffffu, request_of_rows(A, row, 1), 0);
@@ -209,22 +215,31 @@ __global__ void __launch_bounds__(LT) logits_kernel(const Batch A, const LogitAr
         return v < 0 ? bits << -v : bits;
     };
     constexpr uint32_t ALL = (1u << VEC) - 1;
+#pragma unroll 1
+    for (int v0 = base; v0 < c1; v0 += NV * STEP) {
+        uint32_t bits[NV];
 #pragma unroll
-    for (int k = 0; k < NV; k++) {
-        const int v = base + k * LT * VEC;
-        if (v >= V || v + VEC <= 0) continue;
-        const uint32_t bits = allowed(v) & ALL;
-        if (same && bits == ALL) continue;
-        if (v >= 0 && v + VEC <= V) {
-            if (same && bits) x[k] = *reinterpret_cast<const uint4 *>(in + v);
-            *reinterpret_cast<uint4 *>(out + v) = bits == ALL ? x[k] : Logit<E>::refuse(x[k], bits);
-        } else {
-            for (int e = 0; e < VEC; e++) {
-                if (v + e < 0 || v + e >= V) continue;
-                if (!(bits >> e & 1)) out[v + e] = Logit<E>::down(-INFINITY);
-                else if (!same) out[v + e] = in[v + e];
+        for (int k = 0; k < NV; k++) bits[k] = v0 + k * STEP < c1 && v0 + k * STEP + VEC > 0 ? allowed(v0 + k * STEP) & ALL : ALL;
+        if (SAME) {   // only what a mask refuses a part of is read
+#pragma unroll
+            for (int k = 0; k < NV; k++)
+                if (bits[k] && bits[k] != ALL && whole(v0 + k * STEP)) x[k] = *reinterpret_cast<const uint4 *>(in + v0 + k * STEP);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; k++) {
+            const int v = v0 + k * STEP;
+            if (v >= c1 || v + VEC <= 0 || (SAME && bits[k] == ALL)) continue;
+            if (whole(v)) {
+                *reinterpret_cast<uint4 *>(out + v) = bits[k] == ALL ? x[k] : Logit<E>::refuse(x[k], bits[k]);
+            } else {
+                for (int e = 0; e < VEC; e++) {
+                    if (v + e < 0 || v + e >= V) continue;
+                    if (!(bits[k] >> e & 1)) out[v + e] = Logit<E>::down(-INFINITY);
+                    else if (!SAME) out[v + e] = in[v + e];
+                }
             }
         }
+        if (!SAME) fetch(v0 + NV * STEP);
     }
     __syncthreads();
 
@@ -233,35 +248,62 @@ __global__ void __launch_bounds__(LT) logits_kernel(const Batch A, const LogitAr
                 frequency = P.r.frequency ? P.r.frequency[b] : 0.f;
     const int p0 = range[0], p1 = range[1], b0 = range[2], b1 = range[3];
     const int nd = P.penalties ? i : 0;
-    // token v, with its place in the history (-1: not in it) and among the biases (-2: to be looked up)
-    auto put = [&](int v, int prior, int bias) {
-        if (v < c0 || v >= c1) return;
-        if (mask && !(mask[v >> 5] >> (v & 31) & 1)) return;
-        float z = Logit<E>::up(in[v]);
-        int count = prior >= 0 ? P.r.prior_counts[prior] : 0;
-        bool seen = prior >= 0 && P.penalties;
+    const bool kept = b1 - b0 <= BIASES;
+    if (kept && tid < b1 - b0) bias_ids[tid] = P.r.bias_tokens[b0 + tid], bias_done[tid] = 0;
+    if (tid < nd) draft_done[tid] = 0;
+    __syncthreads();
+    // token v with logit z, its count in the history (-1: not in it) and its place among the biases (-2: to be looked up)
+    auto put = [&](int v, float z, int prior, int bias) {
+        const bool refused = mask && !(mask[v >> 5] >> (v & 31) & 1);
+        int count = max(prior, 0);
+        bool seen = prior >= 0;
         for (int j = 0; j < nd; j++)
-            if (drafts[j] == v) count++, seen = true;
+            if (drafts[j] == v) count++, seen = true, draft_done[j] = 1;
+        if (bias == -2) {
+            bias = kept ? find(bias_ids, 0, b1 - b0, v) : find(P.r.bias_tokens, b0, b1, v);
+            if (kept && bias >= 0) {
+                bias_done[bias] = 1;
+                bias += b0;
+            }
+        }
+        if (refused) return;
         if (seen) {
             z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
             z = __fsub_rn(z, __fadd_rn(count > 0 ? presence : 0.f, __fmul_rn(frequency, (float)count)));
         }
-        if (bias == -2) bias = find(P.r.bias_tokens, b0, b1, v);
         if (bias >= 0) z = __fadd_rn(z, P.r.bias_values[bias]);
         out[v] = Logit<E>::down(z);
     };
-    for (int e = p0 + tid; e < p1; e += LT) put(P.r.prior_tokens[e], e, -2);
-    if (tid < nd) {
-        const int v = drafts[tid];
-        bool other = v < c0 || v >= c1;   // another piece's, or an earlier draft's, or the history's
-        for (int j = 0; j < tid && !other; j++) other = drafts[j] == v;
-        if (!other && find(P.r.prior_tokens, p0, p1, v) < 0) put(v, -1, -2);
+    auto here = [&](int v) { return v >= c0 && v < c1; };
+    for (int e = p0 + tid; e < p1; e += 4 * LT) {   // (four entries' loads at a time: 512 requests of 1500 tokens 363 us one by one)
+        int v[4], count[4];
+        float z[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            v[k] = e + k * LT < p1 ? P.r.prior_tokens[e + k * LT] : -1;
+            count[k] = e + k * LT < p1 ? max(P.r.prior_counts[e + k * LT], 0) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) z[k] = here(v[k]) ? Logit<E>::up(in[v[k]]) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (here(v[k])) put(v[k], z[k], count[k], -2);
     }
+    __syncthreads();
+    // drafts that the history has not got, each by its first occurrence
+    bool mine = tid < nd && !draft_done[tid];
+    for (int j = 0; mine && j < tid; j++) mine = drafts[j] != drafts[tid];
+    __syncthreads();
+    if (mine && here(drafts[tid])) put(drafts[tid], Logit<E>::up(in[drafts[tid]]), -1, -2);
+    __syncthreads();
     for (int e = b0 + tid; e < b1; e += LT) {
-        const int v = P.r.bias_tokens[e];
-        bool other = false;
-        for (int j = 0; j < nd && !other; j++) other = drafts[j] == v;
-        if (!other && find(P.r.prior_tokens, p0, p1, v) < 0) put(v, -1, e);
+        const int v = kept ? bias_ids[e - b0] : P.r.bias_tokens[e];
+        bool other = kept && bias_done[e - b0];
+        if (!kept) {
+            for (int j = 0; j < nd && !other; j++) other = drafts[j] == v;
+            other = other || find(P.r.prior_tokens, p0, p1, v) >= 0;
+        }
+        if (!other && here(v)) put(v, Logit<E>::up(in[v]), -1, e);
     }
     // the request's first row reports what is wrong with its lists
     if (i == 0 && blockIdx.y == 0) {
@@ -272,13 +314,22 @@ __global__ void __launch_bounds__(LT) logits_kernel(const Batch A, const LogitAr
 }
 
 template <typename E>
-static cudaError_t launch_logits(const Batch &A, const LogitArgs &P, cudaStream_t st) {
-    constexpr int VEC = Logit<E>::VEC;
-    const bool small = (long long)A.R * P.V < (long long)152 * LT * 8 * VEC * 2;
-    const int piece = LT * (small ? 2 : 8) * VEC;
-    const dim3 grid(A.R, (P.V + VEC - 1 + piece - 1) / piece);
-    return small ? launch_dependent(logits_kernel<E, 2>, grid, dim3(LT), 1, st, A, P)
-                 : launch_dependent(logits_kernel<E, 8>, grid, dim3(LT), 1, st, A, P);
+static cudaError_t launch_logits(const Batch &A, LogitArgs P, cudaStream_t st) {
+    constexpr int VEC = Logit<E>::VEC, STEP = LT * VEC;
+    int dev = 0, nsm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // pieces of a row: about 4 waves of CTAs, 8 a multiprocessor, where the rows are fewer than that
+    const int steps = (int)((P.V + 128 / sizeof(E) - 1 + STEP - 1) / STEP);   // (a row may begin anywhere in 128 bytes)
+    const long long want = 32ll * nsm;
+    const int pieces = (int)(A.R >= want ? 1 : (want + A.R - 1) / A.R < steps ? (want + A.R - 1) / A.R : steps);
+    int per = (steps + pieces - 1) / pieces;
+    if ((P.r.prior_offsets || P.r.bias_offsets) && per > MOST_STEPS) per = MOST_STEPS;
+    P.piece = per * STEP;
+    const dim3 grid(A.R, (steps + per - 1) / per);
+    return P.in == P.out ? launch_dependent(logits_kernel<E, true>, grid, dim3(LT), 1, st, A, P)
+                         : launch_dependent(logits_kernel<E, false>, grid, dim3(LT), 1, st, A, P);
 }
 
 }  // namespace svc
