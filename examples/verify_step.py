@@ -4,7 +4,10 @@ A small random decoder (grouped-query attention with per-head norms and rotation
 with a sliding window and sinks) runs over a paged cache.  Each step drafts k tokens per request,
 here by asking what the request would continue with and getting some of them wrong, and then:
 
-    reserve -> per layer: append, attend -> spec_verify -> rollback -> release
+    reserve -> per layer: append, attend -> (spec_logits) -> spec_verify -> rollback -> release
+
+The cache may be in 8 bits (`dtype`), and the tokens may be bound by rules: a grammar, here that a token's number and
+the one's before it must not add up to a multiple of 3, with a penalty for tokens that the request has seen.
 
 Requests are greedy, so whatever the drafts are, the tokens that come out are the model's own greedy
 continuation; `python examples/verify_step.py` checks them against a plain forward over the whole
@@ -17,7 +20,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from speculative_decoding_verification_12_gb300 import PagedCache, spec_verify, sv_read_device_error, sv_workspace_bytes  # noqa: E402
+from speculative_decoding_verification_12_gb300 import PagedCache, spec_logits, spec_verify, sv_read_device_error, sv_workspace_bytes  # noqa: E402
 
 
 class Decoder:
@@ -63,12 +66,44 @@ class Decoder:
         return x @ self.embed.float().T / 8
 
 
+class Rules:
+    """A grammar over neighbouring tokens, and a repetition penalty."""
+
+    def __init__(self, vocab, penalty=1.2, device="cuda"):
+        self.vocab, self.penalty, self.device = vocab, penalty, device
+        self.ids = torch.arange(vocab, device=device)
+
+    def allowed(self, before):
+        """Which tokens may follow each of `before`."""
+        return (before[..., None] + self.ids) % 3 != 0
+
+    def plain(self, z, seq):
+        """The next token's logits after seq."""
+        seen = torch.zeros_like(z, dtype=torch.bool)
+        seen[seq] = True
+        z = torch.where(seen, torch.where(z > 0, z / self.penalty, z * self.penalty), z)
+        return z.masked_fill(~self.allowed(seq[-1]), -torch.inf)
+
+    def masks(self, before):
+        """Bit masks of a step's rows."""
+        a = torch.nn.functional.pad(self.allowed(before.flatten()), (0, -self.vocab % 32)).view(before.numel(), -1, 32)
+        return (a * 2 ** torch.arange(32, device=self.device)).sum(-1).to(torch.int32)
+
+    def prior(self, seqs):
+        """The requests' tokens so far, ascending and distinct, as seen (count 0)."""
+        lists = [sorted(set(s)) for s in seqs]
+        ends = torch.tensor([0] + [len(x) for x in lists]).cumsum(0)
+        ints = lambda v: torch.as_tensor(v, dtype=torch.int32, device=self.device)
+        tokens = ints([t for x in lists for t in x])
+        return ints(ends), tokens, torch.zeros_like(tokens)
+
+
 class Server:
     """Greedy requests over a paged cache, k drafts a step."""
 
-    def __init__(self, model, slots, k, pages=256, page_size=16, max_pages=32):
-        self.m, self.k, self.B = model, k, slots
-        self.cache = PagedCache(model.layers, slots, pages, page_size, max_pages, model.Hk, model.D)
+    def __init__(self, model, slots, k, pages=256, page_size=16, max_pages=32, dtype=torch.bfloat16, rules=None):
+        self.m, self.k, self.B, self.rules = model, k, slots, rules
+        self.cache = PagedCache(model.layers, slots, pages, page_size, max_pages, model.Hk, model.D, dtype=dtype)
         R, dev = slots * (k + 1), "cuda"
         self.q = torch.empty(slots * 65, model.Hq, model.D, dtype=torch.bfloat16, device=dev)   # (a prompt's rows too)
         self.attended = torch.empty_like(self.q)
@@ -101,10 +136,17 @@ class Server:
         self.forward(tokens[:, :-1].contiguous(), torch.full((B,), n - 2, dtype=torch.int32, device="cuda"), n - 2)
         self.last = tokens[:, -1:]
 
-    def step(self, drafts):
-        """One verify step over drafts [B, k]; returns the new tokens of each request (-1: none)."""
+    def step(self, drafts, seqs=None):
+        """One verify step over drafts [B, k]; returns the new tokens of each request (-1: none).  seqs: the
+        requests' tokens so far, where there are rules."""
         nd = torch.full((self.B,), self.k, dtype=torch.int32, device="cuda")
-        logits = self.forward(torch.cat((self.last, drafts), 1), nd, self.k)
+        tokens = torch.cat((self.last, drafts), 1)
+        logits = self.forward(tokens, nd, self.k)
+        if self.rules:
+            penalty = torch.full((self.B,), self.rules.penalty, device="cuda")
+            rows = torch.arange(tokens.numel(), dtype=torch.int32, device="cuda")
+            spec_logits(logits, drafts.int().contiguous(), nd, None, self.k, penalty, None, None, self.rules.prior(seqs), None,
+                        self.rules.masks(tokens), rows, logits, self.cache.workspace)
         spec_verify(logits, self.draft_probs, drafts.int().contiguous(), nd, None, self.k, *self.params, self.uniforms,
                     self.out_tokens, self.accept_len, None, self.workspace)
         self.cache.commit(self.accept_len, nd)
@@ -112,11 +154,13 @@ class Server:
         return self.out_tokens
 
 
-def run(slots=6, prompt=20, steps=8, k=4, seed=1):
-    """Runs the server; returns (sequences, the largest gap by which a chosen token's plain logit lies
+def run(slots=6, prompt=20, steps=8, k=4, seed=1, dtype=torch.bfloat16, ruled=False):
+    """Runs the server, over a cache of the given type and, with `ruled`, under the rules; returns (sequences, the largest gap by which a chosen token's plain logit lies
     below the plain maximum, accepted drafts per step)."""
     model = Decoder()
-    server = Server(model, slots, k)
+    rules = Rules(model.vocab) if ruled else None
+    server = Server(model, slots, k, dtype=dtype, rules=rules)
+    after = lambda z, seq: rules.plain(z, seq) if rules else z
     g = torch.Generator(device="cuda").manual_seed(seed)
     tokens = torch.randint(0, model.vocab, (slots, prompt), device="cuda", generator=g)
     tokens[slots - 1] = tokens[0]          # the last slot will be a fork of the first: same prompt for now
@@ -137,10 +181,11 @@ def run(slots=6, prompt=20, steps=8, k=4, seed=1):
         for b, seq in enumerate(seqs):
             now = list(seq)
             for i in range(k):
-                t = int(model.plain(torch.tensor(now, device="cuda"))[-1].argmax())
+                seq = torch.tensor(now, device="cuda")
+                t = int(after(model.plain(seq)[-1], seq).argmax())
                 now.append((t + 1) % model.vocab if (b + s + i) % 3 == 2 else t)
             drafts.append(now[-k:])
-        out = server.step(torch.tensor(drafts, device="cuda")).tolist()
+        out = server.step(torch.tensor(drafts, device="cuda"), seqs).tolist()
         accepted += int(server.accept_len.sum())
         for seq, new in zip(seqs, out):
             seq.extend(t for t in new if t >= 0)
@@ -153,13 +198,17 @@ def run(slots=6, prompt=20, steps=8, k=4, seed=1):
     assert held <= used and int(server.cache.ref_count.sum()) == used
     gap = 0.0
     for seq in seqs:
-        z = model.plain(torch.tensor(seq, device="cuda"))[prompt - 1:-1]
+        all_ = torch.tensor(seq, device="cuda")
+        z = model.plain(all_)[prompt - 1:-1]
+        z = torch.stack([after(x, all_[:prompt + i]) for i, x in enumerate(z)])
         chosen = z.gather(1, torch.tensor(seq[prompt:], device="cuda")[:, None])[:, 0]
         gap = max(gap, float((z.amax(-1) - chosen).max()))
     return seqs, gap, accepted / (steps * slots)
 
 
 if __name__ == "__main__":
-    seqs, gap, rate = run()
-    print(f"{len(seqs)} requests of {[len(s) for s in seqs]} tokens, {rate:.2f} drafts accepted a step")
-    print(f"chosen tokens lie at most {gap:.4f} below the plain forward's largest logit")
+    for dtype, ruled in ((torch.bfloat16, False), (torch.bfloat16, True), (torch.float8_e4m3fn, True)):
+        seqs, gap, rate = run(dtype=dtype, ruled=ruled)
+        print(f"{dtype} cache{', with rules' if ruled else ''}:")
+        print(f"  {len(seqs)} requests of {[len(s) for s in seqs]} tokens, {rate:.2f} drafts accepted a step")
+        print(f"  chosen tokens lie at most {gap:.4f} below the plain forward's largest logit")
