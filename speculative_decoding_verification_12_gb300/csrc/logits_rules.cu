@@ -102,7 +102,8 @@ __device__ __forceinline__ bool unsound(const int32_t *ids, const int32_t *count
 // SAME: the output is the input.
 template <typename E, bool SAME>
 __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A, const LogitArgs P) {
-    constexpr int VEC = Logit<E>::VEC, STEP = LT * VEC, NV = 4;   // NV: 16-byte vectors of a thread on their way at a time
+    constexpr int VEC = Logit<E>::VEC, STEP = LT * VEC;
+    constexpr int NV = SAME ? 2 : 4;   // 16-byte vectors of a thread on their way at a time (SAME: registers for 8 CTAs count more)
     __shared__ int drafts[MAXK];
     __shared__ int range[4];              // this piece's entries of the history and of the biases
     __shared__ int ends[4];               // the request's
@@ -205,21 +206,30 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
     } else if (warp >= 4 && lane == 0) {
         range[warp - 4] = 0;
     }
-    // bits of tokens v .. v + VEC - 1, those outside [0, V) clear or not
-    auto allowed = [&](int v) {
-        if (!mask) return 0xffffffffu;
+    // the mask's words of tokens v .. v + VEC - 1, and their bits (those outside [0, V) clear or not)
+    auto words = [&](int v, uint32_t &lo, uint32_t &hi) {
+        lo = hi = 0xffffffffu;
+        if (!mask || v >= c1 || v + VEC <= 0) return;
         const int u = max(v, 0);
-        uint32_t lo = mask[u >> 5], hi = 0;
+        lo = mask[u >> 5];
         if ((u & 31) + VEC > 32 && (u >> 5) + 1 < P.r.mask_words) hi = mask[(u >> 5) + 1];
-        const uint32_t bits = __funnelshift_r(lo, hi, u & 31);
-        return v < 0 ? bits << -v : bits;
     };
     constexpr uint32_t ALL = (1u << VEC) - 1;
+    auto allowed = [&](int v, uint32_t lo, uint32_t hi) {
+        const uint32_t bits = __funnelshift_r(lo, hi, max(v, 0) & 31);
+        return (v < 0 ? bits << -v : bits) & ALL;
+    };
+    uint32_t lo[NV], hi[NV];   // of the next vectors
+#pragma unroll
+    for (int k = 0; k < NV; k++) words(base + k * STEP, lo[k], hi[k]);
 #pragma unroll 1
     for (int v0 = base; v0 < c1; v0 += NV * STEP) {
         uint32_t bits[NV];
 #pragma unroll
-        for (int k = 0; k < NV; k++) bits[k] = v0 + k * STEP < c1 && v0 + k * STEP + VEC > 0 ? allowed(v0 + k * STEP) & ALL : ALL;
+        for (int k = 0; k < NV; k++) {
+            bits[k] = allowed(v0 + k * STEP, lo[k], hi[k]);
+            words(v0 + (NV + k) * STEP, lo[k], hi[k]);
+        }
         if (SAME) {   // only what a mask refuses a part of is read
 #pragma unroll
             for (int k = 0; k < NV; k++)
