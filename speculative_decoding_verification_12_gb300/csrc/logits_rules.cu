@@ -10,6 +10,11 @@
 // entries of the request's sorted lists that lie in the piece: a token in several of history, drafts and biases
 // is the first one's, which looks it up in the others and marks it there, so every element has one writer and one
 // rounding.  What the entries read again of the piece is still in L2.
+//
+// What bounds it: memory, and the entries' loads, one after the other (the token, its logit, its place in the other
+// lists).  1280 bf16 rows of 128 256: copied in 100 us (97 % of the memory's rate), with 1000 tokens of history and 16
+// biases a request 123, with masks on half the rows besides 128.  Masks alone, in place, on 2048 fp32 rows: 232 us, 5
+// TB/s; a 16-byte piece of which a part is refused is read and written whole.  One row of 32 000: 5.8 us, latency.
 #include <math.h>
 
 #include "../../include/spec_logits.h"
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
     // token v with logit z, its count in the history (-1: not in it) and its place among the biases (-2: to be looked up)
     auto put = [&](int v, float z, int prior, int bias) {
         const bool refused = mask && !(mask[v >> 5] >> (v & 31) & 1);
-        int count = max(prior, 0);
+        uint32_t count = max(prior, 0);   // (drafts may take it past 2^31)
         bool seen = prior >= 0;
         for (int j = 0; j < nd; j++)
             if (drafts[j] == v) count++, seen = true, draft_done[j] = 1;

@@ -339,3 +339,53 @@ def test_verify_after_the_rules(sv):
         while a < k and drafts[b, a] == best[b, a]:
             a += 1
         assert int(accept[b]) == a and int(tokens[b, a]) == int(best[b, a])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_largest_vocabulary(sv, dtype):
+    run_and_check(sv, make(18, [1, 0], 1, 1 << 21, dtype, history=300, bias=30, masks=dtype == "fp32"))
+
+
+def test_the_largest_counts(sv):
+    """A history count of 2^31 - 1, and drafts of the same token."""
+    s = make(19, [3], 3, 64, "fp32", history=0, bias=0, masks=False)
+    s["toks"][:] = 9
+    s["freq"][0], s["pres"][0] = 1e-9, 0.5
+    s["prior"] = tuple(torch.tensor(x, dtype=torch.int32) for x in ([0, 2], [9, 12], [2 ** 31 - 1, 0]))
+    run_and_check(sv, s)
+
+
+def test_a_row_that_allows_one_token_or_none(sv):
+    """Whatever the other rules say of them."""
+    s = make(20, [4, 4], 4, 1000, "bf16", history=1000, bias=1000)
+    s["mask"][:] = 0
+    s["mask"][:, 17] = 1 << 5
+    s["mask"][3] = 0
+    s["rows"][:] = torch.tensor([0, 1, 2, 3, 4, 3, 3, 5, 5, 5])
+    out = run_and_check(sv, s)
+    assert (out > -math.inf).sum(1).tolist() == [1, 1, 1, 0, 1, 0, 0, 1, 1, 1]
+
+
+def test_two_graphs_at_once(sv):
+    """Graphs of calls of different sizes, replayed on two streams at a time."""
+    calls = []
+    c = lambda t: None if t is None else tuple(x.cuda() for x in t) if isinstance(t, tuple) else t.cuda()
+    for seed, V, dtype in ((21, 32000, "bf16"), (22, 9001, "fp32")):
+        s = make(seed, [3, 0, 5, 1], 5, V, dtype)
+        z, ws = s["z"].cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(z)
+        args = [z, c(s["toks"]), c(s["nd"]), c(s["ro"]), s["k_max"], c(s["rep"]), c(s["pres"]), c(s["freq"]), c(s["prior"]),
+                c(s["bias"]), c(s["mask"]), c(s["rows"]), out, ws]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                sv.spec_logits(*args)
+        calls.append((s, out, graph, torch.cuda.Stream(), args))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, graph, stream, _ in calls:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for s, out, _, _, _ in calls:
+        check(s, out.cpu(), rows=plain(s)[4])
