@@ -17,19 +17,29 @@
 //     e5m2 leaves 2^-24 of it below.  They are added up along K, in one accumulator: the keys are read three times,
 //     which costs less than the columns that parts side by side would take and a thread would have to add;
 //   - a weight in fp16 is a sum of its top byte, the top byte of the rest, and so on: an fp16's top byte is an e5m2
-//     number.  The parts lie side by side along N, so that the values are read once.  2 (3) of them and the rest rounded to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans
-//     2^-17 to 2^15.8, and the running maximum is kept between 2^12 and 2^15.5, so what is rounded away is below 2^-29 of
-//     a row's largest weight, and unbiased.  (e4m3 parts would end 2^-18 below it: 131 072 small weights
+//     number.  The parts lie side by side along N, so that the values are read once.  2 (3) of them and the rest rounded
+//     to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans 2^-17 to 2^15.8, and the running maximum is kept between 2^12 and 2^15.5, so what is lost of a weight beside its 9 (11) bits
+//     is below 2^-28 of a row's largest.  (e4m3 parts would end 2^-18 below it: 131 072 small weights
 //     would lose a percent of the sum.)
 // The score of a key is c ks_j qs_r S (ks: the key's scale, qs: the row's power of two), and the weight that goes to the
 // product with v is p vs_j: log2 vs_j is added to the exponent, and m is the maximum of the sums.  l adds p alone.
 //
-// A CTA works at two ranges at once.  It has a front warp (the segments of both ranges, half a warp each), a warp for each
-// range that loads keys and values (tensor copies of pages into two rings) and scales (4-byte copies), one that issues all
-// matrix instructions, and a group of 8 softmax warps for each range, which also brings its queries into parts.  While one
-// range changes from a segment to the next, the other keeps the memory busy.  A group's warps decide
-// together, at a barrier per tile, whether a maximum lags too far; every decision that a barrier depends on is taken
-// that way, so a wait that runs out in one warp ends all of them.
+// A CTA works at two ranges at once.  Each has a warp that keeps its queue of segments and loads keys and values
+// (tensor copies of pages into two rings) and scales (4-byte copies), one that issues its matrix instructions, and a
+// group of 8 softmax warps, which also brings its queries into parts.  While one range changes from a segment to the
+// next, the other keeps the memory busy.  A group's warps decide together, at a barrier per tile, whether a maximum
+// lags too far; every decision that a barrier depends on is taken that way, so a wait that runs out in one warp ends
+// all of them.
+//
+// What bounds it.  Few rows: the cache's bytes; 256 requests of one row (4 query heads a key head) over 4096 keys of 8
+// heads of 128 take 328 us, 317 at the memory's rate.  More rows: the chain of a softmax group from a tile's scores to
+// the next one's; with 5 rows a request 365 us, about 3200 cycles a tile and group, while the schedulers issue in 54 %
+// of the cycles and the tensor pipe works in 18.  Heads of 64 columns: the tensor copies, 16 rows of 64 bytes each with
+// pages of 16 (one row a request: 286 us; 237 with pages of 256).  Long chains (16 x 65 rows, 8 query heads a key
+// head, 8192 keys): the groups' instructions, 11 row tiles of 48 rows; 292 us.  Small calls: latency, 10.8 us.
+//
+// What was slower (256 x 5 rows): two groups taking the tiles of one segment in turn, 432 us at best; one warp issuing
+// both ranges' matrix instructions, 459, at 2000 cycles a tile; barriers polled in tight loops, 463 for 433.
 #include "sv_cache8.cuh"
 #include "sv_launch.h"
 #include "sv_segments.cuh"
@@ -40,7 +50,8 @@ namespace svc {
 constexpr int NTHREADS8 = 640;           // 2 x 8 softmax warps, then
 constexpr int W_MMA = 18;                // 16, 17: loads of each range; 18, 19: its matrix instructions
 constexpr int MAX_STAGES8 = 7;           // of a ring: keys and values of each range
-constexpr int SCALES8 = 8;               // tiles whose scales are kept (more than a ring's stages and one)
+constexpr int SCALES8 = 8;               // tiles whose scales are kept
+constexpr int MOST_K_STAGES = SCALES8 - 2;   // with two S, scales of stages + 1 tiles are awaited or in use beside a new one's
 constexpr int MAX_ROWS8 = 48;            // rows of a row tile, at most
 constexpr int READERS8 = 9;              // warps that take each segment
 
@@ -1015,7 +1026,7 @@ static sv_status launch_rows8(const Batch &A, const Cache8 &C, Attn8Args P, cons
     // 64 of 128 columns 84, 73, 62, 57, 60; uniform batches within 1 %.
     P.overhead = 4;
     // (values wait longer than keys for their use: the odd stage is theirs)
-    P.k_stages = stages / 2 < MAX_STAGES8 ? stages / 2 : MAX_STAGES8;
+    P.k_stages = stages / 2 < MOST_K_STAGES ? stages / 2 : MOST_K_STAGES;
     P.v_stages = stages - P.k_stages < MAX_STAGES8 ? stages - P.k_stages : MAX_STAGES8;
     const int smem = SMALL8 + other + 2 * (P.k_stages + P.v_stages) * STAGE8;
     // no more CTAs than the batch can have units

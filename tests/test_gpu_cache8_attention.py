@@ -482,3 +482,66 @@ def test_segments_follow_each_other(sv, tiles, G, k_max):
     for _ in range(20):
         x.call()
         assert torch.equal(x.results()[0], out)
+
+
+def test_a_batch_of_idle_requests(sv):
+    """Nothing to do but to set the rows to zero; and between two replays nothing is left of the calls before."""
+    s = make(81, [40, 300, 7], [2, 2, 2], 2, 8, 2, 64, 16, 16, "bf16", ragged=False)
+    x = OnGpu(sv, s)
+    for drafts in ([-1, -1, -1], [2, -1, 0], [-1, -1, -1]):
+        x.nd.copy_(torch.tensor(drafts))
+        x.out.fill_(3.0)
+        x.lse.fill_(3.0)
+        x.call()
+        out, lse, e = x.results()
+        assert e == (0, -1)
+        if max(drafts) < 0:
+            assert not bool(out.any()) and not bool(lse.any())
+        else:
+            check(dict(s, nd=torch.tensor(drafts, dtype=torch.int32)), out, lse)
+
+
+@pytest.mark.parametrize("lse", [True, False])
+def test_more_requests_than_threads(sv, lse):
+    """Two passes over the batch find where a range begins."""
+    r = random.Random(82)
+    drafts = [r.choice([-1, 0, 1]) for _ in range(1500)]
+    lens = [r.randint(max(k + 1, 1), 200) for k in drafts]
+    s = make(82, lens, drafts, 1, 2, 1, 16, 32, 16, "fp16")
+    x = OnGpu(sv, s)
+    x.call(lse=lse)
+    out, got, e = x.results()
+    assert e == (0, -1)
+    if lse:
+        check(s, out, got)
+    else:
+        assert bool((got == 7.0).all())
+        x.call()
+        assert torch.equal(x.results()[0], out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_the_most_heads_of_a_key_head(sv, dtype):
+    run_and_check(sv, make(83, [9, 300], [2, 0], 2, 1024, 1, 64, 16, 16, dtype))
+
+
+def test_two_graphs_at_once(sv):
+    calls = []
+    for G, k_max, D, dtype in ((4, 4, 128, "bf16"), (7, 3, 64, "fp16")):
+        x = OnGpu(sv, make(84 + G, [k_max + 900, 30, 513], [k_max, 0, k_max], k_max, G, 1, D, 16, 16, dtype))
+        x.call()
+        want = x.results()[0]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                x.call()
+        x.out.fill_(7.0)
+        calls.append((x, want, graph, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, graph, stream in calls:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    for x, want, _, _ in calls:
+        out, _, e = x.results()
+        assert e == (0, -1) and torch.equal(out, want)
