@@ -297,3 +297,42 @@ def test_far_positions_and_a_pool_past_32_bits(sv):
     sv.spec_append8(c(s["q"]), c(s["k"]), c(s["v"]), *map(c, s["w"]), 1e-6, c(s["inv"]), kc, vc, ks, vs, table, c(s["lens"]),
                     c(s["nd"]), c(s["ro"]), 3, out, ws)
     assert torch.equal(kc.view(torch.uint8)[far].cpu(), got["kc"][was]) and torch.equal(vs[far].cpu(), got["vs"][was])
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1024, 1), (1024, 1024)])
+def test_the_most_heads(sv, Hq, Hk):
+    s = make(13, [5, 40], [1, 2], 2, Hq, Hk, 16, 16, 8, "bf16", 16)
+    run_and_check(sv, s)
+
+
+def test_a_batch_of_idle_requests(sv):
+    s = make(14, [30, 7], [1, 1], 1, 4, 2, 64, 16, 16, "bf16", 64, ragged=False)
+    s["nd"] = torch.tensor([-1, -1], dtype=torch.int32)
+    got, e = call(sv, s)
+    assert e == (0, -1) and not bool(got["q"].any())
+    assert all(torch.equal(got[n], s[n].view(torch.uint8) if n in ("kc", "vc") else s[n]) for n in ("kc", "vc", "ks", "vs"))
+
+
+def test_two_graphs_at_once(sv):
+    """Replayed over and over, an append writes what it wrote the first time."""
+    calls = []
+    c = lambda t: None if t is None else t.cuda()
+    for seed, Hq, Hk, D, dtype in ((15, 8, 2, 128, "bf16"), (16, 6, 3, 64, "fp16")):
+        s = make(seed, [50, 17, 100], [4, 0, 4], 4, Hq, Hk, D, 16, 16, dtype, D)
+        want, _ = call(sv, s)
+        q, k, v, kc, vc, ks, vs = (s[n].cuda() for n in ("q", "k", "v", "kc", "vc", "ks", "vs"))
+        out, ws = torch.empty_like(q), torch.zeros(256, dtype=torch.uint8, device="cuda")
+        args = [q, k, v, *map(c, s["w"]), 1e-6, c(s["inv"]), kc, vc, ks, vs, *map(c, (s["table"], s["lens"], s["nd"], s["ro"])), 4, out, ws]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                sv.spec_append8(*args)
+        calls.append((want, dict(q=out, kc=kc.view(torch.uint8), vc=vc.view(torch.uint8), ks=ks, vs=vs), graph, torch.cuda.Stream(), args))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _, _, graph, stream, _ in calls:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for want, got, _, _, _ in calls:
+        assert all(torch.equal(got[n].cpu(), want[n]) for n in want)
