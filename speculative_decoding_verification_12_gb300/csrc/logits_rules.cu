@@ -11,10 +11,10 @@
 // is the first one's, which looks it up in the others and marks it there, so every element has one writer and one
 // rounding.  What the entries read again of the piece is still in L2.
 //
-// What bounds it: memory, and the entries' loads, one after the other (the token, its logit, its place in the other
-// lists).  1280 bf16 rows of 128 256: copied in 100 us (97 % of the memory's rate), with 1000 tokens of history and 16
-// biases a request 123, with masks on half the rows besides 128.  Masks alone, in place, on 2048 fp32 rows: 232 us, 5
-// TB/s; a 16-byte piece of which a part is refused is read and written whole.  One row of 32 000: 5.8 us, latency.
+// What bounds it: memory, and the entries: 1280 bf16 rows of 128 256 are copied in 100 us (97 % of the memory's rate), with
+// 1000 tokens of history and 16 biases a request in 123, with masks on half the rows besides in 128.  (Bringing a piece's
+// entries into shared memory during its copy: 134.)  Masks alone, in place, on 2048 fp32 rows: 208 us, for sectors that
+// are refused in part and so come from memory and go back.  One row of 32 000: 5.8 us, latency.
 #include <math.h>
 
 #include "../../include/spec_logits.h"
@@ -108,7 +108,7 @@ __device__ __forceinline__ bool unsound(const int32_t *ids, const int32_t *count
 template <typename E, bool SAME>
 __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A, const LogitArgs P) {
     constexpr int VEC = Logit<E>::VEC, STEP = LT * VEC;
-    constexpr int NV = SAME ? 2 : 4;   // 16-byte vectors of a thread on their way at a time (SAME: registers for 8 CTAs count more)
+    constexpr int NV = 4;                 // 16-byte vectors of a thread on their way at a time
     __shared__ int drafts[MAXK];
     __shared__ int range[4];              // this piece's entries of the history and of the biases
     __shared__ int ends[4];               // the request's
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
     const int row = blockIdx.x, V = P.V;
     const int64_t row_at = (int64_t)row * V;
     // elements of the row's first 128 bytes that are not its own: the warps' accesses are whole lines
-    const int lead = (int)((((uintptr_t)P.out & 127) / sizeof(E) + row_at) % (128 / sizeof(E)));
+    const int lead = SAME ? 0 : (int)((((uintptr_t)P.out & 127) / sizeof(E) + row_at) % (128 / sizeof(E)));
     const int c0 = max((int)blockIdx.y * P.piece - lead, 0), c1 = (int)min((int64_t)(blockIdx.y + 1) * P.piece - lead, (int64_t)V);
     if (c0 >= c1) return;
     const E *in = static_cast<const E *>(P.in) + row_at;
@@ -224,37 +224,48 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
         const uint32_t bits = __funnelshift_r(lo, hi, max(v, 0) & 31);
         return (v < 0 ? bits << -v : bits) & ALL;
     };
-    uint32_t lo[NV], hi[NV];   // of the next vectors
+    if (SAME) {
+        // Only refused logits are written: a lane has a word of the mask, and the warp an element a lane of each word in turn
+        // (2048 fp32 rows of 128 256: 208 us; 16 bytes a thread, read first where a part is refused, 232).
+        if (mask)
+            for (int u0 = c0 + warp * 1024; u0 < c1; u0 += LT * 32) {
+                const int first = u0 + lane * 32;
+                uint32_t mine = first < c1 ? ~mask[first >> 5] : 0u;   // refused
+                if (first + 32 > V) mine &= first < V ? 0xffffffffu >> (first + 32 - V) : 0u;
+                if (!__any_sync(0xffffffffu, mine != 0)) continue;
+                E *const at = out + u0 + lane;
 #pragma unroll
-    for (int k = 0; k < NV; k++) words(base + k * STEP, lo[k], hi[k]);
+                for (int k = 0; k < 32; k++)
+                    if (__shfl_sync(0xffffffffu, mine, k) >> lane & 1) at[k * 32] = Logit<E>::down(-INFINITY);
+            }
+    } else {
+        uint32_t lo[NV], hi[NV];   // of the next vectors
+#pragma unroll
+        for (int k = 0; k < NV; k++) words(base + k * STEP, lo[k], hi[k]);
 #pragma unroll 1
-    for (int v0 = base; v0 < c1; v0 += NV * STEP) {
-        uint32_t bits[NV];
+        for (int v0 = base; v0 < c1; v0 += NV * STEP) {
+            uint32_t bits[NV];
 #pragma unroll
-        for (int k = 0; k < NV; k++) {
-            bits[k] = allowed(v0 + k * STEP, lo[k], hi[k]);
-            words(v0 + (NV + k) * STEP, lo[k], hi[k]);
-        }
-        if (SAME) {   // only what a mask refuses a part of is read
+            for (int k = 0; k < NV; k++) {
+                bits[k] = allowed(v0 + k * STEP, lo[k], hi[k]);
+                words(v0 + (NV + k) * STEP, lo[k], hi[k]);
+            }
 #pragma unroll
-            for (int k = 0; k < NV; k++)
-                if (bits[k] && bits[k] != ALL && whole(v0 + k * STEP)) x[k] = *reinterpret_cast<const uint4 *>(in + v0 + k * STEP);
-        }
-#pragma unroll
-        for (int k = 0; k < NV; k++) {
-            const int v = v0 + k * STEP;
-            if (v >= c1 || v + VEC <= 0 || (SAME && bits[k] == ALL)) continue;
-            if (whole(v)) {
-                *reinterpret_cast<uint4 *>(out + v) = bits[k] == ALL ? x[k] : Logit<E>::refuse(x[k], bits[k]);
-            } else {
-                for (int e = 0; e < VEC; e++) {
-                    if (v + e < 0 || v + e >= V) continue;
-                    if (!(bits[k] >> e & 1)) out[v + e] = Logit<E>::down(-INFINITY);
-                    else if (!SAME) out[v + e] = in[v + e];
+            for (int k = 0; k < NV; k++) {
+                const int v = v0 + k * STEP;
+                if (v >= c1 || v + VEC <= 0) continue;
+                if (whole(v)) {
+                    *reinterpret_cast<uint4 *>(out + v) = bits[k] == ALL ? x[k] : Logit<E>::refuse(x[k], bits[k]);
+                } else {
+                    for (int e = 0; e < VEC; e++) {
+                        if (v + e < 0 || v + e >= V) continue;
+                        if (!(bits[k] >> e & 1)) out[v + e] = Logit<E>::down(-INFINITY);
+                        else out[v + e] = in[v + e];
+                    }
                 }
             }
+            fetch(v0 + NV * STEP);
         }
-        if (!SAME) fetch(v0 + NV * STEP);
     }
     __syncthreads();
 
