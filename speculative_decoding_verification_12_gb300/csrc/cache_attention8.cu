@@ -39,7 +39,8 @@
 // head, 8192 keys): the groups' instructions, 11 row tiles of 48 rows; 292 us.  Small calls: latency, 10.8 us.
 //
 // What was slower (256 x 5 rows): two groups taking the tiles of one segment in turn, 432 us at best; one warp issuing
-// both ranges' matrix instructions, 459, at 2000 cycles a tile; barriers polled in tight loops, 463 for 433.
+// both ranges' matrix instructions, 459, at 2000 cycles a tile; barriers polled in tight loops, 463 for 433.  With
+// 64 columns, 16-byte copies by the loading warp instead of tensor copies, 689 for 327.
 #include "sv_cache8.cuh"
 #include "sv_launch.h"
 #include "sv_segments.cuh"
