@@ -76,9 +76,9 @@ typedef struct sv_logit_rules {
  *                does not clear it.
  * A request with a device-data error (SV_DEV_BAD_LAYOUT; SV_DEV_BAD_TOKEN: a draft outside [0, V), where
  * penalties are given; SV_DEV_BAD_PENALTY: one that is not finite, or repetition <= 0; offsets of its
- * history or bias out of range; SV_DEV_BAD_MASK of any of its rows) has NaN rows.  Ids that do not ascend, lie outside [0, V) or have a
- * negative count are reported (SV_DEV_BAD_HISTORY, SV_DEV_BAD_BIAS) but leave open which of the request's logits the
- * penalties and biases reach.
+ * history or bias out of range; SV_DEV_BAD_MASK of any of its rows) has NaN rows.  Ids that do not ascend,
+ * lie outside [0, V) or have a negative count are reported (SV_DEV_BAD_HISTORY, SV_DEV_BAD_BIAS) but leave open
+ * which of the request's logits the penalties and biases reach.
  * Results are the same from call to call.
  */
 sv_status spec_logits(const void *logits, sv_dtype dtype, const int32_t *draft_tokens, const int32_t *num_drafts,

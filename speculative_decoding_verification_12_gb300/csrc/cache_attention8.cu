@@ -18,9 +18,9 @@
 //     which costs less than the columns that parts side by side would take and a thread would have to add;
 //   - a weight in fp16 is a sum of its top byte, the top byte of the rest, and so on: an fp16's top byte is an e5m2
 //     number.  The parts lie side by side along N, so that the values are read once.  2 (3) of them and the rest rounded
-//     to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans 2^-17 to 2^15.8, and the running maximum is kept between 2^12 and 2^15.5, so what is lost of a weight beside its 9 (11) bits
-//     is below 2^-28 of a row's largest.  (e4m3 parts would end 2^-18 below it: 131 072 small weights
-//     would lose a percent of the sum.)
+//     to e5m2 hold 9 bits for bf16 (11, all, for fp16).  e5m2 spans 2^-17 to 2^15.8, and the running maximum is kept
+//     between 2^12 and 2^15.5, so what is lost of a weight beside its 9 (11) bits is below 2^-28 of a row's largest.
+//     (e4m3 parts would end 2^-18 below it: 131 072 small weights would lose a percent of the sum.)
 // The score of a key is c ks_j qs_r S (ks: the key's scale, qs: the row's power of two), and the weight that goes to the
 // product with v is p vs_j: log2 vs_j is added to the exponent, and m is the maximum of the sums.  l adds p alone.
 //
