@@ -162,11 +162,13 @@ __device__ __forceinline__ uint32_t e5m2_of(uint32_t half2) {
     return __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E5M2);
 }
 
-// Four fp16 weights (two pairs of rows) as P parts: part i of them in out[i].  `up` is 1 or 2 in each half: with
-// 3 parts the last 2 of 11 bits go, and a tie between two numbers of 9 bits goes up or down by the key's parity.
+// Four fp16 weights (two pairs of rows) as P parts: part i of them in out[i].  3 parts hold 9 bits, so a weight is rounded to
+// as many first, and a tie goes up or down by the key's parity (`up`: 2 or 1 in each half).  What is added has to be masked
+// away again: the parts hold up to 11 bits of a weight whose bits are not all set, and keep what they can of it, which
+// made every output 7e-4 to 1e-3 too large beside the sum of the weights, which are not rounded there.
 template <int P>
 __device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t up, uint32_t *out) {
-    if (P == 3) a += up, b += up;
+    if (P == 3) a = (a + up) & 0xfffcfffcu, b = (b + up) & 0xfffcfffcu;
 #pragma unroll
     for (int i = 0; i < P; i++) {
         out[i] = __byte_perm(a, b, 0x7531);

@@ -545,3 +545,23 @@ def test_two_graphs_at_once(sv):
     for x, want, _, _ in calls:
         out, _, e = x.results()
         assert e == (0, -1) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_outputs_are_not_larger_or_smaller_on_average(sv, dtype):
+    """Weights are rounded to 9 or 11 bits before their product with the values, and not in the sum that divides it: a
+    rounding with a mean would move every output.  Values of one sign, so that nothing cancels.  The mean of the outputs'
+    relative errors: their own rounding, rms eps / (2 sqrt 3), over 10^5 of them, and the weights', rms 8.5e-4 in bf16, over some
+    50 keys that count in each of 1000 rows, are below 5e-6 each; five times both, and sums in 32 bits of up to
+    400 terms, (400 + 16) 2^-23, are 1e-4 together."""
+    r = random.Random(91)
+    drafts = [r.randint(0, 4) for _ in range(64)]
+    lens = [r.randint(250, 400) for _ in drafts]
+    s = make(91, lens, drafts, 4, 8, 2, 128, 16, 16, dtype)
+    s["vc"].view(torch.uint8).bitwise_and_(127)
+    x = OnGpu(sv, s)
+    x.call()
+    out, _, e = x.results()
+    ro, *_ = reference(s)
+    assert e == (0, -1) and bool((ro > 0).all()) and ro.numel() > 10 ** 5
+    assert abs(float(((out.double() - ro) / ro).mean())) < 1e-4
