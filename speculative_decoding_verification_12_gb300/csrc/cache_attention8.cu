@@ -76,7 +76,9 @@ struct Attn8Args {
     int4 *desc;        // as in AttnArgs, per range
     float *part_lse;   // [2 * MAX_RANGES][PART]
     float *part_o;     // [2 * MAX_RANGES][PART][pitch]
-    float c;           // scale log2(e)
+    float c;           // scale log2(e) 2^shift
+    int shift;         // 64 for a scale so small that its product with a key's scale might have too few bits, else 0: rows
+                       // of bf16's largest numbers, 2^127, need one of 2^-127 for scores of 1
     int withhold;
     int Hq, G, window, sinks;
     int k_stages, v_stages;   // of each range
@@ -630,13 +632,15 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                     for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[e])), finite = finite && fabsf(x[e]) < INFINITY;
                     if (!finite) top = INFINITY;
                     for (int o = lpr / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the power of two 2^k with top in (224, 448] 2^k
+                    // the power of two 2^k with top in (224, 448] 2^k, up to 2^120 for a finite top; rows below 2^-117 have
+                    // 2^-126, where the last bit of a bf16, 2^-133, is 2^-7 and so exact
                     const uint32_t b = __float_as_uint(top);
-                    const int k = min(max((int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7), -118), 118);
+                    const int k = max((int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7), -126);
                     const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
                     if (row >= rp) continue;
                     if (ch == 0) {
-                        sm.q_scale[g][row] = top < INFINITY ? __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
+                        // (2^-126 at least: with a shift the scores are none to speak of there)
+                        sm.q_scale[g][row] = top < INFINITY ? __uint_as_float((uint32_t)max(127 + k - P.shift, 1) << 23) : NAN;
                         sm.q_place[g][row] = at[i];
                     }
 #pragma unroll
@@ -1104,7 +1108,8 @@ extern "C" sv_status spec_attention8(const void *q, sv_dtype dtype, int64_t q_st
     P.desc = reinterpret_cast<int4 *>(w + L.desc);
     P.part_lse = reinterpret_cast<float *>(w + L.lse);
     P.part_o = reinterpret_cast<float *>(w + L.o);
-    P.c = scale * 1.4426950408889634f;
+    P.shift = fabsf(scale) < 0x1p-60f ? 64 : 0;
+    P.c = (P.shift ? scale * 0x1p64f : scale) * 1.4426950408889634f;
     P.withhold = sv::withholding();
     P.Hq = num_q_heads;
     P.G = num_q_heads / cache.num_heads;

@@ -565,3 +565,18 @@ def test_outputs_are_not_larger_or_smaller_on_average(sv, dtype):
     ro, *_ = reference(s)
     assert e == (0, -1) and bool((ro > 0).all()) and ro.numel() > 10 ** 5
     assert abs(float(((out.double() - ro) / ro).mean())) < 1e-4
+
+
+@pytest.mark.parametrize("size,scale", [(127, -128), (127, -129), (120, -121), (-127, 125), (-126, 124), (-120, 120)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_of_every_finite_size(sv, D, size, scale):
+    """Rows around 2^size, up to bf16's largest numbers and down into its subnormal ones, with a scale that makes scores
+    of a few of them; beside them rows of zeros, and of ones, whose scores are next to nothing."""
+    s = make(92, [200, 90, 40], [3, 1, 0], 3, 8, 2, D, 16, 16, "bf16")
+    q = s["q"].double().clamp(-1.9, 1.9) * 2.0 ** size
+    q[0, 0, 3], q[1, 1, 5], q[2, 3] = 1.98 * 2.0 ** size, -1.98 * 2.0 ** size, 0.0
+    if size > 0:
+        q[4, 1] = 1.0
+    s["q"], s["scale"] = q.bfloat16(), 2.0 ** scale
+    assert bool(s["q"].isfinite().all())
+    run_and_check(sv, s)
