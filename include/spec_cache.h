@@ -290,11 +290,11 @@ sv_status spec_append8(const void *q, const void *k, const void *v, sv_dtype dty
 /*
  * spec_attention8 -- spec_attention over a cache in 8 bits.
  *
- * The same formula, with k_j and v_j the stored numbers times their scales.  Queries keep all their
- * bits: a query row is a sum of 8-bit parts that are exact for elements down to 2^-14 of the row's largest,
- * and off by at most 2^-24 of that below.  Scores, softmax and sums are fp32; for the product with v each weight
- * times its value's scale is rounded to 9 bits (SV_BF16) or 11 (SV_F16) and loses up to 2^-28 of the row's
- * largest besides; the output is rounded once.  A query row with an infinity or a NaN gives a NaN row.  The
+ * The same formula, with k_j and v_j the stored numbers times their scales.  A query row is a sum of
+ * 8-bit parts, exact for elements from 2^-13.8 of the row's largest on; smaller ones are off by at most
+ * 2^-21.8 (SV_BF16, two parts) or 2^-24.8 (SV_F16, three) of the largest.  Scores, softmax and sums are fp32; for the
+ * product with v each weight times its value's scale is rounded to 9 bits (SV_BF16) or 11 (SV_F16) and loses up to
+ * 2^-28 of the row's largest besides; the output is rounded once.  A query row with an infinity or a NaN gives a NaN row.  The
  * lse is as good as spec_attention's.
  *
  *   dtype        of q and out: SV_BF16 or SV_F16.

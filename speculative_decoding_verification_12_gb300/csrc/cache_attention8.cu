@@ -11,10 +11,11 @@
 // Few rows then cost few columns, and all warps of a softmax group have work: a thread has one
 // key and half of the rows, so a key's scale is a register and the sum of a row is spread over the threads until the end.
 // The B operands are sums of 8-bit parts:
-//   - a query row, times the power of two that brings its largest element into (224, 448], is q0 + q1 + q2 with
-//     q0 = RN(q) in e4m3, 4 bits, q1 = RN(q - q0) and q2 = RN(q - q0 - q1) in e5m2, 3 bits and a sign each: 10 bits and two
-//     signs hold a bf16 and an fp16 without loss, for elements down to 2^-14 of the largest, and the smallest step of
-//     e5m2 leaves 2^-24 of it below.  They are added up along K, in one accumulator: the keys are read three times,
+//   - a query row, times the power of two that brings its largest element into (224, 448], is q0 + q1 (+ q2 for fp16) with
+//     q0 = RN(q) in e4m3, 4 bits, q1 = RN(q - q0) and q2 = RN(q - q0 - q1) in e5m2, 3 bits and a sign each: 4 + 1 + 3 (+ 1 + 3)
+//     bits hold the 8 of a bf16 (11 of an fp16) without loss from 2^-6 on, 2^-13.8 of the row's largest.  Below, q0 has
+//     steps of 2^-9, and what is left, 2^-10 or less, is held to 2^-14 (2^-17 by two parts): 2^-21.8 (2^-24.8) of the largest.
+//     The parts are added up along K, in one accumulator: the keys are read twice (three times),
 //     which costs less than the columns that parts side by side would take and a thread would have to add;
 //   - a weight in fp16 is a sum of its top byte, the top byte of the rest, and so on: an fp16's top byte is an e5m2
 //     number.  The parts lie side by side along N, so that the values are read once.  2 (3) of them and the rest rounded

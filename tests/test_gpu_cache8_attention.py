@@ -580,3 +580,35 @@ def test_queries_of_every_finite_size(sv, D, size, scale):
     s["q"], s["scale"] = q.bfloat16(), 2.0 ** scale
     assert bool(s["q"].isfinite().all())
     run_and_check(sv, s)
+
+
+# what spec_cache.h states of a query's parts: exact from this share of a row's largest element on, and off by that share below
+EXACT_FROM, PARTS_OFF = 2.0 ** -13.8, {"bf16": 2.0 ** -21.8, "fp16": 2.0 ** -24.8}
+
+
+@pytest.mark.parametrize("top", [226.0, 448.0, 337.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_query_element_keeps_its_bits(sv, dtype, top):
+    """All numbers of the type up to the row's largest.  One key, 1 at the element in question and 0 at the largest, so that
+    the lse is the score: the element times 2^20, and off by 2^-21 of itself and of the kernel's largest exponent, 12,
+    in fp32."""
+    dt, G, scale = DT[dtype], 1024, 2.0 ** 20
+    x = torch.arange(0, 1 << 15).to(torch.int16).view(dt)
+    x = x[x.double() <= top]
+    R = -(-len(x) // G)
+    q = torch.zeros(R * G, 1, 64, dtype=dt)
+    q[:len(x), 0, 1], q[:, 0, 0] = x, top
+    one = torch.zeros(1, 8, 1, 64)
+    one[0, 0, 0, 1] = 1.0
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    kc, ks = one.to(E4M3).cuda(), torch.ones(1, 1, 1, device="cuda")
+    out, lse = torch.empty(R, G, 64, dtype=dt, device="cuda"), torch.empty(R, G, device="cuda")
+    ws = torch.zeros(sv.sv_attention_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+    sv.spec_attention8(q.view(R, G, 64).cuda(), kc, kc, ks, ks, ints(*[0] * R).view(R, 1), ints(*[1] * R), ints(*[0] * R), None,
+                       0, scale, 0, 0, out, lse, ws)
+    assert sv.sv_read_device_error(ws) == (0, -1)
+    want = x.double() * scale
+    off = (lse.cpu().double().flatten()[:len(x)] - want).abs()
+    fp32 = 2.0 ** -21 * (want + 12)
+    assert bool((off <= fp32)[x.double() >= EXACT_FROM * top].all())
+    assert bool((off <= fp32 + PARTS_OFF[dtype] * top * scale).all())
