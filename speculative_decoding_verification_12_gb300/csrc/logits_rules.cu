@@ -71,12 +71,14 @@ struct Logit<float> {
     }
 };
 
+// Entries of the lists are counted without a sign: lists may hold 2^31 - 1, and steps and sums go past that.
+
 // First index in [lo, hi) of an ascending list whose id is >= v (hi: none).  A whole warp, 32 ids at a time.
-__device__ __forceinline__ int first_at(const int32_t *ids, int lo, int hi, int v) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint32_t first_at(const int32_t *ids, uint32_t lo, uint32_t hi, int v) {
+    const uint32_t lane = threadIdx.x & 31;
     while (lo < hi) {
-        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const int below = __popc(__ballot_sync(0xffffffffu, i < hi && ids[i] < v));   // of lo, lo + step, ...
+        const uint32_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const uint32_t below = __popc(__ballot_sync(0xffffffffu, i < hi && ids[i] < v));   // of lo, lo + step, ...
         if (below == 0) return lo;
         hi = min(hi, lo + below * step);
         lo += (below - 1) * step + 1;
@@ -84,10 +86,11 @@ __device__ __forceinline__ int first_at(const int32_t *ids, int lo, int hi, int 
     return lo;
 }
 // Index of v in an ascending list, or -1.  One thread.
-__device__ __forceinline__ int find(const int32_t *ids, int lo, int hi, int v) {
+__device__ __forceinline__ int find(const int32_t *ids, uint32_t lo, uint32_t hi, int v) {
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1, x = ids[mid];
-        if (x == v) return mid;
+        const uint32_t mid = (lo + hi) >> 1;
+        const int x = ids[mid];
+        if (x == v) return (int)mid;
         if (x < v) lo = mid + 1;
         else hi = mid;
     }
@@ -95,9 +98,9 @@ __device__ __forceinline__ int find(const int32_t *ids, int lo, int hi, int v) {
 }
 
 // Checks a request's list [lo, hi): ascending ids in [0, V), counts (if any) >= 0.  A whole CTA.
-__device__ __forceinline__ bool unsound(const int32_t *ids, const int32_t *counts, int lo, int hi, int V) {
+__device__ __forceinline__ bool unsound(const int32_t *ids, const int32_t *counts, uint32_t lo, uint32_t hi, int V) {
     bool bad = false;
-    for (int e = lo + (int)threadIdx.x; e < hi; e += LT) {
+    for (uint32_t e = lo + threadIdx.x; e < hi; e += LT) {
         const int v = ids[e];
         bad |= v < 0 || v >= V || (e > lo && ids[e - 1] >= v) || (counts && counts[e] < 0);
     }
@@ -301,13 +304,13 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
         out[v] = Logit<E>::down(z);
     };
     auto here = [&](int v) { return v >= c0 && v < c1; };
-    for (int e = p0 + tid; e < p1; e += 4 * LT) {   // (four entries' loads at a time: 512 requests of 1500 tokens 363 us one by one)
+    for (uint32_t e = p0 + tid; e < (uint32_t)p1; e += 4 * LT) {   // (four entries' loads at a time: 512 requests of 1500 tokens 363 us one by one)
         int v[4], count[4];
         float z[4];
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            v[k] = e + k * LT < p1 ? P.r.prior_tokens[e + k * LT] : -1;
-            count[k] = e + k * LT < p1 ? max(P.r.prior_counts[e + k * LT], 0) : 0;
+            v[k] = e + k * LT < (uint32_t)p1 ? P.r.prior_tokens[e + k * LT] : -1;
+            count[k] = e + k * LT < (uint32_t)p1 ? max(P.r.prior_counts[e + k * LT], 0) : 0;
         }
 #pragma unroll
         for (int k = 0; k < 4; k++) z[k] = here(v[k]) ? Logit<E>::up(in[v[k]]) : 0.f;
@@ -322,14 +325,14 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
     __syncthreads();
     if (mine && here(drafts[tid])) put(drafts[tid], Logit<E>::up(in[drafts[tid]]), -1, -2);
     __syncthreads();
-    for (int e = b0 + tid; e < b1; e += LT) {
+    for (uint32_t e = b0 + tid; e < (uint32_t)b1; e += LT) {
         const int v = kept ? bias_ids[e - b0] : P.r.bias_tokens[e];
         bool other = kept && bias_done[e - b0];
         if (!kept) {
             for (int j = 0; j < nd && !other; j++) other = drafts[j] == v;
             other = other || find(P.r.prior_tokens, p0, p1, v) >= 0;
         }
-        if (!other && here(v)) put(v, Logit<E>::up(in[v]), -1, e);
+        if (!other && here(v)) put(v, Logit<E>::up(in[v]), -1, (int)e);
     }
     // the request's first row reports what is wrong with its lists
     if (i == 0 && blockIdx.y == 0) {

@@ -389,3 +389,30 @@ def test_two_graphs_at_once(sv):
     torch.cuda.synchronize()
     for s, out, _, _, _ in calls:
         check(s, out.cpu(), rows=plain(s)[4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_lists_that_end_at_the_last_index(sv, dtype):
+    """Entries up to number 2^31 - 2 of each list, with more biases in a piece than are kept beside it and histories of
+    several passes of a CTA: the same bits as from lists that begin at 0.  The lists are views of one buffer of 9 GB, each
+    a few thousand entries further on, so that their ends lie side by side."""
+    s = make(24, [5, 3], 5, 4099, dtype, history=4000, bias=4000)
+    n, apart = 2 ** 31 - 1, 8192
+    assert min(s[x][0].diff().min() for x in ("prior", "bias")) > 1500 and max(len(s[x][1]) for x in ("prior", "bias")) < apart
+    want, _ = call(sv, s)
+    buffer = torch.empty(n + 4 * apart, dtype=torch.int32, device="cuda")
+    at = 0
+    for name in ("prior", "bias"):
+        o, t, v = s[name]
+        views = []
+        for x in (t, v):
+            view = buffer[at:at + n]
+            view[n - len(x):] = x.view(torch.int32).cuda()
+            views.append(view.view(x.dtype))
+            at += apart
+        s[name] = (o + (n - len(t)), *views)
+    for in_place in (False, True):
+        out, e = call(sv, s, in_place)
+        assert e == (0, -1)
+        used = torch.cat([torch.arange(int(a), int(b)) for a, b in zip(s["ro"], s["ro"][1:])])
+        assert torch.equal(out[used], want[used])
