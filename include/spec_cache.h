@@ -272,9 +272,10 @@ typedef struct sv_kv_cache8 {
  * finite element x of it; a block that holds tokens of the request from before keeps its scale where that
  * is larger, and where it is smaller the tokens from before are rewritten in the new one.  Each
  * element is then the nearest e4m3 number to x / s (ties to even; |x| > 448 s, at the upper bound of s
- * only, becomes 448 s); what is not finite becomes NaN.  Rewriting in a scale that is a larger power of two
- * loses what falls below 2^-9 s and nothing else, so a block does not lose precision with every token
- * that joins it.  Tokens that a rollback took back leave their scale: it falls when their block is begun anew.
+ * only, becomes 448 s); what is not finite becomes NaN.  A kept scale may be any (a block filled from
+ * elsewhere).  Rewriting from one power of two to a larger one loses what falls below 2^-9 s and nothing else, so
+ * a block does not lose precision with every token that joins it; rewriting from another scale rounds its numbers once
+ * more, to the nearest.  Tokens that a rollback took back leave their scale: it falls when their block is begun anew.
  * The appended tokens' blocks are the request's own (a shared page is always full).
  *
  *   dtype        of q, k, v, the weights and out_q: SV_BF16 or SV_F16.

@@ -5,7 +5,8 @@
 // holds its new elements, or the one it has where it holds older tokens and has a larger one; stored is
 // RN(x / s).  With powers of two, x / s only shifts the exponent, so rewriting older tokens in a grown
 // scale rounds nothing but what falls into e4m3's subnormal numbers: a block that grows with every
-// token is as exact as one that was written at once.  The largest magnitude has to be known before the first
+// token is as exact as one that was written at once.  (A kept scale that is no power of two divides, and is
+// rewritten by a product, both rounded to odd first: see over_odd.)  The largest magnitude has to be known before the first
 // element is rounded, so the new tokens of a block and head belong to one warp.
 //
 // Work.  One or more CTAs per request.  A warp takes a task at a time: the new tokens of one block of one key
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
         float *at = (is_v ? C.v_scale : C.k_scale) + page * C.s_page + (slot0 >> C.block_shift) * C.s_block + h * C.s_head;
         const float had = older ? clean_scale(*at) : 0.f;
         const int batches = (count + STEPS * HPW - 1) / (STEPS * HPW);
-        float amax = 0.f, inv = 0.f;
+        float amax = 0.f, scale = 1.f, inv = 0.f;
         // the elements' maximum, then (again, unless they are all still here) their numbers
         for (int it = 0; it < (batches == 1 ? 1 : 2 * batches); it++) {
             const int i0 = (it < batches ? it : it - batches) * STEPS * HPW + team;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
             if (it == batches - 1) {
 #pragma unroll
                 for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float scale = fmaxf(scale_for(amax), had);
+                scale = fmaxf(scale_for(amax), had);
                 inv = 1.f / scale;
                 if (lane == 0) *at = scale;
                 if (scale > had && older) {   // older tokens in the grown scale
@@ -218,21 +219,27 @@ __global__ void __launch_bounds__(AT8) append8_kernel(const Batch A, const Cache
                         uint32_t *p = reinterpret_cast<uint32_t *>(to + t * C.token_stride) + (i - t * words);
                         const uint32_t v = *p;
                         const float2 a = unpack_e4m3(v & 0xffffu), z = unpack_e4m3(v >> 16);
-                        *p = pack_e4m3(a.x * f, a.y * f) | pack_e4m3(z.x * f, z.y * f) << 16;
+                        *p = pack_e4m3(times_odd(a.x, f), times_odd(a.y, f)) | pack_e4m3(times_odd(z.x, f), times_odd(z.y, f)) << 16;
                     }
                 }
             }
             if (it < batches && batches > 1) continue;
+            // a power of two shifts; a kept scale that is none (from elsewhere) divides
+            const bool shifts = !(__float_as_uint(scale) & 0x7fffffu);
+            const float by = shifts ? inv : 1.f;
 #pragma unroll
             for (int e = 0; e < STEPS; e++) {
                 const int i = i0 + e * HPW;
                 if (!in || i >= count) break;
-                const float *y = reinterpret_cast<const float *>(x[e]);
+                float *y = reinterpret_cast<float *>(x[e]);
+                if (!shifts)
+#pragma unroll
+                    for (int d = 0; d < 8; d++) y[d] = over_odd(y[d], scale);
                 uint32_t two[4];
 #pragma unroll
                 for (int d = 0; d < 4; d++) {
                     const float a = y[2 * d], z = y[2 * d + 1];
-                    two[d] = pack_e4m3(fabsf(a) < INFINITY ? a * inv : NAN, fabsf(z) < INFINITY ? z * inv : NAN);
+                    two[d] = pack_e4m3(fabsf(a) < INFINITY ? a * by : NAN, fabsf(z) < INFINITY ? z * by : NAN);
                 }
                 uint8_t *head = to + (older + i) * C.token_stride;
                 if (PAIR != PAIR_HALVES) {

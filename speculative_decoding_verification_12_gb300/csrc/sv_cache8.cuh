@@ -31,6 +31,17 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float((uint32_t)(min(max(k, -40), 40) + 127) << 23);
 }
 
+// x / s and x f, cut off, and with the last bit set where anything was: what is rounded from there to a few bits is
+// rounded once, from the exact value (the nearest fp32 number may be a tie of e4m3's that x / s is not).
+__device__ __forceinline__ float over_odd(float x, float s) {
+    const float q = __fdiv_rz(x, s);
+    return fmaf(-q, s, x) != 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;   // (the rest is exact)
+}
+__device__ __forceinline__ float times_odd(float x, float f) {
+    const float p = __fmul_rz(x, f);
+    return fmaf(x, f, -p) != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+
 // Two numbers as e4m3, nearest (ties to even), magnitudes above 448 as 448, not a number as NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

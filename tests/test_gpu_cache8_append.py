@@ -336,3 +336,54 @@ def test_two_graphs_at_once(sv):
     torch.cuda.synchronize()
     for want, got, _, _, _ in calls:
         assert all(torch.equal(got[n].cpu(), want[n]) for n in want)
+
+
+def uneven_scales():
+    """Scales that are no powers of two: simple ones, and fp32 neighbours of x / t for ties t of e4m3's, so that x / s (and
+    older numbers in a grown scale, n s / s') is a tie once it is rounded to fp32 and none before."""
+    some = [1.75, 1.25, 3.0, 1.1, 1 + 2.0 ** -23, 2 - 2.0 ** -23, 1.7]
+    some += [x / t for x in (129, 167, 201, 251) for t in (17, 19, 25, 31)]
+    some += [t / n for n in (9, 11, 13, 15) for t in (1.5, 2.5, 17, 25, 31)]
+    return [float(torch.tensor(s, dtype=torch.float32)) / 64 for s in some]
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("fp16", 128)])
+@pytest.mark.parametrize("grow", [False, True])
+def test_kept_scales_that_are_no_powers_of_two(sv, dtype, D, grow):
+    """Every new number is the nearest to x / s with the kept scale (ties of x / s to even, and no others), and every older one
+    to n s / s' where the scale grows.  No norm and no rotation: the elements are known exactly."""
+    had = uneven_scales()
+    B = len(had)
+    s = make(17, [23] * B, [2] * B, 2, 1, 1, D, 32, 32, dtype, 0, norm=False)
+    g = torch.Generator().manual_seed(18)
+    for b, h in enumerate(had):
+        page = int(s["table"][b, 0])
+        s["ks"][page] = s["vs"][page] = h
+        codes = torch.randint(0, 256, (20, D), generator=g, dtype=torch.uint8)
+        s["kc"].view(torch.uint8)[page, :20, 0] = s["vc"].view(torch.uint8)[page, :20, 0] = codes
+    ties = torch.tensor([(n + 0.5) * 2.0 ** e for n in range(8, 16) for e in range(-9, 4)] + [(n + 0.5) * 2.0 ** -9 for n in range(8)])
+    for n in "kv":
+        x = torch.tensor([129.0, 167, 201, 251])[torch.randint(0, 4, s[n].shape, generator=g)] * torch.exp2(
+            torch.randint(-15, 0, s[n].shape, generator=g).float())
+        near = ties[torch.randint(0, len(ties), s[n].shape, generator=g)] * torch.tensor(had).repeat_interleave(3)[:, None, None]
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.5, x / 64, near)
+        x = torch.minimum(x, 220 * torch.tensor(had).repeat_interleave(3)[:, None, None])    # (a power of two below it holds them)
+        if grow:                           # past 448 of the scale, by powers of two up to where older numbers are ties below 2^-6
+            x[:, :, 0] = 1000.0 * torch.exp2(torch.arange(len(x)).float() % 7)[:, None] * torch.tensor(had).repeat_interleave(3)[:, None]
+        s[n] = (x * torch.sign(torch.randn(x.shape, generator=g))).to(s["dt"])
+    got = run_and_check(sv, s)
+    for n, data, scales in (("k", "kc", "ks"), ("v", "vc", "vs")):
+        numbers = got[data].view(E4M3).double()
+        for b, h in enumerate(had):
+            page = int(s["table"][b, 0])
+            scale = float(got[scales][page, 0, 0])
+            assert (scale != h and scale == 2.0 ** round(plain8.math.log2(scale))) if grow else scale == h
+            want = [[plain8.nearest(x / scale) for x in row] for row in s[n][3 * b:3 * b + 3, 0].double().tolist()]
+            assert torch.equal(numbers[page, 20:23, 0], torch.tensor(want, dtype=torch.float64)), (n, h)
+            was = s[data].view(torch.uint8)[page, :20, 0].view(E4M3).double().nan_to_num(999.0)
+            now = numbers[page, :20, 0].nan_to_num(999.0)
+            if not grow:
+                assert torch.equal(was, now)
+                continue
+            want = [[x if x == 999.0 else plain8.nearest(x * h / scale) for x in row] for row in was.tolist()]
+            assert torch.equal(now, torch.tensor(want, dtype=torch.float64)), (n, h)
