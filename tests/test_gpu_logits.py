@@ -416,3 +416,22 @@ def test_lists_that_end_at_the_last_index(sv, dtype):
         assert e == (0, -1)
         used = torch.cat([torch.arange(int(a), int(b)) for a, b in zip(s["ro"], s["ro"][1:])])
         assert torch.equal(out[used], want[used])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("name,code", [("prior", 8), ("bias", 12)])
+def test_offsets_out_of_range_stay_with_their_requests(sv, name, code, in_place):
+    """Past the end, below 0 and decreasing: rows of NaN for the requests whose offsets those are, the others' as ever."""
+    rows = [[0, 1, 2], [3, 4, 5, 6], [7, 8]]
+    for change, bad, sound in (({2: 5}, [1, 2], [0]), ({3: 1}, [2], [0, 1]), ({3: 2 ** 31 - 1}, [2], [0, 1]), ({0: -1}, [0], [1, 2]),
+                               ({0: -2 ** 31}, [0], [1, 2]), ({2: -1}, [1, 2], [0]), ({2: "less"}, [1], [0])):
+        s = make(13, [2, 3, 1], 3, 600, "bf16")
+        o = s[name][0].clone()
+        assert o[2] > o[1] > 0
+        for i, x in change.items():
+            o[i] = int(o[1]) - 1 if x == "less" else x if x < 0 or x == 2 ** 31 - 1 else len(s[name][1]) + x
+        out, e = call(sv, {**s, name: (o, *s[name][1:])}, in_place)
+        assert e == (code, bad[0]), change
+        for b in bad:
+            assert bool(out[rows[b]].isnan().all()), (change, b)
+        check(s, out, in_place, rows=sum((rows[b] for b in sound), []))
