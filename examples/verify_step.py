@@ -155,8 +155,8 @@ class Server:
 
 
 def run(slots=6, prompt=20, steps=8, k=4, seed=1, dtype=torch.bfloat16, ruled=False):
-    """Runs the server, over a cache of the given type and, with `ruled`, under the rules; returns (sequences, the largest gap by which a chosen token's plain logit lies
-    below the plain maximum, accepted drafts per step)."""
+    """Runs the server, over a cache of the given type and, with `ruled`, under the rules; returns (sequences, the
+    largest gap by which a chosen token's plain logit lies below the plain maximum, accepted drafts per step)."""
     model = Decoder()
     rules = Rules(model.vocab) if ruled else None
     server = Server(model, slots, k, dtype=dtype, rules=rules)

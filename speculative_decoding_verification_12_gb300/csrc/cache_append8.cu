@@ -13,9 +13,12 @@
 // or value head (LPH lanes a token, so 2 or 4 tokens side by side, up to 4 such steps kept in registers
 // between the maximum and the rounding, more are computed twice), or 2 or 4 query heads of a row.
 //
-// What bounds it: issue and one wave's latency.  256 x 5 rows of 32 + 2 x 8 heads of 128 take 15.6 us in a graph (18.8 with
-// inputs that are not in L2; 28 MB, 4.2 us at the memory's rate), where a request is 32 000 warp instructions and a CTA's
-// chain is offsets -> length -> page -> rotations -> tasks; one row takes 4.2 us, the launch.  Integer divisions between
+// What bounds it: loads that a task begins with and waits for, with 16 warps a multiprocessor to cover them.  256 x 5 rows of
+// 32 + 2 x 8 heads of 128 take 15.9 us in a graph (19.0 with inputs that are not in L2; 28 MB, 4.2 us at the memory's
+// rate), where a request is 30 200 warp instructions and a CTA's chain is offsets -> length -> page -> rotations -> tasks;
+// the schedulers issue in 36 % of the cycles.  append_kernel, whose threads keep their elements' weights and rotations
+// over all heads, does the same rows in 16 bits in 9.3 us: queries need not be tasks of these warps, and 4096 x 1 rows (89.8 us
+// for 26.4) show it most.  One row takes 4.3 us, the launch.  Integer divisions between
 // tasks, and one per pair of the rotations, were a tenth of the instructions (17.7 us).  Asking for the next task's elements
 // before this one's are worked on: 19.7, the registers then leave fewer CTAs; 8 warps a CTA: 16.9.
 #include "sv_cache8.cuh"

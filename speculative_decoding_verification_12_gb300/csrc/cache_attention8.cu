@@ -33,11 +33,12 @@
 // all of them.
 //
 // What bounds it.  Few rows: the cache's bytes; 256 requests of one row (4 query heads a key head) over 4096 keys of 8
-// heads of 128 take 328 us, 317 at the memory's rate.  More rows: the chain of a softmax group from a tile's scores to
-// the next one's; with 5 rows a request 365 us, about 3200 cycles a tile and group, while the schedulers issue in 54 %
-// of the cycles and the tensor pipe works in 18.  Heads of 64 columns: the tensor copies, 16 rows of 64 bytes each with
-// pages of 16 (one row a request: 286 us; 237 with pages of 256).  Long chains (16 x 65 rows, 8 query heads a key
-// head, 8192 keys): the groups' instructions, 11 row tiles of 48 rows; 292 us.  Small calls: latency, 10.8 us.
+// heads of 128 take 323 us, 317 at the memory's rate (620 in 16 bits).  More rows: the chain of a softmax group from a tile's
+// scores to the next one's; with 5 rows a request 365 us, about 3200 cycles a tile and group, while the schedulers issue in
+// 54 % of the cycles and the tensor pipe works in 18.  One request of 131 071 keys: the same chain, 27 tiles a range at 1.7 us
+// of the 62.  Heads of 64 columns: the tensor copies, 16 rows of 64 bytes each with pages of 16 (one row a request: 290 us;
+// 238 with pages of 256).  Long chains (16 x 65 rows, 8 query heads a key head, 8192 keys): the groups' instructions, 11 row
+// tiles of 48 rows; 294 us, where the 16-bit kernel's tiles of 128 rows take 161.  Small calls: latency, 11 us.
 //
 // What was slower (256 x 5 rows): two groups taking the tiles of one segment in turn, 432 us at best; one warp issuing
 // both ranges' matrix instructions, 459, at 2000 cycles a tile; barriers polled in tight loops, 463 for 433.  With
@@ -565,7 +566,8 @@ attention8_kernel(const Batch A, const Cache8 C, const Attn8Args P, const __grid
                 if (n_o < n_s && mbar_test(bar(sm.p_full[w]), n_o & 1) && mbar_test(bar(sm.v_full[w][vs.stage]), vs.parity)) there |= 2;
                 there = __reduce_and_sync(0xffffffffu, there);
                 if (there & 2) product();
-                const bool next = (there & 1) && (n_s == n_o || !(*reinterpret_cast<volatile int *>(&sm.k_info[w][ks.stage]) & INFO_FIRST));
+                const bool next = (there & 1) &&
+                                  (n_s == n_o || !(*reinterpret_cast<volatile int *>(&sm.k_info[w][ks.stage]) & INFO_FIRST));
                 if (next) scores();
                 if (next || there & 2) {
                     idle_since = 0;

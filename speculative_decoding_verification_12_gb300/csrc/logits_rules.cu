@@ -14,7 +14,9 @@
 // What bounds it: memory, and the entries: 1280 bf16 rows of 128 256 are copied in 100 us (97 % of the memory's rate), with
 // 1000 tokens of history and 16 biases a request in 123, with masks on half the rows besides in 128.  (Bringing a piece's
 // entries into shared memory during its copy: 134.)  Masks alone, in place, on 2048 fp32 rows: 208 us, for sectors that
-// are refused in part and so come from memory and go back.  One row of 32 000: 5.8 us, latency.
+// are refused in part and so come from memory and go back.  In place with lists, the 1280 rows take 77 us (masks on half of
+// them) and 2500 rows of 151 937 with 1500 tokens of history each 140, four times what their sectors need, probably for the
+// entries' loads in turn.  One row of 32 000: 5.8 us, latency.
 #include <math.h>
 
 #include "../../include/spec_logits.h"
