@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(LT, SAME ? 8 : 5) logits_kernel(const Batch A,
     // the entries of this piece
     const float rep = P.r.repetition ? P.r.repetition[b] : 1.f, presence = P.r.presence ? P.r.presence[b] : 0.f,
                 frequency = P.r.frequency ? P.r.frequency[b] : 0.f;
+    // (p0 <= p1 and b0 <= b1 also in lists that do not ascend: what first_at counts can only grow with v)
     const int p0 = range[0], p1 = range[1], b0 = range[2], b1 = range[3];
     const int nd = P.penalties ? i : 0;
     const bool kept = b1 - b0 <= BIASES;

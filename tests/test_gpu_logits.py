@@ -435,3 +435,19 @@ def test_offsets_out_of_range_stay_with_their_requests(sv, name, code, in_place)
         for b in bad:
             assert bool(out[rows[b]].isnan().all()), (change, b)
         check(s, out, in_place, rows=sum((rows[b] for b in sound), []))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_long_lists_in_any_order_stay_with_their_request(sv, dtype):
+    """Shuffled lists of some thousand entries, over several pieces of a row: reported, and the other request's rows as ever."""
+    for name, code in (("prior", 8), ("bias", 12)):
+        for how in ("shuffled", "reversed"):
+            s = make(24, [5, 3], 5, 4099, dtype, history=4000, bias=4000)
+            o, t, v = s[name]
+            lo, hi = int(o[1]), int(o[2])
+            order = torch.arange(lo, hi).flip(0) if how == "reversed" else lo + torch.randperm(hi - lo, generator=torch.Generator().manual_seed(1))
+            t = t.clone()
+            t[lo:hi] = t[order]
+            out, e = call(sv, {**s, name: (o, t, v)})
+            assert e == (code, 1), (name, how)
+            check(s, out, rows=[0, 1, 2, 3, 4, 5])
